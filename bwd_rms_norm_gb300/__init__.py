@@ -31,6 +31,12 @@ The functions carry the names of the C entry points declared in
   ``(dx, dgamma, dbeta)`` (x of shape [n, channels, *spatial])
 * ``layer_norm_fwd(x, gamma, beta, eps)`` -> ``(y, mean, rstd)``
 * ``layer_norm_bwd(dy, x, gamma, mean, rstd)`` -> ``(dx, dgamma, dbeta)``
+* ``rms_norm_block_fwd(x, residual, post_gamma, gate, next_gamma, eps, ...)``
+  -> ``(residual_out, y, rstd_post, rstd_next)``; ``rms_norm_block_bwd(dy,
+  dresidual_out, x, residual_out, rstd_post, rstd_next, ...)`` -> ``(dx,
+  dresidual, dpost, dgate, dnext)``;
+  ``rms_norm_block_bwd_workspace_size(rows, hidden, gate_rows)`` (the norms
+  after and before a block with its gate and the scaled residual sum)
 
 For autograd: ``rms_norm(x, weight, eps, offset=0, cast_mode="round_once")``
 (a ``torch.autograd.Function`` over rms_norm_fwd / rms_norm_bwd) and the
@@ -38,6 +44,7 @@ module ``RMSNorm(hidden, eps, offset=0, cast_mode="round_once")``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -54,6 +61,7 @@ RMSN_OK = 0
 RMSN_MAX_HIDDEN = 65536
 RMSN_MAX_PARTIALS = 1024
 RMSN_DW_CHUNK_BLOCKS = 32
+RMSN_BLOCK_MAX_PARTIALS = 608
 
 DTYPE_CODES = {torch.float32: RMSN_F32, torch.bfloat16: RMSN_BF16, torch.float16: RMSN_F16}
 CAST_MODES = {"round_once": RMSN_ROUND_ONCE, "round_twice": RMSN_ROUND_TWICE}
@@ -85,6 +93,9 @@ EXPORTED = (
     "group_norm_fwd",
     "group_norm_bwd_workspace_size",
     "group_norm_bwd",
+    "rms_norm_block_fwd",
+    "rms_norm_block_bwd_workspace_size",
+    "rms_norm_block_bwd",
 )
 
 
@@ -162,6 +173,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.layer_norm_bwd_workspace_size.restype = SZ
     lib.layer_norm_bwd.argtypes = [P, P, P, P, P, P, P, P, I64, I64, I, P, SZ, P]
     lib.layer_norm_bwd.restype = I
+    lib.rms_norm_block_fwd.argtypes = [P, P, P, P, I64, P, P, P, P, P, I64, I64, F, F, F, I, I, I,
+                                       P]
+    lib.rms_norm_block_fwd.restype = I
+    lib.rms_norm_block_bwd_workspace_size.argtypes = [I64, I64, I64]
+    lib.rms_norm_block_bwd_workspace_size.restype = SZ
+    lib.rms_norm_block_bwd.argtypes = [P, P, P, P, P, P, I64, P, P, P, P, P, P, P, P, I64, I64, F,
+                                       F, I, I, I, P, SZ, P]
+    lib.rms_norm_block_bwd.restype = I
     _lib = lib
     return lib
 
@@ -701,6 +720,169 @@ def group_norm_bwd(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, mean:
     return dx, dgamma, (dbeta if with_dbeta else None)
 
 
+@contextlib.contextmanager
+def _on(device: torch.device, stream: Optional[torch.cuda.Stream]):
+    """``device`` current, and ``stream`` if one is given, so that what a call
+    allocates belongs to the stream that uses it; yields the stream's handle."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device).cuda_stream
+        else:
+            if stream.device != device:
+                raise RuntimeError(f"stream is on {stream.device}, the tensors on {device}")
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
+
+
+def _check_block(x, stream_name, stream, post_gamma, gate, next_gamma) -> Tuple[int, int, int]:
+    """Checks shared by the block-norm calls; returns (rows, hidden, gate rows)."""
+    if x.dtype not in DTYPE_CODES:
+        raise RuntimeError(f"x must be float32, bfloat16 or float16, not {x.dtype}")
+    if post_gamma is None and next_gamma is None:
+        raise RuntimeError("post_gamma and next_gamma are both None: nothing to normalise")
+    rows, hidden = _as_rows(x)
+    if stream is not None and stream.dtype != torch.float32:
+        _check_like(stream_name, stream, x.dtype, x.numel(), x.shape)
+    else:
+        _check_like(stream_name, stream, torch.float32, x.numel(), x.shape)
+    _check_like("post_gamma", post_gamma, x.dtype, hidden, (hidden,))
+    _check_like("next_gamma", next_gamma, x.dtype, hidden, (hidden,))
+    gate_rows = 0
+    if gate is not None:
+        if gate.dim() < 1 or gate.shape[-1] != hidden:
+            raise RuntimeError(f"gate must have {hidden} columns, not shape {tuple(gate.shape)}")
+        gate_rows = gate.numel() // hidden if hidden > 0 else 0
+        _check_like("gate", gate, x.dtype, gate_rows * hidden)
+        if gate_rows < 1 or rows % gate_rows or gate_rows > max(rows, 1):
+            raise RuntimeError(f"gate has {gate_rows} rows, which do not divide the {rows} rows "
+                               "of x")
+    return rows, hidden, gate_rows
+
+
+def rms_norm_block_fwd(x: torch.Tensor, residual: torch.Tensor,
+                       post_gamma: Optional[torch.Tensor] = None,
+                       gate: Optional[torch.Tensor] = None,
+                       next_gamma: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                       offset: int = 0, residual_scale: float = 1.0, branch_scale: float = 1.0,
+                       residual_out: Optional[torch.Tensor] = None,
+                       y: Optional[torch.Tensor] = None,
+                       rstd_post: Optional[torch.Tensor] = None,
+                       rstd_next: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None):
+    """The norms after and before a block, its gate and the residual sum:
+    ``r = residual_scale * residual + branch_scale * gate * norm(x, post_gamma)``
+    and ``y = norm(r, next_gamma)``.  ``x`` is the block's output; ``residual``
+    has its shape and its dtype, or float32.  Either gamma may be None (no norm
+    of x; no y).  ``gate`` is ``[hidden]``, or ``[..., hidden]`` with a number
+    of rows that divides x's: each run of rows / gate rows consecutive rows of
+    x uses one.  Returns ``(r, y, rstd_post, rstd_next)``, None for what a
+    missing norm would give."""
+    lib = load_library()
+    rows, hidden, gate_rows = _check_block(x, "residual", residual, post_gamma, gate, next_gamma)
+    _check_like("residual_out", residual_out, residual.dtype, x.numel(), x.shape)
+    _check_like("y", y, x.dtype, x.numel(), x.shape)
+    _check_like("rstd_post", rstd_post, torch.float32, rows)
+    _check_like("rstd_next", rstd_next, torch.float32, rows)
+    dev = x.device
+    for name, t in (("x", x), ("residual", residual), ("post_gamma", post_gamma), ("gate", gate),
+                    ("next_gamma", next_gamma), ("residual_out", residual_out), ("y", y),
+                    ("rstd_post", rstd_post), ("rstd_next", rstd_next)):
+        if t is not None:
+            _check_cuda(name, t, dev)
+    with _on(dev, stream) as handle:
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+        if post_gamma is None:
+            rstd_post = None
+        elif rstd_post is None:
+            rstd_post = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+        if next_gamma is None:
+            y = rstd_next = None
+        else:
+            y = torch.empty_like(x) if y is None else y
+            if rstd_next is None:
+                rstd_next = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+        st = lib.rms_norm_block_fwd(_ptr(x), _ptr(residual), _ptr(post_gamma), _ptr(gate),
+                                    gate_rows, _ptr(next_gamma), _ptr(residual_out), _ptr(y),
+                                    _ptr(rstd_post), _ptr(rstd_next), rows, hidden,
+                                    float(residual_scale), float(branch_scale), float(eps),
+                                    int(offset), DTYPE_CODES[x.dtype],
+                                    DTYPE_CODES[residual.dtype], handle)
+    if st != RMSN_OK:
+        raise RMSNormError("rms_norm_block_fwd", st)
+    return residual_out, y, rstd_post, rstd_next
+
+
+def rms_norm_block_bwd_workspace_size(rows: int, hidden: int, gate_rows: int = 0) -> int:
+    """Bytes of workspace ``rms_norm_block_bwd`` needs."""
+    return int(load_library().rms_norm_block_bwd_workspace_size(int(rows), int(hidden),
+                                                                int(gate_rows)))
+
+
+def rms_norm_block_bwd(dy: Optional[torch.Tensor], dresidual_out: Optional[torch.Tensor],
+                       x: torch.Tensor, residual_out: torch.Tensor,
+                       rstd_post: Optional[torch.Tensor], rstd_next: Optional[torch.Tensor],
+                       post_gamma: Optional[torch.Tensor] = None,
+                       gate: Optional[torch.Tensor] = None,
+                       next_gamma: Optional[torch.Tensor] = None, offset: int = 0,
+                       residual_scale: float = 1.0, branch_scale: float = 1.0,
+                       with_dgate: bool = True, dx: Optional[torch.Tensor] = None,
+                       dresidual: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None):
+    """Backward of ``rms_norm_block_fwd`` from the gradients of its y (``dy``,
+    only with ``next_gamma``) and of its r (``dresidual_out``; None: none).
+    Returns ``(dx, dresidual, dpost, dgate, dnext)``: the sums over rows are
+    fp32, ``dgate`` shaped like ``gate`` (None without a gate or with
+    ``with_dgate`` False), ``dpost`` / ``dnext`` None for a missing norm."""
+    lib = load_library()
+    rows, hidden, gate_rows = _check_block(x, "residual_out", residual_out, post_gamma, gate,
+                                           next_gamma)
+    if next_gamma is None:
+        dy = None
+        if dresidual_out is None:
+            raise RuntimeError("dresidual_out is needed without next_gamma")
+    elif dy is None or rstd_next is None:
+        raise RuntimeError("dy and rstd_next are needed with next_gamma")
+    if post_gamma is not None and rstd_post is None:
+        raise RuntimeError("rstd_post is needed with post_gamma")
+    _check_like("dy", dy, x.dtype, x.numel(), x.shape)
+    _check_like("dresidual_out", dresidual_out, residual_out.dtype, x.numel(), x.shape)
+    _check_like("rstd_post", rstd_post, torch.float32, rows)
+    _check_like("rstd_next", rstd_next, torch.float32, rows)
+    _check_like("dx", dx, x.dtype, x.numel(), x.shape)
+    _check_like("dresidual", dresidual, residual_out.dtype, x.numel(), x.shape)
+    dev = x.device
+    for name, t in (("x", x), ("residual_out", residual_out), ("dy", dy),
+                    ("dresidual_out", dresidual_out), ("rstd_post", rstd_post),
+                    ("rstd_next", rstd_next), ("post_gamma", post_gamma), ("gate", gate),
+                    ("next_gamma", next_gamma), ("dx", dx), ("dresidual", dresidual),
+                    ("workspace", workspace)):
+        if t is not None:
+            _check_cuda(name, t, dev)
+    with _on(dev, stream) as handle:
+        dx = torch.empty_like(x) if dx is None else dx
+        dresidual = torch.empty_like(residual_out) if dresidual is None else dresidual
+        f32 = dict(dtype=torch.float32, device=dev)
+        dpost = torch.empty(hidden, **f32) if post_gamma is not None else None
+        dnext = torch.empty(hidden, **f32) if next_gamma is not None else None
+        dgate = torch.empty(gate.shape, **f32) if gate is not None and with_dgate else None
+        if workspace is None:
+            need = int(lib.rms_norm_block_bwd_workspace_size(rows, hidden, gate_rows))
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        st = lib.rms_norm_block_bwd(_ptr(dy), _ptr(dresidual_out), _ptr(x), _ptr(residual_out),
+                                    _ptr(post_gamma), _ptr(gate), gate_rows, _ptr(next_gamma),
+                                    _ptr(rstd_post), _ptr(rstd_next), _ptr(dx), _ptr(dresidual),
+                                    _ptr(dpost), _ptr(dgate), _ptr(dnext), rows, hidden,
+                                    float(residual_scale), float(branch_scale), int(offset),
+                                    DTYPE_CODES[x.dtype], DTYPE_CODES[residual_out.dtype],
+                                    workspace.data_ptr(),
+                                    workspace.numel() * workspace.element_size(), handle)
+    if st != RMSN_OK:
+        raise RMSNormError("rms_norm_block_bwd", st)
+    return dx, dresidual, dpost, dgate, dnext
+
+
 class RMSNormFunction(torch.autograd.Function):
     """RMSNorm over the last dimension with this library's forward and
     backward.  The backward's weight gradient, summed in fp32 by the library,
@@ -750,3 +932,87 @@ class RMSNorm(torch.nn.Module):
     def extra_repr(self) -> str:
         return (f"{self.weight.numel()}, eps={self.eps}, offset={self.offset}, "
                 f"cast_mode={self.cast_mode!r}")
+
+
+class RMSNormBlockFunction(torch.autograd.Function):
+    """The block norm with this library's forward and backward.  The fp32 sums
+    of the backward are cast to the parameters' dtype."""
+
+    @staticmethod
+    def forward(ctx, x, residual, post_weight, gate, next_weight, eps, offset, residual_scale,
+                branch_scale):
+        x, residual = x.contiguous(), residual.contiguous()
+        weights = [None if w is None else w.contiguous() for w in (post_weight, gate, next_weight)]
+        r, y, rstd_post, rstd_next = rms_norm_block_fwd(
+            x, residual, *weights, eps, offset, residual_scale, branch_scale)
+        ctx.save_for_backward(x, r, rstd_post, rstd_next, *weights)
+        ctx.scales = offset, residual_scale, branch_scale
+        ctx.set_materialize_grads(False)
+        return r if y is None else (r, y)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dr, dy=None):
+        x, r, rstd_post, rstd_next, post_weight, gate, next_weight = ctx.saved_tensors
+        if dr is None and dy is None:
+            return (None,) * 9
+        if dy is None and post_weight is None:
+            dy = torch.zeros_like(x)       # r alone was used, and there is no other norm
+        used_next = None if dy is None else next_weight
+        dx, dres, dpost, dgate, dnext = rms_norm_block_bwd(
+            None if dy is None else dy.contiguous(), None if dr is None else dr.contiguous(), x, r,
+            rstd_post, rstd_next, post_weight, gate, used_next, *ctx.scales,
+            with_dgate=ctx.needs_input_grad[3])
+        dpost, dgate, dnext = (None if d is None else d.to(x.dtype) for d in (dpost, dgate, dnext))
+        return dx, dres, dpost, dgate, dnext, None, None, None, None
+
+
+def rms_norm_block(x: torch.Tensor, residual: torch.Tensor,
+                   post_weight: Optional[torch.Tensor] = None,
+                   gate: Optional[torch.Tensor] = None,
+                   next_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                   offset: int = 0, residual_scale: float = 1.0, branch_scale: float = 1.0):
+    """Differentiable ``rms_norm_block_fwd``: returns ``(r, y)``, or ``r``
+    alone without ``next_weight``.  Differentiable in x, the residual, both
+    weights and the gate."""
+    return RMSNormBlockFunction.apply(x, residual, post_weight, gate, next_weight, eps, offset,
+                                      residual_scale, branch_scale)
+
+
+class RMSNormBlock(torch.nn.Module):
+    """What stands between one transformer block and the next: the norm of the
+    block's output (``post``), its gate (``gate_init``: a weight for each
+    channel that starts there; or a gate given to the call), the scaled
+    residual sum, and the norm before the next block (``next``)."""
+
+    def __init__(self, hidden: int, eps: float = 1e-6, offset: int = 0, post: bool = True,
+                 next: bool = True, gate_init: Optional[float] = None,
+                 residual_scale: float = 1.0, branch_scale: float = 1.0, device=None, dtype=None):
+        super().__init__()
+        if offset not in (0, 1):
+            raise ValueError("offset must be 0 or 1")
+        if not post and not next:
+            raise ValueError("post and next are both False: nothing to normalise")
+
+        def weight(value):
+            return torch.nn.Parameter(torch.full((hidden,), value, device=device, dtype=dtype))
+
+        start = 0.0 if offset else 1.0
+        self.post_weight = weight(start) if post else None
+        self.next_weight = weight(start) if next else None
+        self.gate = weight(float(gate_init)) if gate_init is not None else None
+        self.eps, self.offset = eps, offset
+        self.residual_scale, self.branch_scale = residual_scale, branch_scale
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor,
+                gate: Optional[torch.Tensor] = None):
+        if gate is not None and self.gate is not None:
+            raise ValueError("this layer has a gate of its own")
+        return rms_norm_block(x, residual, self.post_weight,
+                              self.gate if gate is None else gate, self.next_weight, self.eps,
+                              self.offset, self.residual_scale, self.branch_scale)
+
+    def extra_repr(self) -> str:
+        return (f"post={self.post_weight is not None}, gate={self.gate is not None}, "
+                f"next={self.next_weight is not None}, eps={self.eps}, offset={self.offset}, "
+                f"residual_scale={self.residual_scale}, branch_scale={self.branch_scale}")

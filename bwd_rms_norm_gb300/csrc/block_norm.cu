@@ -1,0 +1,360 @@
+// Block norm for sm_103a: the norms after and before a transformer block
+// fused with the block's gate and the scaled residual sum.
+//
+//   z = x * rstd_post * w1                      w1 = gamma_post + offset
+//   r = a * res + b * gate_q * z                (z = x without a post norm)
+//   y = r * rstd_next * w2                      w2 = gamma_next + offset
+//
+// rstd_post = 1/sqrt(mean(x^2) + eps), rstd_next = 1/sqrt(mean(r^2) + eps);
+// row i uses gate row q = i / rows_per_gate.  Every product and sum is fp32
+// and r, y are rounded once, at their stores: y is formed from the fp32 r,
+// not from the rounded one.
+//
+// The backward, from dy (of y) and dr (of r):
+//   D       = dr + rstd_next * (dy w2 - rh * c1),  rh = r * rstd_next,
+//             c1 = mean(dy w2 rh)
+//   dres    = a * D
+//   dx      = rstd_post * (w D - xh * c2),  xh = x * rstd_post,
+//             w = b gate w1,  c2 = mean(w D xh)
+//   A_q     = b * sum over the rows of gate row q of D * xh
+//   dgate_q = w1 * A_q,  dgamma_post = sum_q gate_q * A_q,
+//   dgamma_next = sum dy * rh
+// (without a post norm xh = x, w1 = 1 and dx = w D).  D is linear in c1, so
+// c2 follows from sums that need no c1,
+//   S1 = sum dy w2 rh,  S2 = sum w xh (dr + rstd_next dy w2),
+//   S3 = sum w xh rh:   c1 = S1 / H,  c2 = (S2 - rstd_next c1 S3) / H,
+// and a row takes one round of reductions instead of two.
+//
+// The gate's and the post norm's gradients share the accumulator A: one
+// fp32 sum a column serves both, whatever the number of gate rows.
+#include "common.cuh"
+#include "launch.h"
+#include "rms_norm.h"
+
+namespace rmsn {
+namespace {
+
+// ---------------------------------------------------------------------------
+// any width and alignment: scalar accesses, a row's values read again (from
+// L1 / L2) after its reductions
+// ---------------------------------------------------------------------------
+constexpr int kLoopThreads = 256;
+
+template <typename T, typename TS>
+__global__ void __launch_bounds__(kLoopThreads) block_fwd_loop(
+    const T* __restrict__ x, const TS* __restrict__ res, const T* __restrict__ gamma_post,
+    const T* __restrict__ gate, const T* __restrict__ gamma_next, TS* __restrict__ res_out,
+    T* __restrict__ y, float* __restrict__ rstd_post, float* __restrict__ rstd_next,
+    int64_t rows, int64_t rows_per_gate, int hidden, float a, float b, float eps, float off) {
+  __shared__ float red[64];
+  pdl_trigger();
+  pdl_wait();
+  int parity = 0;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const T* xr = x + row * hidden;
+    const TS* sr = res + row * hidden;
+    const T* gr = gate == nullptr ? nullptr : gate + row / rows_per_gate * hidden;
+    float rs1 = 1.f;
+    if (gamma_post != nullptr) {
+      float ss = 0.f;
+      for (int j = threadIdx.x; j < hidden; j += kLoopThreads) {
+        const float v = Traits<T>::to_f(xr[j]);
+        ss = fmaf(v, v, ss);
+      }
+      ss = block_sum(ss, red, parity);
+      parity ^= 1;
+      rs1 = rstd_of(ss / (float)hidden, eps);
+      if (isinf(ss)) {  // see kOverflowScale
+        ss = block_sum(scaled_sum_sq(xr, threadIdx.x, kLoopThreads, hidden), red, parity);
+        parity ^= 1;
+        rs1 = rstd_rescaled(ss, hidden, eps);
+      }
+      if (threadIdx.x == 0) rstd_post[row] = rs1;
+    }
+    auto stream = [&](int j) {
+      float w = b;
+      if (gr != nullptr) w *= Traits<T>::to_f(gr[j]);
+      if (gamma_post != nullptr) w *= Traits<T>::to_f(gamma_post[j]) + off;
+      return fmaf(w, Traits<T>::to_f(xr[j]) * rs1, a * Traits<TS>::to_f(sr[j]));
+    };
+    float ss = 0.f;
+    for (int j = threadIdx.x; j < hidden; j += kLoopThreads) {
+      const float r = stream(j);
+      ss = fmaf(r, r, ss);
+      res_out[row * hidden + j] = Traits<TS>::from_f(r);
+    }
+    if (gamma_next == nullptr) continue;
+    ss = block_sum(ss, red, parity);
+    parity ^= 1;
+    float rs2 = rstd_of(ss / (float)hidden, eps);
+    if (isinf(ss)) {
+      float s2 = 0.f;
+      for (int j = threadIdx.x; j < hidden; j += kLoopThreads) {
+        const float t = stream(j) * kOverflowScale;
+        s2 = fmaf(t, t, s2);
+      }
+      s2 = block_sum(s2, red, parity);
+      parity ^= 1;
+      rs2 = rstd_rescaled(s2, hidden, eps);
+    }
+    if (threadIdx.x == 0) rstd_next[row] = rs2;
+    for (int j = threadIdx.x; j < hidden; j += kLoopThreads)
+      y[row * hidden + j] =
+          Traits<T>::from_f((stream(j) * rs2) * (Traits<T>::to_f(gamma_next[j]) + off));
+  }
+}
+
+// Sum of three values over the CTA (as block_sum; `red` holds 2 x 32 float4).
+__device__ __forceinline__ float3 block_sum3(float a, float b, float c, float4* red, int parity) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nwarps = (blockDim.x + 31) >> 5;
+  a = warp_sum(a);
+  b = warp_sum(b);
+  c = warp_sum(c);
+  float4* slot = red + 32 * parity;
+  if (lane == 0) slot[warp] = make_float4(a, b, c, 0.f);
+  __syncthreads();
+  float3 s = make_float3(0.f, 0.f, 0.f);
+  for (int w = 0; w < nwarps; ++w) {
+    s.x += slot[w].x;
+    s.y += slot[w].y;
+    s.z += slot[w].z;
+  }
+  return s;
+}
+
+// Where a unit's rows meet the gate's rows.  Unit u of U owns the rows
+// [u R / U, (u + 1) R / U); gate row q owns rows_per_gate rows.  The pieces
+// in which both are constant are the segments: each step from one segment to
+// the next raises u or q (or both), so u + q numbers the segments without a
+// clash, and below U + gate_rows.  Each segment has its own partial row of A.
+struct BlockBwdParams {
+  const void* dy;
+  const void* dr;
+  const void* x;
+  const void* r;
+  const void* gamma_post;
+  const void* gate;
+  const void* gamma_next;
+  const float* rstd_post;
+  const float* rstd_next;
+  void* dx;
+  void* dres;
+  float* p_next;   // [units, hidden] partial rows of dgamma_next
+  float* p_post;   // [units, hidden] partial rows of dgamma_post
+  float* p_a;      // [units + gate rows, hidden] partial rows of A
+  int64_t rows;
+  int64_t rows_per_gate;
+  int hidden;
+  float a, b, off;
+};
+
+template <typename T, typename TS>
+__global__ void __launch_bounds__(kLoopThreads) block_bwd_loop(const BlockBwdParams p) {
+  __shared__ float4 red[64];
+  pdl_trigger();
+  pdl_wait();
+  const T* dy = static_cast<const T*>(p.dy);
+  const TS* dr = static_cast<const TS*>(p.dr);
+  const T* x = static_cast<const T*>(p.x);
+  const TS* r = static_cast<const TS*>(p.r);
+  const T* gamma_post = static_cast<const T*>(p.gamma_post);
+  const T* gate = static_cast<const T*>(p.gate);
+  const T* gamma_next = static_cast<const T*>(p.gamma_next);
+  const int hidden = p.hidden;
+  const int64_t u = blockIdx.x;
+  const int64_t r0 = u * p.rows / gridDim.x, r1 = (u + 1) * p.rows / gridDim.x;
+  const bool sums = gamma_post != nullptr || gate != nullptr;
+  int parity = 0;
+  float* pn = p.p_next + u * hidden;
+  float* pp = p.p_post + u * hidden;
+  for (int64_t row = r0; row < r1; ++row) {
+    const int64_t q = row / p.rows_per_gate;
+    const bool seg_first = row == r0 || row == q * p.rows_per_gate;
+    const bool seg_last = row + 1 == r1 || row + 1 == (q + 1) * p.rows_per_gate;
+    float* pa = p.p_a + (u + q) * hidden;
+    const T* gr = gate == nullptr ? nullptr : gate + q * hidden;
+    const int64_t at = row * hidden;
+    const float rs1 = gamma_post != nullptr ? p.rstd_post[row] : 1.f;
+    const float rs2 = gamma_next != nullptr ? p.rstd_next[row] : 0.f;
+    auto weight = [&](int j) {
+      float w = p.b;
+      if (gr != nullptr) w *= Traits<T>::to_f(gr[j]);
+      if (gamma_post != nullptr) w *= Traits<T>::to_f(gamma_post[j]) + p.off;
+      return w;
+    };
+    float s1 = 0.f, s2 = 0.f, s3 = 0.f;
+    for (int j = threadIdx.x; j < hidden; j += kLoopThreads) {
+      const float wx = weight(j) * (Traits<T>::to_f(x[at + j]) * rs1);
+      float t = dr != nullptr ? Traits<TS>::to_f(dr[at + j]) : 0.f;
+      if (gamma_next != nullptr) {
+        const float rh = Traits<TS>::to_f(r[at + j]) * rs2;
+        const float g = Traits<T>::to_f(dy[at + j]) * (Traits<T>::to_f(gamma_next[j]) + p.off);
+        s1 = fmaf(g, rh, s1);
+        s3 = fmaf(wx, rh, s3);
+        t = fmaf(rs2, g, t);
+      }
+      s2 = fmaf(wx, t, s2);
+    }
+    const float3 s = block_sum3(s1, s2, s3, red, parity);
+    parity ^= 1;
+    const float c1 = s.x / (float)hidden;
+    const float c2 = gamma_post != nullptr ? fmaf(-rs2 * c1, s.z, s.y) / (float)hidden : 0.f;
+    for (int j = threadIdx.x; j < hidden; j += kLoopThreads) {
+      const float xh = Traits<T>::to_f(x[at + j]) * rs1;
+      float d = dr != nullptr ? Traits<TS>::to_f(dr[at + j]) : 0.f;
+      if (gamma_next != nullptr) {
+        const float rh = Traits<TS>::to_f(r[at + j]) * rs2;
+        const float gy = Traits<T>::to_f(dy[at + j]);
+        const float g = gy * (Traits<T>::to_f(gamma_next[j]) + p.off);
+        d = fmaf(rs2, fmaf(-rh, c1, g), d);
+        pn[j] = fmaf(gy, rh, row == r0 ? 0.f : pn[j]);
+      }
+      static_cast<TS*>(p.dres)[at + j] = Traits<TS>::from_f(p.a * d);
+      static_cast<T*>(p.dx)[at + j] = Traits<T>::from_f(rs1 * fmaf(-xh, c2, weight(j) * d));
+      if (sums) {
+        const float acc = fmaf(p.b * d, xh, seg_first ? 0.f : pa[j]);
+        pa[j] = acc;
+        if (seg_last && gamma_post != nullptr) {
+          const float gq = gr != nullptr ? Traits<T>::to_f(gr[j]) : 1.f;
+          pp[j] = fmaf(gq, acc, q == r0 / p.rows_per_gate ? 0.f : pp[j]);
+        }
+      }
+    }
+  }
+}
+
+// The sums over the partial rows, 16 lanes a column as dw_finalize: block
+// (., 0) the next norm's, (., 1) the post norm's, (., 2 + q) gate row q's,
+// whose segments are u_first + q ... u_last + q.
+constexpr int kSumLanes = 16;
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kSumLanes) block_bwd_sums(
+    const BlockBwdParams p, int units, float* __restrict__ dgamma_post, float* __restrict__ dgate,
+    float* __restrict__ dgamma_next) {
+  __shared__ float s[kSumLanes][33];
+  pdl_trigger();
+  pdl_wait();
+  const int tx = threadIdx.x, ty = threadIdx.y;
+  const int j = blockIdx.x * 32 + tx;
+  const int hidden = p.hidden;
+  for (int64_t job = blockIdx.y; job < 2 + (dgate != nullptr ? p.rows / p.rows_per_gate : 0);
+       job += gridDim.y) {
+    const float* src = p.p_next;
+    float* dst = dgamma_next;
+    float scale = 1.f;
+    int64_t n = units;
+    if (job == 1) {
+      src = p.p_post;
+      dst = dgamma_post;
+    } else if (job >= 2) {
+      const int64_t q = job - 2;
+      // unit of row i: the largest u with floor(u R / U) <= i
+      const int64_t first = ((q * p.rows_per_gate + 1) * units - 1) / p.rows;
+      const int64_t last = ((q + 1) * p.rows_per_gate * units - 1) / p.rows;
+      src = p.p_a + (first + q) * hidden;
+      n = last - first + 1;
+      dst = dgate + q * hidden;
+      if (p.gamma_post != nullptr && j < hidden)
+        scale = Traits<T>::to_f(static_cast<const T*>(p.gamma_post)[j]) + p.off;
+    }
+    if (dst == nullptr) continue;
+    float acc = 0.f;
+    if (j < hidden) {
+#pragma unroll 8
+      for (int64_t i = ty; i < n; i += kSumLanes) acc += src[i * hidden + j];
+    }
+    s[ty][tx] = acc;
+    __syncthreads();
+    if (ty == 0 && j < hidden) {
+      float t = 0.f;
+#pragma unroll
+      for (int l = 0; l < kSumLanes; ++l) t += s[l][tx];
+      dst[j] = t * scale;
+    }
+    __syncthreads();
+  }
+}
+
+template <typename T, typename TS>
+cudaError_t launch_fwd_t(const BlockFwdArgs& a, cudaStream_t s) {
+  auto kern = block_fwd_loop<T, TS>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int64_t most =
+      (int64_t)sm_count(dev) * max_blocks_per_sm((const void*)kern, kLoopThreads, 0);
+  return launch_kernel(kern, dim3((unsigned)(a.rows < most ? a.rows : most)), dim3(kLoopThreads),
+                       0, s, 1, static_cast<const T*>(a.x), static_cast<const TS*>(a.res),
+                       static_cast<const T*>(a.gamma_post), static_cast<const T*>(a.gate),
+                       static_cast<const T*>(a.gamma_next), static_cast<TS*>(a.res_out),
+                       static_cast<T*>(a.y), a.rstd_post, a.rstd_next, a.rows, a.rows_per_gate,
+                       a.hidden, a.res_scale, a.branch_scale, a.eps, a.offset ? 1.f : 0.f);
+}
+
+template <typename T, typename TS>
+cudaError_t launch_bwd_t(const BlockBwdArgs& a, cudaStream_t s, int* launches) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  auto kern = block_bwd_loop<T, TS>;
+  int64_t most = (int64_t)sm_count(dev) * max_blocks_per_sm((const void*)kern, kLoopThreads, 0);
+  if (most > RMSN_BLOCK_MAX_PARTIALS) most = RMSN_BLOCK_MAX_PARTIALS;
+  const int units = (int)(a.rows < most ? a.rows : most);
+  BlockBwdParams p;
+  p.dy = a.dy;
+  p.dr = a.dr;
+  p.x = a.x;
+  p.r = a.r;
+  p.gamma_post = a.gamma_post;
+  p.gate = a.gate;
+  p.gamma_next = a.gamma_next;
+  p.rstd_post = a.rstd_post;
+  p.rstd_next = a.rstd_next;
+  p.dx = a.dx;
+  p.dres = a.dres;
+  p.p_next = a.partial;
+  p.p_post = a.partial + (int64_t)units * a.hidden;
+  p.p_a = a.partial + 2 * (int64_t)units * a.hidden;
+  p.rows = a.rows;
+  p.rows_per_gate = a.rows_per_gate;
+  p.hidden = a.hidden;
+  p.a = a.res_scale;
+  p.b = a.branch_scale;
+  p.off = a.offset ? 1.f : 0.f;
+  e = launch_kernel(kern, dim3((unsigned)units), dim3(kLoopThreads), 0, s, 1, p);
+  if (e != cudaSuccess) return e;
+  *launches += 1;
+  if (a.dgamma_post == nullptr && a.dgate == nullptr && a.dgamma_next == nullptr)
+    return cudaSuccess;
+  const int64_t jobs = 2 + (a.dgate != nullptr ? a.rows / a.rows_per_gate : 0);
+  e = launch_kernel(block_bwd_sums<T>,
+                    dim3((unsigned)((a.hidden + 31) / 32), (unsigned)(jobs < 65535 ? jobs : 65535)),
+                    dim3(32, kSumLanes), 0, s, 1, p, units, a.dgamma_post, a.dgate, a.dgamma_next);
+  if (e == cudaSuccess) *launches += 1;
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_block_fwd(int dtype, int res_dtype, const BlockFwdArgs& a, cudaStream_t s) {
+  if (dtype == RMSN_F32) return launch_fwd_t<float, float>(a, s);
+  if (dtype == RMSN_BF16)
+    return res_dtype == RMSN_F32 ? launch_fwd_t<__nv_bfloat16, float>(a, s)
+                                 : launch_fwd_t<__nv_bfloat16, __nv_bfloat16>(a, s);
+  return res_dtype == RMSN_F32 ? launch_fwd_t<__half, float>(a, s)
+                               : launch_fwd_t<__half, __half>(a, s);
+}
+
+cudaError_t launch_block_bwd(int dtype, int res_dtype, const BlockBwdArgs& a, cudaStream_t s,
+                             int* launches) {
+  if (dtype == RMSN_F32) return launch_bwd_t<float, float>(a, s, launches);
+  if (dtype == RMSN_BF16)
+    return res_dtype == RMSN_F32 ? launch_bwd_t<__nv_bfloat16, float>(a, s, launches)
+                                 : launch_bwd_t<__nv_bfloat16, __nv_bfloat16>(a, s, launches);
+  return res_dtype == RMSN_F32 ? launch_bwd_t<__half, float>(a, s, launches)
+                               : launch_bwd_t<__half, __half>(a, s, launches);
+}
+
+}  // namespace rmsn

@@ -509,6 +509,140 @@ int group_norm_bwd(const void* dy, const void* x, const void* gamma, const float
   return RMSN_OK;
 }
 
+namespace {
+// Checks shared by the block-norm entry points: types, sizes, scales.
+// gate_rows is 0 without a gate.
+int block_check(int64_t rows, int64_t hidden, int64_t gate_rows, bool gated, float res_scale,
+                float branch_scale, int offset, int dtype, int res_dtype) {
+  if (dtype != RMSN_F32 && dtype != RMSN_BF16 && dtype != RMSN_F16) return RMSN_ERR_DTYPE;
+  if (res_dtype != dtype && res_dtype != RMSN_F32) return RMSN_ERR_DTYPE;
+  if (rows < 0 || rows > RMSN_MAX_ROWS || hidden < 1 || hidden > RMSN_MAX_HIDDEN)
+    return RMSN_ERR_SHAPE;
+  if (gated && (gate_rows < 1 || (rows > 0 && gate_rows > rows) || rows % gate_rows != 0))
+    return RMSN_ERR_SHAPE;
+  if (offset != 0 && offset != 1) return RMSN_ERR_ARG;
+  if (!isfinite(res_scale) || !isfinite(branch_scale)) return RMSN_ERR_ARG;
+  return RMSN_OK;
+}
+}  // namespace
+
+int rms_norm_block_fwd(const void* x, const void* residual, const void* gamma_post,
+                       const void* gate, int64_t gate_rows, const void* gamma_next,
+                       void* residual_out, void* y, float* rstd_post, float* rstd_next,
+                       int64_t rows, int64_t hidden, float residual_scale, float branch_scale,
+                       float eps, int offset, int dtype, int residual_dtype, void* stream) {
+  const int st = block_check(rows, hidden, gate_rows, gate != nullptr, residual_scale,
+                             branch_scale, offset, dtype, residual_dtype);
+  if (st != RMSN_OK) return st;
+  if (!(eps >= 0.f) || isinf(eps)) return RMSN_ERR_EPS;
+  begin_call();
+  if (!gamma_post && !gamma_next) return RMSN_ERR_NULL;
+  if (rows == 0) return RMSN_OK;
+  if (!x || !residual || !residual_out || (gamma_post && !rstd_post) ||
+      (gamma_next && (!y || !rstd_next)))
+    return RMSN_ERR_NULL;
+  const int s = elem_bytes(dtype);
+  BlockFwdArgs a;
+  a.x = x;
+  a.res = residual;
+  a.gamma_post = gamma_post;
+  a.gate = gate;
+  a.gamma_next = gamma_next;
+  a.res_out = residual_out;
+  a.y = gamma_next ? y : nullptr;
+  a.rstd_post = rstd_post;
+  a.rstd_next = rstd_next;
+  a.rows = rows;
+  a.rows_per_gate = gate ? rows / gate_rows : rows;
+  a.hidden = (int)hidden;
+  a.res_scale = residual_scale;
+  a.branch_scale = branch_scale;
+  a.eps = eps;
+  a.offset = offset;
+  a.vec_ok = ((hidden * s) % 16 == 0) && aligned16(x) && aligned16(residual) &&
+             aligned16(gamma_post) && aligned16(gate) && aligned16(gamma_next) &&
+             aligned16(residual_out) && aligned16(a.y);
+  const cudaError_t e =
+      launch_block_fwd(dtype, residual_dtype, a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e);
+  t_last_launches = 1;
+  return RMSN_OK;
+}
+
+size_t rms_norm_block_bwd_workspace_size(int64_t rows, int64_t hidden, int64_t gate_rows) {
+  if (rows <= 0 || rows > RMSN_MAX_ROWS || hidden < 1 || hidden > RMSN_MAX_HIDDEN ||
+      gate_rows < 0 || gate_rows > rows)
+    return 0;
+  // partial rows of dgamma_next and dgamma_post, one a unit, and one of A a
+  // segment: fewer than units + gate rows
+  const int64_t parts = rows < RMSN_BLOCK_MAX_PARTIALS ? rows : RMSN_BLOCK_MAX_PARTIALS;
+  return (size_t)(3 * parts + (gate_rows > 0 ? gate_rows : 1)) * (size_t)hidden * sizeof(float);
+}
+
+int rms_norm_block_bwd(const void* dy, const void* dresidual_out, const void* x,
+                       const void* residual_out, const void* gamma_post, const void* gate,
+                       int64_t gate_rows, const void* gamma_next, const float* rstd_post,
+                       const float* rstd_next, void* dx, void* dresidual, float* dgamma_post,
+                       float* dgate, float* dgamma_next, int64_t rows, int64_t hidden,
+                       float residual_scale, float branch_scale, int offset, int dtype,
+                       int residual_dtype, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  const int st = block_check(rows, hidden, gate_rows, gate != nullptr, residual_scale,
+                             branch_scale, offset, dtype, residual_dtype);
+  if (st != RMSN_OK) return st;
+  begin_call();
+  if (!gamma_post && !gamma_next) return RMSN_ERR_NULL;
+  if ((gamma_post && !dgamma_post) || (gamma_next && !dgamma_next)) return RMSN_ERR_NULL;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    cudaError_t e = cudaSuccess;
+    const size_t row = (size_t)hidden * sizeof(float);
+    if (gamma_post) e = cudaMemsetAsync(dgamma_post, 0, row, cs);
+    if (e == cudaSuccess && gamma_next) e = cudaMemsetAsync(dgamma_next, 0, row, cs);
+    if (e == cudaSuccess && gate && dgate)
+      e = cudaMemsetAsync(dgate, 0, row * (size_t)gate_rows, cs);
+    return e == cudaSuccess ? RMSN_OK : cuda_fail(e);
+  }
+  if (!x || !dx || !dresidual || !workspace || (gamma_post && !rstd_post) ||
+      (gamma_next && (!dy || !residual_out || !rstd_next)) || (!gamma_next && !dresidual_out))
+    return RMSN_ERR_NULL;
+  if (!aligned16(workspace)) return RMSN_ERR_ALIGN;
+  if (workspace_bytes <
+      rms_norm_block_bwd_workspace_size(rows, hidden, gate ? gate_rows : 0))
+    return RMSN_ERR_WORKSPACE;
+  const int s = elem_bytes(dtype);
+  BlockBwdArgs a;
+  a.dy = gamma_next ? dy : nullptr;
+  a.dr = dresidual_out;
+  a.x = x;
+  a.r = gamma_next ? residual_out : nullptr;
+  a.gamma_post = gamma_post;
+  a.gate = gate;
+  a.gamma_next = gamma_next;
+  a.rstd_post = rstd_post;
+  a.rstd_next = rstd_next;
+  a.dx = dx;
+  a.dres = dresidual;
+  a.dgamma_post = gamma_post ? dgamma_post : nullptr;
+  a.dgate = gate ? dgate : nullptr;
+  a.dgamma_next = gamma_next ? dgamma_next : nullptr;
+  a.rows = rows;
+  a.rows_per_gate = gate ? rows / gate_rows : rows;
+  a.hidden = (int)hidden;
+  a.res_scale = residual_scale;
+  a.branch_scale = branch_scale;
+  a.offset = offset;
+  a.vec_ok = ((hidden * s) % 16 == 0) && aligned16(a.dy) && aligned16(a.dr) && aligned16(x) &&
+             aligned16(a.r) && aligned16(gamma_post) && aligned16(gate) && aligned16(gamma_next) &&
+             aligned16(dx) && aligned16(dresidual);
+  a.partial = static_cast<float*>(workspace);
+  int launches = 0;
+  const cudaError_t e = launch_block_bwd(dtype, residual_dtype, a, cs, &launches);
+  if (e != cudaSuccess) return cuda_fail(e);
+  t_last_launches = launches;
+  return RMSN_OK;
+}
+
 const char* rms_norm_status_string(int status) {
   switch (status) {
     case RMSN_OK: return "ok";

@@ -234,6 +234,54 @@ cudaError_t launch_gn_fwd(int dtype, const GnArgs& a, cudaStream_t s);
 cudaError_t read_gn_wait_timeouts(unsigned int* out);
 cudaError_t launch_gn_bwd(int dtype, const GnArgs& a, cudaStream_t s, int* launches);
 
+// Inputs of one block-norm forward (block_norm.cu), already validated (rows
+// >= 1; rows_per_gate = rows / gate rows, = rows without a gate).
+struct BlockFwdArgs {
+  const void* x;
+  const void* res;
+  const void* gamma_post;  // may be NULL: no norm of x
+  const void* gate;        // may be NULL: a gate of ones
+  const void* gamma_next;  // may be NULL: no y
+  void* res_out;
+  void* y;
+  float* rstd_post;
+  float* rstd_next;
+  int64_t rows;
+  int64_t rows_per_gate;
+  int hidden;
+  float res_scale, branch_scale, eps;
+  int offset;
+  bool vec_ok;             // 16-byte aligned rows in every tensor
+};
+
+struct BlockBwdArgs {
+  const void* dy;          // NULL without gamma_next
+  const void* dr;          // may be NULL: no gradient from the stream
+  const void* x;
+  const void* r;
+  const void* gamma_post;
+  const void* gate;
+  const void* gamma_next;
+  const float* rstd_post;
+  const float* rstd_next;
+  void* dx;
+  void* dres;
+  float* dgamma_post;
+  float* dgate;            // may be NULL: not computed
+  float* dgamma_next;
+  int64_t rows;
+  int64_t rows_per_gate;
+  int hidden;
+  float res_scale, branch_scale;
+  int offset;
+  bool vec_ok;
+  float* partial;          // rms_norm_block_bwd_workspace_size bytes
+};
+
+cudaError_t launch_block_fwd(int dtype, int res_dtype, const BlockFwdArgs& a, cudaStream_t s);
+cudaError_t launch_block_bwd(int dtype, int res_dtype, const BlockBwdArgs& a, cudaStream_t s,
+                             int* launches);
+
 // Device properties, cached per device.  sm_count honours the SM budget
 // set with rms_norm_set_sm_budget (capi.cu).
 int sm_count(int device);

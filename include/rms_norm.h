@@ -324,6 +324,74 @@ int group_norm_bwd(const void* dy, const void* x, const void* gamma,
                    size_t workspace_bytes, void* stream);
 
 /*
+ * Block norm: the norms after and before a transformer block fused with the
+ * block's gate and the scaled residual sum.  Per row of x, the output of a
+ * block, and of the residual stream:
+ *
+ *   z = x * rstd_post * gain(gamma_post)        (z = x if gamma_post is NULL)
+ *   r = residual_scale * residual + branch_scale * gate * z
+ *   y = r * rstd_next * gain(gamma_next)        (no y if gamma_next is NULL)
+ *
+ * with rstd_post and rstd_next as rstd of rms_norm_fwd, of x and of r, and
+ * gain(g) = g or 1 + g (offset 1).  At least one of the two norms is given.
+ * `gate` (may be NULL: ones) is [gate_rows, hidden]: gate_rows divides rows,
+ * and each run of rows / gate_rows consecutive rows uses one of its rows
+ * (gate_rows 1: a gate for each channel; the batch size: one for each
+ * sequence).  gate_rows is not looked at without a gate.
+ *
+ * x, y, the gammas and the gate have `dtype`; residual and residual_out have
+ * `residual_dtype`, which is `dtype` or RMSN_F32 (a residual stream kept in
+ * fp32 under half activations).  All arithmetic is fp32; r and y are rounded
+ * once, when they are stored: y is formed from the unrounded r.  rstd_post
+ * and rstd_next are fp32 [rows], written for the norms that are given, for
+ * the backward.  Rows whose fp32 sum of squares overflows are handled as in
+ * rms_norm_fwd.  Outputs must not overlap inputs.  Errors as rms_norm_fwd;
+ * RMSN_ERR_SHAPE also for gate_rows that do not divide rows, RMSN_ERR_ARG for
+ * a scale that is not finite.  rows == 0 enqueues nothing.
+ */
+int rms_norm_block_fwd(const void* x, const void* residual, const void* gamma_post,
+                       const void* gate, int64_t gate_rows, const void* gamma_next,
+                       void* residual_out, void* y, float* rstd_post, float* rstd_next,
+                       int64_t rows, int64_t hidden, float residual_scale,
+                       float branch_scale, float eps, int offset, int dtype,
+                       int residual_dtype, void* stream);
+
+/* Most partial rows of one weight gradient that the block norm's backward
+ * keeps in its workspace. */
+#define RMSN_BLOCK_MAX_PARTIALS 608
+
+/*
+ * Bytes of fp32 workspace rms_norm_block_bwd needs (gate_rows 0 without a
+ * gate).  Returns 0 for invalid arguments and for rows == 0.
+ */
+size_t rms_norm_block_bwd_workspace_size(int64_t rows, int64_t hidden, int64_t gate_rows);
+
+/*
+ * Its backward, from dy (the gradient of y; read only with gamma_next) and
+ * dresidual_out (that of r from later blocks; may be NULL, none, when
+ * gamma_next is given).  x and residual_out, rstd_post and rstd_next are the
+ * forward's input and outputs (residual_out and rstd_next are read only with
+ * gamma_next, rstd_post only with gamma_post).  Writes dx (`dtype`) and dresidual
+ * (`residual_dtype`), and OVERWRITES the fp32 sums dgamma_post and
+ * dgamma_next [hidden] of the norms that are given and dgate [gate_rows,
+ * hidden] (NULL: not computed).  The derivative is that of the unrounded
+ * forward, in fp32.  Sums over rows have a fixed order, set by the sizes, the
+ * GPU's SM count and the SM budget: repeated calls give the same bits.
+ * `workspace`: rms_norm_block_bwd_workspace_size bytes of device scratch,
+ * 16-byte aligned, clobbered; calls that may run at the same time need their
+ * own.  rows == 0 zero-fills the sums.
+ */
+int rms_norm_block_bwd(const void* dy, const void* dresidual_out, const void* x,
+                       const void* residual_out, const void* gamma_post,
+                       const void* gate, int64_t gate_rows, const void* gamma_next,
+                       const float* rstd_post, const float* rstd_next, void* dx,
+                       void* dresidual, float* dgamma_post, float* dgate,
+                       float* dgamma_next, int64_t rows, int64_t hidden,
+                       float residual_scale, float branch_scale, int offset, int dtype,
+                       int residual_dtype, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/*
  * Introspection: the device kernels that the last call of any entry point
  * of this library on the calling thread launched, in launch order (at most
  * four are recorded).  names[i] receives a static, NUL-terminated string
