@@ -37,6 +37,9 @@ The functions carry the names of the C entry points declared in
   dresidual, dpost, dgate, dnext)``;
   ``rms_norm_block_bwd_workspace_size(rows, hidden, gate_rows)`` (the norms
   after and before a block with its gate and the scaled residual sum)
+* ``rms_norm_grad_norm(grads)`` -> ``norm``; ``rms_norm_grad_clip(grads,
+  max_norm, ...)`` -> ``norm`` (the 2-norm over a list of gradients, and the
+  list scaled down to a largest norm); ``rms_norm_grad_workspace_size(count)``
 
 For autograd: ``rms_norm(x, weight, eps, offset=0, cast_mode="round_once")``
 (a ``torch.autograd.Function`` over rms_norm_fwd / rms_norm_bwd) and the
@@ -44,6 +47,7 @@ module ``RMSNorm(hidden, eps, offset=0, cast_mode="round_once")``.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import os
@@ -96,6 +100,9 @@ EXPORTED = (
     "rms_norm_block_fwd",
     "rms_norm_block_bwd_workspace_size",
     "rms_norm_block_bwd",
+    "rms_norm_grad_workspace_size",
+    "rms_norm_grad_norm",
+    "rms_norm_grad_clip",
 )
 
 
@@ -181,6 +188,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.rms_norm_block_bwd.argtypes = [P, P, P, P, P, P, I64, P, P, P, P, P, P, P, P, I64, I64, F,
                                        F, I, I, I, P, SZ, P]
     lib.rms_norm_block_bwd.restype = I
+    lib.rms_norm_grad_workspace_size.argtypes = [I64]
+    lib.rms_norm_grad_workspace_size.restype = SZ
+    lib.rms_norm_grad_norm.argtypes = [P, P, P, I64, P, P, SZ, P]
+    lib.rms_norm_grad_norm.restype = I
+    lib.rms_norm_grad_clip.argtypes = [P, P, P, P, P, I64, F, F, P, P, P, SZ, P]
+    lib.rms_norm_grad_clip.restype = I
     _lib = lib
     return lib
 
@@ -881,6 +894,106 @@ def rms_norm_block_bwd(dy: Optional[torch.Tensor], dresidual_out: Optional[torch
     if st != RMSN_OK:
         raise RMSNormError("rms_norm_block_bwd", st)
     return dx, dresidual, dpost, dgate, dnext
+
+
+def rms_norm_grad_workspace_size(count: int) -> int:
+    """Bytes of workspace a norm over ``count`` gradients needs."""
+    return int(load_library().rms_norm_grad_workspace_size(int(count)))
+
+
+def _grad_list(name: str, grads, device: torch.device):
+    """Host arrays (pointers, element counts, dtype codes) of a list of tensors."""
+    for t in grads:
+        if t.dtype not in DTYPE_CODES:
+            raise RuntimeError(f"{name} must be float32, bfloat16 or float16, not {t.dtype}")
+        _check_cuda(name, t, device)
+    return (array.array("Q", [t.data_ptr() for t in grads]),
+            array.array("q", [t.numel() for t in grads]),
+            array.array("i", [DTYPE_CODES[t.dtype] for t in grads]))
+
+
+def _scalar(name: str, t: Optional[torch.Tensor], device: torch.device) -> None:
+    if t is not None:
+        _check_like(name, t, torch.float32, 1)
+        _check_cuda(name, t, device)
+
+
+def _grads_of(grads):
+    grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
+    if not grads:
+        raise RuntimeError("the list of gradients is empty")
+    return grads
+
+
+def rms_norm_grad_norm(grads, norm: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The 2-norm over a list of gradients (contiguous CUDA tensors of one
+    device, of any of the three dtypes): an fp32 tensor of no dimensions."""
+    lib = load_library()
+    grads = _grads_of(grads)
+    dev = grads[0].device
+    ptrs, numels, codes = _grad_list("a gradient", grads, dev)
+    _scalar("norm", norm, dev)
+    with _on(dev, stream) as handle:
+        if norm is None:
+            norm = torch.empty((), dtype=torch.float32, device=dev)
+        if workspace is None:
+            need = int(lib.rms_norm_grad_workspace_size(len(grads)))
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        _check_cuda("workspace", workspace, dev)
+        st = lib.rms_norm_grad_norm(ptrs.buffer_info()[0], numels.buffer_info()[0],
+                                    codes.buffer_info()[0], len(grads), norm.data_ptr(),
+                                    workspace.data_ptr(),
+                                    workspace.numel() * workspace.element_size(), handle)
+    if st != RMSN_OK:
+        raise RMSNormError("rms_norm_grad_norm", st)
+    return norm
+
+
+def rms_norm_grad_clip(grads, max_norm: float, eps: float = 1e-6, out=None,
+                       total_norm: Optional[torch.Tensor] = None,
+                       norm: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Scale a list of gradients by ``min(1, max_norm / (norm + eps))``, in
+    place, or into the tensors of ``out`` (same sizes, the gradient's dtype or
+    float32).  Returns the norm before the scaling, an fp32 tensor of no
+    dimensions; where it is not finite the gradients are not scaled.  With
+    ``total_norm`` (a one-element fp32 tensor) that norm is taken instead of
+    the list's own, e.g. one summed over ranks."""
+    lib = load_library()
+    grads = _grads_of(grads)
+    dev = grads[0].device
+    outs = grads if out is None else _grads_of(out)
+    if len(outs) != len(grads):
+        raise RuntimeError(f"out has {len(outs)} tensors, the list {len(grads)}")
+    for g, o in zip(grads, outs):
+        if o is not g:
+            _check_like("a tensor of out", o, o.dtype if o.dtype == torch.float32 else g.dtype,
+                        g.numel())
+    ptrs, numels, codes = _grad_list("a gradient", grads, dev)
+    outs_of = (ptrs, numels, codes) if out is None else _grad_list("a tensor of out", outs, dev)
+    _scalar("total_norm", total_norm, dev)
+    _scalar("norm", norm, dev)
+    with _on(dev, stream) as handle:
+        if norm is None:
+            norm = torch.empty((), dtype=torch.float32, device=dev)
+        if workspace is None and total_norm is None:
+            need = int(lib.rms_norm_grad_workspace_size(len(grads)))
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        size = 0
+        if workspace is not None:
+            _check_cuda("workspace", workspace, dev)
+            size = workspace.numel() * workspace.element_size()
+        st = lib.rms_norm_grad_clip(ptrs.buffer_info()[0], numels.buffer_info()[0],
+                                    codes.buffer_info()[0], outs_of[0].buffer_info()[0],
+                                    outs_of[2].buffer_info()[0], len(grads), float(max_norm),
+                                    float(eps), _ptr(total_norm), norm.data_ptr(),
+                                    _ptr(workspace), size, handle)
+    if st != RMSN_OK:
+        raise RMSNormError("rms_norm_grad_clip", st)
+    return norm
 
 
 class RMSNormFunction(torch.autograd.Function):

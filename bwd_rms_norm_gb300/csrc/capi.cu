@@ -647,13 +647,14 @@ const char* rms_norm_status_string(int status) {
   switch (status) {
     case RMSN_OK: return "ok";
     case RMSN_ERR_NULL: return "a required pointer is NULL";
-    case RMSN_ERR_SHAPE: return "rows or hidden out of range";
+    case RMSN_ERR_SHAPE: return "rows, hidden or another size out of range";
     case RMSN_ERR_EPS: return "eps must be finite and >= 0";
     case RMSN_ERR_DTYPE: return "unknown dtype";
-    case RMSN_ERR_ALIGN: return "workspace must be 16-byte aligned";
-    case RMSN_ERR_WORKSPACE: return "workspace smaller than rms_norm_bwd_workspace_size";
+    case RMSN_ERR_ALIGN: return "workspace must be 16-byte aligned, a gradient aligned to its element";
+    case RMSN_ERR_WORKSPACE: return "workspace smaller than the call's workspace size";
     case RMSN_ERR_CUDA: return "a CUDA call failed";
-    case RMSN_ERR_ARG: return "offset must be 0 or 1 and cast_mode a rmsn_cast_mode";
+    case RMSN_ERR_ARG: return "an argument out of its range (offset, cast_mode, block_rows, a scale, "
+                              "max_norm, or outputs that overlap)";
     default: return "unknown status";
   }
 }

@@ -73,7 +73,8 @@ enum rmsn_status {
   RMSN_ERR_ALIGN = 5,      /* workspace not 16-byte aligned */
   RMSN_ERR_WORKSPACE = 6,  /* workspace smaller than rms_norm_bwd_workspace_size */
   RMSN_ERR_CUDA = 7,       /* a CUDA call failed (see rms_norm_last_cuda_error) */
-  RMSN_ERR_ARG = 8         /* offset not 0/1 or cast_mode not a rmsn_cast_mode */
+  RMSN_ERR_ARG = 8         /* offset not 0/1, cast_mode not a rmsn_cast_mode, or
+                              another argument out of its range */
 };
 
 #define RMSN_MAX_HIDDEN 65536
@@ -390,6 +391,53 @@ int rms_norm_block_bwd(const void* dy, const void* dresidual_out, const void* x,
                        float residual_scale, float branch_scale, int offset, int dtype,
                        int residual_dtype, void* workspace, size_t workspace_bytes,
                        void* stream);
+
+/*
+ * The 2-norm over a list of gradients, and the list scaled down to a largest
+ * norm -- what a training step does with the gradients of the backwards above
+ * (their fp32 weight gradients among them) before its update:
+ *
+ *   norm   = sqrt(sum over the list of every element squared)
+ *   factor = min(1, max_norm / (norm + eps));  1 if norm is not finite
+ *   outs[i][k] = round(grads[i][k] * factor)
+ *
+ * `grads`, `numels`, `dtypes`, `outs` and `out_dtypes` are HOST arrays of
+ * `count` entries, read during the call; grads[i] points to numels[i]
+ * elements of dtypes[i] in device memory (any element alignment; a tensor of
+ * no elements may be NULL).  The elements of a list are at most
+ * RMSN_GRAD_MAX_ELEMENTS.  Squares are added in fp32 within a few dozen
+ * elements and in double beyond, so that no finite list of a finite fp32 norm
+ * overflows or vanishes; the order is fixed by the sizes, the GPU's SM count
+ * and the SM budget.  `norm` is one fp32 on the device.
+ *
+ * rms_norm_grad_clip writes outs[i] in out_dtypes[i], which is dtypes[i] or
+ * RMSN_F32; outs[i] == grads[i] of the same type scales in place (and writes
+ * nothing when the factor is 1).  An output that shares memory with another
+ * output, or with a gradient other than its own in place, is refused
+ * (RMSN_ERR_ARG), so a tensor may be in the list once.  A norm that is not
+ * finite leaves the gradients unscaled; the caller sees it in `norm`.  With
+ * `total_norm` (one fp32 on the device, may be NULL) the factor is taken from
+ * it instead of the list's own norm -- the norm over every rank's gradients,
+ * say -- and the list is not read for its norm; `norm` and `workspace` may then
+ * be NULL (`norm` receives total_norm).
+ *
+ * `workspace`: rms_norm_grad_workspace_size(count) bytes of device scratch,
+ * 16-byte aligned, clobbered; calls that may run at the same time need their
+ * own.  Errors: RMSN_ERR_SHAPE for a negative or too large count or numel,
+ * RMSN_ERR_ALIGN for a pointer not aligned to its element, RMSN_ERR_EPS for an
+ * eps that is negative or not finite, RMSN_ERR_ARG for a max_norm that is
+ * negative or NaN; otherwise as rms_norm_fwd.
+ */
+#define RMSN_GRAD_MAX_PARTIALS 1216
+#define RMSN_GRAD_MAX_ELEMENTS (1LL << 42)
+size_t rms_norm_grad_workspace_size(int64_t count);
+int rms_norm_grad_norm(const void* const* grads, const int64_t* numels, const int* dtypes,
+                       int64_t count, float* norm, void* workspace, size_t workspace_bytes,
+                       void* stream);
+int rms_norm_grad_clip(const void* const* grads, const int64_t* numels, const int* dtypes,
+                       void* const* outs, const int* out_dtypes, int64_t count,
+                       float max_norm, float eps, const float* total_norm, float* norm,
+                       void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Introspection: the device kernels that the last call of any entry point
