@@ -733,43 +733,73 @@ def group_norm_bwd(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, mean:
     return dx, dgamma, (dbeta if with_dbeta else None)
 
 
-@contextlib.contextmanager
-def _on(device: torch.device, stream: Optional[torch.cuda.Stream]):
+class _On:
     """``device`` current, and ``stream`` if one is given, so that what a call
-    allocates belongs to the stream that uses it; yields the stream's handle."""
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
-        else:
-            if stream.device != device:
-                raise RuntimeError(f"stream is on {stream.device}, the tensors on {device}")
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+    allocates belongs to the stream that uses it; entering gives the stream's
+    handle.  Does nothing where both are current already: a call's fixed cost
+    on the host is what a short call costs."""
+
+    __slots__ = ("index", "stream", "undo")
+
+    def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream]):
+        if stream is not None and stream.device != device:
+            raise RuntimeError(f"stream is on {stream.device}, the tensors on {device}")
+        self.index, self.stream, self.undo = device.index, stream, None
+
+    def __enter__(self) -> int:
+        if self.stream is not None or torch.cuda.current_device() != self.index:
+            self.undo = contextlib.ExitStack()
+            self.undo.enter_context(torch.cuda.device(self.index))
+            if self.stream is not None:
+                self.undo.enter_context(torch.cuda.stream(self.stream))
+        return torch._C._cuda_getCurrentRawStream(self.index)
+
+    def __exit__(self, *exc) -> None:
+        if self.undo is not None:
+            self.undo.close()
 
 
-def _check_block(x, stream_name, stream, post_gamma, gate, next_gamma) -> Tuple[int, int, int]:
-    """Checks shared by the block-norm calls; returns (rows, hidden, gate rows)."""
+def _address(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _plain(index: int, dtype: torch.dtype, shape, *tensors: Optional[torch.Tensor]) -> bool:
+    """Whether every tensor given is contiguous, on GPU ``index``, and of this
+    dtype and shape: the quick look before a call; what it does not pass goes
+    through the checks that say what is wrong."""
+    for t in tensors:
+        if t is not None and not (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                                  and t.get_device() == index):
+            return False
+    return True
+
+
+def _block_sizes(x, post_gamma, gate, next_gamma) -> Tuple[int, int, int]:
+    """(rows, hidden, gate rows) of a block-norm call."""
     if x.dtype not in DTYPE_CODES:
         raise RuntimeError(f"x must be float32, bfloat16 or float16, not {x.dtype}")
     if post_gamma is None and next_gamma is None:
         raise RuntimeError("post_gamma and next_gamma are both None: nothing to normalise")
     rows, hidden = _as_rows(x)
-    if stream is not None and stream.dtype != torch.float32:
-        _check_like(stream_name, stream, x.dtype, x.numel(), x.shape)
-    else:
-        _check_like(stream_name, stream, torch.float32, x.numel(), x.shape)
+    if gate is None:
+        return rows, hidden, 0
+    if gate.dim() < 1 or gate.shape[-1] != hidden:
+        raise RuntimeError(f"gate must have {hidden} columns, not shape {tuple(gate.shape)}")
+    gate_rows = gate.numel() // hidden if hidden > 0 else 0
+    if gate_rows < 1 or rows % gate_rows or gate_rows > max(rows, 1):
+        raise RuntimeError(f"gate has {gate_rows} rows, which do not divide the {rows} rows of x")
+    return rows, hidden, gate_rows
+
+
+def _check_block(x, stream_name, stream, post_gamma, gate, next_gamma) -> None:
+    """Checks shared by the block-norm calls, with a message for each."""
+    hidden = x.shape[-1]
+    want = torch.float32 if stream.dtype == torch.float32 else x.dtype
+    _check_like(stream_name, stream, want, x.numel(), x.shape)
     _check_like("post_gamma", post_gamma, x.dtype, hidden, (hidden,))
     _check_like("next_gamma", next_gamma, x.dtype, hidden, (hidden,))
-    gate_rows = 0
     if gate is not None:
-        if gate.dim() < 1 or gate.shape[-1] != hidden:
-            raise RuntimeError(f"gate must have {hidden} columns, not shape {tuple(gate.shape)}")
-        gate_rows = gate.numel() // hidden if hidden > 0 else 0
-        _check_like("gate", gate, x.dtype, gate_rows * hidden)
-        if gate_rows < 1 or rows % gate_rows or gate_rows > max(rows, 1):
-            raise RuntimeError(f"gate has {gate_rows} rows, which do not divide the {rows} rows "
-                               "of x")
-    return rows, hidden, gate_rows
+        _check_like("gate", gate, x.dtype, gate.numel())
 
 
 def rms_norm_block_fwd(x: torch.Tensor, residual: torch.Tensor,
@@ -791,36 +821,45 @@ def rms_norm_block_fwd(x: torch.Tensor, residual: torch.Tensor,
     x uses one.  Returns ``(r, y, rstd_post, rstd_next)``, None for what a
     missing norm would give."""
     lib = load_library()
-    rows, hidden, gate_rows = _check_block(x, "residual", residual, post_gamma, gate, next_gamma)
-    _check_like("residual_out", residual_out, residual.dtype, x.numel(), x.shape)
-    _check_like("y", y, x.dtype, x.numel(), x.shape)
-    _check_like("rstd_post", rstd_post, torch.float32, rows)
-    _check_like("rstd_next", rstd_next, torch.float32, rows)
-    dev = x.device
-    for name, t in (("x", x), ("residual", residual), ("post_gamma", post_gamma), ("gate", gate),
-                    ("next_gamma", next_gamma), ("residual_out", residual_out), ("y", y),
-                    ("rstd_post", rstd_post), ("rstd_next", rstd_next)):
-        if t is not None:
-            _check_cuda(name, t, dev)
-    with _on(dev, stream) as handle:
+    dev, dtype, shape = x.device, x.dtype, x.shape
+    res_dtype, index = residual.dtype, x.get_device()
+    rows, hidden, gate_rows = _block_sizes(x, post_gamma, gate, next_gamma)
+    if not (index >= 0 and (res_dtype is dtype or res_dtype is torch.float32)
+            and _plain(index, dtype, shape, x, y)
+            and _plain(index, res_dtype, shape, residual, residual_out)
+            and _plain(index, dtype, shape[-1:], post_gamma, next_gamma)
+            and _plain(index, torch.float32, shape[:-1], rstd_post, rstd_next)
+            and (gate is None or _plain(index, dtype, gate.shape, gate))):
+        _check_block(x, "residual", residual, post_gamma, gate, next_gamma)
+        _check_like("residual_out", residual_out, res_dtype, x.numel(), shape)
+        _check_like("y", y, dtype, x.numel(), shape)
+        _check_like("rstd_post", rstd_post, torch.float32, rows)
+        _check_like("rstd_next", rstd_next, torch.float32, rows)
+        for name, t in (("x", x), ("residual", residual), ("post_gamma", post_gamma),
+                        ("gate", gate), ("next_gamma", next_gamma),
+                        ("residual_out", residual_out), ("y", y), ("rstd_post", rstd_post),
+                        ("rstd_next", rstd_next)):
+            if t is not None:
+                _check_cuda(name, t, dev)
+    with _On(dev, stream) as handle:
         if residual_out is None:
             residual_out = torch.empty_like(residual)
         if post_gamma is None:
             rstd_post = None
         elif rstd_post is None:
-            rstd_post = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+            rstd_post = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
         if next_gamma is None:
             y = rstd_next = None
         else:
             y = torch.empty_like(x) if y is None else y
             if rstd_next is None:
-                rstd_next = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-        st = lib.rms_norm_block_fwd(_ptr(x), _ptr(residual), _ptr(post_gamma), _ptr(gate),
-                                    gate_rows, _ptr(next_gamma), _ptr(residual_out), _ptr(y),
-                                    _ptr(rstd_post), _ptr(rstd_next), rows, hidden,
-                                    float(residual_scale), float(branch_scale), float(eps),
-                                    int(offset), DTYPE_CODES[x.dtype],
-                                    DTYPE_CODES[residual.dtype], handle)
+                rstd_next = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+        st = lib.rms_norm_block_fwd(x.data_ptr(), residual.data_ptr(), _address(post_gamma),
+                                    _address(gate), gate_rows, _address(next_gamma),
+                                    residual_out.data_ptr(), _address(y), _address(rstd_post),
+                                    _address(rstd_next), rows, hidden, float(residual_scale),
+                                    float(branch_scale), float(eps), int(offset),
+                                    DTYPE_CODES[dtype], DTYPE_CODES[res_dtype], handle)
     if st != RMSN_OK:
         raise RMSNormError("rms_norm_block_fwd", st)
     return residual_out, y, rstd_post, rstd_next
@@ -849,8 +888,7 @@ def rms_norm_block_bwd(dy: Optional[torch.Tensor], dresidual_out: Optional[torch
     fp32, ``dgate`` shaped like ``gate`` (None without a gate or with
     ``with_dgate`` False), ``dpost`` / ``dnext`` None for a missing norm."""
     lib = load_library()
-    rows, hidden, gate_rows = _check_block(x, "residual_out", residual_out, post_gamma, gate,
-                                           next_gamma)
+    rows, hidden, gate_rows = _block_sizes(x, post_gamma, gate, next_gamma)
     if next_gamma is None:
         dy = None
         if dresidual_out is None:
@@ -859,37 +897,49 @@ def rms_norm_block_bwd(dy: Optional[torch.Tensor], dresidual_out: Optional[torch
         raise RuntimeError("dy and rstd_next are needed with next_gamma")
     if post_gamma is not None and rstd_post is None:
         raise RuntimeError("rstd_post is needed with post_gamma")
-    _check_like("dy", dy, x.dtype, x.numel(), x.shape)
-    _check_like("dresidual_out", dresidual_out, residual_out.dtype, x.numel(), x.shape)
-    _check_like("rstd_post", rstd_post, torch.float32, rows)
-    _check_like("rstd_next", rstd_next, torch.float32, rows)
-    _check_like("dx", dx, x.dtype, x.numel(), x.shape)
-    _check_like("dresidual", dresidual, residual_out.dtype, x.numel(), x.shape)
-    dev = x.device
-    for name, t in (("x", x), ("residual_out", residual_out), ("dy", dy),
-                    ("dresidual_out", dresidual_out), ("rstd_post", rstd_post),
-                    ("rstd_next", rstd_next), ("post_gamma", post_gamma), ("gate", gate),
-                    ("next_gamma", next_gamma), ("dx", dx), ("dresidual", dresidual),
-                    ("workspace", workspace)):
-        if t is not None:
-            _check_cuda(name, t, dev)
-    with _on(dev, stream) as handle:
+    dev, dtype, shape = x.device, x.dtype, x.shape
+    res_dtype, index = residual_out.dtype, x.get_device()
+    if not (index >= 0 and (res_dtype is dtype or res_dtype is torch.float32)
+            and _plain(index, dtype, shape, x, dy, dx)
+            and _plain(index, res_dtype, shape, residual_out, dresidual_out, dresidual)
+            and _plain(index, dtype, shape[-1:], post_gamma, next_gamma)
+            and _plain(index, torch.float32, shape[:-1], rstd_post, rstd_next)
+            and (gate is None or _plain(index, dtype, gate.shape, gate)) and workspace is None):
+        _check_block(x, "residual_out", residual_out, post_gamma, gate, next_gamma)
+        _check_like("dy", dy, dtype, x.numel(), shape)
+        _check_like("dresidual_out", dresidual_out, res_dtype, x.numel(), shape)
+        _check_like("rstd_post", rstd_post, torch.float32, rows)
+        _check_like("rstd_next", rstd_next, torch.float32, rows)
+        _check_like("dx", dx, dtype, x.numel(), shape)
+        _check_like("dresidual", dresidual, res_dtype, x.numel(), shape)
+        for name, t in (("x", x), ("residual_out", residual_out), ("dy", dy),
+                        ("dresidual_out", dresidual_out), ("rstd_post", rstd_post),
+                        ("rstd_next", rstd_next), ("post_gamma", post_gamma), ("gate", gate),
+                        ("next_gamma", next_gamma), ("dx", dx), ("dresidual", dresidual),
+                        ("workspace", workspace)):
+            if t is not None:
+                _check_cuda(name, t, dev)
+    with _On(dev, stream) as handle:
         dx = torch.empty_like(x) if dx is None else dx
         dresidual = torch.empty_like(residual_out) if dresidual is None else dresidual
-        f32 = dict(dtype=torch.float32, device=dev)
-        dpost = torch.empty(hidden, **f32) if post_gamma is not None else None
-        dnext = torch.empty(hidden, **f32) if next_gamma is not None else None
-        dgate = torch.empty(gate.shape, **f32) if gate is not None and with_dgate else None
+        dpost = dnext = dgate = None
+        if post_gamma is not None:
+            dpost = torch.empty(hidden, dtype=torch.float32, device=dev)
+        if next_gamma is not None:
+            dnext = torch.empty(hidden, dtype=torch.float32, device=dev)
+        if gate is not None and with_dgate:
+            dgate = torch.empty(gate.shape, dtype=torch.float32, device=dev)
         if workspace is None:
             need = int(lib.rms_norm_block_bwd_workspace_size(rows, hidden, gate_rows))
             workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        st = lib.rms_norm_block_bwd(_ptr(dy), _ptr(dresidual_out), _ptr(x), _ptr(residual_out),
-                                    _ptr(post_gamma), _ptr(gate), gate_rows, _ptr(next_gamma),
-                                    _ptr(rstd_post), _ptr(rstd_next), _ptr(dx), _ptr(dresidual),
-                                    _ptr(dpost), _ptr(dgate), _ptr(dnext), rows, hidden,
-                                    float(residual_scale), float(branch_scale), int(offset),
-                                    DTYPE_CODES[x.dtype], DTYPE_CODES[residual_out.dtype],
-                                    workspace.data_ptr(),
+        st = lib.rms_norm_block_bwd(_address(dy), _address(dresidual_out), x.data_ptr(),
+                                    residual_out.data_ptr(), _address(post_gamma),
+                                    _address(gate), gate_rows, _address(next_gamma),
+                                    _address(rstd_post), _address(rstd_next), dx.data_ptr(),
+                                    dresidual.data_ptr(), _address(dpost), _address(dgate),
+                                    _address(dnext), rows, hidden, float(residual_scale),
+                                    float(branch_scale), int(offset), DTYPE_CODES[dtype],
+                                    DTYPE_CODES[res_dtype], workspace.data_ptr(),
                                     workspace.numel() * workspace.element_size(), handle)
     if st != RMSN_OK:
         raise RMSNormError("rms_norm_block_bwd", st)
@@ -901,15 +951,30 @@ def rms_norm_grad_workspace_size(count: int) -> int:
     return int(load_library().rms_norm_grad_workspace_size(int(count)))
 
 
+_Tensor = torch.Tensor
+
+
 def _grad_list(name: str, grads, device: torch.device):
-    """Host arrays (pointers, element counts, dtype codes) of a list of tensors."""
-    for t in grads:
-        if t.dtype not in DTYPE_CODES:
-            raise RuntimeError(f"{name} must be float32, bfloat16 or float16, not {t.dtype}")
-        _check_cuda(name, t, device)
-    return (array.array("Q", [t.data_ptr() for t in grads]),
-            array.array("q", [t.numel() for t in grads]),
-            array.array("i", [DTYPE_CODES[t.dtype] for t in grads]))
+    """Host arrays (pointers, element counts, dtype codes) of a list of
+    tensors.  The checks run over the list one property at a time (half the
+    time of tensor by tensor on lists of hundreds)."""
+    if (set(map(_Tensor.get_device, grads)) != {device.index if device.type == "cuda" else None}
+            or not all(map(_Tensor.is_contiguous, grads))):
+        for t in grads:
+            if t.dtype not in DTYPE_CODES:
+                raise RuntimeError(f"{name} must be float32, bfloat16 or float16, not {t.dtype}")
+            _check_cuda(name, t, device)
+    dtypes = [t.dtype for t in grads]
+    kinds = set(dtypes)
+    for d in kinds:
+        if d not in DTYPE_CODES:
+            raise RuntimeError(f"{name} must be float32, bfloat16 or float16, not {d}")
+    if len(kinds) == 1:
+        codes = array.array("i", [DTYPE_CODES[dtypes[0]]]) * len(dtypes)
+    else:
+        codes = array.array("i", [DTYPE_CODES[d] for d in dtypes])
+    return (array.array("Q", list(map(_Tensor.data_ptr, grads))),
+            array.array("q", list(map(_Tensor.numel, grads))), codes)
 
 
 def _scalar(name: str, t: Optional[torch.Tensor], device: torch.device) -> None:
@@ -935,7 +1000,7 @@ def rms_norm_grad_norm(grads, norm: Optional[torch.Tensor] = None,
     dev = grads[0].device
     ptrs, numels, codes = _grad_list("a gradient", grads, dev)
     _scalar("norm", norm, dev)
-    with _on(dev, stream) as handle:
+    with _On(dev, stream) as handle:
         if norm is None:
             norm = torch.empty((), dtype=torch.float32, device=dev)
         if workspace is None:
@@ -968,15 +1033,18 @@ def rms_norm_grad_clip(grads, max_norm: float, eps: float = 1e-6, out=None,
     outs = grads if out is None else _grads_of(out)
     if len(outs) != len(grads):
         raise RuntimeError(f"out has {len(outs)} tensors, the list {len(grads)}")
-    for g, o in zip(grads, outs):
-        if o is not g:
-            _check_like("a tensor of out", o, o.dtype if o.dtype == torch.float32 else g.dtype,
-                        g.numel())
-    ptrs, numels, codes = _grad_list("a gradient", grads, dev)
-    outs_of = (ptrs, numels, codes) if out is None else _grad_list("a tensor of out", outs, dev)
+    if out is not None and (
+            list(map(_Tensor.numel, outs)) != list(map(_Tensor.numel, grads))
+            or any(o.dtype != torch.float32 and o.dtype != g.dtype for g, o in zip(grads, outs))):
+        for g, o in zip(grads, outs):
+            _check_like("a tensor of out", o,
+                        o.dtype if o.dtype == torch.float32 else g.dtype, g.numel())
+    ptrs, numels, codes = outs_of = _grad_list("a gradient", grads, dev)
+    if out is not None:
+        outs_of = _grad_list("a tensor of out", outs, dev)
     _scalar("total_norm", total_norm, dev)
     _scalar("norm", norm, dev)
-    with _on(dev, stream) as handle:
+    with _On(dev, stream) as handle:
         if norm is None:
             norm = torch.empty((), dtype=torch.float32, device=dev)
         if workspace is None and total_norm is None:

@@ -27,6 +27,7 @@
 //
 // The gate's and the post norm's gradients share the accumulator A: one
 // fp32 sum a column serves both, whatever the number of gate rows.
+#include "block_norm.cuh"
 #include "common.cuh"
 #include "launch.h"
 #include "rms_norm.h"
@@ -122,32 +123,6 @@ __device__ __forceinline__ float3 block_sum3(float a, float b, float c, float4* 
   }
   return s;
 }
-
-// Where a unit's rows meet the gate's rows.  Unit u of U owns the rows
-// [u R / U, (u + 1) R / U); gate row q owns rows_per_gate rows.  The pieces
-// in which both are constant are the segments: each step from one segment to
-// the next raises u or q (or both), so u + q numbers the segments without a
-// clash, and below U + gate_rows.  Each segment has its own partial row of A.
-struct BlockBwdParams {
-  const void* dy;
-  const void* dr;
-  const void* x;
-  const void* r;
-  const void* gamma_post;
-  const void* gate;
-  const void* gamma_next;
-  const float* rstd_post;
-  const float* rstd_next;
-  void* dx;
-  void* dres;
-  float* p_next;   // [units, hidden] partial rows of dgamma_next
-  float* p_post;   // [units, hidden] partial rows of dgamma_post
-  float* p_a;      // [units + gate rows, hidden] partial rows of A
-  int64_t rows;
-  int64_t rows_per_gate;
-  int hidden;
-  float a, b, off;
-};
 
 template <typename T, typename TS>
 __global__ void __launch_bounds__(kLoopThreads) block_bwd_loop(const BlockBwdParams p) {
@@ -277,11 +252,18 @@ __global__ void __launch_bounds__(32 * kSumLanes) block_bwd_sums(
   }
 }
 
+template <typename T> constexpr int code();
+template <> constexpr int code<float>() { return RMSN_F32; }
+template <> constexpr int code<__nv_bfloat16>() { return RMSN_BF16; }
+template <> constexpr int code<__half>() { return RMSN_F16; }
+
 template <typename T, typename TS>
 cudaError_t launch_fwd_t(const BlockFwdArgs& a, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  if (try_launch_block_fwd_tma(code<T>(), code<TS>(), a, s, &e)) return e;
   auto kern = block_fwd_loop<T, TS>;
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const int64_t most =
       (int64_t)sm_count(dev) * max_blocks_per_sm((const void*)kern, kLoopThreads, 0);
@@ -295,13 +277,6 @@ cudaError_t launch_fwd_t(const BlockFwdArgs& a, cudaStream_t s) {
 
 template <typename T, typename TS>
 cudaError_t launch_bwd_t(const BlockBwdArgs& a, cudaStream_t s, int* launches) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  auto kern = block_bwd_loop<T, TS>;
-  int64_t most = (int64_t)sm_count(dev) * max_blocks_per_sm((const void*)kern, kLoopThreads, 0);
-  if (most > RMSN_BLOCK_MAX_PARTIALS) most = RMSN_BLOCK_MAX_PARTIALS;
-  const int units = (int)(a.rows < most ? a.rows : most);
   BlockBwdParams p;
   p.dy = a.dy;
   p.dr = a.dr;
@@ -314,16 +289,25 @@ cudaError_t launch_bwd_t(const BlockBwdArgs& a, cudaStream_t s, int* launches) {
   p.rstd_next = a.rstd_next;
   p.dx = a.dx;
   p.dres = a.dres;
-  p.p_next = a.partial;
-  p.p_post = a.partial + (int64_t)units * a.hidden;
-  p.p_a = a.partial + 2 * (int64_t)units * a.hidden;
   p.rows = a.rows;
   p.rows_per_gate = a.rows_per_gate;
   p.hidden = a.hidden;
   p.a = a.res_scale;
   p.b = a.branch_scale;
   p.off = a.offset ? 1.f : 0.f;
-  e = launch_kernel(kern, dim3((unsigned)units), dim3(kLoopThreads), 0, s, 1, p);
+  int units = 0;
+  cudaError_t e = cudaSuccess;
+  if (!try_launch_block_bwd_tma(code<T>(), code<TS>(), a, p, &units, s, &e)) {
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    auto kern = block_bwd_loop<T, TS>;
+    int64_t most = (int64_t)sm_count(dev) * max_blocks_per_sm((const void*)kern, kLoopThreads, 0);
+    if (most > RMSN_BLOCK_MAX_PARTIALS) most = RMSN_BLOCK_MAX_PARTIALS;
+    units = (int)(a.rows < most ? a.rows : most);
+    place_partials(a, units, p);
+    e = launch_kernel(kern, dim3((unsigned)units), dim3(kLoopThreads), 0, s, 1, p);
+  }
   if (e != cudaSuccess) return e;
   *launches += 1;
   if (a.dgamma_post == nullptr && a.dgate == nullptr && a.dgamma_next == nullptr)

@@ -48,6 +48,7 @@
 #include <mutex>
 #include <type_traits>
 
+#include "block_norm.cuh"
 #include "common.cuh"
 #include "cluster.cuh"
 #include "launch.h"
@@ -2054,10 +2055,11 @@ bool try_launch_ln_bwd_tma(int dtype, const LnBwdArgs& a, cudaStream_t s, cudaEr
 }
 
 cudaError_t read_wait_timeouts(unsigned int* out) {
-  unsigned int mine = 0, other = 0;
+  unsigned int mine = 0, other = 0, block = 0;
   cudaError_t e = cudaMemcpyFromSymbol(&mine, g_wait_timeouts, sizeof(unsigned int));
   if (e == cudaSuccess) e = read_gn_wait_timeouts(&other);
-  *out = mine + other;
+  if (e == cudaSuccess) e = read_block_wait_timeouts(&block);
+  *out = mine + other + block;
   return e;
 }
 
