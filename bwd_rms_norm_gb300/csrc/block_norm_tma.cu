@@ -7,28 +7,12 @@
 //
 // A persistent CTA per SM (or cluster of CTAs, for rows too wide for one)
 // streams its rows with 1D bulk copies into a ring of shared-memory stages
-// (producer: warp 0, one thread; full[s] when a stage has landed) and all its
-// other warps are consumers, in teams: a team of H / 8 or H / 16 threads works
-// on one row, and a stage holds one row a team, so that narrow rows fill the
-// CTA as wide ones do.  A thread owns the same columns of every row; their
-// weights, and in the backward their fp32 sums over rows, stay in its
-// registers.
+// (full[s] when a stage has landed, empty[s] when its readers are done).
+// Every wait is bounded (mbar.cuh); a warp whose wait ran out skips the rest
+// of its rows but still reaches the CTA's and the cluster's barriers.
 //
-// The reductions never stop a team.  A warp puts its part of a row's sums
-// into a slot and arrives on the row's barrier (red), of every CTA of the
-// cluster; before it waits for that barrier it does other work:
-//   forward   B(i): r of row i, its sum of squares -> red2
-//             A(i + 1): sum of squares of x of the next row -> red1
-//             C(i): wait red2, y of row i (r kept in registers from B)
-//             and B(i + 1) waits for red1, which C(i) has covered
-//   backward  A(i + 1): the three sums of the next row -> red
-//             B(i): wait red, dx and dresidual of row i, read again from its stage
-// Slots and red barriers of the forward are two deep and those of the
-// backward four deep: a warp writes those of row i + 2 (i + 4) only after a
-// wait that every reader of row i has passed.
-//
-// Every wait is bounded (mbar.cuh); a consumer whose wait ran out skips the
-// rest of its rows but still reaches the CTA's and the cluster's barriers.
+// fp32 arithmetic goes by pairs (the f32x2 instructions): with 16-bit rows the
+// instructions an element count as much as its bytes.
 #include <type_traits>
 
 #include "block_norm.cuh"
@@ -54,22 +38,119 @@ constexpr int kSmemBudget = 224 * 1024;
 template <typename T, typename TS>
 constexpr int kElems = sizeof(T) == 2 && sizeof(TS) == 2 ? 8 : 4;
 
-template <typename U, int E>
-__device__ __forceinline__ void load_elems(const U* p, float (&f)[E]) {
-  if constexpr (E * sizeof(U) == 16) {
-    unpack<U>(*reinterpret_cast<const uint4*>(p), f);
+// ---------------------------------------------------------------------------
+// pairs of fp32 values in 64-bit registers
+// ---------------------------------------------------------------------------
+using f32x2 = unsigned long long;
+
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+
+__device__ __forceinline__ float2 split(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+__device__ __forceinline__ float sum2(f32x2 v) {
+  const float2 f = split(v);
+  return f.x + f.y;
+}
+
+template <typename U>
+__device__ __forceinline__ f32x2 widen(uint32_t w);
+
+template <>
+__device__ __forceinline__ f32x2 widen<__nv_bfloat16>(uint32_t w) {
+  return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+template <>
+__device__ __forceinline__ f32x2 widen<__half>(uint32_t w) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return pair(f.x, f.y);
+}
+
+template <typename U>
+__device__ __forceinline__ uint32_t narrow(f32x2 v);
+
+template <>
+__device__ __forceinline__ uint32_t narrow<__nv_bfloat16>(f32x2 v) {
+  const float2 f = split(v);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <>
+__device__ __forceinline__ uint32_t narrow<__half>(f32x2 v) {
+  const float2 f = split(v);
+  const __half2 h = __floats2half2_rn(f.x, f.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// E = 2 N elements of type U at p, 8 or 16 bytes.
+template <typename U, int N>
+__device__ __forceinline__ void load_pairs(const U* p, f32x2 (&f)[N]) {
+  if constexpr (sizeof(U) == 4) {
+    static_assert(N == 2, "16 bytes");
+    const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(p);
+    f[0] = q.x;
+    f[1] = q.y;
+  } else if constexpr (N == 4) {
+    const uint4 q = *reinterpret_cast<const uint4*>(p);
+    f[0] = widen<U>(q.x);
+    f[1] = widen<U>(q.y);
+    f[2] = widen<U>(q.z);
+    f[3] = widen<U>(q.w);
   } else {
-    static_assert(E * sizeof(U) == 8, "8 or 16 bytes");
-    unpack_h<U>(*reinterpret_cast<const uint2*>(p), f);
+    static_assert(N == 2, "8 bytes");
+    const uint2 q = *reinterpret_cast<const uint2*>(p);
+    f[0] = widen<U>(q.x);
+    f[1] = widen<U>(q.y);
   }
 }
 
-template <typename U, int E>
-__device__ __forceinline__ void store_elems(U* p, const float (&f)[E]) {
-  if constexpr (E * sizeof(U) == 16)
-    st_vec(p, pack<U>(f));
-  else
-    *reinterpret_cast<uint2*>(p) = pack_h<U>(f);
+template <typename U, int N>
+__device__ __forceinline__ void store_pairs(U* p, const f32x2 (&f)[N]) {
+  if constexpr (sizeof(U) == 4) {
+    const float2 a = split(f[0]), b = split(f[1]);
+    st_vec(p, make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x),
+                         __float_as_uint(b.y)));
+  } else if constexpr (N == 4) {
+    st_vec(p, make_uint4(narrow<U>(f[0]), narrow<U>(f[1]), narrow<U>(f[2]), narrow<U>(f[3])));
+  } else {
+    *reinterpret_cast<uint2*>(p) = make_uint2(narrow<U>(f[0]), narrow<U>(f[1]));
+  }
+}
+
+template <int N>
+__device__ __forceinline__ float sum_pairs(f32x2 (&f)[N]) {
+#pragma unroll
+  for (int h = N / 2; h >= 1; h /= 2)
+#pragma unroll
+    for (int i = 0; i < h; ++i) f[i] = add2(f[i], f[i + h]);
+  return sum2(f[0]);
 }
 
 struct Ring {
@@ -147,19 +228,7 @@ __device__ __forceinline__ void st_peer4(float4* local, uint32_t peer, float4 v)
                : "memory");
 }
 
-// Posts the warp's part v (the same in every lane) in slot and arrives.
-__device__ __forceinline__ void post(const Team& t, float* slot, uint64_t* bar, float v) {
-  if (t.cs == 1) {
-    if (t.lane == 0) {
-      slot[t.tw] = v;
-      mbar_arrive(bar);
-    }
-  } else if (t.lane < t.cs) {
-    st_peer(slot + t.rank * t.wpt + t.tw, t.lane, v);
-    mbar_arrive_peer(bar, t.lane);
-  }
-}
-
+// Posts the warp's parts (the same in every lane) in its slot and arrives.
 __device__ __forceinline__ void post3(const Team& t, float4* slot, uint64_t* bar, float4 v) {
   if (t.cs == 1) {
     if (t.lane == 0) {
@@ -170,14 +239,6 @@ __device__ __forceinline__ void post3(const Team& t, float4* slot, uint64_t* bar
     st_peer4(slot + t.rank * t.wpt + t.tw, t.lane, v);
     mbar_arrive_peer(bar, t.lane);
   }
-}
-
-// Sum of a team's parts, in the same order in every thread.
-__device__ __forceinline__ float total(const Team& t, const float* slot) {
-  const int n = t.cs * t.wpt;
-  float v = 0.f;
-  for (int i = t.lane; i < n; i += 32) v += slot[i];
-  return warp_sum(v);
 }
 
 // Three sums over the lanes at once: lanes exchange halves of the values as
@@ -213,6 +274,17 @@ __device__ __forceinline__ float3 total3(const Team& t, const float4* slot) {
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
+// A producer warp and teams of `wpt` warps.  A team takes whole stages (of
+// one row, or several narrow ones) and carries each row through its three
+// passes over shared memory: sum of squares of x; r, stored and kept in fp32
+// in place of x and res (together they have its size), and its sum of
+// squares; y.  With a warp a row there is nothing to wait for but the copy,
+// and the other teams' rows cover the latencies of one; teams are made wider
+// where there are few rows, or where a ring of wide rows holds few.  The
+// weights w = b gate w1 and w2 stand in shared memory in fp32, in planes of
+// four elements of every group of E, so that a warp reads contiguous bytes; a
+// gate of several rows is read from global memory instead, where the rows of
+// a sequence find it in L1.
 struct BlockFwdParams {
   const void* x;
   const void* res;
@@ -227,49 +299,60 @@ struct BlockFwdParams {
   int64_t rows_per_gate;
   int hidden;
   float a, b, eps, off;
-  int teams, wpt, cs, stages, stride;  // stride: bytes a stage
+  int teams, wpt, cs, stages, stage_rows, stride;  // stride: bytes a stage
 };
+
+constexpr int kFwdTeams = 12;
 
 struct FwdShared {
   uint64_t full[kMaxStages];
   uint64_t empty[kMaxStages];
-  uint64_t red1[kMaxWarps][2];   // of a team: sum x^2 of a row
-  uint64_t red2[kMaxWarps][2];   // sum r^2
-  uint64_t redx[kMaxWarps][2];   // the same sums again, rescaled
-  float slot1[2][kMaxWarps * kMaxSplit];
-  float slot2[2][kMaxWarps * kMaxSplit];
-  float slotx[2][kMaxWarps * kMaxSplit];
+  uint64_t red[2];                                // across a cluster
+  float slot[2][kMaxWarps * kMaxSplit];
   int abort;
 };
 
-template <typename T, typename TS, bool POST, bool NEXT, int NV>
-__global__ void __launch_bounds__(32 * (kMaxWarps + 1)) block_fwd_tma(const BlockFwdParams p) {
-  constexpr int E = kElems<T, TS>;
-  extern __shared__ __align__(128) unsigned char ring[];
+template <int N>
+__device__ __forceinline__ void load_plane(const float4* plane, int nvec, int v, f32x2 (&f)[N]) {
+#pragma unroll
+  for (int q = 0; q < N / 2; ++q) {
+    const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(plane + q * nvec + v);
+    f[2 * q] = u.x;
+    f[2 * q + 1] = u.y;
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void store_plane(float4* plane, int nvec, int v,
+                                            const f32x2 (&f)[N]) {
+#pragma unroll
+  for (int q = 0; q < N / 2; ++q)
+    *reinterpret_cast<ulonglong2*>(plane + q * nvec + v) = make_ulonglong2(f[2 * q], f[2 * q + 1]);
+}
+
+template <typename T, typename TS, bool POST, bool NEXT>
+__global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) block_fwd_tma(const BlockFwdParams p) {
+  constexpr int E = kElems<T, TS>, N = E / 2;
+  extern __shared__ __align__(128) unsigned char smem[];
   __shared__ FwdShared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int K = p.teams, stages = p.stages, cs = p.cs;
-  const int cols = p.hidden / cs;
+  const int stages = p.stages, cs = p.cs, K = p.stage_rows;
+  const int cols = p.hidden / cs, nvec = cols / E;
   const uint32_t rank = cs > 1 ? cta_rank() : 0u;
+  const int col0 = (int)rank * cols;
   const int64_t unit = blockIdx.x / cs, units = gridDim.x / cs;
   // stage k of a unit holds the rows [(k units + unit) K, + K): the grid
   // streams one window of consecutive rows
   const int64_t blocks = (p.rows + K - 1) / K;
-  const int64_t nst = blocks > unit ? (blocks - unit + units - 1) / units : 0;
-  for (int i = threadIdx.x; i < kMaxStages + kMaxWarps; i += blockDim.x) {
-    if (i < stages) {
-      mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], K * p.wpt);
-    }
-    if (i >= kMaxStages) {
-      const int t = i - kMaxStages;
-      for (int d = 0; d < 2; ++d) {
-        mbar_init(&sh.red1[t][d], cs * p.wpt);
-        mbar_init(&sh.red2[t][d], cs * p.wpt);
-        mbar_init(&sh.redx[t][d], cs * p.wpt);
-      }
-    }
+  const int nst = blocks > unit ? (int)((blocks - unit + units - 1) / units) : 0;
+  float4* plane1 = reinterpret_cast<float4*>(smem);
+  float4* plane2 = plane1 + cols / 4;
+  unsigned char* ring = reinterpret_cast<unsigned char*>(NEXT ? plane2 + cols / 4 : plane2);
+  if ((int)threadIdx.x < stages) {
+    mbar_init(&sh.full[threadIdx.x], 1);
+    mbar_init(&sh.empty[threadIdx.x], p.wpt);
   }
+  if (threadIdx.x < 2) mbar_init(&sh.red[threadIdx.x], cs * p.wpt);
   if (threadIdx.x == 0) sh.abort = 0;
   fence_mbar_init();
   __syncthreads();
@@ -279,204 +362,211 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1)) block_fwd_tma(const Bloc
   volatile int* abort = &sh.abort;
   const uint32_t xbytes = (uint32_t)(cols * sizeof(T)), sbytes = (uint32_t)(cols * sizeof(TS));
   const int res_at = K * (int)xbytes;
+  auto issue = [&](int k, int stage) {
+    const int64_t row = (k * units + unit) * K;
+    const uint32_t n = (uint32_t)(p.rows - row < K ? p.rows - row : K);
+    unsigned char* st = ring + (size_t)stage * p.stride;
+    const int64_t at = row * p.hidden + col0;  // K is 1 where cs > 1
+    mbar_arrive_expect_tx(&sh.full[stage], n * (xbytes + sbytes));
+    bulk_load(st, static_cast<const T*>(p.x) + at, n * xbytes, &sh.full[stage]);
+    bulk_load(st + res_at, static_cast<const TS*>(p.res) + at, n * sbytes, &sh.full[stage]);
+  };
+  if (threadIdx.x == 0)
+    for (int k = 0; k < stages && k < nst; ++k) issue(k, k);
+  const T* gate = static_cast<const T*>(p.gate);
+  const bool gate_each = gate != nullptr && p.rows_per_gate < p.rows;
+  for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+    f32x2 w[N], f[N];
+    const f32x2 off = pair(p.off, p.off), b = pair(p.b, p.b);
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = b;
+    if (POST) {
+      load_pairs<T, N>(static_cast<const T*>(p.gamma_post) + col0 + v * E, f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] = mul2(w[i], add2(f[i], off));
+    }
+    if (gate != nullptr && !gate_each) {
+      load_pairs<T, N>(gate + col0 + v * E, f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] = mul2(w[i], f[i]);
+    }
+    store_plane<N>(plane1, nvec, v, w);
+    if (NEXT) {
+      load_pairs<T, N>(static_cast<const T*>(p.gamma_next) + col0 + v * E, f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[i] = add2(f[i], off);
+      store_plane<N>(plane2, nvec, v, f);
+    }
+  }
+  __syncthreads();
 
   if (warp == 0) {
     if (lane == 0) {
-      Ring pos{0, 0u};
-      int64_t k = 0;
+      int stage = 0, k = stages;
+      uint32_t phase = 0;
       for (; k < nst; ++k) {
-        if (k >= stages &&
-            !wait_phase_counted(&sh.empty[pos.stage], pos.phase ^ 1u, abort, &g_block_timeouts))
-          break;
-        const int64_t row = (k * units + unit) * K;
-        const uint32_t n = (uint32_t)(p.rows - row < K ? p.rows - row : K);
-        unsigned char* st = ring + (size_t)pos.stage * p.stride;
-        const int64_t at = row * p.hidden + (int64_t)rank * cols;  // K is 1 where cs > 1
-        mbar_arrive_expect_tx(&sh.full[pos.stage], n * (xbytes + sbytes));
-        bulk_load(st, static_cast<const T*>(p.x) + at, n * xbytes, &sh.full[pos.stage]);
-        bulk_load(st + res_at, static_cast<const TS*>(p.res) + at, n * sbytes,
-                  &sh.full[pos.stage]);
-        pos.next(stages);
+        if (!wait_phase_counted(&sh.empty[stage], phase, abort, &g_block_timeouts)) break;
+        issue(k, stage);
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      drain_ring(sh.full, pos, k, stages);
+      // every copy has landed before the CTA may exit
+      const int issued = k < nst ? k : nst;
+      drain_ring(sh.full, Ring{issued % stages, (uint32_t)(issued / stages) & 1u}, issued, stages);
     }
     __syncwarp();
   } else {
-    const int team = (warp - 1) / p.wpt;
-    Team t{p.wpt, cs, (warp - 1) % p.wpt, lane, rank, abort};
-    const bool alone = p.wpt == 1 && cs == 1;  // a warp's sums need no exchange
-    const int tt = t.tw * 32 + lane, threads = p.wpt * 32;
-    const int nvec = cols / E, col0 = (int)rank * cols;
+    const int team = (warp - 1) / p.wpt, tw = (warp - 1) % p.wpt;
+    const Team t{p.wpt, cs, tw, lane, rank, abort};
+    const int tt = tw * 32 + lane, threads = p.wpt * 32;
     const float inv = 1.f / (float)p.hidden;
-    float* slot1[2] = {sh.slot1[0] + team * p.wpt, sh.slot1[1] + team * p.wpt};
-    float* slot2[2] = {sh.slot2[0] + team * p.wpt, sh.slot2[1] + team * p.wpt};
-    float* slotx[2] = {sh.slotx[0] + team * p.wpt, sh.slotx[1] + team * p.wpt};
-    float w[NV][E], w2[NV][E], r[NV][E];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int v = tt + j * threads;
-      float f[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) f[e] = 0.f;
-      if (NEXT && v < nvec) load_elems<T, E>(static_cast<const T*>(p.gamma_next) + col0 + v * E, f);
-#pragma unroll
-      for (int e = 0; e < E; ++e) w2[j][e] = f[e] + p.off;
-    }
-    int64_t gate_row = -1;
-    uint32_t xphase[2] = {0u, 0u};
-    float ss1 = 0.f;  // a lone warp's sum of squares of the next row
     bool ok = true;
-    Ring pos{0, 0u};
-    // A: the stage's row of this team, if it has one
-    auto sum_x = [&](int64_t k, const Ring& at) {
-      ok = ok && wait_all(&sh.full[at.stage], at.phase, abort);
-      if (!POST || !ok || (k * units + unit) * K + team >= p.rows) return;
-      const T* sx = reinterpret_cast<const T*>(ring + (size_t)at.stage * p.stride) + team * cols;
-      float part[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) part[e] = 0.f;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int v = tt + j * threads;
-        if (v >= nvec) continue;
-        float f[E];
-        load_elems<T, E>(sx + v * E, f);
-#pragma unroll
-        for (int e = 0; e < E; ++e) part[e] = fmaf(f[e], f[e], part[e]);
+    uint32_t turn = 0;  // exchanges of this team: slots and barriers are used in turn
+    auto over_team = [&](float v) {
+      v = warp_sum(v);
+      if (threads == 32 && cs == 1) return v;
+      const uint32_t d = turn & 1u, parity = (turn >> 1) & 1u;
+      ++turn;
+      float* slot = sh.slot[d] + team * p.wpt;
+      if (cs == 1) {
+        if (lane == 0) slot[tw] = v;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(threads) : "memory");
+      } else {
+        if (lane < cs) {
+          st_peer(slot + rank * p.wpt + tw, lane, v);
+          mbar_arrive_peer(&sh.red[d], lane);
+        }
+        ok = ok && team_wait(t, &sh.red[d], parity);
       }
-#pragma unroll
-      for (int h = E / 2; h >= 1; h /= 2)
-#pragma unroll
-        for (int e = 0; e < h; ++e) part[e] += part[e + h];
-      ss1 = warp_sum(part[0]);
-      if (!alone) post(t, slot1[k & 1], &sh.red1[team][k & 1], ss1);
+      float s = 0.f;
+      for (int i = lane; i < cs * p.wpt; i += 32) s += slot[i];
+      return warp_sum(s);
     };
-    // the rescaled sums of a row whose squares overflowed (kOverflowScale)
-    auto again = [&](int which, float part) {
-      float s = warp_sum(part);
-      if (alone) return s;
-      post(t, slotx[which], &sh.redx[team][which], s);
-      ok = team_wait(t, &sh.redx[team][which], xphase[which]);
-      xphase[which] ^= 1u;
-      return total(t, slotx[which]);
-    };
-    if (nst > 0) sum_x(0, pos);
-    for (int64_t k = 0; k < nst; ++k) {
-      const int64_t row = (k * units + unit) * K + team;
-      const uint32_t parity = (uint32_t)(k >> 1) & 1u;
-      Ring after = pos;
-      after.next(stages);
-      const bool mine = ok && row < p.rows;
-      float ss2 = 0.f;
-      if (mine) {
-        const unsigned char* st = ring + (size_t)pos.stage * p.stride;
-        const T* sx = reinterpret_cast<const T*>(st) + team * cols;
-        const TS* sr = reinterpret_cast<const TS*>(st + res_at) + team * cols;
+    const f32x2 a2 = pair(p.a, p.a);
+    int stage = team;
+    uint32_t phase = 0;
+    for (int k = team; k < nst; k += p.teams) {
+      ok = ok && wait_all(&sh.full[stage], phase, abort);
+      const int64_t row0 = (k * units + unit) * K;
+      const int n = (int)(p.rows - row0 < K ? p.rows - row0 : K);
+      unsigned char* st = ring + (size_t)stage * p.stride;
+      for (int q = 0; q < n; ++q) {
+        const int64_t row = row0 + q;
+        T* sx = reinterpret_cast<T*>(st) + q * cols;
+        TS* sr = reinterpret_cast<TS*>(st + res_at) + q * cols;
         float rs1 = 1.f;
         if (POST) {
-          float ss = ss1;
-          if (!alone) {
-            ok = team_wait(t, &sh.red1[team][k & 1], parity);
-            ss = total(t, slot1[k & 1]);
-          }
-          rs1 = rstd_of(ss * inv, p.eps);
-          if (isinf(ss) && ok) {
-            float part = 0.f;
-            for (int v = tt; v < nvec; v += threads) {
-              float f[E];
-              load_elems<T, E>(sx + v * E, f);
+          f32x2 part[N];
 #pragma unroll
-              for (int e = 0; e < E; ++e) {
-                const float q = f[e] * kOverflowScale;
-                part = fmaf(q, q, part);
-              }
+          for (int i = 0; i < N; ++i) part[i] = 0;
+#pragma unroll 4
+          for (int v = tt; v < nvec; v += threads) {
+            f32x2 x[N];
+            load_pairs<T, N>(sx + v * E, x);
+#pragma unroll
+            for (int i = 0; i < N; ++i) part[i] = fma2(x[i], x[i], part[i]);
+          }
+          const float ss = over_team(sum_pairs<N>(part));
+          rs1 = rsqrtf(fmaf(ss, inv, p.eps));
+          if (isinf(ss)) {  // the squares overflowed (kOverflowScale)
+            float again = 0.f;
+            for (int j = tt; j < cols; j += threads) {
+              const float f = Traits<T>::to_f(sx[j]) * kOverflowScale;
+              again = fmaf(f, f, again);
             }
-            rs1 = rstd_rescaled(again(0, part), p.hidden, p.eps);
+            rs1 = rstd_rescaled(over_team(again), p.hidden, p.eps);
           }
-          if (tt == 0 && rank == 0) p.rstd_post[row] = rs1;
+          if (tt == 0 && rank == 0 && ok) p.rstd_post[row] = rs1;
         }
-        const int64_t q = row / p.rows_per_gate;
-        if (q != gate_row) {  // the weights of the row's gate
-          gate_row = q;
-#pragma unroll
-          for (int j = 0; j < NV; ++j) {
-            const int v = tt + j * threads;
-            float f[E], g[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-              f[e] = 1.f - p.off;
-              g[e] = 1.f;
-            }
-            if (POST && v < nvec)
-              load_elems<T, E>(static_cast<const T*>(p.gamma_post) + col0 + v * E, f);
-            if (p.gate != nullptr && v < nvec)
-              load_elems<T, E>(static_cast<const T*>(p.gate) + q * p.hidden + col0 + v * E, g);
-#pragma unroll
-            for (int e = 0; e < E; ++e) w[j][e] = p.b * g[e] * (f[e] + p.off);
-          }
-        }
-        float part[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) part[e] = 0.f;
+        const f32x2 rs = pair(rs1, rs1);
+        const T* grow = gate_each ? gate + row / p.rows_per_gate * p.hidden + col0 : nullptr;
         TS* out = static_cast<TS*>(p.res_out) + row * p.hidden + col0;
+        f32x2 part[N];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int v = tt + j * threads;
-          if (v >= nvec) continue;
-          float f[E], g[E];
-          load_elems<T, E>(sx + v * E, f);
-          load_elems<TS, E>(sr + v * E, g);
+        for (int i = 0; i < N; ++i) part[i] = 0;
+#pragma unroll 2
+        for (int v = tt; v < nvec; v += threads) {
+          f32x2 x[N], r[N], w[N];
+          load_pairs<T, N>(sx + v * E, x);
+          load_pairs<TS, N>(sr + v * E, r);
+          load_plane<N>(plane1, nvec, v, w);
+          if (gate_each) {
+            f32x2 g[N];
+            load_pairs<T, N>(grow + v * E, g);
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            r[j][e] = fmaf(w[j][e], f[e] * rs1, p.a * g[e]);
-            part[e] = fmaf(r[j][e], r[j][e], part[e]);
+            for (int i = 0; i < N; ++i) w[i] = mul2(w[i], g[i]);
           }
-          store_elems<TS, E>(out + v * E, r[j]);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            if (POST) x[i] = mul2(x[i], rs);
+            r[i] = fma2(w[i], x[i], mul2(a2, r[i]));
+            if (NEXT) part[i] = fma2(r[i], r[i], part[i]);
+          }
+          if (ok) store_pairs<TS, N>(out + v * E, r);
+          if (NEXT) {
+            if constexpr (N == 4) {
+              *reinterpret_cast<ulonglong2*>(sx + v * E) = make_ulonglong2(r[0], r[1]);
+              *reinterpret_cast<ulonglong2*>(sr + v * E) = make_ulonglong2(r[2], r[3]);
+            } else {
+              *reinterpret_cast<ulonglong2*>(sr + v * E) = make_ulonglong2(r[0], r[1]);
+            }
+          }
         }
-        if (NEXT) {
+        if (!NEXT) continue;
+        auto kept = [&](int v, f32x2 (&r)[N]) {
+          const ulonglong2 hi = *reinterpret_cast<const ulonglong2*>(sr + v * E);
+          if constexpr (N == 4) {
+            const ulonglong2 lo = *reinterpret_cast<const ulonglong2*>(sx + v * E);
+            r[0] = lo.x;
+            r[1] = lo.y;
+            r[2] = hi.x;
+            r[3] = hi.y;
+          } else {
+            r[0] = hi.x;
+            r[1] = hi.y;
+          }
+        };
+        const float ss = over_team(sum_pairs<N>(part));
+        float rs2 = rsqrtf(fmaf(ss, inv, p.eps));
+        if (isinf(ss)) {
+          const f32x2 scale = pair(kOverflowScale, kOverflowScale);
 #pragma unroll
-          for (int h = E / 2; h >= 1; h /= 2)
+          for (int i = 0; i < N; ++i) part[i] = 0;
+          for (int v = tt; v < nvec; v += threads) {
+            f32x2 r[N];
+            kept(v, r);
 #pragma unroll
-            for (int e = 0; e < h; ++e) part[e] += part[e + h];
-          ss2 = warp_sum(part[0]);
-          if (!alone) post(t, slot2[k & 1], &sh.red2[team][k & 1], ss2);
+            for (int i = 0; i < N; ++i) {
+              r[i] = mul2(r[i], scale);
+              part[i] = fma2(r[i], r[i], part[i]);
+            }
+          }
+          rs2 = rstd_rescaled(over_team(sum_pairs<N>(part)), p.hidden, p.eps);
+        }
+        if (tt == 0 && rank == 0 && ok) p.rstd_next[row] = rs2;
+        const f32x2 rn = pair(rs2, rs2);
+        T* yr = static_cast<T*>(p.y) + row * p.hidden + col0;
+#pragma unroll 4
+        for (int v = tt; v < nvec; v += threads) {
+          f32x2 r[N], w[N];
+          kept(v, r);
+          load_plane<N>(plane2, nvec, v, w);
+#pragma unroll
+          for (int i = 0; i < N; ++i) r[i] = mul2(mul2(r[i], rn), w[i]);
+          if (ok) store_pairs<T, N>(yr + v * E, r);
         }
       }
+      // r was written where the next copy will land
+      if (NEXT) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.empty[pos.stage]);
-      if (k + 1 < nst) sum_x(k + 1, after);
-      if (NEXT && mine && ok) {
-        float ss = ss2;
-        if (!alone) {
-          ok = team_wait(t, &sh.red2[team][k & 1], parity);
-          ss = total(t, slot2[k & 1]);
-        }
-        float rs2 = rstd_of(ss * inv, p.eps);
-        if (isinf(ss) && ok) {
-          float part = 0.f;
-#pragma unroll
-          for (int j = 0; j < NV; ++j)
-            if (tt + j * threads < nvec)
-#pragma unroll
-              for (int e = 0; e < E; ++e) {
-                const float q = r[j][e] * kOverflowScale;
-                part = fmaf(q, q, part);
-              }
-          rs2 = rstd_rescaled(again(1, part), p.hidden, p.eps);
-        }
-        if (tt == 0 && rank == 0) p.rstd_next[row] = rs2;
-        T* out = static_cast<T*>(p.y) + row * p.hidden + col0;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int v = tt + j * threads;
-          if (v >= nvec) continue;
-          float o[E];
-#pragma unroll
-          for (int e = 0; e < E; ++e) o[e] = (r[j][e] * rs2) * w2[j][e];
-          store_elems<T, E>(out + v * E, o);
-        }
+      if (lane == 0) mbar_arrive(&sh.empty[stage]);
+      stage += p.teams;
+      if (stage >= stages) {
+        stage -= stages;
+        phase ^= 1u;
       }
-      pos = after;
     }
   }
   __syncwarp();
@@ -486,6 +576,20 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1)) block_fwd_tma(const Bloc
 // ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
+// All warps are in teams; a team works on one row, and a stage holds one row
+// a team.  A thread owns the same 8 or 16 columns of every row: their weights
+// and their fp32 sums over the rows stay in its registers (which is why no
+// warp is set aside for the copies: 16 warps have 128 registers a thread, 17
+// have 96).  The reductions never stop a team: a warp posts its part of a
+// row's sums to a slot, of every CTA of the cluster, arrives on the row's
+// barrier (red), and takes the row up again after the sums of the next one:
+//   A(i + 1): the three sums of row i + 1 -> red
+//   B(i): wait for red of row i; dx and dresidual, read again from its stage
+// Slots and barriers are four deep: a warp posts row i + 4 only after a wait
+// that every reader of row i has passed.  The stage of row i - 1 is filled
+// again by thread 0 between A(i + 1) and B(i), when the other warps are
+// through with it (before A(i + 1) where there are two stages, and it is the
+// one that A(i + 1) reads).
 constexpr int kDepth = 4;
 
 struct BwdShared {
@@ -493,6 +597,9 @@ struct BwdShared {
   uint64_t empty[kMaxStages];
   uint64_t red[kMaxWarps][kDepth];
   float4 slot[kDepth][kMaxWarps * kMaxSplit];
+  int64_t fill_row;   // thread 0's: the next row to copy,
+  int64_t issued;     // the copies issued, and the stage of the next one
+  Ring fill;
   int abort;
 };
 
@@ -518,9 +625,9 @@ __host__ __device__ inline BwdStage bwd_stage(int teams, int cols, bool x, bool 
 }
 
 template <typename T, typename TS, bool POST, bool NEXT, int NV>
-__global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1)
+__global__ void __launch_bounds__(32 * kMaxWarps, 1)
     block_bwd_tma(const BlockBwdParams p, const BwdShape sp) {
-  constexpr int E = kElems<T, TS>;
+  constexpr int E = kElems<T, TS>, N = E / 2;
   extern __shared__ __align__(128) unsigned char ring[];
   __shared__ BwdShared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -538,7 +645,12 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1)
     if (i >= kMaxStages)
       for (int d = 0; d < kDepth; ++d) mbar_init(&sh.red[i - kMaxStages][d], cs * sp.wpt);
   }
-  if (threadIdx.x == 0) sh.abort = 0;
+  if (threadIdx.x == 0) {
+    sh.abort = 0;
+    sh.fill_row = r0;
+    sh.issued = 0;
+    sh.fill = Ring{0, 0u};
+  }
   fence_mbar_init();
   __syncthreads();
   if (cs > 1) cluster_sync();
@@ -547,278 +659,279 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1)
   volatile int* abort = &sh.abort;
   const BwdStage at = bwd_stage<T, TS>(K, cols, has_x, NEXT, has_dr);
 
-  if (warp == 0) {
-    if (lane == 0) {
-      const uint32_t tb = (uint32_t)(cols * sizeof(T)), sb = (uint32_t)(cols * sizeof(TS));
-      const uint32_t row_bytes =
-          (has_x ? tb : 0) + (NEXT ? tb + sb : 0) + (has_dr ? sb : 0);
-      Ring pos{0, 0u};
-      int64_t issued = 0;
-      // a stage never crosses from one gate row to the next
-      for (int64_t row = r0; row < r1;) {
-        const int64_t seg = (row / p.rows_per_gate + 1) * p.rows_per_gate;
-        const int64_t end = seg < r1 ? seg : r1;
-        const uint32_t n = (uint32_t)(end - row < K ? end - row : K);
-        if (issued >= stages &&
-            !wait_phase_counted(&sh.empty[pos.stage], pos.phase ^ 1u, abort, &g_block_timeouts))
-          break;
-        unsigned char* st = ring + (size_t)pos.stage * sp.stride;
-        uint64_t* full = &sh.full[pos.stage];
-        const int64_t from = row * p.hidden + (int64_t)rank * cols;  // K is 1 where cs > 1
-        mbar_arrive_expect_tx(full, n * row_bytes);
-        if (has_x) bulk_load(st, static_cast<const T*>(p.x) + from, n * tb, full);
-        if (NEXT) {
-          bulk_load(st + at.r, static_cast<const TS*>(p.r) + from, n * sb, full);
-          bulk_load(st + at.dy, static_cast<const T*>(p.dy) + from, n * tb, full);
-        }
-        if (has_dr) bulk_load(st + at.dr, static_cast<const TS*>(p.dr) + from, n * sb, full);
-        pos.next(stages);
-        ++issued;
-        row += n;
-      }
-      drain_ring(sh.full, pos, issued, stages);
+  // Thread 0: the copies of the next stage, if there are rows left.  A stage
+  // never crosses from one gate row to the next.
+  auto fill = [&]() {
+    const int64_t row = sh.fill_row;
+    if (row >= r1) return;
+    Ring pos = sh.fill;
+    if (sh.issued >= stages &&
+        !wait_phase_counted(&sh.empty[pos.stage], pos.phase ^ 1u, abort, &g_block_timeouts)) {
+      sh.fill_row = r1;
+      return;
     }
-    __syncwarp();
-  } else {
-    const int team = (warp - 1) / sp.wpt;
-    Team t{sp.wpt, cs, (warp - 1) % sp.wpt, lane, rank, abort};
-    const bool alone = sp.wpt == 1 && cs == 1;
-    const int tt = t.tw * 32 + lane, threads = sp.wpt * 32;
-    const int nvec = cols / E, col0 = (int)rank * cols;
-    const float inv = 1.f / (float)p.hidden;
-    const bool want_a = POST || p.gate != nullptr;
-    const T* gamma_post = static_cast<const T*>(p.gamma_post);
-    const T* gate = static_cast<const T*>(p.gate);
-    float w[NV][E], w2[NV][E], acc_n[NV][E], acc_a[NV][E];
+    const int64_t seg = (row / p.rows_per_gate + 1) * p.rows_per_gate;
+    const int64_t end = seg < r1 ? seg : r1;
+    const uint32_t n = (uint32_t)(end - row < K ? end - row : K);
+    const uint32_t tb = n * (uint32_t)(cols * sizeof(T)), sb = n * (uint32_t)(cols * sizeof(TS));
+    unsigned char* st = ring + (size_t)pos.stage * sp.stride;
+    uint64_t* full = &sh.full[pos.stage];
+    const int64_t from = row * p.hidden + (int64_t)rank * cols;  // K is 1 where cs > 1
+    mbar_arrive_expect_tx(full, (has_x ? tb : 0) + (NEXT ? tb + sb : 0) + (has_dr ? sb : 0));
+    if (has_x) bulk_load(st, static_cast<const T*>(p.x) + from, tb, full);
+    if (NEXT) {
+      bulk_load(st + at.r, static_cast<const TS*>(p.r) + from, sb, full);
+      bulk_load(st + at.dy, static_cast<const T*>(p.dy) + from, tb, full);
+    }
+    if (has_dr) bulk_load(st + at.dr, static_cast<const TS*>(p.dr) + from, sb, full);
+    pos.next(stages);
+    sh.fill = pos;
+    sh.issued += 1;
+    sh.fill_row = row + n;
+  };
+  if (threadIdx.x == 0)
+    for (int k = 0; k < stages; ++k) fill();
+
+  const int team = warp / sp.wpt;
+  const Team t{sp.wpt, cs, warp % sp.wpt, lane, rank, abort};
+  const bool alone = sp.wpt == 1 && cs == 1;  // a warp's sums need no exchange
+  const int tt = t.tw * 32 + lane, threads = sp.wpt * 32;
+  const int nvec = cols / E, col0 = (int)rank * cols;
+  const float inv = 1.f / (float)p.hidden;
+  const bool want_a = POST || p.gate != nullptr;
+  const T* gamma_post = static_cast<const T*>(p.gamma_post);
+  const T* gate = static_cast<const T*>(p.gate);
+  const f32x2 off = pair(p.off, p.off), a2 = pair(p.a, p.a);
+  f32x2 w[NV][N], w2[NV][N], acc_n[NV][N], acc_a[NV][N];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int v = tt + j * threads;
+#pragma unroll
+    for (int i = 0; i < N; ++i) w2[j][i] = 0;
+    if (NEXT && v < nvec) load_pairs<T, N>(static_cast<const T*>(p.gamma_next) + col0 + v * E, w2[j]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      w2[j][i] = add2(w2[j][i], off);
+      acc_n[j][i] = 0;
+      acc_a[j][i] = 0;
+    }
+  }
+  bool ok = true;
+  Ring pos_a{0, 0u}, pos_b{0, 0u};
+  uint32_t posted = 0, taken = 0;  // rows of this team whose sums were posted, used
+  uint32_t steps = 0;              // stages that went through A
+  const bool early = stages < 3;   // the next stage is the one just left
+
+  for (int64_t seg0 = r0; seg0 < r1;) {
+    const int64_t q = seg0 / p.rows_per_gate;
+    const int64_t seg1 = (q + 1) * p.rows_per_gate < r1 ? (q + 1) * p.rows_per_gate : r1;
+    const int nrows = (int)(seg1 - seg0) - team;  // row i of this team: i K < nrows
+    const int nst = (int)((seg1 - seg0 + K - 1) / K);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int v = tt + j * threads;
-      float f[E];
+      f32x2 f[N];
 #pragma unroll
-      for (int e = 0; e < E; ++e) f[e] = 0.f;
-      if (NEXT && v < nvec) load_elems<T, E>(static_cast<const T*>(p.gamma_next) + col0 + v * E, f);
+      for (int i = 0; i < N; ++i) w[j][i] = pair(p.b, p.b);
+      if (v >= nvec) continue;
+      if (POST) {
+        load_pairs<T, N>(gamma_post + col0 + v * E, f);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        w2[j][e] = f[e] + p.off;
-        acc_n[j][e] = 0.f;
-        acc_a[j][e] = 0.f;
+        for (int i = 0; i < N; ++i) w[j][i] = mul2(w[j][i], add2(f[i], off));
+      }
+      if (gate != nullptr) {
+        load_pairs<T, N>(gate + q * p.hidden + col0 + v * E, f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[j][i] = mul2(w[j][i], f[i]);
       }
     }
-    bool ok = true;
-    Ring pos_a{0, 0u}, pos_b{0, 0u};
-    uint32_t posted = 0, taken = 0;  // rows of this team whose sums were posted, used
+    const float* stat1 = p.rstd_post + seg0 + team;
+    const float* stat2 = p.rstd_next + seg0 + team;
+    // the row statistics, loaded a row ahead of their use
+    float rs1_a = 1.f, rs2_a = 0.f;
+    if (POST && nrows > 0) rs1_a = __ldg(stat1);
+    if (NEXT && nrows > 0) rs2_a = __ldg(stat2);
+    float rs1_n = 1.f, rs2_n = 0.f;
     float3 own = make_float3(0.f, 0.f, 0.f);  // a lone warp's sums of the row in A
-    float rs1_a = 1.f, rs2_a = 0.f, rs1_b = 1.f, rs2_b = 0.f;
-    float3 sums_b = own;
-
-    for (int64_t seg0 = r0; seg0 < r1;) {
-      const int64_t q = seg0 / p.rows_per_gate;
-      const int64_t seg1 = (q + 1) * p.rows_per_gate < r1 ? (q + 1) * p.rows_per_gate : r1;
-      const int nst = (int)((seg1 - seg0 + K - 1) / K);
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int v = tt + j * threads;
-        float f[E], g[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          f[e] = 1.f - p.off;
-          g[e] = 1.f;
-        }
-        if (POST && v < nvec) load_elems<T, E>(gamma_post + col0 + v * E, f);
-        if (gate != nullptr && v < nvec)
-          load_elems<T, E>(gate + q * p.hidden + col0 + v * E, g);
-#pragma unroll
-        for (int e = 0; e < E; ++e) w[j][e] = p.b * g[e] * (f[e] + p.off);
+    auto sums = [&](int i) {  // A
+      if (early && steps >= 2 && threadIdx.x == 0) fill();
+      ok = ok && wait_all(&sh.full[pos_a.stage], pos_a.phase, abort);
+      rs1_n = rs1_a;
+      rs2_n = rs2_a;
+      if ((i + 1) * K < nrows) {
+        if (POST) rs1_a = __ldg(stat1 + (i + 1) * K);
+        if (NEXT) rs2_a = __ldg(stat2 + (i + 1) * K);
       }
-      auto row_of = [&](int i) { return seg0 + (int64_t)i * K + team; };
-      auto stats = [&](int i) {  // the row statistics, loaded a row ahead of their use
-        const int64_t row = row_of(i);
-        if (row < seg1) {
-          if (POST) rs1_a = __ldg(p.rstd_post + row);
-          if (NEXT) rs2_a = __ldg(p.rstd_next + row);
-        }
-      };
-      float rs1_n = 1.f, rs2_n = 0.f;
-      auto sums = [&](int i) {  // A
-        ok = ok && wait_all(&sh.full[pos_a.stage], pos_a.phase, abort);
-        rs1_n = rs1_a;
-        rs2_n = rs2_a;
-        if (i + 1 < nst) stats(i + 1);
-        if (ok && row_of(i) < seg1) {
-          const unsigned char* st = ring + (size_t)pos_a.stage * sp.stride;
-          const T* sx = reinterpret_cast<const T*>(st) + team * cols;
-          const TS* sr = reinterpret_cast<const TS*>(st + at.r) + team * cols;
-          const T* sdy = reinterpret_cast<const T*>(st + at.dy) + team * cols;
-          const TS* sdr = reinterpret_cast<const TS*>(st + at.dr) + team * cols;
-          float s1 = 0.f, s2 = 0.f, s3 = 0.f;
+      if (ok && i * K < nrows) {
+        const unsigned char* st = ring + (size_t)pos_a.stage * sp.stride;
+        const T* sx = reinterpret_cast<const T*>(st) + team * cols;
+        const TS* sr = reinterpret_cast<const TS*>(st + at.r) + team * cols;
+        const T* sdy = reinterpret_cast<const T*>(st + at.dy) + team * cols;
+        const TS* sdr = reinterpret_cast<const TS*>(st + at.dr) + team * cols;
+        const f32x2 rs1 = pair(rs1_n, rs1_n), rs2 = pair(rs2_n, rs2_n);
+        f32x2 s1 = 0, s2 = 0, s3 = 0;
 #pragma unroll
-          for (int j = 0; j < NV; ++j) {
-            const int v = tt + j * threads;
-            if (v >= nvec) continue;
-            float x[E], r[E], dy[E], d[E];
-            if (POST) load_elems<T, E>(sx + v * E, x);
-            if (NEXT) {
-              load_elems<TS, E>(sr + v * E, r);
-              load_elems<T, E>(sdy + v * E, dy);
-            }
-            if (POST) {
-              if (has_dr) {
-                load_elems<TS, E>(sdr + v * E, d);
-              } else {
+        for (int j = 0; j < NV; ++j) {
+          const int v = tt + j * threads;
+          if (v >= nvec) continue;
+          f32x2 x[N], d[N];
+          if (POST) {
 #pragma unroll
-                for (int e = 0; e < E; ++e) d[e] = 0.f;
-              }
-            }
+            for (int k = 0; k < N; ++k) d[k] = 0;
+            load_pairs<T, N>(sx + v * E, x);
+            if (has_dr) load_pairs<TS, N>(sdr + v * E, d);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-              float rh = 0.f, g = 0.f;
-              if (NEXT) {
-                rh = r[e] * rs2_n;
-                g = dy[e] * w2[j][e];
-                s1 = fmaf(g, rh, s1);
-              }
+            for (int k = 0; k < N; ++k) x[k] = mul2(w[j][k], mul2(x[k], rs1));
+          }
+          if (NEXT) {
+            f32x2 r[N], dy[N];
+            load_pairs<TS, N>(sr + v * E, r);
+            load_pairs<T, N>(sdy + v * E, dy);
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+              const f32x2 rh = mul2(r[k], rs2), g = mul2(dy[k], w2[j][k]);
+              s1 = fma2(g, rh, s1);
               if (POST) {
-                const float wx = w[j][e] * (x[e] * rs1_n);
-                s2 = fmaf(wx, NEXT ? fmaf(rs2_n, g, d[e]) : d[e], s2);
-                if (NEXT) s3 = fmaf(wx, rh, s3);
+                s3 = fma2(x[k], rh, s3);
+                d[k] = fma2(rs2, g, d[k]);
               }
             }
           }
-          if (POST && NEXT)
-            own = warp_sum3(s1, s2, s3, lane);
-          else
-            own = make_float3(NEXT ? warp_sum(s1) : 0.f, POST ? warp_sum(s2) : 0.f, 0.f);
-          if (!alone)
-            post3(t, sh.slot[posted % kDepth] + team * sp.wpt * cs, &sh.red[team][posted % kDepth],
-                  make_float4(own.x, own.y, own.z, 0.f));
-          ++posted;
+          if (POST)
+#pragma unroll
+            for (int k = 0; k < N; ++k) s2 = fma2(x[k], d[k], s2);
         }
-        pos_a.next(stages);
-      };
-      stats(0);
-      sums(0);
-      for (int i = 0; i < nst; ++i) {
-        rs1_b = rs1_n;
-        rs2_b = rs2_n;
-        sums_b = own;
-        if (i + 1 < nst) sums(i + 1);
-        const int64_t row = row_of(i);
-        if (ok && row < seg1) {  // B
-          float3 s = sums_b;
-          if (!alone) {
-            ok = team_wait(t, &sh.red[team][taken % kDepth], (taken / kDepth) & 1u);
-            s = total3(t, sh.slot[taken % kDepth] + team * sp.wpt * cs);
-          }
-          ++taken;
-          const float c1 = s.x * inv;
-          const float c2 = POST ? fmaf(-rs2_b * c1, s.z, s.y) * inv : 0.f;
-          const unsigned char* st = ring + (size_t)pos_b.stage * sp.stride;
-          const T* sx = reinterpret_cast<const T*>(st) + team * cols;
-          const TS* sr = reinterpret_cast<const TS*>(st + at.r) + team * cols;
-          const T* sdy = reinterpret_cast<const T*>(st + at.dy) + team * cols;
-          const TS* sdr = reinterpret_cast<const TS*>(st + at.dr) + team * cols;
-          T* dx = static_cast<T*>(p.dx) + row * p.hidden + col0;
-          TS* dres = static_cast<TS*>(p.dres) + row * p.hidden + col0;
-#pragma unroll
-          for (int j = 0; j < NV; ++j) {
-            const int v = tt + j * threads;
-            if (v >= nvec) continue;
-            float x[E], r[E], dy[E], d[E], o[E];
-            if (has_x) {
-              load_elems<T, E>(sx + v * E, x);
-            } else {
-#pragma unroll
-              for (int e = 0; e < E; ++e) x[e] = 0.f;
-            }
-            if (has_dr) {
-              load_elems<TS, E>(sdr + v * E, d);
-            } else {
-#pragma unroll
-              for (int e = 0; e < E; ++e) d[e] = 0.f;
-            }
-            if (NEXT) {
-              load_elems<TS, E>(sr + v * E, r);
-              load_elems<T, E>(sdy + v * E, dy);
-#pragma unroll
-              for (int e = 0; e < E; ++e) {
-                const float rh = r[e] * rs2_b;
-                d[e] = fmaf(rs2_b, fmaf(-rh, c1, dy[e] * w2[j][e]), d[e]);
-                acc_n[j][e] = fmaf(dy[e], rh, acc_n[j][e]);
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-              const float xh = POST ? x[e] * rs1_b : x[e];
-              acc_a[j][e] = fmaf(d[e], xh, acc_a[j][e]);
-              o[e] = POST ? rs1_b * fmaf(-xh, c2, w[j][e] * d[e]) : w[j][e] * d[e];
-              d[e] *= p.a;
-            }
-            store_elems<T, E>(dx + v * E, o);
-            store_elems<TS, E>(dres + v * E, d);
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.empty[pos_b.stage]);
-        pos_b.next(stages);
+        if (POST && NEXT)
+          own = warp_sum3(sum2(s1), sum2(s2), sum2(s3), lane);
+        else
+          own = make_float3(NEXT ? warp_sum(sum2(s1)) : 0.f, POST ? warp_sum(sum2(s2)) : 0.f, 0.f);
+        if (!alone)
+          post3(t, sh.slot[posted % kDepth] + team * sp.wpt * cs, &sh.red[team][posted % kDepth],
+                make_float4(own.x, own.y, own.z, 0.f));
+        ++posted;
       }
-
-      // the segment's sum of A, and after the last one that of dgamma_next:
-      // a thread's own columns, or its columns of the teams' sums
-      const bool first = q == r0 / p.rows_per_gate, last = seg1 == r1;
-      float* pa = p.p_a + (unit + q) * p.hidden + col0;
-      float* pp = p.p_post + unit * p.hidden + col0;
-      float* pn = p.p_next + unit * p.hidden + col0;
-      auto put_a = [&](int c, float v) {
-        v *= p.b;
-        if (gate != nullptr) {
-          pa[c] = v;
-          v *= Traits<T>::to_f(gate[q * p.hidden + col0 + c]);
+      pos_a.next(stages);
+      if (!early && steps >= 2 && threadIdx.x == 0) fill();
+      ++steps;
+      __syncwarp();
+    };
+    sums(0);
+    for (int i = 0; i < nst; ++i) {
+      const f32x2 rs1 = pair(rs1_n, rs1_n), rs2 = pair(rs2_n, rs2_n);
+      float3 s = own;
+      if (i + 1 < nst) sums(i + 1);
+      if (ok && i * K < nrows) {  // B
+        if (!alone) {
+          ok = team_wait(t, &sh.red[team][taken % kDepth], (taken / kDepth) & 1u);
+          s = total3(t, sh.slot[taken % kDepth] + team * sp.wpt * cs);
         }
-        if (POST) pp[c] = first ? v : pp[c] + v;
-      };
-      if (K == 1) {
+        ++taken;
+        const float rs2f = split(rs2).x;
+        const float c1f = s.x * inv;
+        const float c2f = POST ? fmaf(-rs2f * c1f, s.z, s.y) * inv : 0.f;
+        const f32x2 c1 = pair(-c1f, -c1f), c2 = pair(-c2f, -c2f);
+        const unsigned char* st = ring + (size_t)pos_b.stage * sp.stride;
+        const T* sx = reinterpret_cast<const T*>(st) + team * cols;
+        const TS* sr = reinterpret_cast<const TS*>(st + at.r) + team * cols;
+        const T* sdy = reinterpret_cast<const T*>(st + at.dy) + team * cols;
+        const TS* sdr = reinterpret_cast<const TS*>(st + at.dr) + team * cols;
+        const int64_t to = (seg0 + team + (int64_t)i * K) * p.hidden + col0;
+        T* dx = static_cast<T*>(p.dx) + to;
+        TS* dres = static_cast<TS*>(p.dres) + to;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const int v = tt + j * threads;
+          if (v >= nvec) continue;
+          f32x2 x[N], d[N];
+#pragma unroll
+          for (int k = 0; k < N; ++k) x[k] = d[k] = 0;
+          if (has_dr) load_pairs<TS, N>(sdr + v * E, d);
+          if (NEXT) {
+            f32x2 r[N], dy[N];
+            load_pairs<TS, N>(sr + v * E, r);
+            load_pairs<T, N>(sdy + v * E, dy);
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+              const f32x2 rh = mul2(r[k], rs2);
+              d[k] = fma2(rs2, fma2(c1, rh, mul2(dy[k], w2[j][k])), d[k]);
+              acc_n[j][k] = fma2(dy[k], rh, acc_n[j][k]);
+            }
+          }
+          if (has_x) load_pairs<T, N>(sx + v * E, x);
+#pragma unroll
+          for (int k = 0; k < N; ++k) {
+            if (POST) x[k] = mul2(x[k], rs1);
+            acc_a[j][k] = fma2(d[k], x[k], acc_a[j][k]);
+            const f32x2 g = mul2(w[j][k], d[k]);
+            x[k] = POST ? mul2(rs1, fma2(c2, x[k], g)) : g;
+            d[k] = mul2(a2, d[k]);
+          }
+          store_pairs<T, N>(dx + v * E, x);
+          store_pairs<TS, N>(dres + v * E, d);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.empty[pos_b.stage]);
+      pos_b.next(stages);
+    }
+
+    // the segment's sum of A, and after the last one that of dgamma_next: a
+    // thread's own columns, or its columns of the teams' sums, added in turn
+    const bool first = q == r0 / p.rows_per_gate, last = seg1 == r1;
+    float* pa = p.p_a + (unit + q) * p.hidden + col0;
+    float* pp = p.p_post + unit * p.hidden + col0;
+    float* pn = p.p_next + unit * p.hidden + col0;
+    auto put_a = [&](int c, float v) {
+      v *= p.b;
+      if (gate != nullptr) {
+        pa[c] = v;
+        v *= Traits<T>::to_f(gate[q * p.hidden + col0 + c]);
+      }
+      if (POST) pp[c] = first ? v : pp[c] + v;
+    };
+    auto put_n = [&](int c, float v) { pn[c] = v; };
+    auto flush = [&](f32x2 (&acc)[NV][N], auto put) {
+      f32x2* comb = reinterpret_cast<f32x2*>(ring + (size_t)stages * sp.stride);
+      if (K > 1)
+        for (int m = 0; m < K; ++m) {
+          if (team == m)
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+              const int v = tt + j * threads;
+              if (v >= nvec) continue;
+#pragma unroll
+              for (int k = 0; k < N; ++k)
+                comb[v * N + k] = m == 0 ? acc[j][k] : add2(comb[v * N + k], acc[j][k]);
+            }
+          __syncthreads();
+        }
+      if (K > 1)
+        for (int c = threadIdx.x; c < cols; c += blockDim.x)
+          put(c, reinterpret_cast<const float*>(comb)[c]);
+      else
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           const int v = tt + j * threads;
           if (v >= nvec) continue;
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            if (want_a) put_a(v * E + e, acc_a[j][e]);
-            if (NEXT && last) pn[v * E + e] = acc_n[j][e];
-            acc_a[j][e] = 0.f;
+          for (int k = 0; k < N; ++k) {
+            const float2 f = split(acc[j][k]);
+            put(v * E + 2 * k, f.x);
+            put(v * E + 2 * k + 1, f.y);
           }
         }
-      } else {
-        float* comb = reinterpret_cast<float*>(ring + (size_t)stages * sp.stride);
-        const int consumers = blockDim.x - 32;
-        auto join = [&](float (&acc)[NV][E], auto put) {
+      if (K > 1) __syncthreads();
+    };
+    if (want_a) flush(acc_a, put_a);
+    if (NEXT && last) flush(acc_n, put_n);
 #pragma unroll
-          for (int j = 0; j < NV; ++j) {
-            const int v = tt + j * threads;
-            if (v >= nvec) continue;
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int e = 0; e < E; e += 4)
-              *reinterpret_cast<float4*>(comb + team * cols + v * E + e) =
-                  make_float4(acc[j][e], acc[j][e + 1], acc[j][e + 2], acc[j][e + 3]);
-          }
-          asm volatile("bar.sync 1, %0;" ::"r"(consumers) : "memory");
-          for (int c = threadIdx.x - 32; c < cols; c += consumers) {
-            float v = 0.f;
-            for (int m = 0; m < K; ++m) v += comb[m * cols + c];
-            put(c, v);
-          }
-          asm volatile("bar.sync 1, %0;" ::"r"(consumers) : "memory");
-        };
-        if (want_a) join(acc_a, put_a);
-        if (NEXT && last) join(acc_n, [&](int c, float v) { pn[c] = v; });
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc_a[j][e] = 0.f;
-      }
-      seg0 = seg1;
-    }
+      for (int k = 0; k < N; ++k) acc_a[j][k] = 0;
+    seg0 = seg1;
   }
+  // after a wait that ran out copies may still be on their way
+  if (threadIdx.x == 0 && *abort) drain_ring(sh.full, sh.fill, sh.issued, stages);
   __syncwarp();
   if (cs > 1) cluster_sync();  // no CTA leaves while a peer may write to its slots
 }
@@ -826,36 +939,80 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1)
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-// Threads and stages for rows of `hidden` elements, `unit_bytes(k, cols)` the
-// bytes of a stage of k rows of cols columns and `extra` those beside the
-// ring.  The row is split over as few CTAs as leave `want` stages (else 2).
-struct Shape {
+constexpr int kSlack = 1024;  // static shared memory beside the kernels' structs
+
+// The forward's teams and stages for `rows` rows on `sms` SMs.  The row is
+// split over as few CTAs as leave two stages beside the weights.
+struct FwdShape {
+  int teams, wpt, cs, stages, stage_rows, stride;
+  size_t smem;
+};
+
+bool fwd_shape(int64_t rows, int hidden, int sms, int row_elem, int planes, int align, int elems,
+               FwdShape* s) {
+  const int budget = kSmemBudget - (int)sizeof(FwdShared) - kSlack;
+  for (int cs = 1; cs <= kMaxSplit; cs *= 2) {
+    if (hidden % (align * cs) != 0) return false;
+    const int cols = hidden / cs, row = cols * row_elem, over = planes * cols * 4;
+    if (over + 2 * ((row + 127) / 128 * 128) > budget) continue;
+    s->cs = cs;
+    const int64_t mine = (rows * cs + sms - 1) / sms;  // rows a CTA, about
+    const int most = (cols / elems + 31) / 32;         // warps a row can use
+    s->stage_rows = 1;
+    if (cs > 1 || mine <= 2) {
+      s->wpt = most < kMaxWarps ? most : kMaxWarps;
+      s->teams = 1;
+    } else {
+      s->wpt = 1;
+      while (s->wpt < kMaxWarps && cols > 4096 * s->wpt) s->wpt *= 2;
+      // narrow rows: several to a stage, as long as every team has its own
+      while (s->stage_rows * row < 8192 && mine >= 2 * kFwdTeams * s->stage_rows) s->stage_rows *= 2;
+      s->teams = kMaxWarps / s->wpt < kFwdTeams ? kMaxWarps / s->wpt : kFwdTeams;
+    }
+    s->stride = (s->stage_rows * row + 127) / 128 * 128;
+    s->stages = (budget - over) / s->stride;
+    if (s->stages > kMaxStages) s->stages = kMaxStages;
+    if (s->teams > s->stages) s->teams = s->stages;
+    s->stages -= s->stages % s->teams;  // a stage is always the same team's
+    s->smem = (size_t)over + (size_t)s->stages * s->stride;
+    return true;
+  }
+  return false;
+}
+
+// The backward's teams and stages: all warps busy and three stages, with 16
+// columns a thread or else 8 (one row a stage), over as few CTAs as can be.
+struct BwdPick {
   int teams, wpt, cs, stages, stride, nv8;  // nv8: groups of 8 columns a thread
   size_t smem;
 };
 
-template <typename F, typename X>
-bool pick_shape(int hidden, int want, F unit_bytes, X extra, int budget, Shape* out) {
-  for (int least = want; least >= 2; least -= want > 2 ? want - 2 : 1) {
+template <typename F>
+bool bwd_pick(int hidden, int align, F stage_bytes, BwdPick* out) {
+  const int budget = kSmemBudget - (int)sizeof(BwdShared) - kSlack;
+  for (int least = 3; least >= 2; --least)
     for (int cs = 1; cs <= kMaxSplit; cs *= 2) {
-      if (hidden % (8 * cs) != 0) break;
+      if (hidden % (align * cs) != 0) break;
       const int cols = hidden / cs;
-      if (cols > 16 * 32 * kMaxWarps) continue;
-      Shape s;
-      s.cs = cs;
-      s.nv8 = cols <= 8 * 32 * kMaxWarps ? 1 : 2;
-      s.wpt = (cols / 8 + s.nv8 * 32 - 1) / (s.nv8 * 32);
-      s.teams = cs > 1 ? 1 : kMaxWarps / s.wpt;
-      s.stride = (unit_bytes(s.teams, cols) + 127) / 128 * 128;
-      const int over = s.teams > 1 ? extra(s.teams, cols) : 0;
-      s.stages = (budget - over) / s.stride;
-      if (s.stages > kMaxStages) s.stages = kMaxStages;
-      if (s.stages < least) continue;
-      s.smem = (size_t)s.stages * s.stride + over;
-      *out = s;
-      return true;
+      for (int nv8 = cols < 512 ? 1 : 2; nv8 >= 1; --nv8) {
+        BwdPick s;
+        s.cs = cs;
+        s.nv8 = nv8;
+        s.wpt = (cols + nv8 * 256 - 1) / (nv8 * 256);
+        if (s.wpt > kMaxWarps) continue;
+        for (s.teams = cs > 1 ? 1 : kMaxWarps / s.wpt; s.teams >= 1; --s.teams) {
+          if (s.teams * s.wpt < kMaxWarps / 2 + 1 && nv8 == 2 && 2 * s.wpt <= kMaxWarps) break;
+          const int comb = s.teams > 1 ? cols * 4 : 0;
+          s.stride = (stage_bytes(s.teams, cols) + 127) / 128 * 128;
+          s.stages = (budget - comb) / s.stride;
+          if (s.stages > kMaxStages) s.stages = kMaxStages;
+          if (s.stages < least) continue;
+          s.smem = (size_t)s.stages * s.stride + comb;
+          *out = s;
+          return true;
+        }
+      }
     }
-  }
   return false;
 }
 
@@ -868,10 +1025,13 @@ cudaError_t allow_smem(K kern, size_t bytes) {
 template <typename T, typename TS, bool POST, bool NEXT>
 bool try_fwd(const BlockFwdArgs& a, cudaStream_t s, cudaError_t* err) {
   constexpr int E = kElems<T, TS>;
-  Shape sh;
-  if (!pick_shape(a.hidden, 3,
-                  [](int k, int cols) { return k * cols * (int)(sizeof(T) + sizeof(TS)); },
-                  [](int, int) { return 0; }, kSmemBudget - (int)sizeof(FwdShared), &sh))
+  int dev = 0;
+  *err = cudaGetDevice(&dev);
+  if (*err != cudaSuccess) return true;
+  const int sms = sm_count(dev);
+  FwdShape sh;
+  if (!fwd_shape(a.rows, a.hidden, sms, (int)(sizeof(T) + sizeof(TS)), NEXT ? 2 : 1,
+                 16 / (int)sizeof(T), E, &sh))
     return false;
   BlockFwdParams p;
   p.x = a.x;
@@ -894,26 +1054,17 @@ bool try_fwd(const BlockFwdArgs& a, cudaStream_t s, cudaError_t* err) {
   p.wpt = sh.wpt;
   p.cs = sh.cs;
   p.stages = sh.stages;
+  p.stage_rows = sh.stage_rows;
   p.stride = sh.stride;
-  int dev = 0;
-  *err = cudaGetDevice(&dev);
+  auto kern = block_fwd_tma<T, TS, POST, NEXT>;
+  *err = allow_smem(kern, sh.smem);
   if (*err != cudaSuccess) return true;
-  auto go = [&](auto kern) {
-    *err = allow_smem(kern, sh.smem);
-    if (*err != cudaSuccess) return;
-    const int threads = 32 * (1 + sh.teams * sh.wpt);
-    const int64_t occ = max_blocks_per_sm((const void*)kern, threads, sh.smem);
-    int64_t units = sm_count(dev) * occ / sh.cs;
-    const int64_t blocks = (a.rows + sh.teams - 1) / sh.teams;
-    if (units > blocks) units = blocks;
-    if (units < 1) units = 1;
-    *err = launch_kernel(kern, dim3((unsigned)(units * sh.cs)), dim3(threads), sh.smem, s, sh.cs,
-                         p);
-  };
-  if (sh.nv8 == 1)
-    go(block_fwd_tma<T, TS, POST, NEXT, 8 / E>);
-  else
-    go(block_fwd_tma<T, TS, POST, NEXT, 16 / E>);
+  int64_t units = sms / sh.cs;
+  const int64_t blocks = (a.rows + sh.stage_rows - 1) / sh.stage_rows;
+  if (units > blocks) units = blocks;
+  if (units < 1) units = 1;
+  *err = launch_kernel(kern, dim3((unsigned)(units * sh.cs)), dim3(32 * (1 + sh.teams * sh.wpt)),
+                       sh.smem, s, sh.cs, p);
   return true;
 }
 
@@ -924,11 +1075,9 @@ bool try_bwd(const BlockBwdArgs& a, BlockBwdParams& p, int* units, cudaStream_t 
   BwdShape sp;
   sp.read_x = POST || a.gate != nullptr;
   const bool dr = a.dr != nullptr, x = sp.read_x;
-  Shape sh;
-  if (!pick_shape(a.hidden, 3,
-                  [=](int k, int cols) { return bwd_stage<T, TS>(k, cols, x, NEXT, dr).bytes; },
-                  [](int k, int cols) { return k * cols * 4; }, kSmemBudget - (int)sizeof(BwdShared),
-                  &sh))
+  BwdPick sh;
+  if (!bwd_pick(a.hidden, 16 / (int)sizeof(T),
+                [=](int k, int cols) { return bwd_stage<T, TS>(k, cols, x, NEXT, dr).bytes; }, &sh))
     return false;
   sp.teams = sh.teams;
   sp.wpt = sh.wpt;
@@ -947,9 +1096,8 @@ bool try_bwd(const BlockBwdArgs& a, BlockBwdParams& p, int* units, cudaStream_t 
   auto go = [&](auto kern) {
     *err = allow_smem(kern, sh.smem);
     if (*err != cudaSuccess) return;
-    const int threads = 32 * (1 + sh.teams * sh.wpt);
-    *err = launch_kernel(kern, dim3((unsigned)(n * sh.cs)), dim3(threads), sh.smem, s, sh.cs, p,
-                         sp);
+    *err = launch_kernel(kern, dim3((unsigned)(n * sh.cs)), dim3(32 * sh.teams * sh.wpt), sh.smem,
+                         s, sh.cs, p, sp);
   };
   if (sh.nv8 == 1)
     go(block_bwd_tma<T, TS, POST, NEXT, 8 / E>);
