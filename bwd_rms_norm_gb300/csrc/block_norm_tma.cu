@@ -29,7 +29,7 @@ __device__ unsigned int g_block_timeouts;
 
 constexpr int kMaxWarps = 16;     // consumer warps of a CTA
 constexpr int kMaxStages = 16;
-constexpr int kMaxSplit = 8;      // CTAs a row is split over
+constexpr int kMaxSplit = 16;      // CTAs a row is split over
 constexpr int kSmemBudget = 224 * 1024;
 
 // Elements a thread loads at a time: 16 bytes of the narrower type, and 16 of
@@ -189,15 +189,6 @@ __device__ void drain_ring(uint64_t* full, Ring pos, int64_t issued, int stages)
   }
 }
 
-// A team's exchange of one sum (or three) of a row over its warps in every
-// CTA of the cluster: `slots` [depth][cs * wpt], `bars` [depth].
-struct Team {
-  int wpt, cs;         // warps a team, CTAs a row
-  int tw, lane;        // this warp in the team, this lane
-  uint32_t rank;       // this CTA in the cluster
-  volatile int* abort;
-};
-
 __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
@@ -210,11 +201,13 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity)
   return done != 0;
 }
 
-__device__ __forceinline__ bool team_wait(const Team& t, uint64_t* bar, uint32_t parity) {
-  if (t.cs == 1) return wait_all(bar, parity, t.abort);
+// A barrier that the CTAs of a cluster of cs arrive on.
+__device__ __forceinline__ bool team_wait(int cs, uint64_t* bar, uint32_t parity,
+                                          volatile int* abort) {
+  if (cs == 1) return wait_all(bar, parity, abort);
   bool done = false;
   for (int i = 0; i < kTries && !done; ++i) done = try_wait_cluster(bar, parity);
-  if (!done) done = wait_cluster_counted(bar, parity, t.abort, &g_block_timeouts);
+  if (!done) done = wait_cluster_counted(bar, parity, abort, &g_block_timeouts);
   return __all_sync(0xffffffffu, done);
 }
 
@@ -226,19 +219,6 @@ __device__ __forceinline__ void st_peer4(float4* local, uint32_t peer, float4 v)
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(remote), "f"(v.x),
                "f"(v.y), "f"(v.z), "f"(v.w)
                : "memory");
-}
-
-// Posts the warp's parts (the same in every lane) in its slot and arrives.
-__device__ __forceinline__ void post3(const Team& t, float4* slot, uint64_t* bar, float4 v) {
-  if (t.cs == 1) {
-    if (t.lane == 0) {
-      slot[t.tw] = v;
-      mbar_arrive(bar);
-    }
-  } else if (t.lane < t.cs) {
-    st_peer4(slot + t.rank * t.wpt + t.tw, t.lane, v);
-    mbar_arrive_peer(bar, t.lane);
-  }
 }
 
 // Three sums over the lanes at once: lanes exchange halves of the values as
@@ -257,18 +237,6 @@ __device__ __forceinline__ float3 warp_sum3(float a, float b, float c, int lane)
   v += __shfl_xor_sync(0xffffffffu, v, 1);
   return make_float3(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 8),
                      __shfl_sync(0xffffffffu, v, 16));
-}
-
-__device__ __forceinline__ float3 total3(const Team& t, const float4* slot) {
-  const int n = t.cs * t.wpt;
-  float a = 0.f, b = 0.f, c = 0.f;
-  for (int i = t.lane; i < n; i += 32) {
-    const float4 q = slot[i];
-    a += q.x;
-    b += q.y;
-    c += q.z;
-  }
-  return warp_sum3(a, b, c, t.lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -419,7 +387,6 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) block_fwd_tma(const B
     __syncwarp();
   } else {
     const int team = (warp - 1) / p.wpt, tw = (warp - 1) % p.wpt;
-    const Team t{p.wpt, cs, tw, lane, rank, abort};
     const int tt = tw * 32 + lane, threads = p.wpt * 32;
     const float inv = 1.f / (float)p.hidden;
     bool ok = true;
@@ -438,7 +405,7 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) block_fwd_tma(const B
           st_peer(slot + rank * p.wpt + tw, lane, v);
           mbar_arrive_peer(&sh.red[d], lane);
         }
-        ok = ok && team_wait(t, &sh.red[d], parity);
+        ok = ok && team_wait(cs, &sh.red[d], parity, abort);
       }
       float s = 0.f;
       for (int i = lane; i < cs * p.wpt; i += 32) s += slot[i];
@@ -576,35 +543,38 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) block_fwd_tma(const B
 // ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
-// All warps are in teams; a team works on one row, and a stage holds one row
-// a team.  A thread owns the same 8 or 16 columns of every row: their weights
-// and their fp32 sums over the rows stay in its registers (which is why no
-// warp is set aside for the copies: 16 warps have 128 registers a thread, 17
-// have 96).  The reductions never stop a team: a warp posts its part of a
-// row's sums to a slot, of every CTA of the cluster, arrives on the row's
-// barrier (red), and takes the row up again after the sums of the next one:
-//   A(i + 1): the three sums of row i + 1 -> red
-//   B(i): wait for red of row i; dx and dresidual, read again from its stage
-// Slots and barriers are four deep: a warp posts row i + 4 only after a wait
-// that every reader of row i has passed.  The stage of row i - 1 is filled
-// again by thread 0 between A(i + 1) and B(i), when the other warps are
-// through with it (before A(i + 1) where there are two stages, and it is the
-// one that A(i + 1) reads).
-constexpr int kDepth = 4;
+// Three roles, which meet at per-stage mbarriers:
+//   producer (warp 0)   copies a stage's rows (one, or several narrow ones):
+//                       x, r, dy and dr                          -> full[s]
+//   reducers            a warp takes every `reducers`-th stage: the three sums
+//                       of each row, c1 and c2 into the row's slot -> red[s]
+//                       (over a cluster the CTAs' parts of a row are exchanged
+//                       first, through slots of every CTA)
+//   appliers            teams of `wpt` warps, a row of the stage each: dx and
+//                       dresidual; a thread owns the same 8 or 16 columns of
+//                       every row, whose weights and fp32 sums over the rows
+//                       stay in its registers                    -> empty[s]
+// A row's sums are taken by one warp because sums exchanged between all the
+// warps of a CTA, every row, cost more than the sums: with 16 warps on a row
+// (each warp its columns, parts posted to slots and taken up a row later)
+// 16384 x 8192 bf16 took 530 to 600 us.  The reducers' weights stand in shared
+// memory as in the forward.
+constexpr int kBwdStages = 8;
+constexpr int kBwdRows = 32;      // rows of a stage, at most
+constexpr int kBwdWarps = 16;     // 128 registers a thread
 
 struct BwdShared {
-  uint64_t full[kMaxStages];
-  uint64_t empty[kMaxStages];
-  uint64_t red[kMaxWarps][kDepth];
-  float4 slot[kDepth][kMaxWarps * kMaxSplit];
-  int64_t fill_row;   // thread 0's: the next row to copy,
-  int64_t issued;     // the copies issued, and the stage of the next one
-  Ring fill;
+  uint64_t full[kBwdStages];
+  uint64_t red[kBwdStages];
+  uint64_t empty[kBwdStages];
+  uint64_t parts[kBwdStages];
+  float4 stat[kBwdStages][kBwdRows];          // c1, c2, rstd_post, rstd_next
+  float4 part[2][kBwdStages][kMaxSplit];      // of the cluster's CTAs
   int abort;
 };
 
 struct BwdShape {
-  int teams, wpt, cs, stages, stride;
+  int reducers, teams, wpt, cs, stages, stage_rows, stride;
   bool read_x;  // x is wanted: a post norm or the gate's gradient
 };
 
@@ -614,9 +584,9 @@ struct BwdStage {
 };
 
 template <typename T, typename TS>
-__host__ __device__ inline BwdStage bwd_stage(int teams, int cols, bool x, bool next, bool dr) {
+__host__ __device__ inline BwdStage bwd_stage(int rows, int cols, bool x, bool next, bool dr) {
   BwdStage s;
-  const int t = teams * cols * (int)sizeof(T), ts = teams * cols * (int)sizeof(TS);
+  const int t = rows * cols * (int)sizeof(T), ts = rows * cols * (int)sizeof(TS);
   s.r = x ? t : 0;
   s.dy = s.r + (next ? ts : 0);
   s.dr = s.dy + (next ? t : 0);
@@ -624,33 +594,54 @@ __host__ __device__ inline BwdStage bwd_stage(int teams, int cols, bool x, bool 
   return s;
 }
 
+// The stages of a unit's rows, in order: n rows from `row` (counted from the
+// unit's first) on, of gate row q; a stage never crosses from one gate row to
+// the next.
+struct Walk {
+  int row, n, end, total, most;
+  int64_t q, rows_per_gate;
+  __device__ Walk(int64_t r0, int64_t r1, int64_t rpg, int stage_rows)
+      : row(0), n(0), total((int)(r1 - r0)), most(stage_rows), q(r0 / rpg), rows_per_gate(rpg) {
+    const int64_t left = (q + 1) * rpg - r0;
+    end = left < total ? (int)left : total;
+  }
+  __device__ __forceinline__ bool next() {
+    row += n;
+    if (row >= total) return false;
+    if (row == end) {
+      ++q;
+      end = rows_per_gate < total - end ? end + (int)rows_per_gate : total;
+    }
+    n = end - row < most ? end - row : most;
+    return true;
+  }
+};
+
 template <typename T, typename TS, bool POST, bool NEXT, int NV>
-__global__ void __launch_bounds__(32 * kMaxWarps, 1)
+__global__ void __launch_bounds__(32 * kBwdWarps, 1)
     block_bwd_tma(const BlockBwdParams p, const BwdShape sp) {
   constexpr int E = kElems<T, TS>, N = E / 2;
-  extern __shared__ __align__(128) unsigned char ring[];
+  extern __shared__ __align__(128) unsigned char smem[];
   __shared__ BwdShared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int K = sp.teams, stages = sp.stages, cs = sp.cs;
-  const int cols = p.hidden / cs;
+  const int stages = sp.stages, cs = sp.cs, K = sp.stage_rows, reducers = sp.reducers;
+  const int applier_warps = sp.teams * sp.wpt;
+  const int cols = p.hidden / cs, nvec = cols / E;
   const uint32_t rank = cs > 1 ? cta_rank() : 0u;
+  const int col0 = (int)rank * cols;
   const int64_t unit = blockIdx.x / cs, units = gridDim.x / cs;
   const int64_t r0 = unit * p.rows / units, r1 = (unit + 1) * p.rows / units;
   const bool has_dr = p.dr != nullptr, has_x = sp.read_x;
-  for (int i = threadIdx.x; i < kMaxStages + kMaxWarps; i += blockDim.x) {
-    if (i < stages) {
-      mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], K * sp.wpt);
-    }
-    if (i >= kMaxStages)
-      for (int d = 0; d < kDepth; ++d) mbar_init(&sh.red[i - kMaxStages][d], cs * sp.wpt);
+  float4* plane1 = reinterpret_cast<float4*>(smem);
+  float4* plane2 = POST ? plane1 + cols / 4 : plane1;
+  unsigned char* ring = reinterpret_cast<unsigned char*>(NEXT ? plane2 + cols / 4 : plane2);
+  if ((int)threadIdx.x < stages) {
+    mbar_init(&sh.full[threadIdx.x], 1);
+    mbar_init(&sh.red[threadIdx.x], 1);
+    mbar_init(&sh.empty[threadIdx.x], 1 + applier_warps);
+    mbar_init(&sh.parts[threadIdx.x], cs);
   }
-  if (threadIdx.x == 0) {
-    sh.abort = 0;
-    sh.fill_row = r0;
-    sh.issued = 0;
-    sh.fill = Ring{0, 0u};
-  }
+  if (threadIdx.x == 0) sh.abort = 0;
   fence_mbar_init();
   __syncthreads();
   if (cs > 1) cluster_sync();
@@ -658,242 +649,295 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
   pdl_wait();
   volatile int* abort = &sh.abort;
   const BwdStage at = bwd_stage<T, TS>(K, cols, has_x, NEXT, has_dr);
-
-  // Thread 0: the copies of the next stage, if there are rows left.  A stage
-  // never crosses from one gate row to the next.
-  auto fill = [&]() {
-    const int64_t row = sh.fill_row;
-    if (row >= r1) return;
-    Ring pos = sh.fill;
-    if (sh.issued >= stages &&
-        !wait_phase_counted(&sh.empty[pos.stage], pos.phase ^ 1u, abort, &g_block_timeouts)) {
-      sh.fill_row = r1;
-      return;
-    }
-    const int64_t seg = (row / p.rows_per_gate + 1) * p.rows_per_gate;
-    const int64_t end = seg < r1 ? seg : r1;
-    const uint32_t n = (uint32_t)(end - row < K ? end - row : K);
-    const uint32_t tb = n * (uint32_t)(cols * sizeof(T)), sb = n * (uint32_t)(cols * sizeof(TS));
-    unsigned char* st = ring + (size_t)pos.stage * sp.stride;
-    uint64_t* full = &sh.full[pos.stage];
-    const int64_t from = row * p.hidden + (int64_t)rank * cols;  // K is 1 where cs > 1
-    mbar_arrive_expect_tx(full, (has_x ? tb : 0) + (NEXT ? tb + sb : 0) + (has_dr ? sb : 0));
-    if (has_x) bulk_load(st, static_cast<const T*>(p.x) + from, tb, full);
-    if (NEXT) {
-      bulk_load(st + at.r, static_cast<const TS*>(p.r) + from, sb, full);
-      bulk_load(st + at.dy, static_cast<const T*>(p.dy) + from, tb, full);
-    }
-    if (has_dr) bulk_load(st + at.dr, static_cast<const TS*>(p.dr) + from, sb, full);
-    pos.next(stages);
-    sh.fill = pos;
-    sh.issued += 1;
-    sh.fill_row = row + n;
-  };
-  if (threadIdx.x == 0)
-    for (int k = 0; k < stages; ++k) fill();
-
-  const int team = warp / sp.wpt;
-  const Team t{sp.wpt, cs, warp % sp.wpt, lane, rank, abort};
-  const bool alone = sp.wpt == 1 && cs == 1;  // a warp's sums need no exchange
-  const int tt = t.tw * 32 + lane, threads = sp.wpt * 32;
-  const int nvec = cols / E, col0 = (int)rank * cols;
-  const float inv = 1.f / (float)p.hidden;
-  const bool want_a = POST || p.gate != nullptr;
   const T* gamma_post = static_cast<const T*>(p.gamma_post);
+  const T* gamma_next = static_cast<const T*>(p.gamma_next);
   const T* gate = static_cast<const T*>(p.gate);
-  const f32x2 off = pair(p.off, p.off), a2 = pair(p.a, p.a);
-  f32x2 w[NV][N], w2[NV][N], acc_n[NV][N], acc_a[NV][N];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int v = tt + j * threads;
-#pragma unroll
-    for (int i = 0; i < N; ++i) w2[j][i] = 0;
-    if (NEXT && v < nvec) load_pairs<T, N>(static_cast<const T*>(p.gamma_next) + col0 + v * E, w2[j]);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      w2[j][i] = add2(w2[j][i], off);
-      acc_n[j][i] = 0;
-      acc_a[j][i] = 0;
-    }
-  }
-  bool ok = true;
-  Ring pos_a{0, 0u}, pos_b{0, 0u};
-  uint32_t posted = 0, taken = 0;  // rows of this team whose sums were posted, used
-  uint32_t steps = 0;              // stages that went through A
-  const bool early = stages < 3;   // the next stage is the one just left
+  const bool gate_each = gate != nullptr && p.rows_per_gate < p.rows;
+  const f32x2 off = pair(p.off, p.off);
+  Walk walk(r0, r1, p.rows_per_gate, K);
+  Ring pos{0, 0u};
 
-  for (int64_t seg0 = r0; seg0 < r1;) {
-    const int64_t q = seg0 / p.rows_per_gate;
-    const int64_t seg1 = (q + 1) * p.rows_per_gate < r1 ? (q + 1) * p.rows_per_gate : r1;
-    const int nrows = (int)(seg1 - seg0) - team;  // row i of this team: i K < nrows
-    const int nst = (int)((seg1 - seg0 + K - 1) / K);
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int v = tt + j * threads;
-      f32x2 f[N];
-#pragma unroll
-      for (int i = 0; i < N; ++i) w[j][i] = pair(p.b, p.b);
-      if (v >= nvec) continue;
+  if (warp == 0) {
+    if (lane == 0) {
+      int issued = 0;
+      while (walk.next()) {
+        if (issued >= stages &&
+            !wait_phase_counted(&sh.empty[pos.stage], pos.phase ^ 1u, abort, &g_block_timeouts))
+          break;
+        const uint32_t tb = (uint32_t)(walk.n * cols) * (uint32_t)sizeof(T);
+        const uint32_t sb = (uint32_t)(walk.n * cols) * (uint32_t)sizeof(TS);
+        unsigned char* st = ring + (size_t)pos.stage * sp.stride;
+        uint64_t* full = &sh.full[pos.stage];
+        const int64_t from = (r0 + walk.row) * p.hidden + col0;  // K is 1 where cs > 1
+        mbar_arrive_expect_tx(full, (has_x ? tb : 0) + (NEXT ? tb + sb : 0) + (has_dr ? sb : 0));
+        if (has_x) bulk_load(st, static_cast<const T*>(p.x) + from, tb, full);
+        if (NEXT) {
+          bulk_load(st + at.r, static_cast<const TS*>(p.r) + from, sb, full);
+          bulk_load(st + at.dy, static_cast<const T*>(p.dy) + from, tb, full);
+        }
+        if (has_dr) bulk_load(st + at.dr, static_cast<const TS*>(p.dr) + from, sb, full);
+        pos.next(stages);
+        ++issued;
+      }
+      drain_ring(sh.full, pos, issued, stages);
+    }
+    __syncwarp();
+  } else if (warp <= reducers) {
+    // The reducers' weights: w (without a gate of several rows, which is read
+    // from global memory, where L1 holds it) and w2.
+    for (int v = threadIdx.x - 32; v < nvec; v += 32 * reducers) {
+      f32x2 f[N], g[N];
       if (POST) {
         load_pairs<T, N>(gamma_post + col0 + v * E, f);
 #pragma unroll
-        for (int i = 0; i < N; ++i) w[j][i] = mul2(w[j][i], add2(f[i], off));
-      }
-      if (gate != nullptr) {
-        load_pairs<T, N>(gate + q * p.hidden + col0 + v * E, f);
+        for (int i = 0; i < N; ++i) f[i] = mul2(pair(p.b, p.b), add2(f[i], off));
+        if (gate != nullptr && !gate_each) {
+          load_pairs<T, N>(gate + col0 + v * E, g);
 #pragma unroll
-        for (int i = 0; i < N; ++i) w[j][i] = mul2(w[j][i], f[i]);
+          for (int i = 0; i < N; ++i) f[i] = mul2(f[i], g[i]);
+        }
+        store_plane<N>(plane1, nvec, v, f);
+      }
+      if (NEXT) {
+        load_pairs<T, N>(gamma_next + col0 + v * E, f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] = add2(f[i], off);
+        store_plane<N>(plane2, nvec, v, f);
       }
     }
-    const float* stat1 = p.rstd_post + seg0 + team;
-    const float* stat2 = p.rstd_next + seg0 + team;
-    // the row statistics, loaded a row ahead of their use
-    float rs1_a = 1.f, rs2_a = 0.f;
-    if (POST && nrows > 0) rs1_a = __ldg(stat1);
-    if (NEXT && nrows > 0) rs2_a = __ldg(stat2);
-    float rs1_n = 1.f, rs2_n = 0.f;
-    float3 own = make_float3(0.f, 0.f, 0.f);  // a lone warp's sums of the row in A
-    auto sums = [&](int i) {  // A
-      if (early && steps >= 2 && threadIdx.x == 0) fill();
-      ok = ok && wait_all(&sh.full[pos_a.stage], pos_a.phase, abort);
-      rs1_n = rs1_a;
-      rs2_n = rs2_a;
-      if ((i + 1) * K < nrows) {
-        if (POST) rs1_a = __ldg(stat1 + (i + 1) * K);
-        if (NEXT) rs2_a = __ldg(stat2 + (i + 1) * K);
-      }
-      if (ok && i * K < nrows) {
-        const unsigned char* st = ring + (size_t)pos_a.stage * sp.stride;
-        const T* sx = reinterpret_cast<const T*>(st) + team * cols;
-        const TS* sr = reinterpret_cast<const TS*>(st + at.r) + team * cols;
-        const T* sdy = reinterpret_cast<const T*>(st + at.dy) + team * cols;
-        const TS* sdr = reinterpret_cast<const TS*>(st + at.dr) + team * cols;
-        const f32x2 rs1 = pair(rs1_n, rs1_n), rs2 = pair(rs2_n, rs2_n);
+    asm volatile("bar.sync 1, %0;" ::"r"(32 * reducers) : "memory");
+    const float inv = 1.f / (float)p.hidden;
+    const int d = warp - 1;
+    bool more = walk.next();
+    for (int i = 0; i < d && more; ++i) {
+      more = walk.next();
+      pos.next(stages);
+    }
+    uint32_t turn = 0;
+    while (more) {
+      // lane i: the statistics of the stage's row i
+      const int64_t row = r0 + walk.row + (lane < walk.n ? lane : 0);
+      const float rs1_l = POST ? __ldg(p.rstd_post + row) : 1.f;
+      const float rs2_l = NEXT ? __ldg(p.rstd_next + row) : 0.f;
+      if (!wait_all(&sh.full[pos.stage], pos.phase, abort)) break;
+      const unsigned char* st = ring + (size_t)pos.stage * sp.stride;
+      const T* grow = gate_each ? gate + walk.q * p.hidden + col0 : nullptr;
+      bool ok = true;
+      for (int q = 0; q < walk.n; ++q) {
+        const T* sx = reinterpret_cast<const T*>(st) + q * cols;
+        const TS* sr = reinterpret_cast<const TS*>(st + at.r) + q * cols;
+        const T* sdy = reinterpret_cast<const T*>(st + at.dy) + q * cols;
+        const TS* sdr = reinterpret_cast<const TS*>(st + at.dr) + q * cols;
+        const float rs1f = __shfl_sync(0xffffffffu, rs1_l, q);
+        const float rs2f = __shfl_sync(0xffffffffu, rs2_l, q);
+        const f32x2 rs1 = pair(rs1f, rs1f), rs2 = pair(rs2f, rs2f);
         f32x2 s1 = 0, s2 = 0, s3 = 0;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int v = tt + j * threads;
-          if (v >= nvec) continue;
-          f32x2 x[N], d[N];
+#pragma unroll 2
+        for (int v = lane; v < nvec; v += 32) {
+          f32x2 x[N], dv[N];
           if (POST) {
-#pragma unroll
-            for (int k = 0; k < N; ++k) d[k] = 0;
+            f32x2 w[N];
             load_pairs<T, N>(sx + v * E, x);
-            if (has_dr) load_pairs<TS, N>(sdr + v * E, d);
+            load_plane<N>(plane1, nvec, v, w);
+            if (gate_each) {
+              f32x2 g[N];
+              load_pairs<T, N>(grow + v * E, g);
 #pragma unroll
-            for (int k = 0; k < N; ++k) x[k] = mul2(w[j][k], mul2(x[k], rs1));
-          }
-          if (NEXT) {
-            f32x2 r[N], dy[N];
-            load_pairs<TS, N>(sr + v * E, r);
-            load_pairs<T, N>(sdy + v * E, dy);
+              for (int k = 0; k < N; ++k) w[k] = mul2(w[k], g[k]);
+            }
 #pragma unroll
             for (int k = 0; k < N; ++k) {
-              const f32x2 rh = mul2(r[k], rs2), g = mul2(dy[k], w2[j][k]);
+              x[k] = mul2(w[k], mul2(x[k], rs1));
+              dv[k] = 0;
+            }
+            if (has_dr) load_pairs<TS, N>(sdr + v * E, dv);
+          }
+          if (NEXT) {
+            f32x2 r[N], dy[N], w2[N];
+            load_pairs<TS, N>(sr + v * E, r);
+            load_pairs<T, N>(sdy + v * E, dy);
+            load_plane<N>(plane2, nvec, v, w2);
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+              const f32x2 rh = mul2(r[k], rs2), g = mul2(dy[k], w2[k]);
               s1 = fma2(g, rh, s1);
               if (POST) {
                 s3 = fma2(x[k], rh, s3);
-                d[k] = fma2(rs2, g, d[k]);
+                dv[k] = fma2(rs2, g, dv[k]);
               }
             }
           }
           if (POST)
 #pragma unroll
-            for (int k = 0; k < N; ++k) s2 = fma2(x[k], d[k], s2);
+            for (int k = 0; k < N; ++k) s2 = fma2(x[k], dv[k], s2);
         }
+        float3 s;
         if (POST && NEXT)
-          own = warp_sum3(sum2(s1), sum2(s2), sum2(s3), lane);
+          s = warp_sum3(sum2(s1), sum2(s2), sum2(s3), lane);
         else
-          own = make_float3(NEXT ? warp_sum(sum2(s1)) : 0.f, POST ? warp_sum(sum2(s2)) : 0.f, 0.f);
-        if (!alone)
-          post3(t, sh.slot[posted % kDepth] + team * sp.wpt * cs, &sh.red[team][posted % kDepth],
-                make_float4(own.x, own.y, own.z, 0.f));
-        ++posted;
-      }
-      pos_a.next(stages);
-      if (!early && steps >= 2 && threadIdx.x == 0) fill();
-      ++steps;
-      __syncwarp();
-    };
-    sums(0);
-    for (int i = 0; i < nst; ++i) {
-      const f32x2 rs1 = pair(rs1_n, rs1_n), rs2 = pair(rs2_n, rs2_n);
-      float3 s = own;
-      if (i + 1 < nst) sums(i + 1);
-      if (ok && i * K < nrows) {  // B
-        if (!alone) {
-          ok = team_wait(t, &sh.red[team][taken % kDepth], (taken / kDepth) & 1u);
-          s = total3(t, sh.slot[taken % kDepth] + team * sp.wpt * cs);
+          s = make_float3(NEXT ? warp_sum(sum2(s1)) : 0.f, POST ? warp_sum(sum2(s2)) : 0.f, 0.f);
+        if (cs > 1) {
+          // parts of every CTA, added in their order; the slots of a stage are
+          // used in turn, so that none is written before it was read
+          float4* slot = sh.part[turn & 1u][pos.stage];
+          if (lane < cs) {
+            st_peer4(slot + rank, lane, make_float4(s.x, s.y, s.z, 0.f));
+            mbar_arrive_peer(&sh.parts[pos.stage], lane);
+          }
+          ok = team_wait(cs, &sh.parts[pos.stage], pos.phase, abort);
+          s = make_float3(0.f, 0.f, 0.f);
+          for (int i = 0; i < cs; ++i) {
+            const float4 f = slot[i];
+            s.x += f.x;
+            s.y += f.y;
+            s.z += f.z;
+          }
         }
-        ++taken;
-        const float rs2f = split(rs2).x;
-        const float c1f = s.x * inv;
-        const float c2f = POST ? fmaf(-rs2f * c1f, s.z, s.y) * inv : 0.f;
-        const f32x2 c1 = pair(-c1f, -c1f), c2 = pair(-c2f, -c2f);
-        const unsigned char* st = ring + (size_t)pos_b.stage * sp.stride;
-        const T* sx = reinterpret_cast<const T*>(st) + team * cols;
-        const TS* sr = reinterpret_cast<const TS*>(st + at.r) + team * cols;
-        const T* sdy = reinterpret_cast<const T*>(st + at.dy) + team * cols;
-        const TS* sdr = reinterpret_cast<const TS*>(st + at.dr) + team * cols;
-        const int64_t to = (seg0 + team + (int64_t)i * K) * p.hidden + col0;
-        T* dx = static_cast<T*>(p.dx) + to;
-        TS* dres = static_cast<TS*>(p.dres) + to;
+        const float c1 = s.x * inv;
+        const float c2 = POST ? fmaf(-rs2f * c1, s.z, s.y) * inv : 0.f;
+        if (lane == 0) sh.stat[pos.stage][q] = make_float4(-c1, -c2, rs1f, rs2f);
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sh.red[pos.stage]);
+        mbar_arrive(&sh.empty[pos.stage]);
+      }
+      // the reducer's next stage is `reducers` on; its turns count the ring's rounds
+      const int before = pos.stage;
+      for (int i = 0; i < reducers && more; ++i) {
+        more = walk.next();
+        pos.next(stages);
+      }
+      if (pos.stage <= before) ++turn;
+    }
+    __syncwarp();
+  } else {
+    const int aw = warp - 1 - reducers;
+    const int team = aw / sp.wpt, tt = (aw % sp.wpt) * 32 + lane, threads = sp.wpt * 32;
+    const bool want_a = POST || gate != nullptr;
+    const f32x2 a2 = pair(p.a, p.a);
+    f32x2 w[NV][N], w2[NV][N], acc_n[NV][N], acc_a[NV][N];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int v = tt + j * threads;
-          if (v >= nvec) continue;
-          f32x2 x[N], d[N];
+    for (int j = 0; j < NV; ++j) {
+      const int v = tt + j * threads;
 #pragma unroll
-          for (int k = 0; k < N; ++k) x[k] = d[k] = 0;
-          if (has_dr) load_pairs<TS, N>(sdr + v * E, d);
-          if (NEXT) {
-            f32x2 r[N], dy[N];
-            load_pairs<TS, N>(sr + v * E, r);
-            load_pairs<T, N>(sdy + v * E, dy);
+      for (int i = 0; i < N; ++i) w2[j][i] = 0;
+      if (NEXT && v < nvec) load_pairs<T, N>(gamma_next + col0 + v * E, w2[j]);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        w2[j][i] = add2(w2[j][i], off);
+        acc_n[j][i] = 0;
+        acc_a[j][i] = 0;
+      }
+    }
+    bool ok = true;
+    bool more = walk.next();
+    while (more) {
+      const int64_t q = walk.q;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {  // the weights of the segment
+        const int v = tt + j * threads;
+        f32x2 f[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[j][i] = pair(p.b, p.b);
+        if (v >= nvec) continue;
+        if (POST) {
+          load_pairs<T, N>(gamma_post + col0 + v * E, f);
+#pragma unroll
+          for (int i = 0; i < N; ++i) w[j][i] = mul2(w[j][i], add2(f[i], off));
+        }
+        if (gate != nullptr) {
+          load_pairs<T, N>(gate + q * p.hidden + col0 + v * E, f);
+#pragma unroll
+          for (int i = 0; i < N; ++i) w[j][i] = mul2(w[j][i], f[i]);
+        }
+      }
+      for (; more && walk.q == q; more = walk.next()) {
+        ok = ok && wait_all(&sh.red[pos.stage], pos.phase, abort) &&
+             wait_all(&sh.full[pos.stage], pos.phase, abort);
+        const unsigned char* st = ring + (size_t)pos.stage * sp.stride;
+        for (int k = team; k < walk.n && ok; k += sp.teams) {
+          const float4 stat = sh.stat[pos.stage][k];
+          const f32x2 c1 = pair(stat.x, stat.x), c2 = pair(stat.y, stat.y);
+          const f32x2 rs1 = pair(stat.z, stat.z), rs2 = pair(stat.w, stat.w);
+          const T* sx = reinterpret_cast<const T*>(st) + k * cols;
+          const TS* sr = reinterpret_cast<const TS*>(st + at.r) + k * cols;
+          const T* sdy = reinterpret_cast<const T*>(st + at.dy) + k * cols;
+          const TS* sdr = reinterpret_cast<const TS*>(st + at.dr) + k * cols;
+          const int64_t to = (r0 + walk.row + k) * p.hidden + col0;
+          T* dx = static_cast<T*>(p.dx) + to;
+          TS* dres = static_cast<TS*>(p.dres) + to;
+#pragma unroll
+          for (int j = 0; j < NV; ++j) {
+            const int v = tt + j * threads;
+            if (v >= nvec) continue;
+            f32x2 x[N], dv[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = dv[i] = 0;
+            if (has_dr) load_pairs<TS, N>(sdr + v * E, dv);
+            if (NEXT) {
+              f32x2 r[N], dy[N];
+              load_pairs<TS, N>(sr + v * E, r);
+              load_pairs<T, N>(sdy + v * E, dy);
+#pragma unroll
+              for (int i = 0; i < N; ++i) {
+                const f32x2 rh = mul2(r[i], rs2);
+                dv[i] = fma2(rs2, fma2(c1, rh, mul2(dy[i], w2[j][i])), dv[i]);
+                acc_n[j][i] = fma2(dy[i], rh, acc_n[j][i]);
+              }
+            }
+            if (has_x) load_pairs<T, N>(sx + v * E, x);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              if (POST) x[i] = mul2(x[i], rs1);
+              acc_a[j][i] = fma2(dv[i], x[i], acc_a[j][i]);
+              const f32x2 g = mul2(w[j][i], dv[i]);
+              x[i] = POST ? mul2(rs1, fma2(c2, x[i], g)) : g;
+              dv[i] = mul2(a2, dv[i]);
+            }
+            store_pairs<T, N>(dx + v * E, x);
+            store_pairs<TS, N>(dres + v * E, dv);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[pos.stage]);
+        pos.next(stages);
+      }
+
+      // the segment's sum of A, and after the last one that of dgamma_next: a
+      // thread's own columns, or its columns of the teams' sums, added in turn
+      const bool first = q == r0 / p.rows_per_gate;
+      float* pa = p.p_a + (unit + q) * p.hidden + col0;
+      float* pp = p.p_post + unit * p.hidden + col0;
+      float* pn = p.p_next + unit * p.hidden + col0;
+      auto put_a = [&](int c, float v) {
+        v *= p.b;
+        if (gate != nullptr) {
+          pa[c] = v;
+          v *= Traits<T>::to_f(gate[q * p.hidden + col0 + c]);
+        }
+        if (POST) pp[c] = first ? v : pp[c] + v;
+      };
+      auto put_n = [&](int c, float v) { pn[c] = v; };
+      const int me = aw * 32 + lane, all = applier_warps * 32;
+      auto flush = [&](auto& acc, auto put) {
+        f32x2* comb = reinterpret_cast<f32x2*>(ring + (size_t)stages * sp.stride);
+        if (sp.teams == 1) {
+#pragma unroll
+          for (int j = 0; j < NV; ++j) {
+            const int v = tt + j * threads;
+            if (v >= nvec) continue;
 #pragma unroll
             for (int k = 0; k < N; ++k) {
-              const f32x2 rh = mul2(r[k], rs2);
-              d[k] = fma2(rs2, fma2(c1, rh, mul2(dy[k], w2[j][k])), d[k]);
-              acc_n[j][k] = fma2(dy[k], rh, acc_n[j][k]);
+              const float2 f = split(acc[j][k]);
+              put(v * E + 2 * k, f.x);
+              put(v * E + 2 * k + 1, f.y);
             }
           }
-          if (has_x) load_pairs<T, N>(sx + v * E, x);
-#pragma unroll
-          for (int k = 0; k < N; ++k) {
-            if (POST) x[k] = mul2(x[k], rs1);
-            acc_a[j][k] = fma2(d[k], x[k], acc_a[j][k]);
-            const f32x2 g = mul2(w[j][k], d[k]);
-            x[k] = POST ? mul2(rs1, fma2(c2, x[k], g)) : g;
-            d[k] = mul2(a2, d[k]);
-          }
-          store_pairs<T, N>(dx + v * E, x);
-          store_pairs<TS, N>(dres + v * E, d);
+          return;
         }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.empty[pos_b.stage]);
-      pos_b.next(stages);
-    }
-
-    // the segment's sum of A, and after the last one that of dgamma_next: a
-    // thread's own columns, or its columns of the teams' sums, added in turn
-    const bool first = q == r0 / p.rows_per_gate, last = seg1 == r1;
-    float* pa = p.p_a + (unit + q) * p.hidden + col0;
-    float* pp = p.p_post + unit * p.hidden + col0;
-    float* pn = p.p_next + unit * p.hidden + col0;
-    auto put_a = [&](int c, float v) {
-      v *= p.b;
-      if (gate != nullptr) {
-        pa[c] = v;
-        v *= Traits<T>::to_f(gate[q * p.hidden + col0 + c]);
-      }
-      if (POST) pp[c] = first ? v : pp[c] + v;
-    };
-    auto put_n = [&](int c, float v) { pn[c] = v; };
-    auto flush = [&](f32x2 (&acc)[NV][N], auto put) {
-      f32x2* comb = reinterpret_cast<f32x2*>(ring + (size_t)stages * sp.stride);
-      if (K > 1)
-        for (int m = 0; m < K; ++m) {
+        for (int m = 0; m < sp.teams; ++m) {
           if (team == m)
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
@@ -903,35 +947,19 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
               for (int k = 0; k < N; ++k)
                 comb[v * N + k] = m == 0 ? acc[j][k] : add2(comb[v * N + k], acc[j][k]);
             }
-          __syncthreads();
+          asm volatile("bar.sync 2, %0;" ::"r"(all) : "memory");
         }
-      if (K > 1)
-        for (int c = threadIdx.x; c < cols; c += blockDim.x)
-          put(c, reinterpret_cast<const float*>(comb)[c]);
-      else
+        for (int c = me; c < cols; c += all) put(c, reinterpret_cast<const float*>(comb)[c]);
+        asm volatile("bar.sync 2, %0;" ::"r"(all) : "memory");
+      };
+      if (want_a) flush(acc_a, put_a);
+      if (NEXT && !more) flush(acc_n, put_n);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int v = tt + j * threads;
-          if (v >= nvec) continue;
+      for (int j = 0; j < NV; ++j)
 #pragma unroll
-          for (int k = 0; k < N; ++k) {
-            const float2 f = split(acc[j][k]);
-            put(v * E + 2 * k, f.x);
-            put(v * E + 2 * k + 1, f.y);
-          }
-        }
-      if (K > 1) __syncthreads();
-    };
-    if (want_a) flush(acc_a, put_a);
-    if (NEXT && last) flush(acc_n, put_n);
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int k = 0; k < N; ++k) acc_a[j][k] = 0;
-    seg0 = seg1;
+        for (int k = 0; k < N; ++k) acc_a[j][k] = 0;
+    }
   }
-  // after a wait that ran out copies may still be on their way
-  if (threadIdx.x == 0 && *abort) drain_ring(sh.full, sh.fill, sh.issued, stages);
   __syncwarp();
   if (cs > 1) cluster_sync();  // no CTA leaves while a peer may write to its slots
 }
@@ -980,38 +1008,37 @@ bool fwd_shape(int64_t rows, int hidden, int sms, int row_elem, int planes, int 
   return false;
 }
 
-// The backward's teams and stages: all warps busy and three stages, with 16
-// columns a thread or else 8 (one row a stage), over as few CTAs as can be.
-struct BwdPick {
-  int teams, wpt, cs, stages, stride, nv8;  // nv8: groups of 8 columns a thread
-  size_t smem;
-};
-
+// The backward's roles and stages, over as few CTAs as leave three stages
+// (else two) beside the reducers' weights.
 template <typename F>
-bool bwd_pick(int hidden, int align, F stage_bytes, BwdPick* out) {
+bool bwd_pick(int64_t rows, int hidden, int sms, int align, int planes, F stage_bytes,
+              BwdShape* s, int* nv8, size_t* smem) {
   const int budget = kSmemBudget - (int)sizeof(BwdShared) - kSlack;
   for (int least = 3; least >= 2; --least)
     for (int cs = 1; cs <= kMaxSplit; cs *= 2) {
       if (hidden % (align * cs) != 0) break;
       const int cols = hidden / cs;
-      for (int nv8 = cols < 512 ? 1 : 2; nv8 >= 1; --nv8) {
-        BwdPick s;
-        s.cs = cs;
-        s.nv8 = nv8;
-        s.wpt = (cols + nv8 * 256 - 1) / (nv8 * 256);
-        if (s.wpt > kMaxWarps) continue;
-        for (s.teams = cs > 1 ? 1 : kMaxWarps / s.wpt; s.teams >= 1; --s.teams) {
-          if (s.teams * s.wpt < kMaxWarps / 2 + 1 && nv8 == 2 && 2 * s.wpt <= kMaxWarps) break;
-          const int comb = s.teams > 1 ? cols * 4 : 0;
-          s.stride = (stage_bytes(s.teams, cols) + 127) / 128 * 128;
-          s.stages = (budget - comb) / s.stride;
-          if (s.stages > kMaxStages) s.stages = kMaxStages;
-          if (s.stages < least) continue;
-          s.smem = (size_t)s.stages * s.stride + comb;
-          *out = s;
-          return true;
-        }
-      }
+      *nv8 = cols < 512 ? 1 : 2;
+      s->cs = cs;
+      s->wpt = (cols + *nv8 * 256 - 1) / (*nv8 * 256);
+      if (s->wpt > kBwdWarps - 3) continue;
+      s->teams = cs > 1 || s->wpt > 4 ? 1 : 8 / s->wpt;
+      // narrow rows: as many to a stage as make it a wide row's, if there are
+      // enough of them for every CTA to fill its ring
+      s->stage_rows = s->teams;
+      while (cs == 1 && 2 * s->stage_rows <= kBwdRows && 2 * s->stage_rows * cols <= 4096 &&
+             rows >= (int64_t)8 * s->stage_rows * sms)
+        s->stage_rows *= 2;
+      const int over = planes * cols * 4 + (s->teams > 1 ? cols * 4 : 0);
+      s->stride = (stage_bytes(s->stage_rows, cols) + 127) / 128 * 128;
+      s->stages = (budget - over) / s->stride;
+      if (s->stages > kBwdStages) s->stages = kBwdStages;
+      if (s->stages < least) continue;
+      s->reducers = kBwdWarps - 1 - s->teams * s->wpt;
+      if (s->reducers > s->stages) s->reducers = s->stages;
+      s->stages -= s->stages % s->reducers;  // a stage is always the same reducer's
+      *smem = (size_t)s->stages * s->stride + over;
+      return true;
     }
   return false;
 }
@@ -1058,6 +1085,7 @@ bool try_fwd(const BlockFwdArgs& a, cudaStream_t s, cudaError_t* err) {
   p.stride = sh.stride;
   auto kern = block_fwd_tma<T, TS, POST, NEXT>;
   *err = allow_smem(kern, sh.smem);
+  if (*err == cudaSuccess) *err = allow_cluster((const void*)kern, sh.cs);
   if (*err != cudaSuccess) return true;
   int64_t units = sms / sh.cs;
   const int64_t blocks = (a.rows + sh.stage_rows - 1) / sh.stage_rows;
@@ -1072,34 +1100,33 @@ template <typename T, typename TS, bool POST, bool NEXT>
 bool try_bwd(const BlockBwdArgs& a, BlockBwdParams& p, int* units, cudaStream_t s,
              cudaError_t* err) {
   constexpr int E = kElems<T, TS>;
-  BwdShape sp;
-  sp.read_x = POST || a.gate != nullptr;
-  const bool dr = a.dr != nullptr, x = sp.read_x;
-  BwdPick sh;
-  if (!bwd_pick(a.hidden, 16 / (int)sizeof(T),
-                [=](int k, int cols) { return bwd_stage<T, TS>(k, cols, x, NEXT, dr).bytes; }, &sh))
-    return false;
-  sp.teams = sh.teams;
-  sp.wpt = sh.wpt;
-  sp.cs = sh.cs;
-  sp.stages = sh.stages;
-  sp.stride = sh.stride;
   int dev = 0;
   *err = cudaGetDevice(&dev);
   if (*err != cudaSuccess) return true;
-  int64_t n = sm_count(dev) / sh.cs;
+  const int sms = sm_count(dev);
+  BwdShape sp;
+  sp.read_x = POST || a.gate != nullptr;
+  const bool dr = a.dr != nullptr, x = sp.read_x;
+  int nv8 = 0;
+  size_t smem = 0;
+  if (!bwd_pick(a.rows, a.hidden, sms, 16 / (int)sizeof(T), (POST ? 1 : 0) + (NEXT ? 1 : 0),
+                [=](int k, int cols) { return bwd_stage<T, TS>(k, cols, x, NEXT, dr).bytes; }, &sp,
+                &nv8, &smem))
+    return false;
+  int64_t n = sms / sp.cs;
   if (n < 1) n = 1;
   if (n > RMSN_BLOCK_MAX_PARTIALS) n = RMSN_BLOCK_MAX_PARTIALS;
   if (n > a.rows) n = a.rows;
   *units = (int)n;
   place_partials(a, *units, p);
   auto go = [&](auto kern) {
-    *err = allow_smem(kern, sh.smem);
+    *err = allow_smem(kern, smem);
+    if (*err == cudaSuccess) *err = allow_cluster((const void*)kern, sp.cs);
     if (*err != cudaSuccess) return;
-    *err = launch_kernel(kern, dim3((unsigned)(n * sh.cs)), dim3(32 * sh.teams * sh.wpt), sh.smem,
-                         s, sh.cs, p, sp);
+    *err = launch_kernel(kern, dim3((unsigned)(n * sp.cs)),
+                         dim3(32 * (1 + sp.reducers + sp.teams * sp.wpt)), smem, s, sp.cs, p, sp);
   };
-  if (sh.nv8 == 1)
+  if (nv8 == 1)
     go(block_bwd_tma<T, TS, POST, NEXT, 8 / E>);
   else
     go(block_bwd_tma<T, TS, POST, NEXT, 16 / E>);
