@@ -190,63 +190,82 @@ __global__ void __launch_bounds__(kLoopThreads) block_bwd_loop(const BlockBwdPar
       if (sums) {
         const float acc = fmaf(p.b * d, xh, seg_first ? 0.f : pa[j]);
         pa[j] = acc;
-        if (seg_last && gamma_post != nullptr) {
-          const float gq = gr != nullptr ? Traits<T>::to_f(gr[j]) : 1.f;
-          pp[j] = fmaf(gq, acc, q == r0 / p.rows_per_gate ? 0.f : pp[j]);
-        }
+        if (seg_last && gamma_post != nullptr && p.rows_per_gate < p.rows)
+          pp[j] = fmaf(Traits<T>::to_f(gr[j]), acc, q == r0 / p.rows_per_gate ? 0.f : pp[j]);
       }
     }
   }
 }
 
-// The sums over the partial rows, 16 lanes a column as dw_finalize: block
-// (., 0) the next norm's, (., 1) the post norm's, (., 2 + q) gate row q's,
-// whose segments are u_first + q ... u_last + q.
+// The sums over the partial rows, in a fixed order: 16 lanes, each adding
+// every 16th row, then the 16 lane sums in order (as dw_finalize), four
+// columns a thread where rows are 16-byte aligned (VEC 4).  Jobs (blockIdx.y):
+// the next norm's sums; with one gate row, or none, the sums of A, which give
+// dgamma_post = gate A and dgate = w1 A; with several, the post norm's sums,
+// and for each gate row those of A over its segments u_first + q ... u_last + q.
 constexpr int kSumLanes = 16;
 
-template <typename T>
+template <typename T, int VEC>
 __global__ void __launch_bounds__(32 * kSumLanes) block_bwd_sums(
     const BlockBwdParams p, int units, float* __restrict__ dgamma_post, float* __restrict__ dgate,
     float* __restrict__ dgamma_next) {
-  __shared__ float s[kSumLanes][33];
+  __shared__ float s[kSumLanes][32 * VEC];
   pdl_trigger();
   pdl_wait();
   const int tx = threadIdx.x, ty = threadIdx.y;
-  const int j = blockIdx.x * 32 + tx;
   const int hidden = p.hidden;
-  for (int64_t job = blockIdx.y; job < 2 + (dgate != nullptr ? p.rows / p.rows_per_gate : 0);
-       job += gridDim.y) {
-    const float* src = p.p_next;
-    float* dst = dgamma_next;
-    float scale = 1.f;
-    int64_t n = units;
-    if (job == 1) {
-      src = p.p_post;
-      dst = dgamma_post;
-    } else if (job >= 2) {
-      const int64_t q = job - 2;
+  const int j0 = (blockIdx.x * 32 + tx) * VEC;
+  const bool one = p.rows_per_gate >= p.rows;
+  const T* gamma_post = static_cast<const T*>(p.gamma_post);
+  const T* gate = static_cast<const T*>(p.gate);
+  const int64_t jobs = 2 + (one || dgate == nullptr ? 0 : p.rows / p.rows_per_gate);
+  for (int64_t job = blockIdx.y; job < jobs; job += gridDim.y) {
+    const float* src = job == 0 ? p.p_next : one ? p.p_a : p.p_post;
+    int64_t n = units, q = 0;
+    if (job == 0 ? dgamma_next == nullptr
+                 : dgamma_post == nullptr && (dgate == nullptr || (job == 1 && !one)))
+      continue;
+    if (job >= 2) {
+      q = job - 2;
       // unit of row i: the largest u with floor(u R / U) <= i
       const int64_t first = ((q * p.rows_per_gate + 1) * units - 1) / p.rows;
       const int64_t last = ((q + 1) * p.rows_per_gate * units - 1) / p.rows;
       src = p.p_a + (first + q) * hidden;
       n = last - first + 1;
-      dst = dgate + q * hidden;
-      if (p.gamma_post != nullptr && j < hidden)
-        scale = Traits<T>::to_f(static_cast<const T*>(p.gamma_post)[j]) + p.off;
     }
-    if (dst == nullptr) continue;
-    float acc = 0.f;
-    if (j < hidden) {
+    float acc[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
+    if (j0 < hidden) {
 #pragma unroll 8
-      for (int64_t i = ty; i < n; i += kSumLanes) acc += src[i * hidden + j];
+      for (int64_t i = ty; i < n; i += kSumLanes) {
+        if constexpr (VEC == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src + i * hidden + j0);
+          acc[0] += v.x;
+          acc[1] += v.y;
+          acc[2] += v.z;
+          acc[3] += v.w;
+        } else {
+          acc[0] += src[i * hidden + j0];
+        }
+      }
     }
-    s[ty][tx] = acc;
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) s[ty][tx * VEC + k] = acc[k];
     __syncthreads();
-    if (ty == 0 && j < hidden) {
+    const int c = ty * 32 + tx, j = blockIdx.x * 32 * VEC + c;
+    if (c < 32 * VEC && j < hidden) {
       float t = 0.f;
 #pragma unroll
-      for (int l = 0; l < kSumLanes; ++l) t += s[l][tx];
-      dst[j] = t * scale;
+      for (int l = 0; l < kSumLanes; ++l) t += s[l][c];
+      if (job == 0) {
+        dgamma_next[j] = t;
+      } else {
+        const float w1 = gamma_post != nullptr ? Traits<T>::to_f(gamma_post[j]) + p.off : 1.f;
+        const float g = gate != nullptr && one ? Traits<T>::to_f(gate[j]) : 1.f;
+        if (job == 1 && dgamma_post != nullptr) dgamma_post[j] = t * g;
+        if (dgate != nullptr && (one || job >= 2)) dgate[q * hidden + j] = t * w1;
+      }
     }
     __syncthreads();
   }
@@ -312,9 +331,12 @@ cudaError_t launch_bwd_t(const BlockBwdArgs& a, cudaStream_t s, int* launches) {
   *launches += 1;
   if (a.dgamma_post == nullptr && a.dgate == nullptr && a.dgamma_next == nullptr)
     return cudaSuccess;
-  const int64_t jobs = 2 + (a.dgate != nullptr ? a.rows / a.rows_per_gate : 0);
-  e = launch_kernel(block_bwd_sums<T>,
-                    dim3((unsigned)((a.hidden + 31) / 32), (unsigned)(jobs < 65535 ? jobs : 65535)),
+  const int64_t gates = a.rows / a.rows_per_gate;
+  const int64_t jobs = 2 + (a.dgate != nullptr && gates > 1 ? gates : 0);
+  const int vec = a.hidden % 4 == 0 ? 4 : 1;  // the partial rows start on 16 bytes
+  const dim3 grid((unsigned)((a.hidden + 32 * vec - 1) / (32 * vec)),
+                  (unsigned)(jobs < 65535 ? jobs : 65535));
+  e = launch_kernel(vec == 4 ? block_bwd_sums<T, 4> : block_bwd_sums<T, 1>, grid,
                     dim3(32, kSumLanes), 0, s, 1, p, units, a.dgamma_post, a.dgate, a.dgamma_next);
   if (e == cudaSuccess) *launches += 1;
   return e;

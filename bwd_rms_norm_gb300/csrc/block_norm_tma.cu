@@ -164,14 +164,29 @@ struct Ring {
   }
 };
 
-// A team's waits are short: a few tries before the bounded wait with its
-// timer and its sleeps.
-constexpr int kTries = 64;
+// A bounded wait of a whole warp for phase `parity` of `bar`.  A try suspends
+// the warp for some hundred cycles; between tries it does next to nothing (a
+// look at the timer and the abort flag every 64 of them), since what waiting
+// warps issue is taken from those that have work.
+__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  unsigned long long t0 = 0;
+  for (int i = 1;; ++i) {
+    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+    if (i & 63) continue;
+    if (*abort) return false;
+    if (t0 == 0) {
+      t0 = global_ns();
+    } else if (global_ns() - t0 > kWaitLimitNs) {
+      *abort = 1;
+      atomicAdd(&g_block_timeouts, 1u);
+      return false;
+    }
+  }
+}
 
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  bool done = false;
-  for (int i = 0; i < kTries && !done; ++i) done = mbar_try_wait(bar, parity);
-  if (!done) done = wait_phase_counted(bar, parity, abort, &g_block_timeouts);
+  bool done = mbar_try_wait(bar, parity);
+  if (!done) done = wait_long(bar, parity, abort);
   return __all_sync(0xffffffffu, done);
 }
 
@@ -205,8 +220,7 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity)
 __device__ __forceinline__ bool team_wait(int cs, uint64_t* bar, uint32_t parity,
                                           volatile int* abort) {
   if (cs == 1) return wait_all(bar, parity, abort);
-  bool done = false;
-  for (int i = 0; i < kTries && !done; ++i) done = try_wait_cluster(bar, parity);
+  bool done = try_wait_cluster(bar, parity);
   if (!done) done = wait_cluster_counted(bar, parity, abort, &g_block_timeouts);
   return __all_sync(0xffffffffu, done);
 }
@@ -412,6 +426,20 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) block_fwd_tma(const B
       return warp_sum(s);
     };
     const f32x2 a2 = pair(p.a, p.a);
+    // f for each of the thread's groups of columns, four at a time; the step of
+    // a lone warp's lanes is a constant of the addresses
+    auto each = [&](auto f) {
+      int v = tt;
+      if (threads == 32) {
+        for (; v + 96 < nvec; v += 128) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) f(v + 32 * u);
+        }
+        for (; v < nvec; v += 32) f(v);
+      } else {
+        for (; v < nvec; v += threads) f(v);
+      }
+    };
     int stage = team;
     uint32_t phase = 0;
     for (int k = team; k < nst; k += p.teams) {
@@ -428,13 +456,12 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) block_fwd_tma(const B
           f32x2 part[N];
 #pragma unroll
           for (int i = 0; i < N; ++i) part[i] = 0;
-#pragma unroll 4
-          for (int v = tt; v < nvec; v += threads) {
+          each([&](int v) {
             f32x2 x[N];
             load_pairs<T, N>(sx + v * E, x);
 #pragma unroll
             for (int i = 0; i < N; ++i) part[i] = fma2(x[i], x[i], part[i]);
-          }
+          });
           const float ss = over_team(sum_pairs<N>(part));
           rs1 = rsqrtf(fmaf(ss, inv, p.eps));
           if (isinf(ss)) {  // the squares overflowed (kOverflowScale)
@@ -453,8 +480,7 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) block_fwd_tma(const B
         f32x2 part[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) part[i] = 0;
-#pragma unroll 2
-        for (int v = tt; v < nvec; v += threads) {
+        each([&](int v) {
           f32x2 x[N], r[N], w[N];
           load_pairs<T, N>(sx + v * E, x);
           load_pairs<TS, N>(sr + v * E, r);
@@ -480,7 +506,7 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) block_fwd_tma(const B
               *reinterpret_cast<ulonglong2*>(sr + v * E) = make_ulonglong2(r[0], r[1]);
             }
           }
-        }
+        });
         if (!NEXT) continue;
         auto kept = [&](int v, f32x2 (&r)[N]) {
           const ulonglong2 hi = *reinterpret_cast<const ulonglong2*>(sr + v * E);
@@ -515,15 +541,14 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) block_fwd_tma(const B
         if (tt == 0 && rank == 0 && ok) p.rstd_next[row] = rs2;
         const f32x2 rn = pair(rs2, rs2);
         T* yr = static_cast<T*>(p.y) + row * p.hidden + col0;
-#pragma unroll 4
-        for (int v = tt; v < nvec; v += threads) {
+        each([&](int v) {
           f32x2 r[N], w[N];
           kept(v, r);
           load_plane<N>(plane2, nvec, v, w);
 #pragma unroll
           for (int i = 0; i < N; ++i) r[i] = mul2(mul2(r[i], rn), w[i]);
           if (ok) store_pairs<T, N>(yr + v * E, r);
-        }
+        });
       }
       // r was written where the next copy will land
       if (NEXT) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -617,7 +642,7 @@ struct Walk {
   }
 };
 
-template <typename T, typename TS, bool POST, bool NEXT, int NV>
+template <typename T, typename TS, bool POST, bool NEXT, bool DR, int NV>
 __global__ void __launch_bounds__(32 * kBwdWarps, 1)
     block_bwd_tma(const BlockBwdParams p, const BwdShape sp) {
   constexpr int E = kElems<T, TS>, N = E / 2;
@@ -631,7 +656,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
   const int col0 = (int)rank * cols;
   const int64_t unit = blockIdx.x / cs, units = gridDim.x / cs;
   const int64_t r0 = unit * p.rows / units, r1 = (unit + 1) * p.rows / units;
-  const bool has_dr = p.dr != nullptr, has_x = sp.read_x;
+  const bool has_x = POST || sp.read_x;
   float4* plane1 = reinterpret_cast<float4*>(smem);
   float4* plane2 = POST ? plane1 + cols / 4 : plane1;
   unsigned char* ring = reinterpret_cast<unsigned char*>(NEXT ? plane2 + cols / 4 : plane2);
@@ -648,7 +673,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
   pdl_trigger();
   pdl_wait();
   volatile int* abort = &sh.abort;
-  const BwdStage at = bwd_stage<T, TS>(K, cols, has_x, NEXT, has_dr);
+  const BwdStage at = bwd_stage<T, TS>(K, cols, has_x, NEXT, DR);
   const T* gamma_post = static_cast<const T*>(p.gamma_post);
   const T* gamma_next = static_cast<const T*>(p.gamma_next);
   const T* gate = static_cast<const T*>(p.gate);
@@ -669,13 +694,13 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
         unsigned char* st = ring + (size_t)pos.stage * sp.stride;
         uint64_t* full = &sh.full[pos.stage];
         const int64_t from = (r0 + walk.row) * p.hidden + col0;  // K is 1 where cs > 1
-        mbar_arrive_expect_tx(full, (has_x ? tb : 0) + (NEXT ? tb + sb : 0) + (has_dr ? sb : 0));
+        mbar_arrive_expect_tx(full, (has_x ? tb : 0) + (NEXT ? tb + sb : 0) + (DR ? sb : 0));
         if (has_x) bulk_load(st, static_cast<const T*>(p.x) + from, tb, full);
         if (NEXT) {
           bulk_load(st + at.r, static_cast<const TS*>(p.r) + from, sb, full);
           bulk_load(st + at.dy, static_cast<const T*>(p.dy) + from, tb, full);
         }
-        if (has_dr) bulk_load(st + at.dr, static_cast<const TS*>(p.dr) + from, sb, full);
+        if (DR) bulk_load(st + at.dr, static_cast<const TS*>(p.dr) + from, sb, full);
         pos.next(stages);
         ++issued;
       }
@@ -730,10 +755,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
         const TS* sdr = reinterpret_cast<const TS*>(st + at.dr) + q * cols;
         const float rs1f = __shfl_sync(0xffffffffu, rs1_l, q);
         const float rs2f = __shfl_sync(0xffffffffu, rs2_l, q);
-        const f32x2 rs1 = pair(rs1f, rs1f), rs2 = pair(rs2f, rs2f);
-        f32x2 s1 = 0, s2 = 0, s3 = 0;
-#pragma unroll 2
-        for (int v = lane; v < nvec; v += 32) {
+        const f32x2 rs2 = pair(rs2f, rs2f);
+        f32x2 s1 = 0, s2 = 0, s3 = 0;  // S1, and S2 and S3 over rstd_post
+        auto add = [&](int v) {
           f32x2 x[N], dv[N];
           if (POST) {
             f32x2 w[N];
@@ -746,11 +770,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
               for (int k = 0; k < N; ++k) w[k] = mul2(w[k], g[k]);
             }
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-              x[k] = mul2(w[k], mul2(x[k], rs1));
-              dv[k] = 0;
-            }
-            if (has_dr) load_pairs<TS, N>(sdr + v * E, dv);
+            for (int k = 0; k < N; ++k) x[k] = mul2(w[k], x[k]);
+            if (DR) load_pairs<TS, N>(sdr + v * E, dv);
           }
           if (NEXT) {
             f32x2 r[N], dy[N], w2[N];
@@ -763,14 +784,20 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
               s1 = fma2(g, rh, s1);
               if (POST) {
                 s3 = fma2(x[k], rh, s3);
-                dv[k] = fma2(rs2, g, dv[k]);
+                dv[k] = DR ? fma2(rs2, g, dv[k]) : mul2(rs2, g);
               }
             }
           }
           if (POST)
 #pragma unroll
             for (int k = 0; k < N; ++k) s2 = fma2(x[k], dv[k], s2);
+        };
+        int v = lane;
+        for (; v + 96 < nvec; v += 128) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) add(v + 32 * u);
         }
+        for (; v < nvec; v += 32) add(v);
         float3 s;
         if (POST && NEXT)
           s = warp_sum3(sum2(s1), sum2(s2), sum2(s3), lane);
@@ -794,7 +821,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
           }
         }
         const float c1 = s.x * inv;
-        const float c2 = POST ? fmaf(-rs2f * c1, s.z, s.y) * inv : 0.f;
+        const float c2 = POST ? fmaf(-rs2f * c1, s.z, s.y) * (rs1f * inv) : 0.f;
         if (lane == 0) sh.stat[pos.stage][q] = make_float4(-c1, -c2, rs1f, rs2f);
       }
       if (!ok) break;
@@ -817,13 +844,24 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
     const int team = aw / sp.wpt, tt = (aw % sp.wpt) * 32 + lane, threads = sp.wpt * 32;
     const bool want_a = POST || gate != nullptr;
     const f32x2 a2 = pair(p.a, p.a);
+    unsigned char* dx = reinterpret_cast<unsigned char*>(
+        static_cast<T*>(p.dx) + r0 * p.hidden + col0);
+    unsigned char* dres = reinterpret_cast<unsigned char*>(
+        static_cast<TS*>(p.dres) + r0 * p.hidden + col0);
+    const uint32_t tbytes = (uint32_t)(cols * (int)sizeof(T)), sbytes = (uint32_t)(cols * (int)sizeof(TS));
+    const uint32_t hbytes_t = (uint32_t)(p.hidden * (int)sizeof(T));
+    const uint32_t hbytes_s = (uint32_t)(p.hidden * (int)sizeof(TS));
+    // The thread's first columns; threads past the row take its last ones and
+    // store nothing.
+    int e0[NV];
     f32x2 w[NV][N], w2[NV][N], acc_n[NV][N], acc_a[NV][N];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int v = tt + j * threads;
+      e0[j] = (v < nvec ? v : nvec - 1) * E;
 #pragma unroll
       for (int i = 0; i < N; ++i) w2[j][i] = 0;
-      if (NEXT && v < nvec) load_pairs<T, N>(gamma_next + col0 + v * E, w2[j]);
+      if (NEXT) load_pairs<T, N>(gamma_next + col0 + e0[j], w2[j]);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         w2[j][i] = add2(w2[j][i], off);
@@ -837,18 +875,16 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
       const int64_t q = walk.q;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {  // the weights of the segment
-        const int v = tt + j * threads;
         f32x2 f[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) w[j][i] = pair(p.b, p.b);
-        if (v >= nvec) continue;
         if (POST) {
-          load_pairs<T, N>(gamma_post + col0 + v * E, f);
+          load_pairs<T, N>(gamma_post + col0 + e0[j], f);
 #pragma unroll
           for (int i = 0; i < N; ++i) w[j][i] = mul2(w[j][i], add2(f[i], off));
         }
         if (gate != nullptr) {
-          load_pairs<T, N>(gate + q * p.hidden + col0 + v * E, f);
+          load_pairs<T, N>(gate + q * p.hidden + col0 + e0[j], f);
 #pragma unroll
           for (int i = 0; i < N; ++i) w[j][i] = mul2(w[j][i], f[i]);
         }
@@ -856,48 +892,43 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
       for (; more && walk.q == q; more = walk.next()) {
         ok = ok && wait_all(&sh.red[pos.stage], pos.phase, abort) &&
              wait_all(&sh.full[pos.stage], pos.phase, abort);
-        const unsigned char* st = ring + (size_t)pos.stage * sp.stride;
+        const unsigned char* st = ring + (uint32_t)(pos.stage * sp.stride);
         for (int k = team; k < walk.n && ok; k += sp.teams) {
           const float4 stat = sh.stat[pos.stage][k];
           const f32x2 c1 = pair(stat.x, stat.x), c2 = pair(stat.y, stat.y);
           const f32x2 rs1 = pair(stat.z, stat.z), rs2 = pair(stat.w, stat.w);
-          const T* sx = reinterpret_cast<const T*>(st) + k * cols;
-          const TS* sr = reinterpret_cast<const TS*>(st + at.r) + k * cols;
-          const T* sdy = reinterpret_cast<const T*>(st + at.dy) + k * cols;
-          const TS* sdr = reinterpret_cast<const TS*>(st + at.dr) + k * cols;
-          const int64_t to = (r0 + walk.row + k) * p.hidden + col0;
-          T* dx = static_cast<T*>(p.dx) + to;
-          TS* dres = static_cast<TS*>(p.dres) + to;
+          const uint32_t row = (uint32_t)(walk.row + k);
+          const unsigned char* rt = st + (uint32_t)k * tbytes;
+          const unsigned char* rs = st + (uint32_t)k * sbytes;
 #pragma unroll
           for (int j = 0; j < NV; ++j) {
-            const int v = tt + j * threads;
-            if (v >= nvec) continue;
             f32x2 x[N], dv[N];
-#pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = dv[i] = 0;
-            if (has_dr) load_pairs<TS, N>(sdr + v * E, dv);
+            if (DR) load_pairs<TS, N>(reinterpret_cast<const TS*>(rs + at.dr) + e0[j], dv);
             if (NEXT) {
               f32x2 r[N], dy[N];
-              load_pairs<TS, N>(sr + v * E, r);
-              load_pairs<T, N>(sdy + v * E, dy);
+              load_pairs<TS, N>(reinterpret_cast<const TS*>(rs + at.r) + e0[j], r);
+              load_pairs<T, N>(reinterpret_cast<const T*>(rt + at.dy) + e0[j], dy);
 #pragma unroll
               for (int i = 0; i < N; ++i) {
                 const f32x2 rh = mul2(r[i], rs2);
-                dv[i] = fma2(rs2, fma2(c1, rh, mul2(dy[i], w2[j][i])), dv[i]);
+                const f32x2 g = fma2(c1, rh, mul2(dy[i], w2[j][i]));
+                dv[i] = DR ? fma2(rs2, g, dv[i]) : mul2(rs2, g);
                 acc_n[j][i] = fma2(dy[i], rh, acc_n[j][i]);
               }
             }
-            if (has_x) load_pairs<T, N>(sx + v * E, x);
+            if (has_x) load_pairs<T, N>(reinterpret_cast<const T*>(rt) + e0[j], x);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
               if (POST) x[i] = mul2(x[i], rs1);
-              acc_a[j][i] = fma2(dv[i], x[i], acc_a[j][i]);
+              if (has_x) acc_a[j][i] = fma2(dv[i], x[i], acc_a[j][i]);
               const f32x2 g = mul2(w[j][i], dv[i]);
               x[i] = POST ? mul2(rs1, fma2(c2, x[i], g)) : g;
               dv[i] = mul2(a2, dv[i]);
             }
-            store_pairs<T, N>(dx + v * E, x);
-            store_pairs<TS, N>(dres + v * E, dv);
+            if (tt + j * threads < nvec) {
+              store_pairs<T, N>(reinterpret_cast<T*>(dx + (uint64_t)row * hbytes_t) + e0[j], x);
+              store_pairs<TS, N>(reinterpret_cast<TS*>(dres + (uint64_t)row * hbytes_s) + e0[j], dv);
+            }
           }
         }
         __syncwarp();
@@ -911,15 +942,20 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
       float* pa = p.p_a + (unit + q) * p.hidden + col0;
       float* pp = p.p_post + unit * p.hidden + col0;
       float* pn = p.p_next + unit * p.hidden + col0;
-      auto put_a = [&](int c, float v) {
-        v *= p.b;
-        if (gate != nullptr) {
-          pa[c] = v;
-          v *= Traits<T>::to_f(gate[q * p.hidden + col0 + c]);
+      // With one gate row the sums of A give dgamma_post too (block_bwd_sums).
+      auto put_a = [&](int c, float4 v) {
+        v = make_float4(v.x * p.b, v.y * p.b, v.z * p.b, v.w * p.b);
+        *reinterpret_cast<float4*>(pa + c) = v;
+        if (POST && gate_each) {
+          f32x2 f[2], g[2] = {pair(v.x, v.y), pair(v.z, v.w)};
+          load_pairs<T, 2>(gate + q * p.hidden + col0 + c, f);
+          const float2 lo = split(mul2(f[0], g[0])), hi = split(mul2(f[1], g[1]));
+          float4 s = first ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<float4*>(pp + c);
+          s = make_float4(s.x + lo.x, s.y + lo.y, s.z + hi.x, s.w + hi.y);
+          *reinterpret_cast<float4*>(pp + c) = s;
         }
-        if (POST) pp[c] = first ? v : pp[c] + v;
       };
-      auto put_n = [&](int c, float v) { pn[c] = v; };
+      auto put_n = [&](int c, float4 v) { *reinterpret_cast<float4*>(pn + c) = v; };
       const int me = aw * 32 + lane, all = applier_warps * 32;
       auto flush = [&](auto& acc, auto put) {
         f32x2* comb = reinterpret_cast<f32x2*>(ring + (size_t)stages * sp.stride);
@@ -929,10 +965,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
             const int v = tt + j * threads;
             if (v >= nvec) continue;
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-              const float2 f = split(acc[j][k]);
-              put(v * E + 2 * k, f.x);
-              put(v * E + 2 * k + 1, f.y);
+            for (int k = 0; k < N; k += 2) {
+              const float2 f = split(acc[j][k]), g = split(acc[j][k + 1]);
+              put(v * E + 2 * k, make_float4(f.x, f.y, g.x, g.y));
             }
           }
           return;
@@ -949,7 +984,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
             }
           asm volatile("bar.sync 2, %0;" ::"r"(all) : "memory");
         }
-        for (int c = me; c < cols; c += all) put(c, reinterpret_cast<const float*>(comb)[c]);
+        for (int c = 4 * me; c < cols; c += 4 * all)
+          put(c, *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(comb) + c));
         asm volatile("bar.sync 2, %0;" ::"r"(all) : "memory");
       };
       if (want_a) flush(acc_a, put_a);
@@ -1126,10 +1162,17 @@ bool try_bwd(const BlockBwdArgs& a, BlockBwdParams& p, int* units, cudaStream_t 
     *err = launch_kernel(kern, dim3((unsigned)(n * sp.cs)),
                          dim3(32 * (1 + sp.reducers + sp.teams * sp.wpt)), smem, s, sp.cs, p, sp);
   };
-  if (nv8 == 1)
-    go(block_bwd_tma<T, TS, POST, NEXT, 8 / E>);
-  else
-    go(block_bwd_tma<T, TS, POST, NEXT, 16 / E>);
+  if (dr || !NEXT) {
+    if (nv8 == 1)
+      go(block_bwd_tma<T, TS, POST, NEXT, true, 8 / E>);
+    else
+      go(block_bwd_tma<T, TS, POST, NEXT, true, 16 / E>);
+  } else {
+    if (nv8 == 1)
+      go(block_bwd_tma<T, TS, POST, true, false, 8 / E>);
+    else
+      go(block_bwd_tma<T, TS, POST, true, false, 16 / E>);
+  }
   return true;
 }
 
