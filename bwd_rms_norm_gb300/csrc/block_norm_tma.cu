@@ -282,14 +282,19 @@ struct BlockFwdParams {
   int hidden;
   float a, b, eps, off;
   int teams, wpt, cs, stages, stage_rows, stride;  // stride: bytes a stage
+  int lanes;  // of a warp on a row: 32, or kNarrowLanes where wpt is 1
 };
 
-constexpr int kFwdTeams = 12;
+// Rows of up to kNarrowGroups groups of columns take kNarrowLanes lanes, and
+// a warp takes 32 / kNarrowLanes of them at a time: their reductions share
+// their shuffles.
+constexpr int kNarrowLanes = 8;
+constexpr int kNarrowGroups = 64;
 
 struct FwdShared {
   uint64_t full[kMaxStages];
   uint64_t empty[kMaxStages];
-  uint64_t red[2];                                // across a cluster
+  uint64_t red[kMaxWarps][2];                     // a team's, across a cluster
   float slot[2][kMaxWarps * kMaxSplit];
   int abort;
 };
@@ -334,7 +339,8 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) block_fwd_tma(const B
     mbar_init(&sh.full[threadIdx.x], 1);
     mbar_init(&sh.empty[threadIdx.x], p.wpt);
   }
-  if (threadIdx.x < 2) mbar_init(&sh.red[threadIdx.x], cs * p.wpt);
+  if ((int)threadIdx.x < p.teams)
+    for (int d = 0; d < 2; ++d) mbar_init(&sh.red[threadIdx.x][d], cs * p.wpt);
   if (threadIdx.x == 0) sh.abort = 0;
   fence_mbar_init();
   __syncthreads();
@@ -401,44 +407,59 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) block_fwd_tma(const B
     __syncwarp();
   } else {
     const int team = (warp - 1) / p.wpt, tw = (warp - 1) % p.wpt;
-    const int tt = tw * 32 + lane, threads = p.wpt * 32;
+    const int lanes = p.lanes, threads = p.wpt * 32;
+    const int tt = tw * 32 + (lane & (lanes - 1)), step = lanes < 32 ? lanes : threads;
+    const int at_once = 32 / lanes, sub = lane / lanes;  // rows a warp takes at a time
     const float inv = 1.f / (float)p.hidden;
     bool ok = true;
     uint32_t turn = 0;  // exchanges of this team: slots and barriers are used in turn
-    auto over_team = [&](float v) {
-      v = warp_sum(v);
+    auto over_team = [&](float v) {  // the sum over the row's lanes
+      if (lanes == 32) {
+        v += __shfl_xor_sync(0xffffffffu, v, 16);
+        v += __shfl_xor_sync(0xffffffffu, v, 8);
+      }
+      v += __shfl_xor_sync(0xffffffffu, v, 4);
+      v += __shfl_xor_sync(0xffffffffu, v, 2);
+      v += __shfl_xor_sync(0xffffffffu, v, 1);
       if (threads == 32 && cs == 1) return v;
       const uint32_t d = turn & 1u, parity = (turn >> 1) & 1u;
       ++turn;
-      float* slot = sh.slot[d] + team * p.wpt;
+      float* slot = sh.slot[d] + team * p.wpt * cs;
       if (cs == 1) {
         if (lane == 0) slot[tw] = v;
         asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(threads) : "memory");
       } else {
         if (lane < cs) {
           st_peer(slot + rank * p.wpt + tw, lane, v);
-          mbar_arrive_peer(&sh.red[d], lane);
+          mbar_arrive_peer(&sh.red[team][d], lane);
         }
-        ok = ok && team_wait(cs, &sh.red[d], parity, abort);
+        ok = ok && team_wait(cs, &sh.red[team][d], parity, abort);
       }
       float s = 0.f;
       for (int i = lane; i < cs * p.wpt; i += 32) s += slot[i];
       return warp_sum(s);
     };
     const f32x2 a2 = pair(p.a, p.a);
-    // f for each of the thread's groups of columns, four at a time; the step of
-    // a lone warp's lanes is a constant of the addresses
-    auto each = [&](auto f) {
+    // f for each of the thread's groups of columns, four at a time; the usual
+    // steps are constants of the addresses
+    auto by = [&](auto f, auto step_of) {
+      constexpr int S = decltype(step_of)::value;
       int v = tt;
-      if (threads == 32) {
-        for (; v + 96 < nvec; v += 128) {
+      for (; v + 3 * S < nvec; v += 4 * S) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) f(v + 32 * u);
-        }
-        for (; v < nvec; v += 32) f(v);
-      } else {
-        for (; v < nvec; v += threads) f(v);
+        for (int u = 0; u < 4; ++u) f(v + S * u);
       }
+      for (; v < nvec; v += S) f(v);
+    };
+    auto each = [&](auto f) {
+      if (step == 32)
+        by(f, std::integral_constant<int, 32>{});
+      else if (step == 128)
+        by(f, std::integral_constant<int, 128>{});
+      else if (step == kNarrowLanes)
+        by(f, std::integral_constant<int, kNarrowLanes>{});
+      else
+        for (int v = tt; v < nvec; v += step) f(v);
     };
     int stage = team;
     uint32_t phase = 0;
@@ -447,7 +468,12 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) block_fwd_tma(const B
       const int64_t row0 = (k * units + unit) * K;
       const int n = (int)(p.rows - row0 < K ? p.rows - row0 : K);
       unsigned char* st = ring + (size_t)stage * p.stride;
-      for (int q = 0; q < n; ++q) {
+      for (int q0 = 0; q0 < n; q0 += at_once) {
+        // every lane takes part in the shuffles; those past the last row work
+        // on the stage's first row and write nothing
+        const int qt = q0 + sub;
+        const bool mine = qt < n && ok;
+        const int q = qt < n ? qt : 0;
         const int64_t row = row0 + q;
         T* sx = reinterpret_cast<T*>(st) + q * cols;
         TS* sr = reinterpret_cast<TS*>(st + res_at) + q * cols;
@@ -464,15 +490,16 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) block_fwd_tma(const B
           });
           const float ss = over_team(sum_pairs<N>(part));
           rs1 = rsqrtf(fmaf(ss, inv, p.eps));
-          if (isinf(ss)) {  // the squares overflowed (kOverflowScale)
+          if (__any_sync(0xffffffffu, isinf(ss))) {  // squares overflowed (kOverflowScale)
             float again = 0.f;
-            for (int j = tt; j < cols; j += threads) {
+            for (int j = tt; j < cols; j += step) {
               const float f = Traits<T>::to_f(sx[j]) * kOverflowScale;
               again = fmaf(f, f, again);
             }
-            rs1 = rstd_rescaled(over_team(again), p.hidden, p.eps);
+            again = over_team(again);
+            if (isinf(ss)) rs1 = rstd_rescaled(again, p.hidden, p.eps);
           }
-          if (tt == 0 && rank == 0 && ok) p.rstd_post[row] = rs1;
+          if (tt == 0 && rank == 0 && mine) p.rstd_post[row] = rs1;
         }
         const f32x2 rs = pair(rs1, rs1);
         const T* grow = gate_each ? gate + row / p.rows_per_gate * p.hidden + col0 : nullptr;
@@ -497,8 +524,8 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) block_fwd_tma(const B
             r[i] = fma2(w[i], x[i], mul2(a2, r[i]));
             if (NEXT) part[i] = fma2(r[i], r[i], part[i]);
           }
-          if (ok) store_pairs<TS, N>(out + v * E, r);
-          if (NEXT) {
+          if (mine) store_pairs<TS, N>(out + v * E, r);
+          if (NEXT && mine) {
             if constexpr (N == 4) {
               *reinterpret_cast<ulonglong2*>(sx + v * E) = make_ulonglong2(r[0], r[1]);
               *reinterpret_cast<ulonglong2*>(sr + v * E) = make_ulonglong2(r[2], r[3]);
@@ -523,11 +550,11 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) block_fwd_tma(const B
         };
         const float ss = over_team(sum_pairs<N>(part));
         float rs2 = rsqrtf(fmaf(ss, inv, p.eps));
-        if (isinf(ss)) {
+        if (__any_sync(0xffffffffu, isinf(ss))) {
           const f32x2 scale = pair(kOverflowScale, kOverflowScale);
 #pragma unroll
           for (int i = 0; i < N; ++i) part[i] = 0;
-          for (int v = tt; v < nvec; v += threads) {
+          for (int v = tt; v < nvec; v += step) {
             f32x2 r[N];
             kept(v, r);
 #pragma unroll
@@ -536,9 +563,10 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) block_fwd_tma(const B
               part[i] = fma2(r[i], r[i], part[i]);
             }
           }
-          rs2 = rstd_rescaled(over_team(sum_pairs<N>(part)), p.hidden, p.eps);
+          const float again = over_team(sum_pairs<N>(part));
+          if (isinf(ss)) rs2 = rstd_rescaled(again, p.hidden, p.eps);
         }
-        if (tt == 0 && rank == 0 && ok) p.rstd_next[row] = rs2;
+        if (tt == 0 && rank == 0 && mine) p.rstd_next[row] = rs2;
         const f32x2 rn = pair(rs2, rs2);
         T* yr = static_cast<T*>(p.y) + row * p.hidden + col0;
         each([&](int v) {
@@ -547,7 +575,7 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) block_fwd_tma(const B
           load_plane<N>(plane2, nvec, v, w);
 #pragma unroll
           for (int i = 0; i < N; ++i) r[i] = mul2(mul2(r[i], rn), w[i]);
-          if (ok) store_pairs<T, N>(yr + v * E, r);
+          if (mine) store_pairs<T, N>(yr + v * E, r);
         });
       }
       // r was written where the next copy will land
@@ -600,6 +628,7 @@ struct BwdShared {
 
 struct BwdShape {
   int reducers, teams, wpt, cs, stages, stage_rows, stride;
+  int lanes;    // of a reducer on a row (kNarrowLanes: as in the forward)
   bool read_x;  // x is wanted: a post norm or the gate's gradient
 };
 
@@ -732,7 +761,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
     }
     asm volatile("bar.sync 1, %0;" ::"r"(32 * reducers) : "memory");
     const float inv = 1.f / (float)p.hidden;
-    const int d = warp - 1;
+    const int d = warp - 1, lanes = sp.lanes, at_once = 32 / lanes, sub = lane / lanes;
     bool more = walk.next();
     for (int i = 0; i < d && more; ++i) {
       more = walk.next();
@@ -748,7 +777,10 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
       const unsigned char* st = ring + (size_t)pos.stage * sp.stride;
       const T* grow = gate_each ? gate + walk.q * p.hidden + col0 : nullptr;
       bool ok = true;
-      for (int q = 0; q < walk.n; ++q) {
+      for (int q0 = 0; q0 < walk.n; q0 += at_once) {
+        // lanes past the stage's rows work on its first one, for the shuffles
+        const bool mine = q0 + sub < walk.n;
+        const int q = mine ? q0 + sub : 0;
         const T* sx = reinterpret_cast<const T*>(st) + q * cols;
         const TS* sr = reinterpret_cast<const TS*>(st + at.r) + q * cols;
         const T* sdy = reinterpret_cast<const T*>(st + at.dy) + q * cols;
@@ -792,17 +824,33 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
 #pragma unroll
             for (int k = 0; k < N; ++k) s2 = fma2(x[k], dv[k], s2);
         };
-        int v = lane;
-        for (; v + 96 < nvec; v += 128) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) add(v + 32 * u);
-        }
-        for (; v < nvec; v += 32) add(v);
         float3 s;
-        if (POST && NEXT)
-          s = warp_sum3(sum2(s1), sum2(s2), sum2(s3), lane);
-        else
-          s = make_float3(NEXT ? warp_sum(sum2(s1)) : 0.f, POST ? warp_sum(sum2(s2)) : 0.f, 0.f);
+        if (lanes < 32) {
+          int v = lane & (kNarrowLanes - 1);
+          for (; v + 3 * kNarrowLanes < nvec; v += 4 * kNarrowLanes) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) add(v + kNarrowLanes * u);
+          }
+          for (; v < nvec; v += kNarrowLanes) add(v);
+          s = make_float3(sum2(s1), sum2(s2), sum2(s3));
+#pragma unroll
+          for (int m = kNarrowLanes / 2; m >= 1; m /= 2) {
+            if (NEXT) s.x += __shfl_xor_sync(0xffffffffu, s.x, m);
+            if (POST) s.y += __shfl_xor_sync(0xffffffffu, s.y, m);
+            if (POST && NEXT) s.z += __shfl_xor_sync(0xffffffffu, s.z, m);
+          }
+        } else {
+          int v = lane;
+          for (; v + 96 < nvec; v += 128) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) add(v + 32 * u);
+          }
+          for (; v < nvec; v += 32) add(v);
+          if (POST && NEXT)
+            s = warp_sum3(sum2(s1), sum2(s2), sum2(s3), lane);
+          else
+            s = make_float3(NEXT ? warp_sum(sum2(s1)) : 0.f, POST ? warp_sum(sum2(s2)) : 0.f, 0.f);
+        }
         if (cs > 1) {
           // parts of every CTA, added in their order; the slots of a stage are
           // used in turn, so that none is written before it was read
@@ -822,7 +870,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
         }
         const float c1 = s.x * inv;
         const float c2 = POST ? fmaf(-rs2f * c1, s.z, s.y) * (rs1f * inv) : 0.f;
-        if (lane == 0) sh.stat[pos.stage][q] = make_float4(-c1, -c2, rs1f, rs2f);
+        if ((lane & (lanes - 1)) == 0 && mine)
+          sh.stat[pos.stage][q] = make_float4(-c1, -c2, rs1f, rs2f);
       }
       if (!ok) break;
       __syncwarp();
@@ -1008,30 +1057,50 @@ constexpr int kSlack = 1024;  // static shared memory beside the kernels' struct
 // The forward's teams and stages for `rows` rows on `sms` SMs.  The row is
 // split over as few CTAs as leave two stages beside the weights.
 struct FwdShape {
-  int teams, wpt, cs, stages, stage_rows, stride;
+  int teams, wpt, cs, stages, stage_rows, stride, lanes, ctas;  // ctas: on an SM
   size_t smem;
 };
 
-bool fwd_shape(int64_t rows, int hidden, int sms, int row_elem, int planes, int align, int elems,
-               FwdShape* s) {
-  const int budget = kSmemBudget - (int)sizeof(FwdShared) - kSlack;
+bool fwd_shape(int64_t rows, int hidden, int sms, int row_elem, int planes, bool post, int align,
+               int elems, FwdShape* s) {
   for (int cs = 1; cs <= kMaxSplit; cs *= 2) {
     if (hidden % (align * cs) != 0) return false;
     const int cols = hidden / cs, row = cols * row_elem, over = planes * cols * 4;
-    if (over + 2 * ((row + 127) / 128 * 128) > budget) continue;
+    const int64_t mine = (rows * cs + sms - 1) / sms;            // rows an SM, about
+    const int groups = cols / elems, most = (groups + 31) / 32;  // warps a row can use
+    // Narrow rows in two CTAs an SM, of which one starts while the other
+    // ends: 4096 x 1024 fp16 14.0 -> 10.0 us, 32768 x 512 bf16 29.0 -> 27.0
+    // (4096 columns: 28.1 -> 31.3).
+    s->ctas = cs == 1 && cols <= 1024 && mine > 4 ? 2 : 1;
+    const int budget = kSmemBudget / s->ctas - (int)sizeof(FwdShared) - kSlack;
+    int stages = (budget - over) / ((row + 127) / 128 * 128);
+    if (stages < 2) continue;
     s->cs = cs;
-    const int64_t mine = (rows * cs + sms - 1) / sms;  // rows a CTA, about
-    const int most = (cols / elems + 31) / 32;         // warps a row can use
     s->stage_rows = 1;
-    if (cs > 1 || mine <= 2) {
+    s->lanes = 32;
+    if (mine <= 2) {  // few rows: all the warps on one
       s->wpt = most < kMaxWarps ? most : kMaxWarps;
       s->teams = 1;
-    } else {
+    } else if (s->ctas == 2 || (post && stages >= 8)) {
+      // A warp a row, without exchanges, as many as the ring has stages (16
+      // on an SM): 4096 x 4096 bf16 with both norms 28.1 us, 30.0 with 4
+      // teams of four warps.
       s->wpt = 1;
-      while (s->wpt < kMaxWarps && cols > 4096 * s->wpt) s->wpt *= 2;
-      // narrow rows: several to a stage, as long as every team has its own
-      while (s->stage_rows * row < 8192 && mine >= 2 * kFwdTeams * s->stage_rows) s->stage_rows *= 2;
-      s->teams = kMaxWarps / s->wpt < kFwdTeams ? kMaxWarps / s->wpt : kFwdTeams;
+      s->teams = kMaxWarps / s->ctas;
+      // several narrow rows to a stage, as long as every team has its own
+      while (s->stage_rows * row < 8192 && mine >= 2 * s->ctas * s->teams * s->stage_rows)
+        s->stage_rows *= 2;
+      if (groups <= kNarrowGroups && s->stage_rows > 1) s->lanes = kNarrowLanes;
+    } else {
+      // Teams of four warps leave more of a short ring to the copies, and have
+      // one exchange a row without the post norm: 16384 x 8192 bf16 175 us,
+      // 194 with teams of two; 4096 x 4096 without the post norm 24.1 us,
+      // 25.6 with a warp a row.  fp32 rows have twice the time: two teams,
+      // 8192 x 4096 85 us against 89 with four; 16-bit rows under an fp32
+      // stream, whose ring holds three stages, teams of two warps: 16384 x
+      // 8192 251 us against 266.
+      s->wpt = row_elem == 6 ? 2 : 4;
+      s->teams = row_elem == 8 ? 2 : 4;
     }
     s->stride = (s->stage_rows * row + 127) / 128 * 128;
     s->stages = (budget - over) / s->stride;
@@ -1047,7 +1116,7 @@ bool fwd_shape(int64_t rows, int hidden, int sms, int row_elem, int planes, int 
 // The backward's roles and stages, over as few CTAs as leave three stages
 // (else two) beside the reducers' weights.
 template <typename F>
-bool bwd_pick(int64_t rows, int hidden, int sms, int align, int planes, F stage_bytes,
+bool bwd_pick(int64_t rows, int hidden, int sms, int align, int elems, int planes, F stage_bytes,
               BwdShape* s, int* nv8, size_t* smem) {
   const int budget = kSmemBudget - (int)sizeof(BwdShared) - kSlack;
   for (int least = 3; least >= 2; --least)
@@ -1065,6 +1134,7 @@ bool bwd_pick(int64_t rows, int hidden, int sms, int align, int planes, F stage_
       while (cs == 1 && 2 * s->stage_rows <= kBwdRows && 2 * s->stage_rows * cols <= 4096 &&
              rows >= (int64_t)8 * s->stage_rows * sms)
         s->stage_rows *= 2;
+      s->lanes = cs == 1 && cols / elems <= kNarrowGroups && s->stage_rows > 1 ? kNarrowLanes : 32;
       const int over = planes * cols * 4 + (s->teams > 1 ? cols * 4 : 0);
       s->stride = (stage_bytes(s->stage_rows, cols) + 127) / 128 * 128;
       s->stages = (budget - over) / s->stride;
@@ -1094,7 +1164,7 @@ bool try_fwd(const BlockFwdArgs& a, cudaStream_t s, cudaError_t* err) {
   const int sms = sm_count(dev);
   FwdShape sh;
   if (!fwd_shape(a.rows, a.hidden, sms, (int)(sizeof(T) + sizeof(TS)), NEXT ? 2 : 1,
-                 16 / (int)sizeof(T), E, &sh))
+                 POST, 16 / (int)sizeof(T), E, &sh))
     return false;
   BlockFwdParams p;
   p.x = a.x;
@@ -1119,16 +1189,18 @@ bool try_fwd(const BlockFwdArgs& a, cudaStream_t s, cudaError_t* err) {
   p.stages = sh.stages;
   p.stage_rows = sh.stage_rows;
   p.stride = sh.stride;
+  p.lanes = sh.lanes;
   auto kern = block_fwd_tma<T, TS, POST, NEXT>;
   *err = allow_smem(kern, sh.smem);
   if (*err == cudaSuccess) *err = allow_cluster((const void*)kern, sh.cs);
   if (*err != cudaSuccess) return true;
-  int64_t units = sms / sh.cs;
+  const int threads = 32 * (1 + sh.teams * sh.wpt);
+  int64_t units = sh.cs == 1 ? (int64_t)sms * sh.ctas : max_clusters((const void*)kern, threads, sh.smem, sh.cs, sms);
   const int64_t blocks = (a.rows + sh.stage_rows - 1) / sh.stage_rows;
   if (units > blocks) units = blocks;
   if (units < 1) units = 1;
-  *err = launch_kernel(kern, dim3((unsigned)(units * sh.cs)), dim3(32 * (1 + sh.teams * sh.wpt)),
-                       sh.smem, s, sh.cs, p);
+  *err = launch_kernel(kern, dim3((unsigned)(units * sh.cs)), dim3(threads), sh.smem, s,
+                       sh.cs, p);
   return true;
 }
 
@@ -1145,22 +1217,22 @@ bool try_bwd(const BlockBwdArgs& a, BlockBwdParams& p, int* units, cudaStream_t 
   const bool dr = a.dr != nullptr, x = sp.read_x;
   int nv8 = 0;
   size_t smem = 0;
-  if (!bwd_pick(a.rows, a.hidden, sms, 16 / (int)sizeof(T), (POST ? 1 : 0) + (NEXT ? 1 : 0),
+  if (!bwd_pick(a.rows, a.hidden, sms, 16 / (int)sizeof(T), E, (POST ? 1 : 0) + (NEXT ? 1 : 0),
                 [=](int k, int cols) { return bwd_stage<T, TS>(k, cols, x, NEXT, dr).bytes; }, &sp,
                 &nv8, &smem))
     return false;
-  int64_t n = sms / sp.cs;
-  if (n < 1) n = 1;
-  if (n > RMSN_BLOCK_MAX_PARTIALS) n = RMSN_BLOCK_MAX_PARTIALS;
-  if (n > a.rows) n = a.rows;
-  *units = (int)n;
-  place_partials(a, *units, p);
   auto go = [&](auto kern) {
     *err = allow_smem(kern, smem);
     if (*err == cudaSuccess) *err = allow_cluster((const void*)kern, sp.cs);
     if (*err != cudaSuccess) return;
-    *err = launch_kernel(kern, dim3((unsigned)(n * sp.cs)),
-                         dim3(32 * (1 + sp.reducers + sp.teams * sp.wpt)), smem, s, sp.cs, p, sp);
+    const int threads = 32 * (1 + sp.reducers + sp.teams * sp.wpt);
+    int64_t n = sp.cs == 1 ? sms : max_clusters((const void*)kern, threads, smem, sp.cs, sms);
+    if (n < 1) n = 1;
+    if (n > RMSN_BLOCK_MAX_PARTIALS) n = RMSN_BLOCK_MAX_PARTIALS;
+    if (n > a.rows) n = a.rows;
+    *units = (int)n;
+    place_partials(a, *units, p);
+    *err = launch_kernel(kern, dim3((unsigned)(n * sp.cs)), dim3(threads), smem, s, sp.cs, p, sp);
   };
   if (dr || !NEXT) {
     if (nv8 == 1)

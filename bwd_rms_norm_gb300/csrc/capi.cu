@@ -26,6 +26,7 @@ struct OccEntry {
   size_t smem;
   int device;
   int value;
+  int cluster;
 };
 std::mutex g_occ_mutex;
 OccEntry g_occ[256];
@@ -73,15 +74,45 @@ int max_blocks_per_sm(const void* func, int block, size_t smem) {
     std::lock_guard<std::mutex> lock(g_occ_mutex);
     for (int i = 0; i < g_occ_n; ++i)
       if (g_occ[i].func == func && g_occ[i].block == block && g_occ[i].smem == smem &&
-          g_occ[i].device == dev)
+          g_occ[i].device == dev && g_occ[i].cluster == 1)
         return g_occ[i].value;
   }
   int n = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, func, block, smem) != cudaSuccess) n = 1;
   if (n < 1) n = 1;
   std::lock_guard<std::mutex> lock(g_occ_mutex);
-  if (g_occ_n < 256) g_occ[g_occ_n++] = OccEntry{func, block, smem, dev, n};
+  if (g_occ_n < 256) g_occ[g_occ_n++] = OccEntry{func, block, smem, dev, n, 1};
   return n;
+}
+
+int max_clusters(const void* func, int block, size_t smem, int cluster, int sms) {
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  {
+    std::lock_guard<std::mutex> lock(g_occ_mutex);
+    for (int i = 0; i < g_occ_n; ++i)
+      if (g_occ[i].func == func && g_occ[i].block == block && g_occ[i].smem == smem &&
+          g_occ[i].device == dev && g_occ[i].cluster == cluster)
+        n = g_occ[i].value;
+  }
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)cluster);
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, func, &cfg) != cudaSuccess || n < 1) n = 1;
+    std::lock_guard<std::mutex> lock(g_occ_mutex);
+    if (g_occ_n < 256) g_occ[g_occ_n++] = OccEntry{func, block, smem, dev, n, cluster};
+  }
+  const int fit = sms / cluster < 1 ? 1 : sms / cluster;
+  return n < fit ? n : fit;
 }
 
 }  // namespace rmsn

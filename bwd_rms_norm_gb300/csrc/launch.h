@@ -286,5 +286,9 @@ cudaError_t launch_block_bwd(int dtype, int res_dtype, const BlockBwdArgs& a, cu
 // set with rms_norm_set_sm_budget (capi.cu).
 int sm_count(int device);
 int max_blocks_per_sm(const void* func, int block, size_t smem);
+// Clusters of `cluster` CTAs of this launch shape that the current device
+// holds at once (a cluster stays within one group of SMs, so fewer than its
+// SMs over the cluster's size), at most those on `sms` SMs; cached.
+int max_clusters(const void* func, int block, size_t smem, int cluster, int sms);
 
 }  // namespace rmsn
