@@ -5,9 +5,9 @@
 //   factor = min(1, max_norm / (norm + eps)), 1 where norm is not finite
 //   out_i  = round(g_i * factor)
 //
-// Two launches.  grad_squares reads the list once and leaves one double a
-// CTA; grad_scale (or grad_norm_final, where only the norm is wanted) adds
-// those doubles, every CTA in the same order, and writes the scaled list.
+// Two launches.  grad_squares reads the list once and leaves one sum a CTA;
+// grad_scale (or grad_norm_final, where only the norm is wanted) adds those
+// sums, every CTA in the same order, and writes the scaled list.
 //
 // Bound by HBM bandwidth: the list is read for the norm, and read again and
 // written for the scaling.  The list is cut into chunks of at most
@@ -20,11 +20,15 @@
 // and a captured call keeps its list.
 //
 // Numerics: a thread squares and adds the elements of its share of one chunk
-// in fp32 (at most kChunkElems / kThreads of them), and its shares in double.
-// Squares of fp32 and bf16 values can leave the fp32 range although their
-// root does not: a share whose fp32 sum is infinite or below 2^-90 is summed
-// again, scaled by 2^-73 or 2^100 (fp16 squares are all in range).  The
-// double sum of squares holds any fp32 list.
+// in fp32 (at most kChunkElems / kThreads of them).  Shares are added as pairs
+// of fp32 values, a sum and what its roundings lost (Knuth's two-sum), to
+// about 2^-45: the same in double cost 7 us a kernel and 11 us in front of the
+// scaling (1216 CTAs adding 500 partial sums each), since an SM adds two
+// doubles a cycle.  Squares of fp32 and bf16 values can leave the fp32 range
+// although their root does not: a share whose fp32 sum is above 2^60 or below
+// 2^-90 (fp16: cannot be) is summed again scaled by 2^-73 or 2^100 where its
+// squares are lost, and goes to a sum in double beside the pair, which is
+// looked at only where it is not zero.
 #include <algorithm>
 #include <new>
 #include <type_traits>
@@ -85,6 +89,7 @@ __device__ __forceinline__ float chunk_squares(const T* __restrict__ p, int n, f
   float part[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) part[e] = 0.f;
+#pragma unroll 1
   for (int v0 = threadIdx.x; v0 < nvec; v0 += UN * kThreads) {
     uint4 q[UN];
 #pragma unroll
@@ -117,67 +122,132 @@ __device__ __forceinline__ float chunk_squares(const T* __restrict__ p, int n, f
   return part[0];
 }
 
-template <typename T>
-__device__ __forceinline__ double chunk_sum(const void* in, int64_t e0, int n) {
-  const T* p = static_cast<const T*>(in) + e0;
-  float s = chunk_squares<T>(p, n, 1.f);
-  if constexpr (sizeof(T) == 4 || std::is_same<T, __nv_bfloat16>::value) {
-    if (isinf(s)) return (double)chunk_squares<T>(p, n, kOverflowScale) * 0x1p146;
-    if (s < 0x1p-90f) return (double)chunk_squares<T>(p, n, 0x1p100f) * 0x1p-200;
-  }
-  return (double)s;
+// A sum: hi + lo + extra.
+struct GradSum {
+  float hi, lo;
+  double extra;
+};
+
+// hi + lo = the old sum + v, to the last bit of lo.
+__device__ __forceinline__ void add_to(float& hi, float& lo, float v) {
+  const float s = __fadd_rn(hi, v);
+  const float b = __fadd_rn(s, -hi);
+  lo += __fadd_rn(hi, -__fadd_rn(s, -b)) + __fadd_rn(v, -b);
+  hi = s;
 }
 
-__device__ __forceinline__ double block_sum_double(double v, double* red) {
+template <typename T>
+__device__ __forceinline__ void add_chunk(GradSum& sum, const void* in, int64_t e0, int n) {
+  constexpr bool wide = !std::is_same<T, __half>::value;  // of fp32's exponents
+  const T* p = static_cast<const T*>(in) + e0;
+  const float s = chunk_squares<T>(p, n, 1.f);
+  if (s <= 0x1p60f && s >= (wide ? 0x1p-90f : 0.f)) {
+    add_to(sum.hi, sum.lo, s);
+  } else if (!wide || isnan(s) || (s > 0x1p60f && !isinf(s))) {
+    sum.extra += (double)s;
+  } else {
+    const float again = chunk_squares<T>(p, n, s < 1.f ? 0x1p100f : kOverflowScale);
+    if (again != 0.f) sum.extra += (double)again * (s < 1.f ? 0x1p-200 : 0x1p146);
+  }
+}
+
+// The CTA's sum, the same in every thread, in a fixed order.
+__device__ __forceinline__ GradSum block_sum_grads(GradSum v, GradSum* red) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
-  for (int m = 16; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  for (int m = 16; m >= 1; m >>= 1) {
+    const float hi = __shfl_xor_sync(0xffffffffu, v.hi, m);
+    v.lo += __shfl_xor_sync(0xffffffffu, v.lo, m);
+    add_to(v.hi, v.lo, hi);
+  }
+  const unsigned any = __ballot_sync(0xffffffffu, !(v.extra == 0.0));
+  if (any)
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) v.extra += __shfl_xor_sync(0xffffffffu, v.extra, m);
+  if (lane == 0) red[warp] = v;
   __syncthreads();
-  double s = 0.0;
+  GradSum s = {0.f, 0.f, 0.0};
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) s += red[w];
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const GradSum r = red[w];
+    add_to(s.hi, s.lo, r.hi);
+    s.lo += r.lo;
+    if (!(r.extra == 0.0)) s.extra += r.extra;
+  }
   return s;
 }
 
 template <int N>
 __global__ void __launch_bounds__(kThreads) grad_squares(const __grid_constant__ GradTable<N> t,
-                                                         double* __restrict__ partial) {
-  __shared__ double red[kThreads / 32];
+                                                         GradSum* __restrict__ partial) {
+  __shared__ GradSum red[kThreads / 32];
   pdl_trigger();
   pdl_wait();
   const int chunks = t.first[t.count];
-  double sum = 0.0;
+  GradSum sum = {0.f, 0.f, 0.0};
   for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
     const int i = find_tensor(t, c);
     const int64_t e0 = (int64_t)(c - t.first[i]) * t.chunk;
     const int64_t left = t.numel[i] - e0;
     const int n = left < t.chunk ? (int)left : t.chunk;
     if (t.in_type[i] == RMSN_F32)
-      sum += chunk_sum<float>(t.in[i], e0, n);
+      add_chunk<float>(sum, t.in[i], e0, n);
     else if (t.in_type[i] == RMSN_BF16)
-      sum += chunk_sum<__nv_bfloat16>(t.in[i], e0, n);
+      add_chunk<__nv_bfloat16>(sum, t.in[i], e0, n);
     else
-      sum += chunk_sum<__half>(t.in[i], e0, n);
+      add_chunk<__half>(sum, t.in[i], e0, n);
   }
-  sum = block_sum_double(sum, red);
+  sum = block_sum_grads(sum, red);
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
-// The norm from the CTAs' partial sums, the same bits in every CTA.
-__device__ __forceinline__ double norm_of(const double* __restrict__ partial, int nparts,
-                                          double* red) {
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < nparts; i += kThreads) sum += partial[i];
-  return sqrt(block_sum_double(sum, red));
+// The norm from the CTAs' partial sums, the same bits in every CTA: nearest +
+// rest, nearest its fp32 value.
+struct GradNorm {
+  float nearest, rest;
+};
+
+__device__ __forceinline__ GradNorm norm_of(const GradSum* __restrict__ partial, int nparts,
+                                            GradSum* red) {
+  GradSum sum = {0.f, 0.f, 0.0};
+  for (int i = threadIdx.x; i < nparts; i += kThreads) {
+    const GradSum p = partial[i];
+    add_to(sum.hi, sum.lo, p.hi);
+    sum.lo += p.lo;
+    if (!(p.extra == 0.0)) sum.extra += p.extra;
+  }
+  sum = block_sum_grads(sum, red);
+  if (!(sum.extra == 0.0)) {
+    const double v = sqrt((double)sum.hi + (double)sum.lo + sum.extra);
+    const float f = (float)v;
+    return {f, isfinite(f) ? (float)(v - (double)f) : 0.f};
+  }
+  // sqrt(s + e) = r + (s - r^2 + e) / (2 r), r = sqrt(s), the difference exact
+  const float s = sum.hi + sum.lo, e = sum.lo - (s - sum.hi);
+  if (!(s > 0.f)) return {s, 0.f};
+  const float r = sqrtf(s);
+  const float d = (fmaf(-r, r, s) + e) / (2.f * r);
+  const float f = r + d;
+  return {f, d - (f - r)};
 }
 
-__global__ void __launch_bounds__(kThreads) grad_norm_final(const double* __restrict__ partial,
+// min(1, max_norm / (norm + eps)), 1 where the norm is not finite.
+__device__ __forceinline__ float factor_of(const GradNorm& n, float max_norm, float eps) {
+  float hi = n.nearest, lo = n.rest;
+  add_to(hi, lo, eps);
+  const float d = hi + lo, rest = lo - (d - hi);
+  if (!isfinite(n.nearest) || !(d > max_norm || (d == max_norm && rest > 0.f))) return 1.f;
+  const float q = max_norm / d;
+  return q - q * (rest / d);
+}
+
+__global__ void __launch_bounds__(kThreads) grad_norm_final(const GradSum* __restrict__ partial,
                                                             int nparts, float* __restrict__ norm) {
-  __shared__ double red[kThreads / 32];
+  __shared__ GradSum red[kThreads / 32];
   pdl_trigger();
   pdl_wait();
-  const double v = norm_of(partial, nparts, red);
-  if (threadIdx.x == 0) *norm = (float)v;
+  const GradNorm v = norm_of(partial, nparts, red);
+  if (threadIdx.x == 0) *norm = v.nearest;
 }
 
 // out = round(in * factor) over a chunk: V elements an access where both
@@ -195,27 +265,28 @@ __device__ __forceinline__ void scale_chunk(const void* in, void* out, int64_t e
   if (head > n) head = n;
   const bool vec = ((uintptr_t)(p + head) % sizeof(VT)) == 0;
   const int nvec = vec ? (n - head) / V : 0;
-  for (int v0 = threadIdx.x; v0 < nvec; v0 += UN * kThreads) {
+  auto put = [&](int v, const VT& q) {
+    float f[V];
+    if constexpr (sizeof(VT) == 16)
+      unpack<T>(q, f);
+    else
+      unpack_h<T>(q, f);
+#pragma unroll
+    for (int e = 0; e < V; ++e) f[e] *= factor;
+    st_vec(o + head + (int64_t)v * V, pack<O>(f));
+  };
+  auto get = [&](int v) { return *reinterpret_cast<const VT*>(p + head + (int64_t)v * V); };
+  int v0 = threadIdx.x;
+#pragma unroll 1
+  for (; v0 + (UN - 1) * kThreads < nvec; v0 += UN * kThreads) {
     VT q[UN];
 #pragma unroll
-    for (int k = 0; k < UN; ++k) {
-      const int v = v0 + k * kThreads;
-      if (v < nvec) q[k] = *reinterpret_cast<const VT*>(p + head + (int64_t)v * V);
-    }
+    for (int k = 0; k < UN; ++k) q[k] = get(v0 + k * kThreads);
 #pragma unroll
-    for (int k = 0; k < UN; ++k) {
-      const int v = v0 + k * kThreads;
-      if (v >= nvec) continue;
-      float f[V];
-      if constexpr (sizeof(VT) == 16)
-        unpack<T>(q[k], f);
-      else
-        unpack_h<T>(q[k], f);
-#pragma unroll
-      for (int e = 0; e < V; ++e) f[e] *= factor;
-      st_vec(o + head + (int64_t)v * V, pack<O>(f));
-    }
+    for (int k = 0; k < UN; ++k) put(v0 + k * kThreads, q[k]);
   }
+#pragma unroll 1
+  for (; v0 < nvec; v0 += kThreads) put(v0, get(v0));
   const int rest = n - nvec * V;
   if (rest < 2 * V) {
     if ((int)threadIdx.x < rest) {
@@ -224,34 +295,35 @@ __device__ __forceinline__ void scale_chunk(const void* in, void* out, int64_t e
     }
   } else {  // no common alignment: nvec is 0
     constexpr int US = 8;
-    for (int i0 = threadIdx.x; i0 < n; i0 += US * kThreads) {
+    int i0 = threadIdx.x;
+#pragma unroll 1
+    for (; i0 + (US - 1) * kThreads < n; i0 += US * kThreads) {
       T q[US];
 #pragma unroll
-      for (int k = 0; k < US; ++k)
-        if (i0 + k * kThreads < n) q[k] = p[i0 + k * kThreads];
+      for (int k = 0; k < US; ++k) q[k] = p[i0 + k * kThreads];
 #pragma unroll
       for (int k = 0; k < US; ++k)
-        if (i0 + k * kThreads < n)
-          o[i0 + k * kThreads] = Traits<O>::from_f(Traits<T>::to_f(q[k]) * factor);
+        o[i0 + k * kThreads] = Traits<O>::from_f(Traits<T>::to_f(q[k]) * factor);
     }
+#pragma unroll 1
+    for (; i0 < n; i0 += kThreads) o[i0] = Traits<O>::from_f(Traits<T>::to_f(p[i0]) * factor);
   }
 }
 
 template <int N>
 __global__ void __launch_bounds__(kThreads) grad_scale(const __grid_constant__ GradTable<N> t,
-                                                       const double* __restrict__ partial,
+                                                       const GradSum* __restrict__ partial,
                                                        int nparts,
                                                        const float* __restrict__ total_norm,
                                                        float max_norm, float eps,
                                                        float* __restrict__ norm) {
-  __shared__ double red[kThreads / 32];
+  __shared__ GradSum red[kThreads / 32];
   pdl_trigger();
   pdl_wait();
-  const double v = total_norm != nullptr ? (double)*total_norm : norm_of(partial, nparts, red);
-  if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)v;
-  float factor = 1.f;
-  if (isfinite((float)v) && v + (double)eps > (double)max_norm)
-    factor = (float)((double)max_norm / (v + (double)eps));
+  const GradNorm v = total_norm != nullptr ? GradNorm{*total_norm, 0.f}
+                                           : norm_of(partial, nparts, red);
+  if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = v.nearest;
+  const float factor = factor_of(v, max_norm, eps);
   const int chunks = t.first[t.count];
   for (int c = chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
     const int i = find_tensor(t, c);
@@ -301,7 +373,7 @@ struct GradList {
   float max_norm, eps;
   const float* total_norm;
   float* norm;
-  double* partial;
+  GradSum* partial;
 };
 
 int elem_size(int dtype) { return dtype == RMSN_F32 ? 4 : 2; }
@@ -345,7 +417,7 @@ cudaError_t run_list(const GradList& g, int chunk, cudaStream_t s, int* launches
       const int chunks = fill_table<N>(g, chunk, &at, t);
       if (chunks == 0) break;
       const int grid = chunks < most ? chunks : most;
-      double* slot = g.partial + nparts;
+      GradSum* slot = g.partial + nparts;
       void* args[] = {&t, &slot};
       e = launch_table(kern, grid, s, args);
       if (e != cudaSuccess) return e;
@@ -354,14 +426,14 @@ cudaError_t run_list(const GradList& g, int chunk, cudaStream_t s, int* launches
     }
   }
   if (g.out == nullptr) {
-    e = launch_kernel(grad_norm_final, dim3(1), dim3(kThreads), 0, s, 1, (const double*)g.partial,
+    e = launch_kernel(grad_norm_final, dim3(1), dim3(kThreads), 0, s, 1, (const GradSum*)g.partial,
                       nparts, g.norm);
     if (e == cudaSuccess) *launches += 1;
     return e;
   }
   const void* kern = (const void*)grad_scale<N>;
   const int most = sms * max_blocks_per_sm(kern, kThreads, 0);
-  const double* partial = g.partial;
+  const GradSum* partial = g.partial;
   float max_norm = g.max_norm, eps = g.eps;
   float* norm = g.norm;
   const float* total = g.total_norm;
@@ -449,7 +521,7 @@ bool overlaps(const void* const* grads, const int64_t* numels, const int* dtypes
 // Room for the partial sums of every launch, a table's tensors each.
 size_t workspace_bytes_of(int64_t count) {
   const int64_t tables = count <= kMaxTable ? 1 : ceil_div(count, kMaxTable);
-  return (size_t)tables * RMSN_GRAD_MAX_PARTIALS * sizeof(double);
+  return (size_t)tables * RMSN_GRAD_MAX_PARTIALS * sizeof(GradSum);
 }
 
 }  // namespace
@@ -472,7 +544,7 @@ int rms_norm_grad_norm(const void* const* grads, const int64_t* numels, const in
   if ((uintptr_t)workspace % 16 != 0) return RMSN_ERR_ALIGN;
   if (workspace_bytes < workspace_bytes_of(count)) return RMSN_ERR_WORKSPACE;
   GradList g = {grads, nullptr, numels, dtypes, nullptr, count, 0.f, 0.f, nullptr, norm,
-                static_cast<double*>(workspace)};
+                static_cast<GradSum*>(workspace)};
   int launches = 0;
   const cudaError_t e = launch_list(g, static_cast<cudaStream_t>(stream), &launches);
   if (e != cudaSuccess) return cuda_fail(e);
@@ -501,7 +573,7 @@ int rms_norm_grad_clip(const void* const* grads, const int64_t* numels, const in
   if (failed) return cuda_fail(cudaErrorMemoryAllocation);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   GradList g = {grads, outs, numels, dtypes, out_dtypes, count, max_norm, eps, total_norm, norm,
-                static_cast<double*>(workspace)};
+                static_cast<GradSum*>(workspace)};
   int launches = 0;
   cudaError_t e = cudaSuccess;
   if (count == 0) {  // nothing to scale: the norm of nothing, or the given one

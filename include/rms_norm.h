@@ -406,8 +406,9 @@ int rms_norm_block_bwd(const void* dy, const void* dresidual_out, const void* x,
  * elements of dtypes[i] in device memory (any element alignment; a tensor of
  * no elements may be NULL).  The elements of a list are at most
  * RMSN_GRAD_MAX_ELEMENTS.  Squares are added in fp32 within a few dozen
- * elements and in double beyond, so that no finite list of a finite fp32 norm
- * overflows or vanishes; the order is fixed by the sizes, the GPU's SM count
+ * elements and to twice its precision beyond, with what leaves its range in
+ * double, so that no finite list of a finite fp32 norm overflows or vanishes;
+ * the order is fixed by the sizes, the GPU's SM count
  * and the SM budget.  `norm` is one fp32 on the device.
  *
  * rms_norm_grad_clip writes outs[i] in out_dtypes[i], which is dtypes[i] or

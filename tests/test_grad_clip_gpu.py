@@ -2,7 +2,7 @@
 
 Tolerances, from u = 2^-24: squares are added in fp32 within at most 32
 elements of a thread in a tree of 8 (at most 32 + 3 roundings, one of them
-the square's own), in double beyond, so the sum is within 36 u, its root
+the square's own), to about u^2 beyond, so the sum is within 36 u, its root
 within 18 u, and the fp32 norm within 19 u.  The factor has that error and one
 rounding, an output the product's and that of its type: h + 22 u, h =
 finfo(T).eps / 2, plus the smallest subnormal where it underflows."""

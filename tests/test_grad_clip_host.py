@@ -75,8 +75,8 @@ def test_clip_refusals(L):
 
 def test_workspace_size(L):
     size = L.rms_norm_grad_workspace_size
-    assert size(1) == size(1024) == 1216 * 8
-    assert size(1025) == size(2048) == 2 * 1216 * 8
+    assert size(1) == size(1024) == 1216 * 16
+    assert size(1025) == size(2048) == 2 * 1216 * 16
     assert size(-1) == 0
 
 
