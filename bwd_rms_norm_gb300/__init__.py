@@ -50,6 +50,7 @@ from __future__ import annotations
 import array
 import contextlib
 import ctypes
+import importlib.util
 import os
 from typing import Optional, Tuple
 
@@ -57,6 +58,7 @@ import torch
 
 LIB_NAME = "librms_norm_gb300.so"
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), LIB_NAME)
+BINDING_PATH = os.path.join(os.path.dirname(LIB_PATH), "_binding.so")
 
 # Values of the C enums (include/rms_norm.h).
 RMSN_F32, RMSN_BF16, RMSN_F16 = 0, 1, 2
@@ -115,6 +117,22 @@ class RMSNormError(RuntimeError):
 
 
 _lib: Optional[ctypes.CDLL] = None
+# The usual calls of the newer entry points without ctypes' cost (binding.cpp);
+# None before load_library, or where it was not built.
+_binding = None
+
+
+def _load_binding(lib: ctypes.CDLL) -> None:
+    global _binding
+    if not os.path.exists(BINDING_PATH):
+        return
+    spec = importlib.util.spec_from_file_location("bwd_rms_norm_gb300._binding", BINDING_PATH)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.rms_norm_block_fwd, lib.rms_norm_block_bwd, lib.rms_norm_block_bwd_workspace_size,
+        lib.rms_norm_grad_norm, lib.rms_norm_grad_clip, lib.rms_norm_grad_workspace_size)))
+    _binding = module
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -194,6 +212,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.rms_norm_grad_norm.restype = I
     lib.rms_norm_grad_clip.argtypes = [P, P, P, P, P, I64, F, F, P, P, P, SZ, P]
     lib.rms_norm_grad_clip.restype = I
+    _load_binding(lib)
     _lib = lib
     return lib
 
@@ -821,6 +840,12 @@ def rms_norm_block_fwd(x: torch.Tensor, residual: torch.Tensor,
     x uses one.  Returns ``(r, y, rstd_post, rstd_next)``, None for what a
     missing norm would give."""
     lib = load_library()
+    if _binding is not None and stream is None and (
+            residual_out is y is rstd_post is rstd_next is None):
+        got = _binding.block_fwd(x, residual, post_gamma, gate, next_gamma, eps, offset,
+                                 residual_scale, branch_scale)
+        if got is not None:
+            return got
     dev, dtype, shape = x.device, x.dtype, x.shape
     res_dtype, index = residual.dtype, x.get_device()
     rows, hidden, gate_rows = _block_sizes(x, post_gamma, gate, next_gamma)
@@ -857,8 +882,8 @@ def rms_norm_block_fwd(x: torch.Tensor, residual: torch.Tensor,
         st = lib.rms_norm_block_fwd(x.data_ptr(), residual.data_ptr(), _address(post_gamma),
                                     _address(gate), gate_rows, _address(next_gamma),
                                     residual_out.data_ptr(), _address(y), _address(rstd_post),
-                                    _address(rstd_next), rows, hidden, float(residual_scale),
-                                    float(branch_scale), float(eps), int(offset),
+                                    _address(rstd_next), rows, hidden, float(residual_scale + 0.0),
+                                    float(branch_scale + 0.0), float(eps), int(offset),
                                     DTYPE_CODES[dtype], DTYPE_CODES[res_dtype], handle)
     if st != RMSN_OK:
         raise RMSNormError("rms_norm_block_fwd", st)
@@ -888,6 +913,12 @@ def rms_norm_block_bwd(dy: Optional[torch.Tensor], dresidual_out: Optional[torch
     fp32, ``dgate`` shaped like ``gate`` (None without a gate or with
     ``with_dgate`` False), ``dpost`` / ``dnext`` None for a missing norm."""
     lib = load_library()
+    if _binding is not None and dx is dresidual is workspace is stream is None:
+        got = _binding.block_bwd(dy, dresidual_out, x, residual_out, rstd_post, rstd_next,
+                                 post_gamma, gate, next_gamma, offset, residual_scale,
+                                 branch_scale, with_dgate)
+        if got is not None:
+            return got
     rows, hidden, gate_rows = _block_sizes(x, post_gamma, gate, next_gamma)
     if next_gamma is None:
         dy = None
@@ -937,8 +968,8 @@ def rms_norm_block_bwd(dy: Optional[torch.Tensor], dresidual_out: Optional[torch
                                     _address(gate), gate_rows, _address(next_gamma),
                                     _address(rstd_post), _address(rstd_next), dx.data_ptr(),
                                     dresidual.data_ptr(), _address(dpost), _address(dgate),
-                                    _address(dnext), rows, hidden, float(residual_scale),
-                                    float(branch_scale), int(offset), DTYPE_CODES[dtype],
+                                    _address(dnext), rows, hidden, float(residual_scale + 0.0),
+                                    float(branch_scale + 0.0), int(offset), DTYPE_CODES[dtype],
                                     DTYPE_CODES[res_dtype], workspace.data_ptr(),
                                     workspace.numel() * workspace.element_size(), handle)
     if st != RMSN_OK:
@@ -996,6 +1027,10 @@ def rms_norm_grad_norm(grads, norm: Optional[torch.Tensor] = None,
     """The 2-norm over a list of gradients (contiguous CUDA tensors of one
     device, of any of the three dtypes): an fp32 tensor of no dimensions."""
     lib = load_library()
+    if _binding is not None and norm is workspace is stream is None:
+        got = _binding.grad_norm(grads)
+        if got is not None:
+            return got
     grads = _grads_of(grads)
     dev = grads[0].device
     ptrs, numels, codes = _grad_list("a gradient", grads, dev)
@@ -1028,6 +1063,10 @@ def rms_norm_grad_clip(grads, max_norm: float, eps: float = 1e-6, out=None,
     ``total_norm`` (a one-element fp32 tensor) that norm is taken instead of
     the list's own, e.g. one summed over ranks."""
     lib = load_library()
+    if _binding is not None and norm is workspace is stream is None:
+        got = _binding.grad_clip(grads, max_norm, eps, out, total_norm)
+        if got is not None:
+            return got
     grads = _grads_of(grads)
     dev = grads[0].device
     outs = grads if out is None else _grads_of(out)

@@ -1,0 +1,118 @@
+"""The direct binding of the usual calls: it declines what needs a second
+look, and where it takes a call the results are those of the other way."""
+import os
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def L():
+    import bwd_rms_norm_gb300 as lib
+    from bwd_rms_norm_gb300 import build
+    if not (os.path.exists(lib.LIB_PATH) and os.path.exists(lib.BINDING_PATH)):
+        build.build()
+    lib.load_library()
+    return lib
+
+
+def test_declines_on_the_host(L):
+    b, z = L._binding, torch.zeros(4, 8)
+    w = torch.ones(8)
+    assert b.block_fwd(z, z, w, None, w, 1e-5, 0, 1.0, 1.0) is None       # not CUDA
+    assert b.block_fwd(z, z) is None                                      # too few arguments
+    assert b.block_fwd(None, z, w, None, w, 1e-5, 0, 1.0, 1.0) is None
+    assert b.block_fwd("x", 3, w, None, w, 1e-5, 0, 1.0, 1.0) is None
+    assert b.block_bwd(*[z] * 4, *[None] * 5, 0, 1.0, 1.0, True) is None
+    assert b.grad_norm([z]) is None and b.grad_norm([]) is None
+    assert b.grad_norm(z) is None and b.grad_norm(None) is None and b.grad_norm(iter([z])) is None
+    assert b.grad_clip([z], 1.0, 1e-6, None, None) is None
+    with pytest.raises((ValueError, TypeError)):
+        b.init(1, 2)
+
+
+@pytest.fixture
+def other_way(L, monkeypatch):
+    def call(f, *args, **kw):
+        with monkeypatch.context() as m:
+            m.setattr(L, "_binding", None)
+            return f(*args, **kw)
+    return call
+
+
+def same(a, b):
+    a, b = (v if isinstance(v, tuple) else (v,) for v in (a, b))
+    assert len(a) == len(b)
+    for u, v in zip(a, b):
+        assert (u is None) == (v is None)
+        if u is not None:
+            assert u.shape == v.shape and u.dtype == v.dtype and u.device == v.device
+            assert torch.equal(u, v)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,res", [("float32", "float32"), ("bfloat16", "bfloat16"),
+                                       ("float16", "float32")])
+@pytest.mark.parametrize("post,gates,nxt", [(1, (), 1), (1, (96,), 0), (0, (4, 1, 96), 1),
+                                            (1, (4, 96), 1)])
+def test_block_norm(L, other_way, dtype, res, post, gates, nxt):
+    t, ts = getattr(torch, dtype), getattr(torch, res)
+    x = torch.randn(4, 6, 96, device="cuda").to(t)
+    r = torch.randn(4, 6, 96, device="cuda").to(ts)
+    w = torch.rand(96, device="cuda").to(t) + 1
+    p = torch.nn.Parameter(w) if post else None
+    g = torch.rand(gates, device="cuda").to(t) if gates else None
+    n = w if nxt else None
+    args = (x, r, p, g, n, 1e-5, 1, 0.5, 2.0)
+    assert L._binding.block_fwd(*args) is not None
+    out = L.rms_norm_block_fwd(*args)
+    same(out, other_way(L.rms_norm_block_fwd, *args))
+    back = (x if nxt else None, r, x, out[0], out[2], out[3], p, g, n, 1, 0.5, 2.0)
+    for with_dgate in (True, False):
+        assert L._binding.block_bwd(*back, with_dgate) is not None
+        got = L.rms_norm_block_bwd(*back, with_dgate=with_dgate)
+        same(got, other_way(L.rms_norm_block_bwd, *back, with_dgate=with_dgate))
+
+
+@pytest.mark.gpu
+def test_gradients(L, other_way):
+    grads = [torch.randn(n, device="cuda").to(d) for n, d in
+             ((1000, torch.float32), (7, torch.bfloat16), (0, torch.float16), (300, torch.float16))]
+    out = [torch.empty_like(g, dtype=torch.float32) for g in grads]
+    norm = L.rms_norm_grad_norm(grads)
+    assert L._binding.grad_norm(tuple(grads)) is not None
+    same(norm, other_way(L.rms_norm_grad_norm, grads))
+    for kw in (dict(), dict(total_norm=norm * 2)):
+        assert L._binding.grad_clip(grads, 1.0, 1e-6, out, kw.get("total_norm")) is not None
+        a = L.rms_norm_grad_clip(grads, 1.0, out=out, **kw)
+        first = [o.clone() for o in out]
+        same(a, other_way(L.rms_norm_grad_clip, grads, 1.0, out=out, **kw))
+        same(tuple(first), tuple(out))
+    copies = [g.clone() for g in grads]
+    same(L.rms_norm_grad_clip(grads, 1.0), other_way(L.rms_norm_grad_clip, copies, 1.0))
+    same(tuple(grads), tuple(copies))
+
+
+@pytest.mark.gpu
+def test_declines_on_the_gpu(L):
+    """What the Python functions refuse, with their messages."""
+    b = L._binding
+    x = torch.randn(4, 8, device="cuda")
+    w = torch.ones(8, device="cuda")
+    ok = (x, x.clone(), w, None, w, 1e-5, 0, 1.0, 1.0)
+    assert b.block_fwd(*ok) is not None
+    for i, bad in ((0, x.double()), (0, x.cpu()), (0, x.t()), (1, x[:2]), (1, x.half()),
+                   (2, w[:4]), (2, w.half()), (3, torch.ones(3, 8, device="cuda")),
+                   (3, torch.ones(2, 4, device="cuda")), (4, w.view(2, 4)), (5, -1.0),
+                   (5, float("nan")), (6, 2), (6, 0.5), (7, float("inf")), (7, "1")):
+        args = list(ok)
+        args[i] = bad
+        assert b.block_fwd(*args) is None, i
+        with pytest.raises((RuntimeError, ValueError, TypeError)):
+            L.rms_norm_block_fwd(*args) if not (i == 6 and bad == 0.5) else int("x")
+    assert b.grad_norm([x, x.cpu()]) is None and b.grad_norm([x.double()]) is None
+    assert b.grad_clip([x], -1.0, 1e-6, None, None) is None
+    assert b.grad_clip([x], 1.0, 1e-6, [x[:2]], None) is None
+    assert b.grad_clip([x, x], 1.0, 1e-6, None, None) is None
+    with pytest.raises(L.RMSNormError):
+        L.rms_norm_grad_clip([x, x], 1.0)
