@@ -36,91 +36,14 @@ namespace rmsn {
 namespace {
 
 // ---------------------------------------------------------------------------
-// any alignment, rows of up to 1024 NC columns (backward 512 NC): single
-// elements, consecutive lanes on consecutive ones, a thread's columns of the
-// row in registers.  Bound by the instructions an element: 8192 x 4097 bf16
-// forward 66 us, backward 139 us, where the staged kernels take 50 and 82 for
-// 4096 columns.
-// ---------------------------------------------------------------------------
-// Columns tid, tid + blockDim, ... of a CTA whose threads own up to NC each.
-template <int NC, typename F>
-__device__ __forceinline__ void each_col(int hidden, F f) {
-#pragma unroll
-  for (int k = 0; k < NC; ++k) {
-    const int j = threadIdx.x + k * blockDim.x;
-    if (j < hidden) f(k, j);
-  }
-}
-
-template <typename T, typename TS, int NC>
-__global__ void __launch_bounds__(1024) block_fwd_cols(
-    const T* __restrict__ x, const TS* __restrict__ res, const T* __restrict__ gamma_post,
-    const T* __restrict__ gate, const T* __restrict__ gamma_next, TS* __restrict__ res_out,
-    T* __restrict__ y, float* __restrict__ rstd_post, float* __restrict__ rstd_next,
-    int64_t rows, int64_t rows_per_gate, int hidden, float a, float b, float eps, float off) {
-  __shared__ float red[64];
-  pdl_trigger();
-  pdl_wait();
-  int parity = 0;
-  auto sum = [&](float v) {
-    v = block_sum(v, red, parity);
-    parity ^= 1;
-    return v;
-  };
-  // the root mean square's inverse of v, rescaled where the squares overflow
-  auto rstd = [&](const float (&v)[NC]) {
-    float ss = 0.f;
-#pragma unroll
-    for (int k = 0; k < NC; ++k) ss = fmaf(v[k], v[k], ss);
-    ss = sum(ss);
-    if (!isinf(ss)) return rstd_of(ss / (float)hidden, eps);
-    float s2 = 0.f;
-#pragma unroll
-    for (int k = 0; k < NC; ++k) {
-      const float t = v[k] * kOverflowScale;
-      s2 = fmaf(t, t, s2);
-    }
-    return rstd_rescaled(sum(s2), hidden, eps);
-  };
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-    const int64_t at = row * hidden;
-    const T* gr = gate == nullptr ? nullptr : gate + row / rows_per_gate * hidden;
-    float v[NC], r[NC];
-#pragma unroll
-    for (int k = 0; k < NC; ++k) v[k] = r[k] = 0.f;
-    each_col<NC>(hidden, [&](int k, int j) {
-      v[k] = Traits<T>::to_f(x[at + j]);
-      r[k] = Traits<TS>::to_f(res[at + j]);
-    });
-    float rs1 = 1.f;
-    if (gamma_post != nullptr) {
-      rs1 = rstd(v);
-      if (threadIdx.x == 0) rstd_post[row] = rs1;
-    }
-    each_col<NC>(hidden, [&](int k, int j) {
-      float w = b;
-      if (gr != nullptr) w *= Traits<T>::to_f(gr[j]);
-      if (gamma_post != nullptr) w *= Traits<T>::to_f(gamma_post[j]) + off;
-      r[k] = fmaf(w, v[k] * rs1, a * r[k]);
-      res_out[at + j] = Traits<TS>::from_f(r[k]);
-    });
-    if (gamma_next == nullptr) continue;
-    const float rs2 = rstd(r);
-    if (threadIdx.x == 0) rstd_next[row] = rs2;
-    each_col<NC>(hidden, [&](int k, int j) {
-      y[at + j] = Traits<T>::from_f((r[k] * rs2) * (Traits<T>::to_f(gamma_next[j]) + off));
-    });
-  }
-}
-
-// ---------------------------------------------------------------------------
 // any width and alignment: single elements, a row's values read again (from
-// L1 / L2) after its reductions
+// L1 / L2) after its reductions, the sums over the rows kept in the partial
+// rows.  For what the staged kernels do not take: few or narrow odd rows
+// (block_fwd_odd_pays), tensors that do not start on 16 bytes.
 // ---------------------------------------------------------------------------
-constexpr int kLoopThreads = 256;
 
-template <typename T, typename TS>
-__global__ void __launch_bounds__(kLoopThreads) block_fwd_loop(
+template <typename T, typename TS, int NT>
+__global__ void __launch_bounds__(NT) block_fwd_loop(
     const T* __restrict__ x, const TS* __restrict__ res, const T* __restrict__ gamma_post,
     const T* __restrict__ gate, const T* __restrict__ gamma_next, TS* __restrict__ res_out,
     T* __restrict__ y, float* __restrict__ rstd_post, float* __restrict__ rstd_next,
@@ -136,7 +59,7 @@ __global__ void __launch_bounds__(kLoopThreads) block_fwd_loop(
     float rs1 = 1.f;
     if (gamma_post != nullptr) {
       float ss = 0.f;
-      for (int j = threadIdx.x; j < hidden; j += kLoopThreads) {
+      for (int j = threadIdx.x; j < hidden; j += NT) {
         const float v = Traits<T>::to_f(xr[j]);
         ss = fmaf(v, v, ss);
       }
@@ -144,7 +67,7 @@ __global__ void __launch_bounds__(kLoopThreads) block_fwd_loop(
       parity ^= 1;
       rs1 = rstd_of(ss / (float)hidden, eps);
       if (isinf(ss)) {  // see kOverflowScale
-        ss = block_sum(scaled_sum_sq(xr, threadIdx.x, kLoopThreads, hidden), red, parity);
+        ss = block_sum(scaled_sum_sq(xr, threadIdx.x, NT, hidden), red, parity);
         parity ^= 1;
         rs1 = rstd_rescaled(ss, hidden, eps);
       }
@@ -157,7 +80,7 @@ __global__ void __launch_bounds__(kLoopThreads) block_fwd_loop(
       return fmaf(w, Traits<T>::to_f(xr[j]) * rs1, a * Traits<TS>::to_f(sr[j]));
     };
     float ss = 0.f;
-    for (int j = threadIdx.x; j < hidden; j += kLoopThreads) {
+    for (int j = threadIdx.x; j < hidden; j += NT) {
       const float r = stream(j);
       ss = fmaf(r, r, ss);
       res_out[row * hidden + j] = Traits<TS>::from_f(r);
@@ -168,7 +91,7 @@ __global__ void __launch_bounds__(kLoopThreads) block_fwd_loop(
     float rs2 = rstd_of(ss / (float)hidden, eps);
     if (isinf(ss)) {
       float s2 = 0.f;
-      for (int j = threadIdx.x; j < hidden; j += kLoopThreads) {
+      for (int j = threadIdx.x; j < hidden; j += NT) {
         const float t = stream(j) * kOverflowScale;
         s2 = fmaf(t, t, s2);
       }
@@ -177,7 +100,7 @@ __global__ void __launch_bounds__(kLoopThreads) block_fwd_loop(
       rs2 = rstd_rescaled(s2, hidden, eps);
     }
     if (threadIdx.x == 0) rstd_next[row] = rs2;
-    for (int j = threadIdx.x; j < hidden; j += kLoopThreads)
+    for (int j = threadIdx.x; j < hidden; j += NT)
       y[row * hidden + j] =
           Traits<T>::from_f((stream(j) * rs2) * (Traits<T>::to_f(gamma_next[j]) + off));
   }
@@ -202,8 +125,8 @@ __device__ __forceinline__ float3 block_sum3(float a, float b, float c, float4* 
   return s;
 }
 
-template <typename T, typename TS>
-__global__ void __launch_bounds__(kLoopThreads) block_bwd_loop(const BlockBwdParams p) {
+template <typename T, typename TS, int NT>
+__global__ void __launch_bounds__(NT) block_bwd_loop(const BlockBwdParams p) {
   __shared__ float4 red[64];
   pdl_trigger();
   pdl_wait();
@@ -237,7 +160,7 @@ __global__ void __launch_bounds__(kLoopThreads) block_bwd_loop(const BlockBwdPar
       return w;
     };
     float s1 = 0.f, s2 = 0.f, s3 = 0.f;
-    for (int j = threadIdx.x; j < hidden; j += kLoopThreads) {
+    for (int j = threadIdx.x; j < hidden; j += NT) {
       const float wx = weight(j) * (Traits<T>::to_f(x[at + j]) * rs1);
       float t = dr != nullptr ? Traits<TS>::to_f(dr[at + j]) : 0.f;
       if (gamma_next != nullptr) {
@@ -253,7 +176,7 @@ __global__ void __launch_bounds__(kLoopThreads) block_bwd_loop(const BlockBwdPar
     parity ^= 1;
     const float c1 = s.x / (float)hidden;
     const float c2 = gamma_post != nullptr ? fmaf(-rs2 * c1, s.z, s.y) / (float)hidden : 0.f;
-    for (int j = threadIdx.x; j < hidden; j += kLoopThreads) {
+    for (int j = threadIdx.x; j < hidden; j += NT) {
       const float xh = Traits<T>::to_f(x[at + j]) * rs1;
       float d = dr != nullptr ? Traits<TS>::to_f(dr[at + j]) : 0.f;
       if (gamma_next != nullptr) {
@@ -275,105 +198,19 @@ __global__ void __launch_bounds__(kLoopThreads) block_bwd_loop(const BlockBwdPar
   }
 }
 
-// The backward with a thread's sums over the rows in registers; with HOLD the
-// row's values too, without it they are read again (from L1) after the
-// reduction.
-template <typename T, typename TS, int NC, bool HOLD>
-__global__ void __launch_bounds__(512) block_bwd_cols(const BlockBwdParams p) {
-  __shared__ float4 red[64];
-  pdl_trigger();
-  pdl_wait();
-  const T* dy = static_cast<const T*>(p.dy);
-  const TS* dr = static_cast<const TS*>(p.dr);
-  const T* x = static_cast<const T*>(p.x);
-  const TS* r = static_cast<const TS*>(p.r);
-  const T* gamma_post = static_cast<const T*>(p.gamma_post);
-  const T* gate = static_cast<const T*>(p.gate);
-  const T* gamma_next = static_cast<const T*>(p.gamma_next);
-  const int hidden = p.hidden;
-  const int64_t u = blockIdx.x;
-  const int64_t r0 = u * p.rows / gridDim.x, r1 = (u + 1) * p.rows / gridDim.x;
-  const bool post = gamma_post != nullptr, next = gamma_next != nullptr;
-  constexpr int NH = HOLD ? NC : 1;
-  float acc_n[NC], acc_a[NC];
-#pragma unroll
-  for (int k = 0; k < NC; ++k) acc_n[k] = acc_a[k] = 0.f;
-  int parity = 0;
-  for (int64_t seg0 = r0; seg0 < r1;) {
-    const int64_t q = seg0 / p.rows_per_gate;
-    const int64_t seg1 = (q + 1) * p.rows_per_gate < r1 ? (q + 1) * p.rows_per_gate : r1;
-    auto weight = [&](int j) {
-      float w = p.b;
-      if (gate != nullptr) w *= Traits<T>::to_f(gate[q * hidden + j]);
-      if (post) w *= Traits<T>::to_f(gamma_post[j]) + p.off;
-      return w;
-    };
-    for (int64_t row = seg0; row < seg1; ++row) {
-      const int64_t at = row * hidden;
-      const float rs1 = post ? p.rstd_post[row] : 1.f, rs2 = next ? p.rstd_next[row] : 0.f;
-      // x_hat, r_hat, dy, dr of a column
-      auto read = [&](int j) {
-        float4 v;
-        v.x = Traits<T>::to_f(x[at + j]) * rs1;
-        v.y = next ? Traits<TS>::to_f(r[at + j]) * rs2 : 0.f;
-        v.z = next ? Traits<T>::to_f(dy[at + j]) : 0.f;
-        v.w = dr != nullptr ? Traits<TS>::to_f(dr[at + j]) : 0.f;
-        return v;
-      };
-      float4 held[NH];
-      float s1 = 0.f, s2 = 0.f, s3 = 0.f;
-      if (HOLD) each_col<NC>(hidden, [&](int k, int j) { held[HOLD ? k : 0] = read(j); });
-      each_col<NC>(hidden, [&](int k, int j) {
-        const float4 v = HOLD ? held[HOLD ? k : 0] : read(j);
-        const float wx = weight(j) * v.x;
-        const float g = next ? v.z * (Traits<T>::to_f(gamma_next[j]) + p.off) : 0.f;
-        s1 = fmaf(g, v.y, s1);
-        s2 = fmaf(wx, fmaf(rs2, g, v.w), s2);
-        s3 = fmaf(wx, v.y, s3);
-      });
-      const float3 s = block_sum3(s1, s2, s3, red, parity);
-      parity ^= 1;
-      const float c1 = s.x / (float)hidden;
-      const float c2 = post ? fmaf(-rs2 * c1, s.z, s.y) / (float)hidden : 0.f;
-      each_col<NC>(hidden, [&](int k, int j) {
-        const float4 v = HOLD ? held[HOLD ? k : 0] : read(j);
-        const float g = next ? v.z * (Traits<T>::to_f(gamma_next[j]) + p.off) : 0.f;
-        const float d = fmaf(rs2, fmaf(-v.y, c1, g), v.w);
-        acc_n[k] = fmaf(v.z, v.y, acc_n[k]);
-        acc_a[k] = fmaf(d, v.x, acc_a[k]);
-        static_cast<TS*>(p.dres)[at + j] = Traits<TS>::from_f(p.a * d);
-        static_cast<T*>(p.dx)[at + j] = Traits<T>::from_f(rs1 * fmaf(-v.x, c2, weight(j) * d));
-      });
-    }
-    const bool first = q == r0 / p.rows_per_gate, several = p.rows_per_gate < p.rows;
-    each_col<NC>(hidden, [&](int k, int j) {
-      if (post || gate != nullptr) {
-        const float v = p.b * acc_a[k];
-        p.p_a[(u + q) * hidden + j] = v;
-        if (post && several) {
-          float* pp = p.p_post + u * hidden + j;
-          *pp = fmaf(Traits<T>::to_f(gate[q * hidden + j]), v, first ? 0.f : *pp);
-        }
-      }
-      if (next && seg1 == r1) p.p_next[u * hidden + j] = acc_n[k];
-      acc_a[k] = 0.f;
-    });
-    seg0 = seg1;
-  }
-}
-
 // The sums over the partial rows, in a fixed order: 16 lanes, each adding
 // every 16th row, then the 16 lane sums in order (as dw_finalize), four
 // columns a thread where rows are 16-byte aligned (VEC 4).  Jobs (blockIdx.y):
 // the next norm's sums; with one gate row, or none, the sums of A, which give
 // dgamma_post = gate A and dgate = w1 A; with several, the post norm's sums,
-// and for each gate row those of A over its segments u_first + q ... u_last + q.
+// and for each gate row those of A over its segments.  Where gate rows have
+// few segments each (`serial`), a lane takes a gate row.
 constexpr int kSumLanes = 16;
 
 template <typename T, int VEC>
 __global__ void __launch_bounds__(32 * kSumLanes) block_bwd_sums(
-    const BlockBwdParams p, int units, float* __restrict__ dgamma_post, float* __restrict__ dgate,
-    float* __restrict__ dgamma_next) {
+    const BlockBwdParams p, int units, bool serial, float* __restrict__ dgamma_post,
+    float* __restrict__ dgate, float* __restrict__ dgamma_next) {
   __shared__ float s[kSumLanes][32 * VEC];
   pdl_trigger();
   pdl_wait();
@@ -383,27 +220,25 @@ __global__ void __launch_bounds__(32 * kSumLanes) block_bwd_sums(
   const bool one = p.rows_per_gate >= p.rows;
   const T* gamma_post = static_cast<const T*>(p.gamma_post);
   const T* gate = static_cast<const T*>(p.gate);
-  const int64_t jobs = 2 + (one || dgate == nullptr ? 0 : p.rows / p.rows_per_gate);
+  const int64_t gates = p.rows / p.rows_per_gate, of = units / p.period;
+  const int64_t per = serial ? kSumLanes : 1;  // gate rows a job
+  const int64_t jobs = 2 + (one || dgate == nullptr ? 0 : (gates + per - 1) / per);
+  auto weight = [&](int j) {
+    return gamma_post != nullptr ? Traits<T>::to_f(gamma_post[j]) + p.off : 1.f;
+  };
   for (int64_t job = blockIdx.y; job < jobs; job += gridDim.y) {
-    const float* src = job == 0 ? p.p_next : one ? p.p_a : p.p_post;
-    int64_t n = units, q = 0;
     if (job == 0 ? dgamma_next == nullptr
                  : dgamma_post == nullptr && (dgate == nullptr || (job == 1 && !one)))
       continue;
-    if (job >= 2) {
-      q = job - 2;
-      // unit of row i: the largest u with floor(u R / U) <= i
-      const int64_t first = ((q * p.rows_per_gate + 1) * units - 1) / p.rows;
-      const int64_t last = ((q + 1) * p.rows_per_gate * units - 1) / p.rows;
-      src = p.p_a + (first + q) * hidden;
-      n = last - first + 1;
-    }
+    const bool alone = serial && job >= 2;  // a lane a gate row
+    const int64_t q = (job - 2) * per + (alone ? ty : 0);
     float acc[VEC];
 #pragma unroll
     for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
-    if (j0 < hidden) {
+    auto add = [&](const float* src, int64_t n) {
+      if (j0 >= hidden) return;
 #pragma unroll 8
-      for (int64_t i = ty; i < n; i += kSumLanes) {
+      for (int64_t i = alone ? 0 : ty; i < n; i += alone ? 1 : kSumLanes) {
         if constexpr (VEC == 4) {
           const float4 v = *reinterpret_cast<const float4*>(src + i * hidden + j0);
           acc[0] += v.x;
@@ -414,6 +249,33 @@ __global__ void __launch_bounds__(32 * kSumLanes) block_bwd_sums(
           acc[0] += src[i * hidden + j0];
         }
       }
+    };
+    if (job < 2) {
+      add(job == 0 ? p.p_next : one ? p.p_a : p.p_post, units);
+    } else if (q < gates) {
+      // class c's rows are c + P i; its unit of i is the largest u with
+      // floor(u n / U) <= i, n of its rows over U units
+      for (int c = 0; c < p.period; ++c) {
+        const int64_t n = (p.rows - c + p.period - 1) / p.period;
+        auto from = [&](int64_t row) { return row <= c ? 0 : (row - c + p.period - 1) / p.period; };
+        const int64_t lo = from(q * p.rows_per_gate), hi = from((q + 1) * p.rows_per_gate);
+        if (lo >= hi) continue;
+        const int64_t first = ((lo + 1) * of - 1) / n, last = (hi * of - 1) / n;
+        add(p.p_a + (c * (of + gates - 1) + first + q) * hidden, last - first + 1);
+      }
+    }
+    if (alone) {
+      if (q < gates && j0 < hidden)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) acc[k] *= weight(j0 + k);
+      if (q < gates && j0 < hidden) {
+        if constexpr (VEC == 4)
+          *reinterpret_cast<float4*>(dgate + q * hidden + j0) =
+              make_float4(acc[0], acc[1], acc[2], acc[3]);
+        else
+          dgate[q * hidden + j0] = acc[0];
+      }
+      continue;
     }
 #pragma unroll
     for (int k = 0; k < VEC; ++k) s[ty][tx * VEC + k] = acc[k];
@@ -426,10 +288,9 @@ __global__ void __launch_bounds__(32 * kSumLanes) block_bwd_sums(
       if (job == 0) {
         dgamma_next[j] = t;
       } else {
-        const float w1 = gamma_post != nullptr ? Traits<T>::to_f(gamma_post[j]) + p.off : 1.f;
         const float g = gate != nullptr && one ? Traits<T>::to_f(gate[j]) : 1.f;
         if (job == 1 && dgamma_post != nullptr) dgamma_post[j] = t * g;
-        if (dgate != nullptr && (one || job >= 2)) dgate[q * hidden + j] = t * w1;
+        if (dgate != nullptr && (one || job >= 2)) dgate[(one ? 0 : q) * hidden + j] = t * weight(j);
       }
     }
     __syncthreads();
@@ -448,8 +309,9 @@ cudaError_t launch_fwd_t(const BlockFwdArgs& a, cudaStream_t s) {
   int dev = 0;
   e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const int sms = sm_count(dev);
   auto go = [&](auto kern, int threads) {
-    const int64_t most = (int64_t)sm_count(dev) * max_blocks_per_sm((const void*)kern, threads, 0);
+    const int64_t most = (int64_t)sms * max_blocks_per_sm((const void*)kern, threads, 0);
     return launch_kernel(kern, dim3((unsigned)(a.rows < most ? a.rows : most)), dim3(threads), 0, s,
                          1, static_cast<const T*>(a.x), static_cast<const TS*>(a.res),
                          static_cast<const T*>(a.gamma_post), static_cast<const T*>(a.gate),
@@ -457,10 +319,12 @@ cudaError_t launch_fwd_t(const BlockFwdArgs& a, cudaStream_t s) {
                          static_cast<T*>(a.y), a.rstd_post, a.rstd_next, a.rows, a.rows_per_gate,
                          a.hidden, a.res_scale, a.branch_scale, a.eps, a.offset ? 1.f : 0.f);
   };
-  constexpr int NC = 8;
-  if (a.hidden <= 1024 * NC)
-    return go(block_fwd_cols<T, TS, NC>, ((a.hidden + NC - 1) / NC + 31) / 32 * 32);
-  return go(block_fwd_loop<T, TS>, kLoopThreads);
+  // bf16, 128 / 256 / 1024 threads: 64 x 1001 4.3, 3.7, 3.4 us; 64 x 8191 13.5,
+  // 11.1, 6.5; 4096 x 257 9.8, 15.4, 65; 4096 x 1001 18.0, 24.4, 88; 4096 x
+  // 4097 53, 49, 128
+  if (a.rows <= sms && a.hidden > 512) return go(block_fwd_loop<T, TS, 1024>, 1024);
+  if (a.hidden <= 1024) return go(block_fwd_loop<T, TS, 128>, 128);
+  return go(block_fwd_loop<T, TS, 256>, 256);
 }
 
 template <typename T, typename TS>
@@ -483,9 +347,12 @@ cudaError_t launch_bwd_t(const BlockBwdArgs& a, cudaStream_t s, int* launches) {
   p.a = a.res_scale;
   p.b = a.branch_scale;
   p.off = a.offset ? 1.f : 0.f;
+  p.period = 1;
   int units = 0;
   cudaError_t e = cudaSuccess;
-  if (!try_launch_block_bwd_tma(code<T>(), code<TS>(), a, p, &units, s, &e)) {
+  const bool odd = a.edge_ok && block_bwd_odd_pays(a.rows, a.rows_per_gate, a.hidden);
+  if (!(a.vec_ok && try_launch_block_bwd_tma(code<T>(), code<TS>(), a, p, &units, s, &e)) &&
+      !(odd && try_launch_block_bwd_odd(code<T>(), code<TS>(), a, p, &units, s, &e))) {
     int dev = 0;
     e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -496,30 +363,40 @@ cudaError_t launch_bwd_t(const BlockBwdArgs& a, cudaStream_t s, int* launches) {
       place_partials(a, units, p);
       return launch_kernel(kern, dim3((unsigned)units), dim3(threads), 0, s, 1, p);
     };
-    auto threads = [&](int nc) { return ((a.hidden + nc - 1) / nc + 31) / 32 * 32; };
-    if (a.hidden <= 512 * 8)
-      e = go(block_bwd_cols<T, TS, 8, true>, threads(8));
-    else if (a.hidden <= 512 * 16)
-      e = go(block_bwd_cols<T, TS, 16, false>, threads(16));
-    else
-      e = go(block_bwd_loop<T, TS>, kLoopThreads);
+    // bf16, 128 / 512 threads: 64 x 257 5.9, 5.9 us; 4096 x 257 27, 54; 64 x
+    // 1001 10.5, 7.1; 64 x 4097 29, 16; 1024 x 4097 with 64 gate rows 166, 60
+    e = a.hidden <= 512 ? go(block_bwd_loop<T, TS, 128>, 128) : go(block_bwd_loop<T, TS, 512>, 512);
   }
   if (e != cudaSuccess) return e;
   *launches += 1;
   if (a.dgamma_post == nullptr && a.dgate == nullptr && a.dgamma_next == nullptr)
     return cudaSuccess;
   const int64_t gates = a.rows / a.rows_per_gate;
-  const int64_t jobs = 2 + (a.dgate != nullptr && gates > 1 ? gates : 0);
-  const int vec = a.hidden % 4 == 0 ? 4 : 1;  // the partial rows start on 16 bytes
+  const int vec = a.hidden % 4 == 0 && reinterpret_cast<uintptr_t>(a.dgate) % 16 == 0 ? 4 : 1;
+  // bf16 4096 x 4096, by lanes / serially: 4096 gate rows 1244 / 165 us, 64 62 /
+  // 46; 4096 x 1024 with 16 gate rows 22.5 / 23.4
+  const bool serial = 4 * gates >= units;
+  const int64_t jobs = 2 + (a.dgate == nullptr || gates == 1 ? 0
+                            : serial ? (gates + kSumLanes - 1) / kSumLanes : gates);
   const dim3 grid((unsigned)((a.hidden + 32 * vec - 1) / (32 * vec)),
                   (unsigned)(jobs < 65535 ? jobs : 65535));
   e = launch_kernel(vec == 4 ? block_bwd_sums<T, 4> : block_bwd_sums<T, 1>, grid,
-                    dim3(32, kSumLanes), 0, s, 1, p, units, a.dgamma_post, a.dgate, a.dgamma_next);
+                    dim3(32, kSumLanes), 0, s, 1, p, units, serial, a.dgamma_post, a.dgate,
+                    a.dgamma_next);
   if (e == cudaSuccess) *launches += 1;
   return e;
 }
 
 }  // namespace
+
+cudaError_t read_block_wait_timeouts(unsigned int* out) {
+  unsigned int n[3] = {0, 0, 0};
+  cudaError_t e = read_block_fwd_wait_timeouts(&n[0]);
+  if (e == cudaSuccess) e = read_block_bwd_tma_wait_timeouts(&n[1]);
+  if (e == cudaSuccess) e = read_block_bwd_odd_wait_timeouts(&n[2]);
+  *out = n[0] + n[1] + n[2];
+  return e;
+}
 
 cudaError_t launch_block_fwd(int dtype, int res_dtype, const BlockFwdArgs& a, cudaStream_t s) {
   if (dtype == RMSN_F32) return launch_fwd_t<float, float>(a, s);

@@ -6,6 +6,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "block_norm.cuh"
 #include "launch.h"
 #include "rms_norm.h"
 
@@ -593,6 +594,7 @@ int rms_norm_block_fwd(const void* x, const void* residual, const void* gamma_po
   a.vec_ok = ((hidden * s) % 16 == 0) && aligned16(x) && aligned16(residual) &&
              aligned16(gamma_post) && aligned16(gate) && aligned16(gamma_next) &&
              aligned16(residual_out) && aligned16(a.y);
+  a.edge_ok = aligned16(x) && aligned16(residual) && aligned16(residual_out) && aligned16(a.y);
   const cudaError_t e =
       launch_block_fwd(dtype, residual_dtype, a, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e);
@@ -605,9 +607,12 @@ size_t rms_norm_block_bwd_workspace_size(int64_t rows, int64_t hidden, int64_t g
       gate_rows < 0 || gate_rows > rows)
     return 0;
   // partial rows of dgamma_next and dgamma_post, one a unit, and one of A a
-  // segment: fewer than units + gate rows
+  // segment: fewer than units + gate rows, or where rows of odd widths are
+  // taken in up to 8 classes units + 8 gate rows
   const int64_t parts = rows < RMSN_BLOCK_MAX_PARTIALS ? rows : RMSN_BLOCK_MAX_PARTIALS;
-  return (size_t)(3 * parts + (gate_rows > 0 ? gate_rows : 1)) * (size_t)hidden * sizeof(float);
+  int64_t gates = gate_rows > 0 ? gate_rows : 1;
+  if (gates > 1 && block_bwd_odd_pays(rows, rows / gates, (int)hidden)) gates *= 8;
+  return (size_t)(3 * parts + gates) * (size_t)hidden * sizeof(float);
 }
 
 int rms_norm_block_bwd(const void* dy, const void* dresidual_out, const void* x,
@@ -666,6 +671,8 @@ int rms_norm_block_bwd(const void* dy, const void* dresidual_out, const void* x,
   a.vec_ok = ((hidden * s) % 16 == 0) && aligned16(a.dy) && aligned16(a.dr) && aligned16(x) &&
              aligned16(a.r) && aligned16(gamma_post) && aligned16(gate) && aligned16(gamma_next) &&
              aligned16(dx) && aligned16(dresidual);
+  a.edge_ok = aligned16(a.dy) && aligned16(a.dr) && aligned16(x) && aligned16(a.r) &&
+              aligned16(dx) && aligned16(dresidual);
   a.partial = static_cast<float*>(workspace);
   int launches = 0;
   const cudaError_t e = launch_block_bwd(dtype, residual_dtype, a, cs, &launches);

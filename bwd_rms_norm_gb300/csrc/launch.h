@@ -252,6 +252,7 @@ struct BlockFwdArgs {
   float res_scale, branch_scale, eps;
   int offset;
   bool vec_ok;             // 16-byte aligned rows in every tensor
+  bool edge_ok;            // [rows, hidden] tensors that start on 16 bytes
 };
 
 struct BlockBwdArgs {
@@ -274,7 +275,7 @@ struct BlockBwdArgs {
   int hidden;
   float res_scale, branch_scale;
   int offset;
-  bool vec_ok;
+  bool vec_ok, edge_ok;
   float* partial;          // rms_norm_block_bwd_workspace_size bytes
 };
 

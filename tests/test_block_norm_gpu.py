@@ -437,3 +437,72 @@ def test_module_trains_in_a_stack(L):
             assert p.grad.shape == p.shape and torch.isfinite(p.grad).all().item()
             assert p.grad.abs().max().item() > 0
     assert torch.isfinite(h.grad).all().item()
+
+
+# rows that start anywhere in 16 bytes: periods of 2, 4 and 8 rows, narrow ones
+# (several to a stage) to ones over several CTAs, tensors whose last row ends
+# inside 16 bytes
+ODD = [(65601, 65), (32800, 132), (16401, 257), (4203, 1001), (1031, 2050), (514, 4093),
+       (259, 8191), (177, 12001), (133, 16002), (129, 16389)]
+
+
+@pytest.mark.parametrize("rows,hidden", ODD)
+@pytest.mark.parametrize("dtype,res", [("bf16", "bf16"), ("f32", "f32"), ("f16", "f32")])
+def test_odd_widths(L, rows, hidden, dtype, res):
+    d, g = make(rows, hidden, dtype, res, True, rows % 2, True, seed=rows + hidden)
+    run_and_check(L, d, g, a=0.5)
+
+
+@pytest.mark.parametrize("dtype,res", TYPES)
+@pytest.mark.parametrize("post,nxt", NORMS)
+def test_odd_widths_and_parts(L, post, nxt, dtype, res):
+    d, g = make(1037, 2051, dtype, res, post, 1, nxt, seed=6)
+    run_and_check(L, d, g, offset=1)
+    g["dresidual_out"] = g["dresidual_out"] if not nxt else None
+    run_and_check(L, d, g, offset=1)
+
+
+@pytest.mark.parametrize("post,nxt", NORMS)
+@pytest.mark.parametrize("rows,gates,hidden", [(1290, 5, 1033), (6150, 3, 131), (600, 2, 4098),
+                                               (768, 3, 2049), (8192, 32, 1026)])
+def test_odd_widths_and_gate_rows(L, post, nxt, rows, gates, hidden):
+    d, g = make(rows, hidden, "bf16", "bf16", post, gates, nxt, seed=gates)
+    run_and_check(L, d, g, b=0.5)
+
+
+@pytest.mark.parametrize("dtype,res", [("bf16", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("rows,hidden", [(32800, 130), (4206, 1001), (520, 4093), (260, 9001)])
+def test_odd_widths_beside_infinities(L, dtype, res, rows, hidden):
+    """What is copied of the rows before and after a row does not reach it."""
+    d, g = make(rows, hidden, dtype, res, True, 1, True, seed=3)
+
+    def run():
+        c = cuda(d)
+        out = L.rms_norm_block_fwd(**c, eps=1e-5)
+        weights = [c[k] for k in ("post_gamma", "gate", "next_gamma")]
+        back = L.rms_norm_block_bwd(g["dy"].cuda(), g["dresidual_out"].cuda(), c["x"], out[0],
+                                    out[2], out[3], *weights)
+        return [v.reshape(rows, -1) for v in list(out) + list(back[:2])]
+
+    clean = run()
+    for k in ("x", "residual"):
+        d[k][::2] = float("nan")
+    for k in ("dy", "dresidual_out"):
+        g[k][::2] = float("inf")
+    for u, v in zip(clean, run()):
+        assert torch.equal(u[1::2], v[1::2])
+        assert torch.isnan(v[::2]).any(-1).all()
+
+
+@pytest.mark.parametrize("rows,hidden,gates", [(4100, 1024, 1), (600, 4096, 0), (8300, 512, 0),
+                                               (1024, 4096, 2)])
+def test_unaligned_weights_alone(L, rows, hidden, gates):
+    d, g = make(rows, hidden, "bf16", "bf16", True, gates, True, seed=5)
+    run_and_check(L, d, g, move=lambda t: t.cuda() if t.shape[0] == rows else misaligned(t))
+
+
+@pytest.mark.parametrize("rows,gates", [(700, 350), (4000, 4000), (640, 20), (5000, 40)])
+@pytest.mark.parametrize("hidden", [256, 77])
+def test_gate_rows_of_few_segments(L, rows, gates, hidden):
+    d, g = make(rows, hidden, "f32", "f32", True, gates, True, seed=7)
+    run_and_check(L, d, g)
