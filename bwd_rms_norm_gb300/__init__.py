@@ -43,7 +43,9 @@ The functions carry the names of the C entry points declared in
 
 For autograd: ``rms_norm(x, weight, eps, offset=0, cast_mode="round_once")``
 (a ``torch.autograd.Function`` over rms_norm_fwd / rms_norm_bwd) and the
-module ``RMSNorm(hidden, eps, offset=0, cast_mode="round_once")``.
+module ``RMSNorm(hidden, eps, offset=0, cast_mode="round_once")``; likewise
+``rms_norm_block`` and the module ``RMSNormBlock`` over rms_norm_block_fwd /
+rms_norm_block_bwd.
 """
 from __future__ import annotations
 
@@ -118,7 +120,8 @@ class RMSNormError(RuntimeError):
 
 _lib: Optional[ctypes.CDLL] = None
 # The usual calls of the newer entry points without ctypes' cost (binding.cpp);
-# None before load_library, or where it was not built.
+# None before load_library, or where it was not built, or against another
+# PyTorch: the calls then take ctypes.
 _binding = None
 
 
@@ -127,8 +130,13 @@ def _load_binding(lib: ctypes.CDLL) -> None:
     if not os.path.exists(BINDING_PATH):
         return
     spec = importlib.util.spec_from_file_location("bwd_rms_norm_gb300._binding", BINDING_PATH)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
+    try:
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError:                 # built against another PyTorch
+        return
+    if module.built_for != torch.__version__:
+        return
     module.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.rms_norm_block_fwd, lib.rms_norm_block_bwd, lib.rms_norm_block_bwd_workspace_size,
         lib.rms_norm_grad_norm, lib.rms_norm_grad_clip, lib.rms_norm_grad_workspace_size)))
@@ -805,9 +813,29 @@ def _block_sizes(x, post_gamma, gate, next_gamma) -> Tuple[int, int, int]:
     if gate.dim() < 1 or gate.shape[-1] != hidden:
         raise RuntimeError(f"gate must have {hidden} columns, not shape {tuple(gate.shape)}")
     gate_rows = gate.numel() // hidden if hidden > 0 else 0
-    if gate_rows < 1 or rows % gate_rows or gate_rows > max(rows, 1):
+    if rows == gate_rows == 0:
+        return rows, hidden, 0
+    if gate_rows < 1 or rows % gate_rows:
         raise RuntimeError(f"gate has {gate_rows} rows, which do not divide the {rows} rows of x")
+    if gate_rows > 1 and x.dim() > 2 and _broadcasts_otherwise(gate.shape[:-1], x.shape[:-1]):
+        raise RuntimeError(f"gate of shape {tuple(gate.shape)} would repeat over dimensions of x "
+                           f"{tuple(x.shape)} before its own, but a gate row is for consecutive "
+                           "rows: expand it, or give it x's leading dimensions")
     return rows, hidden, gate_rows
+
+
+def _broadcasts_otherwise(gate, x) -> bool:
+    """Whether these leading dimensions of a gate broadcast to x's, by the
+    usual rules, and not to runs of consecutive rows."""
+    gate = (1,) * (len(x) - len(gate)) + tuple(gate)
+    if len(gate) > len(x) or any(a not in (1, b) for a, b in zip(gate, x)):
+        return False
+    repeated = False
+    for a, b in zip(gate, x):
+        if a > 1 and repeated:
+            return True
+        repeated = repeated or a < b
+    return False
 
 
 def _check_block(x, stream_name, stream, post_gamma, gate, next_gamma) -> None:
@@ -837,8 +865,9 @@ def rms_norm_block_fwd(x: torch.Tensor, residual: torch.Tensor,
     has its shape and its dtype, or float32.  Either gamma may be None (no norm
     of x; no y).  ``gate`` is ``[hidden]``, or ``[..., hidden]`` with a number
     of rows that divides x's: each run of rows / gate rows consecutive rows of
-    x uses one.  Returns ``(r, y, rstd_post, rstd_next)``, None for what a
-    missing norm would give."""
+    x uses one (a gate that would broadcast to x in another way is refused).
+    Returns ``(r, y, rstd_post, rstd_next)``, None for what a missing norm
+    would give; an output given must not share memory with an input."""
     lib = load_library()
     if _binding is not None and stream is None and (
             residual_out is y is rstd_post is rstd_next is None):
@@ -1100,6 +1129,9 @@ def rms_norm_grad_clip(grads, max_norm: float, eps: float = 1e-6, out=None,
                                     _ptr(workspace), size, handle)
     if st != RMSN_OK:
         raise RMSNormError("rms_norm_grad_clip", st)
+    for t in outs:                      # autograd's check of saved tensors
+        if not t.is_inference():
+            torch.autograd.graph.increment_version(t)
     return norm
 
 
@@ -1194,7 +1226,9 @@ def rms_norm_block(x: torch.Tensor, residual: torch.Tensor,
                    offset: int = 0, residual_scale: float = 1.0, branch_scale: float = 1.0):
     """Differentiable ``rms_norm_block_fwd``: returns ``(r, y)``, or ``r``
     alone without ``next_weight``.  Differentiable in x, the residual, both
-    weights and the gate."""
+    weights and the gate.  A training step captured into a CUDA graph is, as
+    any with autograd, warmed up on a side stream, with no eager graph of the
+    same leaves alive during the capture."""
     return RMSNormBlockFunction.apply(x, residual, post_weight, gate, next_weight, eps, offset,
                                       residual_scale, branch_scale)
 

@@ -59,7 +59,8 @@ def _build_binding() -> None:
     root = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     tmp = BINDING_PATH + ".tmp"
-    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I", INCLUDE,
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+           f'-DBUILT_FOR="{torch.__version__}"', "-I", INCLUDE,
            "-I", os.path.join(root, "include"),
            "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
            "-I", sysconfig.get_paths()["include"], "-I", cuda,

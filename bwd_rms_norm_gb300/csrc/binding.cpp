@@ -90,6 +90,12 @@ bool usual_call(const Arg& x, const Arg& res, const Arg& post, const Arg& gate, 
       return false;
     c->gate_rows = gate.t->numel() / c->hidden;
     if (c->gate_rows < 1 || c->rows % c->gate_rows != 0) return false;
+    // rows for runs of x's rows for certain (a gate may broadcast otherwise)
+    const int64_t nx = x.t->dim(), ng = gate.t->dim();
+    if (c->gate_rows > 1 && nx != 2 &&
+        !(nx == 3 && ng == 3 && gate.t->size(0) == x.t->size(0)) &&
+        !(nx == 3 && ng == 2 && gate.t->size(0) != x.t->size(1)))
+      return false;
   } else if (!gate.usual) {
     return false;
   }
@@ -273,12 +279,23 @@ PyObject* grad_clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const List& out = in_place ? g : o;
     at::Tensor norm = at::empty({}, floats(*g.first)), ws;
     if (!total) ws = bytes(*g.first, entry.grad_ws(count));
+    PyObject* result = wrap(norm);  // before the call: in place there is no second one
+    if (!result) return nullptr;
     const int st = entry.grad_clip(
         g.ptrs.data(), g.numels.data(), g.codes.data(), out.ptrs.data(), out.codes.data(), count,
         (float)v[0], (float)v[1], static_cast<const float*>(total.ptr()),
         static_cast<float*>(norm.data_ptr()), ptr(ws), ws.defined() ? (size_t)ws.numel() : 0,
         c10::cuda::getCurrentCUDAStream(device).stream());
-    return st == RMSN_OK ? wrap(norm) : nullptr;
+    if (st != RMSN_OK) {
+      Py_DECREF(result);
+      return nullptr;
+    }
+    PyObject* written = in_place ? a[0] : a[3];
+    for (int64_t i = 0; i < count; ++i) {  // autograd's check of saved tensors
+      const at::Tensor& t = THPVariable_Unpack(PySequence_Fast_GET_ITEM(written, (Py_ssize_t)i));
+      if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+    }
+    return result;
   });
 }
 
@@ -311,4 +328,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__binding() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", BUILT_FOR) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -120,6 +120,28 @@ int max_clusters(const void* func, int block, size_t smem, int cluster, int sms)
 
 using namespace rmsn;
 
+namespace {
+// An argument's memory; empty where it is not given.
+struct Span {
+  uintptr_t lo, hi;
+  Span(const void* p, size_t bytes)
+      : lo(reinterpret_cast<uintptr_t>(p)), hi(p ? reinterpret_cast<uintptr_t>(p) + bytes : 0) {}
+};
+
+// Whether an output shares memory with an input or with another output: the
+// kernels read ahead of what they write, and some read a row again.
+template <int NO, int NI>
+bool overlap(const Span (&outs)[NO], const Span (&ins)[NI]) {
+  for (int i = 0; i < NO; ++i) {
+    for (int k = i + 1; k < NO; ++k)
+      if (outs[i].lo < outs[k].hi && outs[k].lo < outs[i].hi) return true;
+    for (int k = 0; k < NI; ++k)
+      if (outs[i].lo < ins[k].hi && ins[k].lo < outs[i].hi) return true;
+  }
+  return false;
+}
+}  // namespace
+
 extern "C" {
 
 int rms_norm_fwd(const void* x, const void* gamma, void* y, float* rstd, int64_t rows,
@@ -574,6 +596,15 @@ int rms_norm_block_fwd(const void* x, const void* residual, const void* gamma_po
       (gamma_next && (!y || !rstd_next)))
     return RMSN_ERR_NULL;
   const int s = elem_bytes(dtype);
+  const size_t row = (size_t)hidden * s, all = (size_t)rows * row;
+  const size_t all_res = (size_t)rows * hidden * elem_bytes(residual_dtype);
+  const size_t per_row = (size_t)rows * sizeof(float);
+  const Span outs[] = {{residual_out, all_res}, {gamma_next ? y : nullptr, all},
+                       {gamma_post ? rstd_post : nullptr, per_row},
+                       {gamma_next ? rstd_next : nullptr, per_row}};
+  const Span ins[] = {{x, all}, {residual, all_res}, {gamma_post, row}, {gamma_next, row},
+                      {gate, gate ? (size_t)gate_rows * row : 0}};
+  if (overlap(outs, ins)) return RMSN_ERR_ARG;
   BlockFwdArgs a;
   a.x = x;
   a.res = residual;
@@ -647,6 +678,18 @@ int rms_norm_block_bwd(const void* dy, const void* dresidual_out, const void* x,
       rms_norm_block_bwd_workspace_size(rows, hidden, gate ? gate_rows : 0))
     return RMSN_ERR_WORKSPACE;
   const int s = elem_bytes(dtype);
+  const size_t row = (size_t)hidden * s, all = (size_t)rows * row;
+  const size_t all_res = (size_t)rows * hidden * elem_bytes(residual_dtype);
+  const size_t sums = (size_t)hidden * sizeof(float), per_row = (size_t)rows * sizeof(float);
+  const Span outs[] = {{dx, all}, {dresidual, all_res}, {gamma_post ? dgamma_post : nullptr, sums},
+                       {gate ? dgate : nullptr, gate ? (size_t)gate_rows * sums : 0},
+                       {gamma_next ? dgamma_next : nullptr, sums}, {workspace, workspace_bytes}};
+  const Span ins[] = {{gamma_next ? dy : nullptr, all}, {dresidual_out, all_res}, {x, all},
+                      {gamma_next ? residual_out : nullptr, all_res}, {gamma_post, row},
+                      {gamma_next, row}, {gate, gate ? (size_t)gate_rows * row : 0},
+                      {gamma_post ? rstd_post : nullptr, per_row},
+                      {gamma_next ? rstd_next : nullptr, per_row}};
+  if (overlap(outs, ins)) return RMSN_ERR_ARG;
   BlockBwdArgs a;
   a.dy = gamma_next ? dy : nullptr;
   a.dr = dresidual_out;

@@ -346,9 +346,10 @@ int group_norm_bwd(const void* dy, const void* x, const void* gamma,
  * once, when they are stored: y is formed from the unrounded r.  rstd_post
  * and rstd_next are fp32 [rows], written for the norms that are given, for
  * the backward.  Rows whose fp32 sum of squares overflows are handled as in
- * rms_norm_fwd.  Outputs must not overlap inputs.  Errors as rms_norm_fwd;
- * RMSN_ERR_SHAPE also for gate_rows that do not divide rows, RMSN_ERR_ARG for
- * a scale that is not finite.  rows == 0 enqueues nothing.
+ * rms_norm_fwd.  Errors as rms_norm_fwd; RMSN_ERR_SHAPE also for gate_rows
+ * that do not divide rows, RMSN_ERR_ARG for a scale that is not finite and
+ * for an output that shares memory with an input or another output.  rows ==
+ * 0 enqueues nothing.
  */
 int rms_norm_block_fwd(const void* x, const void* residual, const void* gamma_post,
                        const void* gate, int64_t gate_rows, const void* gamma_next,
@@ -380,7 +381,8 @@ size_t rms_norm_block_bwd_workspace_size(int64_t rows, int64_t hidden, int64_t g
  * GPU's SM count and the SM budget: repeated calls give the same bits.
  * `workspace`: rms_norm_block_bwd_workspace_size bytes of device scratch,
  * 16-byte aligned, clobbered; calls that may run at the same time need their
- * own.  rows == 0 zero-fills the sums.
+ * own.  An output or workspace that shares memory with another argument is
+ * refused (RMSN_ERR_ARG).  rows == 0 zero-fills the sums.
  */
 int rms_norm_block_bwd(const void* dy, const void* dresidual_out, const void* x,
                        const void* residual_out, const void* gamma_post,

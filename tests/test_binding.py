@@ -116,3 +116,52 @@ def test_declines_on_the_gpu(L):
     assert b.grad_clip([x, x], 1.0, 1e-6, None, None) is None
     with pytest.raises(L.RMSNormError):
         L.rms_norm_grad_clip([x, x], 1.0)
+
+
+def test_built_for_this_pytorch(L):
+    assert L._binding.built_for == torch.__version__
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("direct", [True, False])
+def test_scaling_is_seen_by_autograd(L, other_way, direct):
+    """A tensor that a graph has saved and that is scaled in place is noticed."""
+    clip = L.rms_norm_grad_clip if direct else (
+        lambda *a, **k: other_way(L.rms_norm_grad_clip, *a, **k))
+    w = torch.ones(8, device="cuda", requires_grad=True)
+    t = torch.full((8,), 3.0, device="cuda")
+    loss = (w * t).sum()
+    clip([t], 1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    out = torch.empty_like(t)
+    v = out._version
+    clip([t], 1.0, out=[out])
+    assert out._version > v
+    with torch.inference_mode():
+        u = torch.full((8,), 3.0, device="cuda")
+    clip([u], 1.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("x,gate", [((4, 6, 96), (4, 1, 96)), ((4, 6, 96), (4, 96)),
+                                    ((2, 3, 4, 96), (2, 3, 1, 96)), ((3, 4, 96), (3, 4, 96))])
+def test_gates_of_leading_dimensions(L, x, gate):
+    a, r, g = (torch.randn(s, device="cuda") for s in (x, x, gate))
+    w = torch.ones(96, device="cuda")
+    got = L.rms_norm_block_fwd(a, r, None, g, w)[0]
+    full = g.reshape(gate[:-1] + (1,) * (len(x) - len(gate)) + (96,))
+    assert torch.allclose(got, r + full * a, rtol=1e-6, atol=1e-6)
+
+
+@pytest.mark.gpu
+def test_no_rows_and_no_gate_rows(L):
+    e = lambda *s: torch.empty(*s, device="cuda")  # noqa: E731
+    w = torch.ones(96, device="cuda")
+    for gate in (e(0, 1, 96), e(4, 96), e(96)):
+        x = e(0, 5, 96)
+        r, y, r1, r2 = L.rms_norm_block_fwd(x, x, w, gate, w)
+        assert r.shape == y.shape == x.shape
+        got = L.rms_norm_block_bwd(x, x, x, r, r1, r2, w, gate, w)
+        assert got[3].shape == gate.shape
+        assert all(torch.count_nonzero(v).item() == 0 for v in got)

@@ -443,7 +443,7 @@ def test_module_trains_in_a_stack(L):
 # (several to a stage) to ones over several CTAs, tensors whose last row ends
 # inside 16 bytes
 ODD = [(65601, 65), (32800, 132), (16401, 257), (4203, 1001), (1031, 2050), (514, 4093),
-       (259, 8191), (177, 12001), (133, 16002), (129, 16389)]
+       (259, 8191), (177, 12001), (133, 16002), (129, 16389), (128, 65535)]
 
 
 @pytest.mark.parametrize("rows,hidden", ODD)
@@ -505,4 +505,11 @@ def test_unaligned_weights_alone(L, rows, hidden, gates):
 @pytest.mark.parametrize("hidden", [256, 77])
 def test_gate_rows_of_few_segments(L, rows, gates, hidden):
     d, g = make(rows, hidden, "f32", "f32", True, gates, True, seed=7)
+    run_and_check(L, d, g)
+
+
+@pytest.mark.parametrize("rows,hidden", [(3, 65536), (200, 65536), (5, 65535), (2, 1), (300, 1)])
+@pytest.mark.parametrize("dtype,res", [("bf16", "f32"), ("f32", "f32")])
+def test_widest_and_narrowest(L, rows, hidden, dtype, res):
+    d, g = make(rows, hidden, dtype, res, True, 1, True, seed=8)
     run_and_check(L, d, g)

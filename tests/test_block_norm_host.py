@@ -151,3 +151,45 @@ def test_module_host_side(L):
         L.RMSNormBlock(16, gate_init=1.0)(torch.zeros(2, 16), torch.zeros(2, 16), torch.ones(16))
     with pytest.raises(RuntimeError, match="CUDA"):
         m(torch.zeros(3, 16, dtype=torch.bfloat16), torch.zeros(3, 16, dtype=torch.bfloat16))
+
+
+def apart(n):
+    return {k: ctypes.c_void_p(0x100000 * (i + 1)) for i, k in enumerate(n)}
+
+
+FWD = ("x", "res", "post", "gate", "next", "r", "y", "r1", "r2")
+BWD = ("dy", "dr", "x", "r", "post", "gate", "next", "r1", "r2", "dx", "dres", "dpost", "dgate",
+       "dnext", "ws")
+
+
+@pytest.mark.parametrize("call,names,outs", [
+    (fwd, FWD, ("r", "y", "r1", "r2")),
+    (bwd, BWD, ("dx", "dres", "dpost", "dgate", "dnext", "ws"))])
+def test_outputs_that_share_memory(L, call, names, outs):
+    """Every pair of an output with another argument: at the same address, and
+    where the argument's last byte is the output's first."""
+    size = dict(x=512, res=512, post=128, gate=256, next=128, r=512, y=512, r1=16, r2=16, dy=512,
+                dr=512, dx=512, dres=512, dpost=256, dgate=512, dnext=256, ws=0)
+    for o in outs:
+        for k in names:
+            if k == o:
+                continue
+            at = apart(names)
+            at[k] = at[o]
+            assert call(L, **at) == 8, (o, k)
+            if k != "ws" and o != "ws":
+                at[o] = ctypes.c_void_p(at[k].value + size[k] - 4)
+                assert call(L, **at) == 8, (o, k)
+
+
+@pytest.mark.parametrize("x,gate,runs", [
+    ((4, 6, 8), (4, 8), True), ((4, 6, 8), (4, 1, 8), True), ((4, 6, 8), (4, 6, 8), True),
+    ((4, 6, 8), (8,), True), ((4, 6, 8), (1, 1, 8), True), ((4, 6, 8), (24, 8), True),
+    ((1, 6, 8), (1, 6, 8), True), ((4, 1, 8), (4, 8), True), ((12, 8), (4, 8), True),
+    ((4, 6, 8), (1, 6, 8), False), ((4, 6, 8), (6, 8), False), ((4, 4, 8), (4, 8), False),
+    ((2, 3, 4, 8), (2, 1, 4, 8), False), ((2, 3, 4, 8), (2, 3, 1, 8), True),
+    ((2, 3, 4, 8), (2, 3, 8), True), ((2, 3, 3, 8), (3, 1, 8), False)])
+def test_gates_that_broadcast_otherwise(L, x, gate, runs):
+    t = good(x=torch.zeros(x), residual=torch.zeros(x), gate=torch.ones(gate))
+    with pytest.raises(RuntimeError, match="CUDA" if runs else "repeat|divide"):
+        L.rms_norm_block_fwd(**t)
