@@ -42,7 +42,8 @@ namespace {
 // (block_fwd_odd_pays), tensors that do not start on 16 bytes.
 // ---------------------------------------------------------------------------
 
-template <typename T, typename TS, int NT>
+// HELD: columns of a row that stay in a thread's registers.
+template <typename T, typename TS, int NT, int HELD>
 __global__ void __launch_bounds__(NT) block_fwd_loop(
     const T* __restrict__ x, const TS* __restrict__ res, const T* __restrict__ gamma_post,
     const T* __restrict__ gate, const T* __restrict__ gamma_next, TS* __restrict__ res_out,
@@ -52,17 +53,32 @@ __global__ void __launch_bounds__(NT) block_fwd_loop(
   pdl_trigger();
   pdl_wait();
   int parity = 0;
+  // f(k, j) for the thread's columns that are held, g(j) for its others
+  auto each = [&](auto f, auto g) {
+#pragma unroll
+    for (int k = 0; k < HELD; ++k)
+      if ((int)threadIdx.x + k * NT < hidden) f(k, (int)threadIdx.x + k * NT);
+    for (int j = threadIdx.x + HELD * NT; j < hidden; j += NT) g(j);
+  };
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
     const T* xr = x + row * hidden;
     const TS* sr = res + row * hidden;
     const T* gr = gate == nullptr ? nullptr : gate + row / rows_per_gate * hidden;
+    float xv[HELD + 1], r[HELD + 1];
+#pragma unroll
+    for (int k = 0; k < HELD; ++k) xv[k] = r[k] = 0.f;
+    float ss = 0.f;
+    each([&](int k, int j) {
+      xv[k] = Traits<T>::to_f(xr[j]);
+      r[k] = a * Traits<TS>::to_f(sr[j]);
+    }, [&](int j) {
+      const float v = Traits<T>::to_f(xr[j]);
+      ss = fmaf(v, v, ss);
+    });
     float rs1 = 1.f;
     if (gamma_post != nullptr) {
-      float ss = 0.f;
-      for (int j = threadIdx.x; j < hidden; j += NT) {
-        const float v = Traits<T>::to_f(xr[j]);
-        ss = fmaf(v, v, ss);
-      }
+#pragma unroll
+      for (int k = 0; k < HELD; ++k) ss = fmaf(xv[k], xv[k], ss);
       ss = block_sum(ss, red, parity);
       parity ^= 1;
       rs1 = rstd_of(ss / (float)hidden, eps);
@@ -73,18 +89,24 @@ __global__ void __launch_bounds__(NT) block_fwd_loop(
       }
       if (threadIdx.x == 0) rstd_post[row] = rs1;
     }
-    auto stream = [&](int j) {
+    auto weight = [&](int j) {
       float w = b;
       if (gr != nullptr) w *= Traits<T>::to_f(gr[j]);
       if (gamma_post != nullptr) w *= Traits<T>::to_f(gamma_post[j]) + off;
-      return fmaf(w, Traits<T>::to_f(xr[j]) * rs1, a * Traits<TS>::to_f(sr[j]));
+      return w;
     };
-    float ss = 0.f;
-    for (int j = threadIdx.x; j < hidden; j += NT) {
-      const float r = stream(j);
-      ss = fmaf(r, r, ss);
-      res_out[row * hidden + j] = Traits<TS>::from_f(r);
-    }
+    auto stream = [&](int j) {
+      return fmaf(weight(j), Traits<T>::to_f(xr[j]) * rs1, a * Traits<TS>::to_f(sr[j]));
+    };
+    ss = 0.f;
+    auto put = [&](int j, float v) {
+      ss = fmaf(v, v, ss);
+      res_out[row * hidden + j] = Traits<TS>::from_f(v);
+    };
+    each([&](int k, int j) {
+      r[k] = fmaf(weight(j), xv[k] * rs1, r[k]);
+      put(j, r[k]);
+    }, [&](int j) { put(j, stream(j)); });
     if (gamma_next == nullptr) continue;
     ss = block_sum(ss, red, parity);
     parity ^= 1;
@@ -100,9 +122,10 @@ __global__ void __launch_bounds__(NT) block_fwd_loop(
       rs2 = rstd_rescaled(s2, hidden, eps);
     }
     if (threadIdx.x == 0) rstd_next[row] = rs2;
-    for (int j = threadIdx.x; j < hidden; j += NT)
-      y[row * hidden + j] =
-          Traits<T>::from_f((stream(j) * rs2) * (Traits<T>::to_f(gamma_next[j]) + off));
+    auto out = [&](int j, float v) {
+      y[row * hidden + j] = Traits<T>::from_f((v * rs2) * (Traits<T>::to_f(gamma_next[j]) + off));
+    };
+    each([&](int k, int j) { out(j, r[k]); }, [&](int j) { out(j, stream(j)); });
   }
 }
 
@@ -319,12 +342,15 @@ cudaError_t launch_fwd_t(const BlockFwdArgs& a, cudaStream_t s) {
                          static_cast<T*>(a.y), a.rstd_post, a.rstd_next, a.rows, a.rows_per_gate,
                          a.hidden, a.res_scale, a.branch_scale, a.eps, a.offset ? 1.f : 0.f);
   };
-  // bf16, 128 / 256 / 1024 threads: 64 x 1001 4.3, 3.7, 3.4 us; 64 x 8191 13.5,
-  // 11.1, 6.5; 4096 x 257 9.8, 15.4, 65; 4096 x 1001 18.0, 24.4, 88; 4096 x
-  // 4097 53, 49, 128
-  if (a.rows <= sms && a.hidden > 512) return go(block_fwd_loop<T, TS, 1024>, 1024);
-  if (a.hidden <= 1024) return go(block_fwd_loop<T, TS, 128>, 128);
-  return go(block_fwd_loop<T, TS, 256>, 256);
+  // bf16, 128 / 256 / 1024 threads with nothing held: 64 x 1001 4.3, 3.7, 3.4
+  // us; 64 x 8191 13.5, 11.1, 6.5; 4096 x 257 9.8, 15.4, 65; 4096 x 4097 53, 49,
+  // 128.  Held / not: 1024 x 257 3.8 / 4.7, 1024 x 1001 5.0 / 7.6, 4096 x 1500
+  // 29 / 32, but 4096 x 33 9.9 / 7.2 and 4096 x 4097 58 / 47.
+  if (a.rows <= sms && a.hidden > 512) return go(block_fwd_loop<T, TS, 1024, 0>, 1024);
+  if (a.hidden <= 128) return go(block_fwd_loop<T, TS, 128, 0>, 128);
+  if (a.hidden <= 1024) return go(block_fwd_loop<T, TS, 128, 8>, 128);
+  if (a.hidden <= 2048) return go(block_fwd_loop<T, TS, 256, 8>, 256);
+  return go(block_fwd_loop<T, TS, 256, 0>, 256);
 }
 
 template <typename T, typename TS>
