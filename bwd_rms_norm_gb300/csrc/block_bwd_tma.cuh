@@ -584,9 +584,9 @@ bool try_bwd(const BlockBwdArgs& a, BlockBwdParams& p, int* units, cudaStream_t 
                 &nv8, &smem))
     return false;
   p.period = EDGE ? row_period(a.hidden, 16 / (int)sizeof(T)) : 1;
-  auto go = [&](auto kern) {
-    *err = allow_smem(kern, smem);
-    if (*err == cudaSuccess) *err = allow_cluster((const void*)kern, sp.cs);
+  auto go = [&](auto which) {
+    constexpr auto kern = decltype(which)::value;
+    *err = allow<kern>(dev, kSmemBudget - sizeof(BwdShared));
     if (*err != cudaSuccess) return;
     const int threads = 32 * (1 + sp.reducers + sp.teams * sp.wpt);
     int64_t n = sp.cs == 1 ? sms : max_clusters((const void*)kern, threads, smem, sp.cs, sms);
@@ -600,14 +600,14 @@ bool try_bwd(const BlockBwdArgs& a, BlockBwdParams& p, int* units, cudaStream_t 
   };
   if (dr || !NEXT) {
     if (nv8 == 1)
-      go(block_bwd_tma<T, TS, POST, NEXT, true, 8 / E, EDGE>);
+      go(Kern<block_bwd_tma<T, TS, POST, NEXT, true, 8 / E, EDGE>>{});
     else
-      go(block_bwd_tma<T, TS, POST, NEXT, true, 16 / E, EDGE>);
+      go(Kern<block_bwd_tma<T, TS, POST, NEXT, true, 16 / E, EDGE>>{});
   } else {
     if (nv8 == 1)
-      go(block_bwd_tma<T, TS, POST, true, false, 8 / E, EDGE>);
+      go(Kern<block_bwd_tma<T, TS, POST, true, false, 8 / E, EDGE>>{});
     else
-      go(block_bwd_tma<T, TS, POST, true, false, 16 / E, EDGE>);
+      go(Kern<block_bwd_tma<T, TS, POST, true, false, 16 / E, EDGE>>{});
   }
   return true;
 }

@@ -483,9 +483,8 @@ bool try_fwd(const BlockFwdArgs& a, cudaStream_t s, cudaError_t* err) {
   p.stride = sh.stride;
   p.lanes = sh.lanes;
   p.period = EDGE ? row_period(a.hidden, 16 / (int)sizeof(T)) : 1;
-  auto kern = block_fwd_tma<T, TS, POST, NEXT, EDGE>;
-  *err = allow_smem(kern, sh.smem);
-  if (*err == cudaSuccess) *err = allow_cluster((const void*)kern, sh.cs);
+  constexpr auto kern = block_fwd_tma<T, TS, POST, NEXT, EDGE>;
+  *err = allow<kern>(dev, kSmemBudget - sizeof(FwdShared));
   if (*err != cudaSuccess) return true;
   const int threads = 32 * (1 + sh.teams * sh.wpt);
   int64_t units = sh.cs == 1 ? (int64_t)sms * sh.ctas
