@@ -109,6 +109,18 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
   const int64_t of = EDGE ? units / P : units, idx = EDGE ? unit / P : unit;
   const int64_t i0 = idx * ours / of, i1 = (idx + 1) * ours / of;
   const bool has_x = POST || sp.read_x;
+  if (!EDGE && threadIdx.x == 0) {  // the first rows into L2 (prefetch_l2)
+    int64_t n = K * kFirstStages;
+    if (n > i1 - i0) n = i1 - i0;
+    for (int64_t i = i0; i < i0 + n; i += cs == 1 ? n : 1) {  // consecutive, or this CTA's part
+      const int64_t from = i * p.hidden + col0;
+      const uint32_t m = (uint32_t)((cs == 1 ? n : 1) * pitch);
+      if (has_x) prefetch_l2(static_cast<const T*>(p.x) + from, m * (uint32_t)sizeof(T));
+      if (NEXT) prefetch_l2(static_cast<const TS*>(p.r) + from, m * (uint32_t)sizeof(TS));
+      if (NEXT) prefetch_l2(static_cast<const T*>(p.dy) + from, m * (uint32_t)sizeof(T));
+      if (DR) prefetch_l2(static_cast<const TS*>(p.dr) + from, m * (uint32_t)sizeof(TS));
+    }
+  }
   float4* plane1 = reinterpret_cast<float4*>(smem);
   float4* plane2 = POST ? plane1 + pitch / 4 : plane1;
   unsigned char* ring = reinterpret_cast<unsigned char*>(NEXT ? plane2 + pitch / 4 : plane2);

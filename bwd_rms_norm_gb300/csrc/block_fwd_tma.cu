@@ -69,6 +69,13 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) block_fwd_tma(const B
     const int64_t left = EDGE ? (p.rows - first + P - 1) / P : p.rows - first;
     return left < 0 ? 0 : left < K ? (int)left : K;
   };
+  if (!EDGE && threadIdx.x == 0)  // the first rows into L2 (prefetch_l2)
+    for (int k = 0; k < kFirstStages && k < nst; ++k) {
+      const int64_t first = first_row(k), at = first * p.hidden + col0;
+      const uint32_t n = (uint32_t)(rows_from(first) * pitch);
+      prefetch_l2(static_cast<const T*>(p.x) + at, n * (uint32_t)sizeof(T));
+      prefetch_l2(static_cast<const TS*>(p.res) + at, n * (uint32_t)sizeof(TS));
+    }
   float4* plane1 = reinterpret_cast<float4*>(smem);
   float4* plane2 = plane1 + pitch / 4;
   unsigned char* ring = reinterpret_cast<unsigned char*>(NEXT ? plane2 + pitch / 4 : plane2);
@@ -388,7 +395,9 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) block_fwd_tma(const B
 }
 
 // The forward's teams and stages for `rows` rows on `sms` SMs.  The row is
-// split over as few CTAs as leave two stages beside the weights.
+// split over as few CTAs as leave two stages beside the weights.  (The times
+// that compare shapes were taken without kFirstStages, which takes about 1 us
+// off each.)
 struct FwdShape {
   int teams, wpt, cs, stages, stage_rows, stride, lanes, ctas;  // ctas: on an SM
   size_t smem;
