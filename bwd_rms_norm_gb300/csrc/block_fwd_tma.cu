@@ -430,6 +430,12 @@ bool fwd_shape(int64_t rows, int hidden, int sms, int row_elem, int planes, bool
       // teams of four warps.
       s->wpt = 1;
       s->teams = kMaxWarps / s->ctas;
+      // Rows of 12 KB and more (x and res): ten at once, not what the ring
+      // holds: 32768 x 4096 bf16 179 -> 168 us, 32768 x 3584 162 -> 146, 32768
+      // x 2048 bf16 under fp32 138 -> 132, 4096 x 4096 the same; narrower ones
+      // lose by it (65536 x 2048 168 -> 188), and odd ones (32768 x 4097 230 ->
+      // 236).
+      if (!edge && row >= 12 * 1024) s->teams = 10;
       // several narrow rows to a stage, as long as every team has its own
       while (s->stage_rows * row < 8192 && mine >= 2 * s->ctas * s->teams * s->stage_rows)
         s->stage_rows *= 2;
