@@ -542,8 +542,12 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
   if (cs > 1) cluster_sync();  // no CTA leaves while a peer may write to its slots
 }
 
-// The backward's roles and stages, over as few CTAs as leave three stages
-// (else two) beside the reducers' weights.
+// The backward's roles and stages, over as few CTAs as leave three stages, or
+// four where the row's sums are exchanged (else one less), beside the reducers'
+// weights, and three reducers beside the appliers.  (8192 rows, bf16: 6656
+// columns with two reducers 149 us, over two CTAs 113; 12288 over two with three
+// stages 269, over four with four 218; but 6144 over one with three 108, over two
+// 109, and 3584 fp32 96 and 108.)
 template <typename F>
 bool bwd_pick(int64_t rows, int hidden, int sms, int align, int elems, int planes,
               bool edge, F stage_bytes, BwdShape* s, int* nv8, size_t* smem) {
@@ -555,7 +559,7 @@ bool bwd_pick(int64_t rows, int hidden, int sms, int align, int elems, int plane
       *nv8 = cols < 512 ? 1 : 2;
       s->cs = cs;
       s->wpt = (cols + *nv8 * 256 - 1) / (*nv8 * 256);
-      if (s->wpt > kBwdWarps - 3) continue;
+      if (s->wpt > kBwdWarps - 4) continue;
       s->teams = cs > 1 || s->wpt > 4 ? 1 : 8 / s->wpt;
       // narrow rows: as many to a stage as make it a wide row's, if there are
       // enough of them for every CTA to fill its ring
@@ -568,7 +572,7 @@ bool bwd_pick(int64_t rows, int hidden, int sms, int align, int elems, int plane
       s->stride = (stage_bytes(s->stage_rows, cols) + 127) / 128 * 128;
       s->stages = (budget - over) / s->stride;
       if (s->stages > kBwdStages) s->stages = kBwdStages;
-      if (s->stages < least) continue;
+      if (s->stages < (cs > 1 ? least + 1 : least)) continue;
       s->reducers = kBwdWarps - 1 - s->teams * s->wpt;
       if (s->reducers > s->stages) s->reducers = s->stages;
       s->stages -= s->stages % s->reducers;  // a stage is always the same reducer's
