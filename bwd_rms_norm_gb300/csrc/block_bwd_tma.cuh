@@ -560,11 +560,20 @@ bool bwd_pick(int64_t rows, int hidden, int sms, int align, int elems, int plane
       s->cs = cs;
       s->wpt = (cols + *nv8 * 256 - 1) / (*nv8 * 256);
       if (s->wpt > kBwdWarps - 4) continue;
+      // Teams share a stage, which then is as many rows: up to 48 KB of them
+      // (fp32, 32768 x 2048 336 -> 206 us with one team), and only where a CTA
+      // has two such stages or more, or its rows would wait for one reducer
+      // (256 x 1024 fp32 9.2 -> 7.5 us, 2048 x 512 bf16 12.5 -> 10.7).
       s->teams = cs > 1 || s->wpt > 4 ? 1 : 8 / s->wpt;
-      // narrow rows: as many to a stage as make it a wide row's, if there are
-      // enough of them for every CTA to fill its ring
+      while (s->teams > 1 && (stage_bytes(s->teams, cols) > 48 * 1024 ||
+                              rows <= (int64_t)2 * s->teams * sms))
+        s->teams /= 2;
+      // narrow rows: as many to a stage as make it a wide row's (40 KB: fp32,
+      // 65536 x 512 128 -> 108 us against 64 KB), if there are enough of them
+      // for every CTA to fill its ring
       s->stage_rows = s->teams;
-      while (cs == 1 && 2 * s->stage_rows <= kBwdRows && 2 * s->stage_rows * cols <= 4096 &&
+      while (cs == 1 && 2 * s->stage_rows <= kBwdRows &&
+             stage_bytes(2 * s->stage_rows, cols) <= 40 * 1024 &&
              rows >= (int64_t)8 * s->stage_rows * sms)
         s->stage_rows *= 2;
       s->lanes = cs == 1 && cols / elems <= kNarrowGroups && s->stage_rows > 1 ? kNarrowLanes : 32;
