@@ -513,3 +513,26 @@ def test_gate_rows_of_few_segments(L, rows, gates, hidden):
 def test_widest_and_narrowest(L, rows, hidden, dtype, res):
     d, g = make(rows, hidden, dtype, res, True, 1, True, seed=8)
     run_and_check(L, d, g)
+
+
+# which kernels a shape runs: one that falls to a slower family keeps every
+# comparison of results green
+@pytest.mark.parametrize("rows,hidden,gates,fwd,bwd", [
+    (8, 4096, 0, "block_fwd_tma", "block_bwd_tma"), (512, 128, 1, "block_fwd_tma", "block_bwd_tma"),
+    (300, 4096, 3, "block_fwd_tma", "block_bwd_tma"), (64, 65536, 1, "block_fwd_tma",
+                                                       "block_bwd_tma"),
+    (300, 8200, 1, "block_fwd_tma", "block_bwd_tma"), (1100, 4097, 1, "block_fwd_tma",
+                                                       "block_bwd_tma"),
+    (1000, 1001, 8, "block_fwd_loop", "block_bwd_loop"), (777, 1001, 0, "block_fwd_loop",
+                                                          "block_bwd_tma"),
+    (8, 4097, 0, "block_fwd_loop", "block_bwd_loop"), (1100, 33, 1, "block_fwd_loop",
+                                                       "block_bwd_loop")])
+def test_kernels_a_shape_runs(L, rows, hidden, gates, fwd, bwd):
+    d, g = make(rows, hidden, "bf16", "bf16", True, gates, True)
+    dc, gc = cuda(d), cuda(g)
+    out = L.rms_norm_block_fwd(**dc)
+    assert fwd in L.last_kernels()[0], L.last_kernels()
+    L.rms_norm_block_bwd(gc["dy"], gc["dresidual_out"], dc["x"], out[0], out[2], out[3],
+                         dc["post_gamma"], dc["gate"], dc["next_gamma"])
+    names = L.last_kernels()
+    assert len(names) == 2 and bwd in names[0] and "block_bwd_sums" in names[1], names
