@@ -249,14 +249,16 @@ __device__ __forceinline__ GradNorm norm_of(const GradSum* __restrict__ partial,
   return {f, d - (f - r)};
 }
 
-// min(1, max_norm / (norm + eps)), 1 where the norm is not finite.
+// min(1, max_norm / (norm + eps)), 1 where the norm is not finite; the quotient
+// corrected by what its division and the norm's rounding left, so that it is
+// rounded once.
 __device__ __forceinline__ float factor_of(const GradNorm& n, float max_norm, float eps) {
   float hi = n.nearest, lo = n.rest;
   add_to(hi, lo, eps);
   const float d = hi + lo, rest = lo - (d - hi);
   if (!isfinite(n.nearest) || !(d > max_norm || (d == max_norm && rest > 0.f))) return 1.f;
   const float q = max_norm / d;
-  return q - q * (rest / d);
+  return q + (fmaf(-q, d, max_norm) - q * rest) / d;
 }
 
 __global__ void __launch_bounds__(kThreads) grad_norm_final(const GradSum* __restrict__ partial,
