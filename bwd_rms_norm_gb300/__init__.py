@@ -869,10 +869,10 @@ def rms_norm_block_fwd(x: torch.Tensor, residual: torch.Tensor,
     Returns ``(r, y, rstd_post, rstd_next)``, None for what a missing norm
     would give; an output given must not share memory with an input."""
     lib = load_library()
-    if _binding is not None and stream is None and (
-            residual_out is y is rstd_post is rstd_next is None):
+    if _binding is not None and stream is None:
         got = _binding.block_fwd(x, residual, post_gamma, gate, next_gamma, eps, offset,
-                                 residual_scale, branch_scale)
+                                 residual_scale, branch_scale, residual_out, y, rstd_post,
+                                 rstd_next)
         if got is not None:
             return got
     dev, dtype, shape = x.device, x.dtype, x.shape
@@ -942,10 +942,10 @@ def rms_norm_block_bwd(dy: Optional[torch.Tensor], dresidual_out: Optional[torch
     fp32, ``dgate`` shaped like ``gate`` (None without a gate or with
     ``with_dgate`` False), ``dpost`` / ``dnext`` None for a missing norm."""
     lib = load_library()
-    if _binding is not None and dx is dresidual is workspace is stream is None:
+    if _binding is not None and stream is None:
         got = _binding.block_bwd(dy, dresidual_out, x, residual_out, rstd_post, rstd_next,
                                  post_gamma, gate, next_gamma, offset, residual_scale,
-                                 branch_scale, with_dgate)
+                                 branch_scale, with_dgate, dx, dresidual, workspace)
         if got is not None:
             return got
     rows, hidden, gate_rows = _block_sizes(x, post_gamma, gate, next_gamma)

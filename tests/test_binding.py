@@ -165,3 +165,32 @@ def test_no_rows_and_no_gate_rows(L):
         got = L.rms_norm_block_bwd(x, x, x, r, r1, r2, w, gate, w)
         assert got[3].shape == gate.shape
         assert all(torch.count_nonzero(v).item() == 0 for v in got)
+
+
+@pytest.mark.gpu
+def test_outputs_that_are_given(L):
+    x, r = (torch.randn(4, 6, 96, device="cuda") for _ in range(2))
+    w = torch.rand(96, device="cuda") + 1
+    args = (x, r, w, None, w, 1e-5, 0, 1.0, 1.0)
+    want = L.rms_norm_block_fwd(*args)
+    outs = [torch.empty_like(v) for v in want]
+    got = L._binding.block_fwd(*args, *outs)
+    assert all(g.data_ptr() == o.data_ptr() for g, o in zip(got, outs))
+    same(got, want)
+    same(L.rms_norm_block_fwd(*args, *outs), want)
+    for k, bad in ((0, torch.empty(24, 96, device="cuda")), (1, outs[1].half()),
+                   (2, torch.empty(24, device="cuda")), (3, torch.empty(4, 6))):
+        assert L._binding.block_fwd(*args, *outs[:k], bad, *outs[k + 1:]) is None
+    back = (x, r, x, want[0], want[2], want[3], w, None, w, 0, 1.0, 1.0, True)
+    ref = L.rms_norm_block_bwd(*back)
+    ws = torch.empty(L.rms_norm_block_bwd_workspace_size(24, 96, 0), dtype=torch.uint8,
+                     device="cuda")
+    dx, dr = torch.empty_like(x), torch.empty_like(r)
+    got = L._binding.block_bwd(*back, dx, dr, ws)
+    assert got[0].data_ptr() == dx.data_ptr() and got[1].data_ptr() == dr.data_ptr()
+    same(got, ref)
+    same(L.rms_norm_block_bwd(*back, dx, dr, ws), ref)
+    with pytest.raises(L.RMSNormError):                # too small: said by the other way
+        L.rms_norm_block_bwd(*back, dx, dr, ws[:-16])
+    with pytest.raises(L.RMSNormError):                # an output in an input
+        L.rms_norm_block_fwd(*args, r, *outs[1:])
