@@ -5,9 +5,10 @@
 //
 // Argument marshalling only, and only of arguments that need no second look:
 // plain contiguous CUDA tensors of one device, the current one, with matching
-// types and shapes, the current stream.  Every function returns None for anything else, and for a status
-// that is not RMSN_OK; the Python functions then take their own way, with
-// their checks and messages.  No exception leaves this file.
+// types and shapes, the current stream.  Every function returns None for
+// anything else, and for a status that is not RMSN_OK; the Python functions
+// then take their own way, with their checks and messages.  No exception
+// leaves this file.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>

@@ -608,14 +608,16 @@ bool try_bwd(const BlockBwdArgs& a, BlockBwdParams& p, int* units, cudaStream_t 
                 [=](int k, int cols) { return bwd_stage<T, TS>(k, cols, x, NEXT, dr).bytes; }, &sp,
                 &nv8, &smem))
     return false;
-  p.period = EDGE ? row_period(a.hidden, 16 / (int)sizeof(T)) : 1;
+  const int period = EDGE ? row_period(a.hidden, 16 / (int)sizeof(T)) : 1;
+  if (EDGE && sms / sp.cs < period) return false;  // an SM budget below a unit for each class
+  p.period = period;
   auto go = [&](auto which) {
     constexpr auto kern = decltype(which)::value;
     *err = allow<kern>(dev, kSmemBudget - sizeof(BwdShared));
     if (*err != cudaSuccess) return;
     const int threads = 32 * (1 + sp.reducers + sp.teams * sp.wpt);
     int64_t n = sp.cs == 1 ? sms : max_clusters((const void*)kern, threads, smem, sp.cs, sms);
-    if (n < p.period) n = p.period;
+    if (n < p.period) n = p.period;  // (fewer fit at once: they wait their turn)
     if (n > RMSN_BLOCK_MAX_PARTIALS) n = RMSN_BLOCK_MAX_PARTIALS;
     if (n > a.rows) n = a.rows;
     n -= n % p.period;  // a unit's rows are of one class, at least one each

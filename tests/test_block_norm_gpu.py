@@ -536,3 +536,16 @@ def test_kernels_a_shape_runs(L, rows, hidden, gates, fwd, bwd):
                          dc["post_gamma"], dc["gate"], dc["next_gamma"])
     names = L.last_kernels()
     assert len(names) == 2 and bwd in names[0] and "block_bwd_sums" in names[1], names
+
+
+@pytest.mark.parametrize("sms", [1, 7, 8, 20, 100])
+@pytest.mark.parametrize("rows,hidden,gates", [(1100, 4097, 1), (1280, 1033, 5), (300, 8200, 0)])
+def test_odd_widths_on_few_sms(L, sms, rows, hidden, gates):
+    d, g = make(rows, hidden, "bf16", "bf16", True, gates, True, seed=sms)
+    L.rms_norm_set_sm_budget(sms)
+    try:
+        run_and_check(L, d, g)
+        if sms < 8 and hidden % 2:
+            assert "block_bwd_loop" in L.last_kernels()[0]
+    finally:
+        L.rms_norm_set_sm_budget(0)
