@@ -1,0 +1,41 @@
+"""The gradient norm and clip where values leave the usual range or repeat.
+Tolerances are those of test_grad_clip_gpu.py: h + 22 u and the smallest
+subnormal of the output's type."""
+import pytest
+import torch
+
+from test_grad_clip_gpu import TINY, U, check, factor64, make, norm64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def L():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    import bwd_rms_norm_gb300 as lib
+    lib.load_library()
+    return lib
+
+
+def near(got, kept, f):
+    for o, k in zip(got, kept):
+        ref = k.double() * f
+        most = (torch.finfo(o.dtype).eps / 2 + 22 * U) * ref.abs() + TINY[o.dtype]
+        bad = ~((o.double() - ref).abs() <= most)
+        assert not bool(bad.any()), (k.dtype, o.dtype, o[bad][0].item(), ref[bad][0].item())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("large,max_norm", [(30, 2.0 ** -110), (100, 2.0 ** -40), (100, 2.0 ** -72),
+                                            (110, 0.01), (20, 2.0 ** -110), (100, 2.0 ** -130)])
+def test_factors_below_the_normal_numbers(L, dtype, large, max_norm):
+    """The factor is a subnormal fp32 value, or none; the results are not."""
+    std = 2.0 ** large
+    check(L, make([5000, 3, 999], [dtype], seed=1, std=std), max_norm)
+    out = [torch.empty(n, device="cuda") for n in (5000, 3, 999)]
+    check(L, make([5000, 3, 999], [dtype], seed=2, std=std), max_norm, out=out)
+    grads = make([5000, 3, 999], [dtype], seed=3, std=std)
+    total = L.rms_norm_grad_norm(grads)
+    keep = [g.clone() for g in grads]
+    L.rms_norm_grad_clip(grads, max_norm, total_norm=total)
+    near(grads, keep, factor64(total.item(), max_norm))
