@@ -1088,9 +1088,11 @@ def rms_norm_grad_clip(grads, max_norm: float, eps: float = 1e-6, out=None,
     """Scale a list of gradients by ``min(1, max_norm / (norm + eps))``, in
     place, or into the tensors of ``out`` (same sizes, the gradient's dtype or
     float32).  Returns the norm before the scaling, an fp32 tensor of no
-    dimensions; where it is not finite the gradients are not scaled.  With
-    ``total_norm`` (a one-element fp32 tensor) that norm is taken instead of
-    the list's own, e.g. one summed over ranks."""
+    dimensions.  Where an element, or ``total_norm``, is not finite the
+    gradients are not scaled: look at the norm before the update.  (A finite
+    list whose norm is beyond fp32 is scaled, and its norm comes out
+    infinite.)  With ``total_norm`` (a one-element fp32 tensor) that norm is
+    taken instead of the list's own, e.g. one summed over ranks."""
     lib = load_library()
     if _binding is not None and norm is workspace is stream is None:
         got = _binding.grad_clip(grads, max_norm, eps, out, total_norm)

@@ -2,7 +2,7 @@
 // norm, for sm_103a.
 //
 //   norm   = sqrt(sum over every tensor and element of g^2)
-//   factor = min(1, max_norm / (norm + eps)), 1 where norm is not finite
+//   factor = min(1, max_norm / (norm + eps)), 1 where an element is not finite
 //   out_i  = round(g_i * factor)
 //
 // Two launches.  grad_squares reads the list once and leaves one sum a CTA;
@@ -220,9 +220,11 @@ __global__ void __launch_bounds__(kThreads, 8) grad_squares(const __grid_constan
 }
 
 // The norm from the CTAs' partial sums, the same bits in every CTA: nearest +
-// rest, nearest its fp32 value.
+// rest, nearest its fp32 value.  `wide` is the norm where it is finite and
+// nearest is not (16 values of 3e38), else 0.
 struct GradNorm {
   float nearest, rest;
+  double wide;
 };
 
 __device__ __forceinline__ GradNorm norm_of(const GradSum* __restrict__ partial, int nparts,
@@ -238,15 +240,16 @@ __device__ __forceinline__ GradNorm norm_of(const GradSum* __restrict__ partial,
   if (!(sum.extra == 0.0)) {
     const double v = sqrt((double)sum.hi + (double)sum.lo + sum.extra);
     const float f = (float)v;
-    return {f, isfinite(f) ? (float)(v - (double)f) : 0.f};
+    if (isfinite(f)) return {f, (float)(v - (double)f), 0.0};
+    return {f, 0.f, isfinite(v) ? v : 0.0};
   }
   // sqrt(s + e) = r + (s - r^2 + e) / (2 r), r = sqrt(s), the difference exact
   const float s = sum.hi + sum.lo, e = sum.lo - (s - sum.hi);
-  if (!(s > 0.f)) return {s, 0.f};
+  if (!(s > 0.f)) return {s, 0.f, 0.0};
   const float r = sqrtf(s);
   const float d = (fmaf(-r, r, s) + e) / (2.f * r);
   const float f = r + d;
-  return {f, d - (f - r)};
+  return {f, d - (f - r), 0.0};
 }
 
 // What a gradient is multiplied by: by `by`, then by `post`, which is 1 unless
@@ -256,18 +259,27 @@ struct Factor {
   float by, post;
 };
 
-// min(1, max_norm / (norm + eps)), 1 where the norm is not finite; the quotient
-// corrected by what its division and the norm's rounding left, so that it is
-// rounded once.
+// min(1, max_norm / (norm + eps)), 1 where an element (or a given norm) is not
+// finite; the quotient corrected by what its division and the norm's rounding
+// left, so that it is rounded once.  In double where norm + eps is beyond fp32
+// or the quotient below its normal numbers.
 __device__ __forceinline__ Factor factor_of(const GradNorm& n, float max_norm, float eps) {
+  if (!isfinite(n.nearest) && n.wide == 0.0) return {1.f, 1.f};
   float hi = n.nearest, lo = n.rest;
   add_to(hi, lo, eps);
   const float d = hi + lo, rest = lo - (d - hi);
-  if (!isfinite(n.nearest) || !(d > max_norm || (d == max_norm && rest > 0.f))) return {1.f, 1.f};
-  const float q = max_norm / d;
-  const float f = q + (fmaf(-q, d, max_norm) - q * rest) / d;
-  if (f >= 0x1p-126f) return {f, 1.f};
-  const double e = (double)max_norm / ((double)d + (double)rest);
+  double e;
+  if (isfinite(d)) {
+    if (!(d > max_norm || (d == max_norm && rest > 0.f))) return {1.f, 1.f};
+    const float q = max_norm / d;
+    const float f = q + (fmaf(-q, d, max_norm) - q * rest) / d;
+    if (f >= 0x1p-126f) return {f, 1.f};
+    e = (double)max_norm / ((double)d + (double)rest);
+  } else {
+    e = (double)max_norm / ((n.wide != 0.0 ? n.wide : (double)n.nearest + n.rest) + (double)eps);
+    if (!(e < 1.0)) return {1.f, 1.f};
+    if (e >= 0x1p-126) return {(float)e, 1.f};
+  }
   return e < 0x1p-200 ? Factor{(float)(e * 0x1p149), 0x1p-149f}
                       : Factor{(float)(e * 0x1p100), 0x1p-100f};
 }
@@ -370,7 +382,7 @@ __global__ void __launch_bounds__(kThreads) grad_scale(const __grid_constant__ G
   __shared__ GradSum red[kThreads / 32];
   pdl_trigger();
   pdl_wait();
-  const GradNorm v = total_norm != nullptr ? GradNorm{*total_norm, 0.f}
+  const GradNorm v = total_norm != nullptr ? GradNorm{*total_norm, 0.f, 0.0}
                                            : norm_of(partial, nparts, red);
   if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = v.nearest;
   const Factor f = factor_of(v, max_norm, eps);

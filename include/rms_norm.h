@@ -400,7 +400,7 @@ int rms_norm_block_bwd(const void* dy, const void* dresidual_out, const void* x,
  * (their fp32 weight gradients among them) before its update:
  *
  *   norm   = sqrt(sum over the list of every element squared)
- *   factor = min(1, max_norm / (norm + eps));  1 if norm is not finite
+ *   factor = min(1, max_norm / (norm + eps));  1 if an element is not finite
  *   outs[i][k] = round(grads[i][k] * factor)
  *
  * `grads`, `numels`, `dtypes`, `outs` and `out_dtypes` are HOST arrays of
@@ -417,8 +417,10 @@ int rms_norm_block_bwd(const void* dy, const void* dresidual_out, const void* x,
  * RMSN_F32; outs[i] == grads[i] of the same type scales in place (and writes
  * nothing when the factor is 1).  An output that shares memory with another
  * output, or with a gradient other than its own in place, is refused
- * (RMSN_ERR_ARG), so a tensor may be in the list once.  A norm that is not
- * finite leaves the gradients unscaled; the caller sees it in `norm`.  With
+ * (RMSN_ERR_ARG), so a tensor may be in the list once.  An infinite or NaN
+ * element leaves the gradients unscaled; the caller sees it in `norm`.  (A
+ * finite list whose norm is beyond fp32 is scaled by its factor, and `norm` is
+ * infinite; a `total_norm` that is not finite leaves the list unscaled.)  With
  * `total_norm` (one fp32 on the device, may be NULL) the factor is taken from
  * it instead of the list's own norm -- the norm over every rank's gradients,
  * say -- and the list is not read for its norm; `norm` and `workspace` may then

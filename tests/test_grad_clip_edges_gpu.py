@@ -39,3 +39,33 @@ def test_factors_below_the_normal_numbers(L, dtype, large, max_norm):
     keep = [g.clone() for g in grads]
     L.rms_norm_grad_clip(grads, max_norm, total_norm=total)
     near(grads, keep, factor64(total.item(), max_norm))
+
+
+@pytest.mark.parametrize("value,dtype,n", [
+    (3e38, torch.float32, 16), (3e38, torch.bfloat16, 16), (1e38, torch.float32, 1_000_003),
+    (-3.3e38, torch.bfloat16, 70_001), (2e38, torch.float32, 3)])
+@pytest.mark.parametrize("max_norm", [1.0, 1e30, 3e38, 2.0 ** -20, 0.0, float("inf")])
+def test_finite_lists_whose_norm_is_beyond_fp32(L, value, dtype, n, max_norm):
+    """The norm is infinite in fp32, but the list is clipped by its own."""
+    grads = [torch.full((n,), value, device="cuda").to(dtype),
+             torch.tensor([1.0, -2.0 ** 100, 0.0], device="cuda").to(dtype)]
+    keep = [g.clone() for g in grads]
+    f = factor64(norm64(keep), max_norm)
+    out = [torch.empty_like(g, dtype=torch.float32) for g in grads]
+    assert L.rms_norm_grad_norm(grads).item() == float("inf")
+    assert L.rms_norm_grad_clip(grads, max_norm, out=out).item() == float("inf")
+    near(out, keep, f)
+    assert L.rms_norm_grad_clip(grads, max_norm).item() == float("inf")
+    near(grads, keep, f)
+
+
+@pytest.mark.parametrize("eps", [1e38, 3.4e38])
+def test_norm_and_eps_together_beyond_fp32(L, eps):
+    grads = [torch.full((4,), 1.5e38, device="cuda")]
+    keep = [g.clone() for g in grads]
+    assert L.rms_norm_grad_clip(grads, 2.0, eps=eps).item() == pytest.approx(3e38, rel=1e-6)
+    near(grads, keep, factor64(norm64(keep), 2.0, eps))
+    total = torch.tensor(3e38, device="cuda")
+    grads = [g.clone() for g in keep]
+    L.rms_norm_grad_clip(grads, 2.0, eps=eps, total_norm=total)
+    near(grads, keep, factor64(total.double().item(), 2.0, eps))
