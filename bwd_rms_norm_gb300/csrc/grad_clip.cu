@@ -600,6 +600,19 @@ bool overlaps(const void* const* grads, const int64_t* numels, const int* dtypes
   return hit;
 }
 
+bool meet(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t p = (uintptr_t)a, q = (uintptr_t)b;
+  return a && b && na && nb && p < q + nb && q < p + na;
+}
+
+// Whether `bytes` at p share memory with a tensor of the list.
+bool in_list(const void* p, size_t bytes, const void* const* list, const int64_t* numels,
+             const int* dtypes, int64_t count) {
+  for (int64_t i = 0; i < count; ++i)
+    if (meet(p, bytes, list[i], (size_t)numels[i] * elem_size(dtypes[i]))) return true;
+  return false;
+}
+
 // Room for the partial sums of every launch, a table's tensors each.
 size_t workspace_bytes_of(int64_t count) {
   const int64_t tables = count <= kMaxTable ? 1 : ceil_div(count, kMaxTable);
@@ -625,6 +638,10 @@ int rms_norm_grad_norm(const void* const* grads, const int64_t* numels, const in
   if (!norm || !workspace) return RMSN_ERR_NULL;
   if ((uintptr_t)workspace % 16 != 0) return RMSN_ERR_ALIGN;
   if (workspace_bytes < workspace_bytes_of(count)) return RMSN_ERR_WORKSPACE;
+  if (meet(norm, sizeof(float), workspace, workspace_bytes) ||
+      in_list(norm, sizeof(float), grads, numels, dtypes, count) ||
+      in_list(workspace, workspace_bytes, grads, numels, dtypes, count))
+    return RMSN_ERR_ARG;
   GradList g = {grads, nullptr, numels, dtypes, nullptr, count, 0.f, 0.f, nullptr, norm,
                 static_cast<GradSum*>(workspace)};
   int launches = 0;
@@ -653,6 +670,19 @@ int rms_norm_grad_clip(const void* const* grads, const int64_t* numels, const in
   bool failed = false;
   if (overlaps(grads, numels, dtypes, outs, out_dtypes, count, &failed)) return RMSN_ERR_ARG;
   if (failed) return cuda_fail(cudaErrorMemoryAllocation);
+  const void* const* written = const_cast<const void* const*>(outs);
+  if (in_list(norm, sizeof(float), grads, numels, dtypes, count) ||
+      in_list(norm, sizeof(float), written, numels, out_dtypes, count))
+    return RMSN_ERR_ARG;
+  if (total_norm) {  // the same address as norm's: it receives its own value
+    if ((total_norm != norm && meet(norm, sizeof(float), total_norm, sizeof(float))) ||
+        in_list(total_norm, sizeof(float), written, numels, out_dtypes, count))
+      return RMSN_ERR_ARG;
+  } else if (meet(norm, sizeof(float), workspace, workspace_bytes) ||
+             in_list(workspace, workspace_bytes, grads, numels, dtypes, count) ||
+             in_list(workspace, workspace_bytes, written, numels, out_dtypes, count)) {
+    return RMSN_ERR_ARG;
+  }
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   GradList g = {grads, outs, numels, dtypes, out_dtypes, count, max_norm, eps, total_norm, norm,
                 static_cast<GradSum*>(workspace)};

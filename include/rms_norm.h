@@ -417,7 +417,9 @@ int rms_norm_block_bwd(const void* dy, const void* dresidual_out, const void* x,
  * RMSN_F32; outs[i] == grads[i] of the same type scales in place (and writes
  * nothing when the factor is 1).  An output that shares memory with another
  * output, or with a gradient other than its own in place, is refused
- * (RMSN_ERR_ARG), so a tensor may be in the list once.  An infinite or NaN
+ * (RMSN_ERR_ARG), so a tensor may be in the list once; so is, in both calls, a
+ * `norm` or workspace that shares memory with a tensor of the lists or with the
+ * other, and a `total_norm` inside an output.  An infinite or NaN
  * element leaves the gradients unscaled; the caller sees it in `norm`.  (A
  * finite list whose norm is beyond fp32 is scaled by its factor, and `norm` is
  * infinite; a `total_norm` that is not finite leaves the list unscaled.)  With
