@@ -66,6 +66,7 @@ BINDING_PATH = os.path.join(os.path.dirname(LIB_PATH), "_binding.so")
 RMSN_F32, RMSN_BF16, RMSN_F16 = 0, 1, 2
 RMSN_ROUND_ONCE, RMSN_ROUND_TWICE = 0, 1
 RMSN_OK = 0
+RMSN_ERR_ARG = 8
 RMSN_MAX_HIDDEN = 65536
 RMSN_MAX_PARTIALS = 1024
 RMSN_DW_CHUNK_BLOCKS = 32
@@ -838,6 +839,11 @@ def _broadcasts_otherwise(gate, x) -> bool:
     return False
 
 
+def _check_offset(fn: str, offset) -> None:
+    if offset not in (0, 1):            # int() would cut 0.5 to 0
+        raise RMSNormError(fn, RMSN_ERR_ARG)
+
+
 def _check_block(x, stream_name, stream, post_gamma, gate, next_gamma) -> None:
     """Checks shared by the block-norm calls, with a message for each."""
     hidden = x.shape[-1]
@@ -875,6 +881,7 @@ def rms_norm_block_fwd(x: torch.Tensor, residual: torch.Tensor,
                                  rstd_next)
         if got is not None:
             return got
+    _check_offset("rms_norm_block_fwd", offset)
     dev, dtype, shape = x.device, x.dtype, x.shape
     res_dtype, index = residual.dtype, x.get_device()
     rows, hidden, gate_rows = _block_sizes(x, post_gamma, gate, next_gamma)
@@ -948,6 +955,7 @@ def rms_norm_block_bwd(dy: Optional[torch.Tensor], dresidual_out: Optional[torch
                                  branch_scale, with_dgate, dx, dresidual, workspace)
         if got is not None:
             return got
+    _check_offset("rms_norm_block_bwd", offset)
     rows, hidden, gate_rows = _block_sizes(x, post_gamma, gate, next_gamma)
     if next_gamma is None:
         dy = None
