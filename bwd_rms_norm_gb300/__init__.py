@@ -787,6 +787,14 @@ class _On:
             self.undo.close()
 
 
+def _written(*tensors: Optional[torch.Tensor]) -> None:
+    """Counts a version of each caller's tensor that a call wrote, which is how
+    autograd notices that a tensor it saved has changed."""
+    for t in tensors:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def _address(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -902,6 +910,9 @@ def rms_norm_block_fwd(x: torch.Tensor, residual: torch.Tensor,
                         ("rstd_next", rstd_next)):
             if t is not None:
                 _check_cuda(name, t, dev)
+    given = (residual_out, y if next_gamma is not None else None,
+             rstd_post if post_gamma is not None else None,
+             rstd_next if next_gamma is not None else None)
     with _On(dev, stream) as handle:
         if residual_out is None:
             residual_out = torch.empty_like(residual)
@@ -923,6 +934,7 @@ def rms_norm_block_fwd(x: torch.Tensor, residual: torch.Tensor,
                                     DTYPE_CODES[dtype], DTYPE_CODES[res_dtype], handle)
     if st != RMSN_OK:
         raise RMSNormError("rms_norm_block_fwd", st)
+    _written(*given)
     return residual_out, y, rstd_post, rstd_next
 
 
@@ -987,6 +999,7 @@ def rms_norm_block_bwd(dy: Optional[torch.Tensor], dresidual_out: Optional[torch
                         ("workspace", workspace)):
             if t is not None:
                 _check_cuda(name, t, dev)
+    given = (dx, dresidual)
     with _On(dev, stream) as handle:
         dx = torch.empty_like(x) if dx is None else dx
         dresidual = torch.empty_like(residual_out) if dresidual is None else dresidual
@@ -1011,6 +1024,7 @@ def rms_norm_block_bwd(dy: Optional[torch.Tensor], dresidual_out: Optional[torch
                                     workspace.numel() * workspace.element_size(), handle)
     if st != RMSN_OK:
         raise RMSNormError("rms_norm_block_bwd", st)
+    _written(*given)
     return dx, dresidual, dpost, dgate, dnext
 
 
@@ -1072,6 +1086,7 @@ def rms_norm_grad_norm(grads, norm: Optional[torch.Tensor] = None,
     dev = grads[0].device
     ptrs, numels, codes = _grad_list("a gradient", grads, dev)
     _scalar("norm", norm, dev)
+    given = norm
     with _On(dev, stream) as handle:
         if norm is None:
             norm = torch.empty((), dtype=torch.float32, device=dev)
@@ -1085,6 +1100,7 @@ def rms_norm_grad_norm(grads, norm: Optional[torch.Tensor] = None,
                                     workspace.numel() * workspace.element_size(), handle)
     if st != RMSN_OK:
         raise RMSNormError("rms_norm_grad_norm", st)
+    _written(given)
     return norm
 
 
@@ -1122,6 +1138,7 @@ def rms_norm_grad_clip(grads, max_norm: float, eps: float = 1e-6, out=None,
         outs_of = _grad_list("a tensor of out", outs, dev)
     _scalar("total_norm", total_norm, dev)
     _scalar("norm", norm, dev)
+    given = norm
     with _On(dev, stream) as handle:
         if norm is None:
             norm = torch.empty((), dtype=torch.float32, device=dev)
@@ -1139,9 +1156,7 @@ def rms_norm_grad_clip(grads, max_norm: float, eps: float = 1e-6, out=None,
                                     _ptr(workspace), size, handle)
     if st != RMSN_OK:
         raise RMSNormError("rms_norm_grad_clip", st)
-    for t in outs:                      # autograd's check of saved tensors
-        if not t.is_inference():
-            torch.autograd.graph.increment_version(t)
+    _written(given, *outs)
     return norm
 
 

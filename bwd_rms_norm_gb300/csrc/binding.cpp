@@ -167,6 +167,17 @@ at::Tensor output(PyObject* const* a, Py_ssize_t n, int i, at::IntArrayRef sizes
   return o.fits(type, sizes, device) ? *o.t : at::Tensor();
 }
 
+// Counts a version of a tensor that a call wrote: autograd's check of what it
+// has saved.
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
+// The same for the output that was given as argument i, if one was.
+void written(PyObject* const* a, Py_ssize_t n, int i) {
+  if (i < n && a[i] != Py_None) written(THPVariable_Unpack(a[i]));
+}
+
 // block_fwd(x, residual, post, gate, next, eps, offset, residual_scale, branch_scale[,
 //           residual_out, y, rstd_post, rstd_next])
 PyObject* block_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -190,7 +201,11 @@ PyObject* block_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         static_cast<float*>(ptr(r1)), static_cast<float*>(ptr(r2)), c.rows, c.hidden, (float)v[2],
         (float)v[3], (float)v[0], (int)v[1], c.dtype, c.stream_dtype,
         c10::cuda::getCurrentCUDAStream(c.device).stream());
-    return st == RMSN_OK ? tuple_of({out, y, r1, r2}) : nullptr;
+    if (st != RMSN_OK) return nullptr;
+    written(a, n, 9);
+    if (post) written(a, n, 11);
+    if (next) written(a, n, 10), written(a, n, 12);
+    return tuple_of({out, y, r1, r2});
   });
 }
 
@@ -233,7 +248,10 @@ PyObject* block_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         static_cast<float*>(ptr(dnext)), c.rows, c.hidden, (float)v[1], (float)v[2], (int)v[0],
         c.dtype, c.stream_dtype, ptr(ws), (size_t)ws.nbytes(),
         c10::cuda::getCurrentCUDAStream(c.device).stream());
-    return st == RMSN_OK ? tuple_of({dx, dres, dpost, dgate, dnext}) : nullptr;
+    if (st != RMSN_OK) return nullptr;
+    written(a, n, 13);
+    written(a, n, 14);
+    return tuple_of({dx, dres, dpost, dgate, dnext});
   });
 }
 
@@ -316,11 +334,9 @@ PyObject* grad_clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
       Py_DECREF(result);
       return nullptr;
     }
-    PyObject* written = in_place ? a[0] : a[3];
-    for (int64_t i = 0; i < count; ++i) {  // autograd's check of saved tensors
-      const at::Tensor& t = THPVariable_Unpack(PySequence_Fast_GET_ITEM(written, (Py_ssize_t)i));
-      if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
-    }
+    PyObject* outs = in_place ? a[0] : a[3];
+    for (int64_t i = 0; i < count; ++i)
+      written(THPVariable_Unpack(PySequence_Fast_GET_ITEM(outs, (Py_ssize_t)i)));
     return result;
   });
 }
