@@ -6,9 +6,10 @@
 // Argument marshalling only, and only of arguments that need no second look:
 // plain contiguous CUDA tensors of one device, the current one, with matching
 // types and shapes, the current stream.  Every function returns None for
-// anything else, and for a status that is not RMSN_OK; the Python functions
-// then take their own way, with their checks and messages.  No exception
-// leaves this file.
+// anything else, and for arguments that the C entry refuses; the Python
+// functions then take their own way, with their checks and messages.  A CUDA
+// error raises RMSNormError from here: what was enqueued before it must not run
+// twice.  No C++ exception leaves this file.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -146,14 +147,31 @@ bool numbers(PyObject* const* a, int n, double* out) {
   return true;
 }
 
-// The body of a call: None where it is not a usual one, or throws.
+// Sets RMSNormError(fn, RMSN_ERR_CUDA).
+void set_cuda_error(const char* fn) {
+  PyObject* package = PyImport_ImportModule("bwd_rms_norm_gb300");
+  PyObject* type = package ? PyObject_GetAttrString(package, "RMSNormError") : nullptr;
+  PyObject* error = type ? PyObject_CallFunction(type, "si", fn, (int)RMSN_ERR_CUDA) : nullptr;
+  if (error) PyErr_SetObject(type, error);
+  Py_XDECREF(error);
+  Py_XDECREF(type);
+  Py_XDECREF(package);
+}
+
+// The body of a call of the C entry `fn`: None where it is not a usual one, or
+// throws.  f(st) leaves the entry's status in st, once it has called it.
 template <typename F>
-PyObject* guarded(F f) {
+PyObject* guarded(const char* fn, F f) {
+  int st = RMSN_OK;
   try {
-    PyObject* r = f();
+    PyObject* r = f(st);
     if (r) return r;
-    if (PyErr_Occurred()) PyErr_Clear();
   } catch (...) {
+  }
+  if (PyErr_Occurred()) PyErr_Clear();
+  if (st == RMSN_ERR_CUDA) {
+    set_cuda_error(fn);
+    return nullptr;
   }
   Py_RETURN_NONE;
 }
@@ -181,7 +199,7 @@ void written(PyObject* const* a, Py_ssize_t n, int i) {
 // block_fwd(x, residual, post, gate, next, eps, offset, residual_scale, branch_scale[,
 //           residual_out, y, rstd_post, rstd_next])
 PyObject* block_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded([&]() -> PyObject* {
+  return guarded("rms_norm_block_fwd", [&](int& st) -> PyObject* {
     if (n != 9 && n != 13) return nullptr;
     const Arg x(a[0]), res(a[1]), post(a[2]), gate(a[3]), next(a[4]);
     Call c;
@@ -196,7 +214,7 @@ PyObject* block_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     if (!out.defined() || (post && !r1.defined()) || (next && (!y.defined() || !r2.defined())))
       return nullptr;
-    const int st = entry.block_fwd(
+    st = entry.block_fwd(
         x.ptr(), res.ptr(), post.ptr(), gate.ptr(), c.gate_rows, next.ptr(), ptr(out), ptr(y),
         static_cast<float*>(ptr(r1)), static_cast<float*>(ptr(r2)), c.rows, c.hidden, (float)v[2],
         (float)v[3], (float)v[0], (int)v[1], c.dtype, c.stream_dtype,
@@ -212,7 +230,7 @@ PyObject* block_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // block_bwd(dy, dresidual_out, x, residual_out, rstd_post, rstd_next, post, gate, next, offset,
 //           residual_scale, branch_scale, with_dgate[, dx, dresidual, workspace])
 PyObject* block_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded([&]() -> PyObject* {
+  return guarded("rms_norm_block_bwd", [&](int& st) -> PyObject* {
     if (n != 13 && n != 16) return nullptr;
     const Arg dy(a[0]), dr(a[1]), x(a[2]), res(a[3]), r1(a[4]), r2(a[5]), post(a[6]), gate(a[7]),
         next(a[8]);
@@ -241,7 +259,7 @@ PyObject* block_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     } else {
       ws = bytes(need, c.device);
     }
-    const int st = entry.block_bwd(
+    st = entry.block_bwd(
         next ? dy.ptr() : nullptr, dr.ptr(), x.ptr(), res.ptr(), post.ptr(), gate.ptr(),
         c.gate_rows, next.ptr(), static_cast<float*>(r1.ptr()), static_cast<float*>(r2.ptr()),
         ptr(dx), ptr(dres), static_cast<float*>(ptr(dpost)), static_cast<float*>(ptr(dgate)),
@@ -287,24 +305,23 @@ struct List {
 
 // grad_norm(grads)
 PyObject* grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded([&]() -> PyObject* {
+  return guarded("rms_norm_grad_norm", [&](int& st) -> PyObject* {
     List g;
     if (n != 1 || !g.read(a[0], -1)) return nullptr;
     const int64_t count = (int64_t)g.ptrs.size();
     const int device = (int)g.first->get_device();
     at::Tensor norm = empty({}, at::kFloat, device);
     at::Tensor ws = bytes(entry.grad_ws(count), device);
-    const int st = entry.grad_norm(g.ptrs.data(), g.numels.data(), g.codes.data(), count,
-                                   static_cast<float*>(norm.data_ptr()), ws.data_ptr(),
-                                   (size_t)ws.numel(),
-                                   c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream());
+    st = entry.grad_norm(g.ptrs.data(), g.numels.data(), g.codes.data(), count,
+                         static_cast<float*>(norm.data_ptr()), ws.data_ptr(), (size_t)ws.numel(),
+                         c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream());
     return st == RMSN_OK ? wrap(norm) : nullptr;
   });
 }
 
 // grad_clip(grads, max_norm, eps, out or None, total_norm or None)
 PyObject* grad_clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded([&]() -> PyObject* {
+  return guarded("rms_norm_grad_clip", [&](int& st) -> PyObject* {
     List g, o;
     double v[2];
     if (n != 5 || !g.read(a[0], -1) || !numbers(a + 1, 2, v)) return nullptr;
@@ -325,7 +342,7 @@ PyObject* grad_clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!total) ws = bytes(entry.grad_ws(count), device);
     PyObject* result = wrap(norm);  // before the call: in place there is no second one
     if (!result) return nullptr;
-    const int st = entry.grad_clip(
+    st = entry.grad_clip(
         g.ptrs.data(), g.numels.data(), g.codes.data(), out.ptrs.data(), out.codes.data(), count,
         (float)v[0], (float)v[1], static_cast<const float*>(total.ptr()),
         static_cast<float*>(norm.data_ptr()), ptr(ws), ws.defined() ? (size_t)ws.numel() : 0,

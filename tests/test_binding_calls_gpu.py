@@ -1,5 +1,8 @@
 """What a call through the direct binding, or past it, does to its process:
 version counters, errors, other threads."""
+import ctypes
+import subprocess
+
 import pytest
 import torch
 
@@ -48,3 +51,66 @@ def test_outputs_that_are_given_count_a_version(L, monkeypatch, direct):
         dx = torch.zeros_like(x)
     L.rms_norm_block_fwd(x, dres, w, None, w, 1e-6, 0, 1.0, 1.0, *outs)
     L.rms_norm_block_bwd(x, dres, x, outs[0], outs[2], outs[3], w, None, w, dx=dx)
+
+
+STUB = r"""
+#include <stddef.h>
+#include <unistd.h>
+volatile int calls, status, released, waits, saw;
+/* In place of a C entry point: counts, and answers with `status`; where `waits`
+   is set it first waits for another thread's `released`, 2 s at most, and says
+   whether it saw it. */
+int entry(void) {
+  ++calls;
+  for (int ms = 0; waits && !released && ms < 2000; ++ms) usleep(1000);
+  saw = released;
+  return status;
+}
+size_t workspace(void) { return 64; }
+"""
+
+
+@pytest.fixture(scope="module")
+def stub(tmp_path_factory):
+    """A library of entry points that launch nothing."""
+    d = tmp_path_factory.mktemp("stub")
+    (d / "stub.c").write_text(STUB)
+    subprocess.run(["gcc", "-shared", "-fPIC", "-O1", str(d / "stub.c"), "-o",
+                    str(d / "stub.so")], check=True)
+    return ctypes.CDLL(str(d / "stub.so"))
+
+
+@pytest.fixture
+def stubbed(L, stub):
+    """The binding on the stub's entry points, its counters at zero."""
+    at = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
+    entry, workspace = at(stub.entry), at(stub.workspace)
+    names = ("calls", "status", "released", "waits", "saw")
+    v = {k: ctypes.c_int.in_dll(stub, k) for k in names}
+    for c in v.values():
+        c.value = 0
+    L._binding.init(entry, entry, workspace, entry, entry, workspace)
+    yield v
+    L._load_binding(L.load_library())
+
+
+def calls_of(L):
+    x, w, s = torch.ones(4, 8, device="cuda"), torch.ones(8, device="cuda"), torch.ones(
+        4, device="cuda")
+    return {"rms_norm_block_fwd": lambda: L.rms_norm_block_fwd(x, x, w, None, w),
+            "rms_norm_block_bwd": lambda: L.rms_norm_block_bwd(x, x, x, x, s, s, w, None, w),
+            "rms_norm_grad_norm": lambda: L.rms_norm_grad_norm([x]),
+            "rms_norm_grad_clip": lambda: L.rms_norm_grad_clip([x], 1e-3)}, x
+
+
+@pytest.mark.parametrize("name", ["rms_norm_block_fwd", "rms_norm_block_bwd",
+                                  "rms_norm_grad_norm", "rms_norm_grad_clip"])
+def test_a_failed_launch_is_not_made_again(L, stubbed, name):
+    """A call that failed on its way may have scaled some tensors already: its
+    error is raised, and nothing runs a second time."""
+    calls, x = calls_of(L)
+    stubbed["status"].value = 7
+    with pytest.raises(L.RMSNormError, match=name + ".*status 7") as e:
+        calls[name]()
+    assert e.value.status == 7 and stubbed["calls"].value == 1
+    assert bool((x == 1).all())
