@@ -176,14 +176,39 @@ PyObject* guarded(const char* fn, F f) {
   Py_RETURN_NONE;
 }
 
-// The output given as argument i, or a new one; undefined where one is given
-// that is not usual.
-at::Tensor output(PyObject* const* a, Py_ssize_t n, int i, at::IntArrayRef sizes,
-                  at::ScalarType type, int device) {
-  if (i >= n || a[i] == Py_None) return empty(sizes, type, device);
-  const Arg o(a[i]);
-  return o.fits(type, sizes, device) ? *o.t : at::Tensor();
-}
+// Other threads of Python run while one of these lives: allocations may free
+// memory and launches may wait for room in their queue.  Nothing of Python's is
+// touched meanwhile; the arguments are held by the caller, or by a List.
+class Unlocked {
+  PyThreadState* state_ = PyEval_SaveThread();
+
+ public:
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state_); }
+};
+
+// An output of a call: the tensor given as argument i, or a new one (`make`,
+// which Unlocked allows).
+struct Output {
+  at::Tensor t;
+  at::IntArrayRef sizes;
+  at::ScalarType type = at::kFloat;
+  int device = 0;
+  bool wanted = false, usual = true;
+  Output() = default;
+  Output(PyObject* const* a, Py_ssize_t n, int i, at::IntArrayRef s, at::ScalarType ty, int dev)
+      : sizes(s), type(ty), device(dev), wanted(true) {
+    if (i >= n || a[i] == Py_None) return;
+    const Arg o(a[i]);
+    usual = o.fits(type, sizes, device);
+    if (usual) t = *o.t;
+  }
+  void make() {
+    if (wanted && !t.defined()) t = empty(sizes, type, device);
+  }
+  void* ptr() const { return t.defined() ? t.data_ptr() : nullptr; }
+};
 
 // Counts a version of a tensor that a call wrote: autograd's check of what it
 // has saved.
@@ -206,24 +231,27 @@ PyObject* block_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     double v[4];
     if (!usual_call(x, res, post, gate, next, &c) || !numbers(a + 5, 4, v)) return nullptr;
     if (v[1] != 0.0 && v[1] != 1.0) return nullptr;
-    at::Tensor out = output(a, n, 9, c.sizes, res.t->scalar_type(), c.device), y, r1, r2;
-    if (post) r1 = output(a, n, 11, c.row_sizes, at::kFloat, c.device);
+    Output out(a, n, 9, c.sizes, res.t->scalar_type(), c.device), y, r1, r2;
+    if (post) r1 = Output(a, n, 11, c.row_sizes, at::kFloat, c.device);
     if (next) {
-      y = output(a, n, 10, c.sizes, x.t->scalar_type(), c.device);
-      r2 = output(a, n, 12, c.row_sizes, at::kFloat, c.device);
+      y = Output(a, n, 10, c.sizes, x.t->scalar_type(), c.device);
+      r2 = Output(a, n, 12, c.row_sizes, at::kFloat, c.device);
     }
-    if (!out.defined() || (post && !r1.defined()) || (next && (!y.defined() || !r2.defined())))
-      return nullptr;
-    st = entry.block_fwd(
-        x.ptr(), res.ptr(), post.ptr(), gate.ptr(), c.gate_rows, next.ptr(), ptr(out), ptr(y),
-        static_cast<float*>(ptr(r1)), static_cast<float*>(ptr(r2)), c.rows, c.hidden, (float)v[2],
-        (float)v[3], (float)v[0], (int)v[1], c.dtype, c.stream_dtype,
-        c10::cuda::getCurrentCUDAStream(c.device).stream());
+    if (!out.usual || !y.usual || !r1.usual || !r2.usual) return nullptr;
+    {
+      const Unlocked unlocked;
+      for (Output* o : {&out, &y, &r1, &r2}) o->make();
+      st = entry.block_fwd(
+          x.ptr(), res.ptr(), post.ptr(), gate.ptr(), c.gate_rows, next.ptr(), out.ptr(), y.ptr(),
+          static_cast<float*>(r1.ptr()), static_cast<float*>(r2.ptr()), c.rows, c.hidden,
+          (float)v[2], (float)v[3], (float)v[0], (int)v[1], c.dtype, c.stream_dtype,
+          c10::cuda::getCurrentCUDAStream(c.device).stream());
+    }
     if (st != RMSN_OK) return nullptr;
     written(a, n, 9);
     if (post) written(a, n, 11);
     if (next) written(a, n, 10), written(a, n, 12);
-    return tuple_of({out, y, r1, r2});
+    return tuple_of({out.t, y.t, r1.t, r2.t});
   });
 }
 
@@ -243,58 +271,68 @@ PyObject* block_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         !dr.fits(res.t->scalar_type(), c.sizes, c.device) ||
         !r1.fits(at::kFloat, c.row_sizes, c.device) || !r2.fits(at::kFloat, c.row_sizes, c.device))
       return nullptr;
-    const at::Tensor dx = output(a, n, 13, c.sizes, x.t->scalar_type(), c.device);
-    const at::Tensor dres = output(a, n, 14, c.sizes, res.t->scalar_type(), c.device);
-    if (!dx.defined() || !dres.defined()) return nullptr;
-    at::Tensor dpost, dgate, dnext;
-    if (post) dpost = empty({c.hidden}, at::kFloat, c.device);
-    if (next) dnext = empty({c.hidden}, at::kFloat, c.device);
-    if (gate && v[3] != 0.0) dgate = empty(gate.t->sizes(), at::kFloat, c.device);
-    const size_t need = entry.block_ws(c.rows, c.hidden, c.gate_rows);
-    at::Tensor ws;
+    Output dx(a, n, 13, c.sizes, x.t->scalar_type(), c.device);
+    Output dres(a, n, 14, c.sizes, res.t->scalar_type(), c.device);
+    if (!dx.usual || !dres.usual) return nullptr;
+    at::Tensor dpost, dgate, dnext, ws;
     if (n > 15 && a[15] != Py_None) {
       if (!THPVariable_CheckExact(a[15])) return nullptr;
       ws = THPVariable_Unpack(a[15]);
       if (!ws.is_cuda() || !ws.is_contiguous() || ws.get_device() != c.device) return nullptr;
-    } else {
-      ws = bytes(need, c.device);
     }
-    st = entry.block_bwd(
-        next ? dy.ptr() : nullptr, dr.ptr(), x.ptr(), res.ptr(), post.ptr(), gate.ptr(),
-        c.gate_rows, next.ptr(), static_cast<float*>(r1.ptr()), static_cast<float*>(r2.ptr()),
-        ptr(dx), ptr(dres), static_cast<float*>(ptr(dpost)), static_cast<float*>(ptr(dgate)),
-        static_cast<float*>(ptr(dnext)), c.rows, c.hidden, (float)v[1], (float)v[2], (int)v[0],
-        c.dtype, c.stream_dtype, ptr(ws), (size_t)ws.nbytes(),
-        c10::cuda::getCurrentCUDAStream(c.device).stream());
+    {
+      const Unlocked unlocked;
+      dx.make();
+      dres.make();
+      if (post) dpost = empty({c.hidden}, at::kFloat, c.device);
+      if (next) dnext = empty({c.hidden}, at::kFloat, c.device);
+      if (gate && v[3] != 0.0) dgate = empty(gate.t->sizes(), at::kFloat, c.device);
+      if (!ws.defined()) ws = bytes(entry.block_ws(c.rows, c.hidden, c.gate_rows), c.device);
+      st = entry.block_bwd(
+          next ? dy.ptr() : nullptr, dr.ptr(), x.ptr(), res.ptr(), post.ptr(), gate.ptr(),
+          c.gate_rows, next.ptr(), static_cast<float*>(r1.ptr()), static_cast<float*>(r2.ptr()),
+          dx.ptr(), dres.ptr(), static_cast<float*>(ptr(dpost)), static_cast<float*>(ptr(dgate)),
+          static_cast<float*>(ptr(dnext)), c.rows, c.hidden, (float)v[1], (float)v[2], (int)v[0],
+          c.dtype, c.stream_dtype, ptr(ws), (size_t)ws.nbytes(),
+          c10::cuda::getCurrentCUDAStream(c.device).stream());
+    }
     if (st != RMSN_OK) return nullptr;
     written(a, n, 13);
     written(a, n, 14);
-    return tuple_of({dx, dres, dpost, dgate, dnext});
+    return tuple_of({dx.t, dres.t, dpost, dgate, dnext});
   });
 }
 
+// A list of tensors, as it was when it was read: it holds them, since the
+// caller's list may change while other threads run.
 struct List {
   std::vector<void*> ptrs;
   std::vector<int64_t> numels;
   std::vector<int> codes;
-  const at::Tensor* first = nullptr;
+  PyObject* held = nullptr;  // a tuple
+  List() = default;
+  List(const List&) = delete;
+  ~List() { Py_XDECREF(held); }
+  const at::Tensor& tensor(Py_ssize_t i) const {
+    return THPVariable_Unpack(PyTuple_GET_ITEM(held, i));
+  }
   // A list or tuple of usual tensors on one device, `device` if that is >= 0.
   bool read(PyObject* o, int device) {
     if (!PyList_CheckExact(o) && !PyTuple_CheckExact(o)) return false;
-    const Py_ssize_t n = PySequence_Fast_GET_SIZE(o);
+    held = PySequence_Tuple(o);
+    if (!held) return false;
+    const Py_ssize_t n = PyTuple_GET_SIZE(held);
     if (n == 0) return false;
-    PyObject** items = PySequence_Fast_ITEMS(o);
     ptrs.reserve(n);
     numels.reserve(n);
     codes.reserve(n);
     for (Py_ssize_t i = 0; i < n; ++i) {
-      if (!THPVariable_CheckExact(items[i])) return false;
-      const at::Tensor& t = THPVariable_Unpack(items[i]);
+      if (!THPVariable_CheckExact(PyTuple_GET_ITEM(held, i))) return false;
+      const at::Tensor& t = tensor(i);
       const int code = code_of(t);
       if (code < 0 || !t.is_cuda() || !t.is_contiguous()) return false;
       if (device < 0) device = t.get_device();
       if (t.get_device() != device) return false;
-      if (!first) first = &t;
       ptrs.push_back(t.data_ptr());
       numels.push_back(t.numel());
       codes.push_back(code);
@@ -309,12 +347,16 @@ PyObject* grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     List g;
     if (n != 1 || !g.read(a[0], -1)) return nullptr;
     const int64_t count = (int64_t)g.ptrs.size();
-    const int device = (int)g.first->get_device();
-    at::Tensor norm = empty({}, at::kFloat, device);
-    at::Tensor ws = bytes(entry.grad_ws(count), device);
-    st = entry.grad_norm(g.ptrs.data(), g.numels.data(), g.codes.data(), count,
-                         static_cast<float*>(norm.data_ptr()), ws.data_ptr(), (size_t)ws.numel(),
-                         c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream());
+    const int device = (int)g.tensor(0).get_device();
+    at::Tensor norm, ws;
+    {
+      const Unlocked unlocked;
+      norm = empty({}, at::kFloat, device);
+      ws = bytes(entry.grad_ws(count), device);
+      st = entry.grad_norm(g.ptrs.data(), g.numels.data(), g.codes.data(), count,
+                           static_cast<float*>(norm.data_ptr()), ws.data_ptr(), (size_t)ws.numel(),
+                           c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream());
+    }
     return st == RMSN_OK ? wrap(norm) : nullptr;
   });
 }
@@ -325,7 +367,7 @@ PyObject* grad_clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
     List g, o;
     double v[2];
     if (n != 5 || !g.read(a[0], -1) || !numbers(a + 1, 2, v)) return nullptr;
-    const int device = g.first->get_device();
+    const int device = (int)g.tensor(0).get_device();
     const int64_t count = (int64_t)g.ptrs.size();
     const bool in_place = a[3] == Py_None;
     if (!in_place) {
@@ -338,22 +380,27 @@ PyObject* grad_clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                    total.t->get_device() != device)))
       return nullptr;
     const List& out = in_place ? g : o;
-    at::Tensor norm = empty({}, at::kFloat, device), ws;
-    if (!total) ws = bytes(entry.grad_ws(count), device);
+    at::Tensor norm, ws;
+    {
+      const Unlocked unlocked;
+      norm = empty({}, at::kFloat, device);
+      if (!total) ws = bytes(entry.grad_ws(count), device);
+    }
     PyObject* result = wrap(norm);  // before the call: in place there is no second one
     if (!result) return nullptr;
-    st = entry.grad_clip(
-        g.ptrs.data(), g.numels.data(), g.codes.data(), out.ptrs.data(), out.codes.data(), count,
-        (float)v[0], (float)v[1], static_cast<const float*>(total.ptr()),
-        static_cast<float*>(norm.data_ptr()), ptr(ws), ws.defined() ? (size_t)ws.numel() : 0,
-        c10::cuda::getCurrentCUDAStream(device).stream());
+    {
+      const Unlocked unlocked;
+      st = entry.grad_clip(
+          g.ptrs.data(), g.numels.data(), g.codes.data(), out.ptrs.data(), out.codes.data(), count,
+          (float)v[0], (float)v[1], static_cast<const float*>(total.ptr()),
+          static_cast<float*>(norm.data_ptr()), ptr(ws), ws.defined() ? (size_t)ws.numel() : 0,
+          c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream());
+    }
     if (st != RMSN_OK) {
       Py_DECREF(result);
       return nullptr;
     }
-    PyObject* outs = in_place ? a[0] : a[3];
-    for (int64_t i = 0; i < count; ++i)
-      written(THPVariable_Unpack(PySequence_Fast_GET_ITEM(outs, (Py_ssize_t)i)));
+    for (int64_t i = 0; i < count; ++i) written(out.tensor((Py_ssize_t)i));
     return result;
   });
 }

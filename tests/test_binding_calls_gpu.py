@@ -2,6 +2,8 @@
 version counters, errors, other threads."""
 import ctypes
 import subprocess
+import threading
+import time
 
 import pytest
 import torch
@@ -114,3 +116,51 @@ def test_a_failed_launch_is_not_made_again(L, stubbed, name):
         calls[name]()
     assert e.value.status == 7 and stubbed["calls"].value == 1
     assert bool((x == 1).all())
+
+
+@pytest.mark.parametrize("name", ["rms_norm_block_fwd", "rms_norm_block_bwd",
+                                  "rms_norm_grad_norm", "rms_norm_grad_clip"])
+def test_other_threads_run_during_a_call(L, stubbed, name):
+    """A launch that waits for room in its queue, say, holds up its thread alone."""
+    calls, _ = calls_of(L)
+    stubbed["waits"].value = 1
+
+    def release():
+        while stubbed["calls"].value == 0:
+            time.sleep(0.001)
+        stubbed["released"].value = 1
+
+    other = threading.Thread(target=release)
+    other.start()
+    try:
+        calls[name]()
+    finally:
+        stubbed["calls"].value += 1
+        other.join()
+    assert stubbed["calls"].value == 2 and stubbed["saw"].value == 1
+
+
+def test_lists_that_change_during_a_call(L, stubbed):
+    """The call keeps what it read: another thread may empty the lists."""
+    stubbed["waits"].value = 1
+    grads = [torch.ones(8, device="cuda") for _ in range(3)]
+    out = [torch.ones(8, device="cuda") for _ in range(3)]
+    kept = list(out)
+
+    def release():
+        while stubbed["calls"].value == 0:
+            time.sleep(0.001)
+        grads.clear()
+        out.clear()
+        stubbed["released"].value = 1
+
+    before = [o._version for o in out]
+    other = threading.Thread(target=release)
+    other.start()
+    try:
+        L.rms_norm_grad_clip(grads, 1.0, out=out)
+    finally:
+        stubbed["calls"].value += 1
+        other.join()
+    assert stubbed["saw"].value == 1 and not grads
+    assert all(o._version > v for o, v in zip(kept, before))
