@@ -4,7 +4,9 @@ One translation unit per source file, compiled in parallel with nvcc for
 sm_103a only, then linked into a shared library next to this file.  The
 CUDA runtime is linked statically, so the library needs only the driver.
 Beside it, _binding.so (binding.cpp, host code against PyTorch's headers)
-takes the usual Python calls to the library's entry points.
+takes the usual Python calls to the library's entry points; where it cannot be
+built (no Python.h, a PyTorch without CUDA) the library is built all the same,
+and those calls go through ctypes.
 Usage: ``python -m bwd_rms_norm_gb300.build [--verbose]``.
 """
 from __future__ import annotations
@@ -72,12 +74,24 @@ def _build_binding() -> None:
     os.replace(tmp, BINDING_PATH)
 
 
+def _try_binding() -> None:
+    """Builds the binding, or says why not and leaves none: one of an earlier
+    build could be of other sources than the library beside it."""
+    try:
+        _build_binding()
+    except Exception as e:
+        sys.stderr.write(f"_binding.so is not built, its calls go through ctypes: {e}\n")
+        if os.path.exists(BINDING_PATH):
+            os.remove(BINDING_PATH)
+
+
 def build(verbose: bool = False) -> str:
-    """Build the shared library; returns its path."""
+    """Build the shared library, and the binding if it can be; returns the
+    library's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sources()
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
-        binding = ex.submit(_build_binding)
+        binding = ex.submit(_try_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
         binding.result()
     tmp = LIB_PATH + ".tmp"
