@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
       if (issued >= stages && lane == 0)
         go = wait_phase_counted(&sh.empty[pos.stage], pos.phase ^ 1u, abort, &g_block_timeouts);
       if (!__shfl_sync(0xffffffffu, go, 0)) break;
+      if (EDGE) __syncwarp();  // lane 0's wait comes before every lane's stores
       unsigned char* st = ring + (size_t)pos.stage * sp.stride;
       uint64_t* full = &sh.full[pos.stage];
       if constexpr (!EDGE) {  // consecutive rows; K is 1 where cs > 1
@@ -186,6 +187,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
           if (DR) bytes += copy_tail(sts + at.dr, dr, from, m, all);
         }
         bytes = __reduce_add_sync(0xffffffffu, bytes);
+        __syncwarp();  // every lane's tails come before lane 0's arrival
         if (lane == 0) mbar_arrive_expect_tx(full, bytes);
         __syncwarp();
         if (lane < walk.n) {

@@ -115,6 +115,7 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) block_fwd_tma(const B
       uint32_t bytes = 0;
       if (lane < n) bytes = copy_tail(sx, x, at, m, all) + copy_tail(sr, res, at, m, all);
       bytes = __reduce_add_sync(0xffffffffu, bytes);
+      __syncwarp();  // every lane's tails come before lane 0's arrival
       if (lane == 0) mbar_arrive_expect_tx(full, bytes);
       __syncwarp();
       if (lane < n) {
@@ -160,6 +161,7 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) block_fwd_tma(const B
       bool go = true;
       if (lane == 0) go = wait_phase_counted(&sh.empty[stage], phase, abort, &g_block_timeouts);
       if (!__shfl_sync(0xffffffffu, go, 0)) break;
+      if (EDGE) __syncwarp();  // lane 0's wait comes before every lane's stores
       issue(k, stage);
       if (++stage == stages) {
         stage = 0;

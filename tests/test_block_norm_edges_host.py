@@ -33,3 +33,22 @@ def test_offsets_that_are_0_or_1(L, offset):
     x, w = torch.zeros(4, 8), torch.ones(8)
     with pytest.raises(RuntimeError, match="CUDA"):              # past the offset
         L.rms_norm_block_fwd(x, x, w, None, w, 1e-6, offset)
+
+
+@pytest.mark.parametrize("source", ["block_fwd_tma.cu", "block_bwd_tma.cuh"])
+def test_order_of_the_odd_widths_copies(source):
+    """A stage of odd rows is filled by the lanes of a warp, of which lane 0
+    alone waits for the stage and arrives on its barrier.  Shuffles and warp
+    reductions do not order memory, so a __syncwarp stands after the wait, before
+    the arrival (the tails stored by other lanes), and after it (the copies)."""
+    import bwd_rms_norm_gb300 as lib
+    path = os.path.join(os.path.dirname(lib.LIB_PATH), "csrc", source)
+    text = re.sub(r"//[^\n]*", "", open(path).read())
+    told = text.index("__shfl_sync(0xffffffffu, go, 0)")
+    assert re.match(r"[^;]*\)\) break;\s*(if \(EDGE\) )?__syncwarp\(\);", text[told:])
+    tails = [m.start() for m in re.finditer(r"\bcopy_tail\(", text)]
+    arrive = text.index("mbar_arrive_expect_tx(full, bytes)")
+    copies = text.index("copy_row(", arrive)
+    assert tails and max(tails) < arrive
+    assert "__syncwarp();" in text[max(tails):arrive]
+    assert "__syncwarp();" in text[arrive:copies]
