@@ -30,7 +30,11 @@
 // although their root does not: a share whose fp32 sum is above 2^60 or below
 // 2^-90 (fp16: cannot be) is summed again scaled by 2^-73 or 2^100 where its
 // squares are lost, and goes to a sum in double beside the pair, which is
-// looked at only where it is not zero.
+// looked at only where it is not zero.  A small share needs no second look once
+// the thread's sum is 2^-20 or more, 2^70 times it: so the zeros of a list (an
+// embedding's unused rows) are read once, but for those before a thread's first
+// other element (a list of nothing else takes 1.45 times as long).  Telling
+// zeros from small values in the first look cost every bf16 list 1 to 2 %.
 #include <algorithm>
 #include <new>
 #include <type_traits>
@@ -159,7 +163,7 @@ __device__ __forceinline__ void add_chunk(GradSum& sum, const void* in, int64_t 
     add_to(sum.hi, sum.lo, s);
   } else if (!wide || isnan(s) || (s > 0x1p60f && !isinf(s))) {
     sum.extra += (double)s;
-  } else {
+  } else if (s > 1.f || sum.hi < 0x1p-20f) {
     const float again = chunk_squares<T>(p, n, s < 1.f ? 0x1p100f : kOverflowScale, policy);
     if (again != 0.f) sum.extra += (double)again * (s < 1.f ? 0x1p-200 : 0x1p146);
   }

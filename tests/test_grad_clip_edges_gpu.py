@@ -69,3 +69,53 @@ def test_norm_and_eps_together_beyond_fp32(L, eps):
     grads = [g.clone() for g in keep]
     L.rms_norm_grad_clip(grads, 2.0, eps=eps, total_norm=total)
     near(grads, keep, factor64(total.double().item(), 2.0, eps))
+
+
+def best_us(f, n=20):
+    times = []
+    for _ in range(n):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        f()
+        b.record()
+        b.synchronize()
+        times.append(a.elapsed_time(b) * 1e3)
+    return sorted(times)[n // 4]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("zero", [0.0, -0.0])
+def test_zeros_are_read_once(L, dtype, zero):
+    """Zeros among other gradients (an embedding's unused rows, a frozen branch)
+    take the time of any others; read twice they take 1.45 times that."""
+    first = torch.full((1 << 25,), 0.01, dtype=dtype, device="cuda")
+    lists = [[first, torch.full((1 << 27,), v, dtype=dtype, device="cuda")] for v in (0.01, zero)]
+    want = norm64(lists[1])
+    assert abs(L.rms_norm_grad_norm(lists[1]).item() - want) <= 19 * U * want
+    for _ in range(3):
+        L.rms_norm_grad_norm(lists[0])
+    a, b = (best_us(lambda g=g: L.rms_norm_grad_norm(g)) for g in lists)
+    assert b <= 1.2 * a, (a, b)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_smallest_values_among_zeros(L, dtype):
+    """Squares that vanish in fp32, one a share of a thread at most, and signs."""
+    tiny = 2.0 ** -149 if dtype is torch.float32 else 2.0 ** -133
+    for at in (0, 1, 7, 8, 4099, 16383, 16384, 29_999):
+        for value in (tiny, -tiny, 2.0 ** -80):
+            g = torch.full((30_000,), -0.0, dtype=dtype, device="cuda")
+            g[at] = value
+            assert L.rms_norm_grad_norm([g]).item() == abs(value)
+            assert L.rms_norm_grad_norm([g[1:], g[:1]]).item() == abs(value)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("large", [2.0 ** -5, 2.0 ** -9, 2.0 ** -12, 2.0 ** -20, 2.0 ** -40])
+@pytest.mark.parametrize("small", [2.0 ** -46, 2.0 ** -60, 2.0 ** -90])
+def test_small_shares_beside_larger_ones(L, dtype, large, small):
+    """Around the sums from which a small share is taken as it is."""
+    g = torch.full((30_000_000,), small, dtype=dtype, device="cuda")
+    g[:20_000_000:64] = large
+    want = norm64([g])
+    assert abs(L.rms_norm_grad_norm([g]).item() - want) <= 19 * U * want
