@@ -1,7 +1,7 @@
 // The usual calls of the block norm and of the gradient norm and clip, from
 // Python straight to the C entry points: a short call costs what it costs on
-// the host (8 x 4096: 20 us through ctypes, 6 here, 2.9 with outputs given; the
-// kernel takes 4).
+// the host (8 x 4096: 20 us through ctypes, 6.3 here; with outputs given 4.4, of
+// which the kernel takes 4.2).
 //
 // Argument marshalling only, and only of arguments that need no second look:
 // plain contiguous CUDA tensors of one device, the current one, with matching

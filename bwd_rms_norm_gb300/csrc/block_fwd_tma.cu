@@ -274,6 +274,10 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) block_fwd_tma(const B
             for (int i = 0; i < N; ++i) sums[i] = fma2(x[i], x[i], sums[i]);
           });
           const float ss = over_team(sum_pairs<N>(sums));
+          // The approximate root (2 ulp) of a mean by 1 / H, well inside the
+          // error of the sum; the loops and rms_norm_fwd divide and round the
+          // root correctly, which here every row waits for twice: 4096 x 4096
+          // bf16 28.3 us, 28.8 with it.
           rs1 = rsqrtf(fmaf(ss, inv, p.eps));
           if (__any_sync(0xffffffffu, isinf(ss))) {  // squares overflowed (kOverflowScale)
             float again = 0.f;

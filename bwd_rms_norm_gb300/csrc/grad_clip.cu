@@ -33,7 +33,7 @@
 // looked at only where it is not zero.  A small share needs no second look once
 // the thread's sum is 2^-20 or more, 2^70 times it: so the zeros of a list (an
 // embedding's unused rows) are read once, but for those before a thread's first
-// other element (a list of nothing else takes 1.45 times as long).  Telling
+// other element (a list of nothing else takes 1.2 to 1.45 times as long).  Telling
 // zeros from small values in the first look cost every bf16 list 1 to 2 %.
 #include <algorithm>
 #include <new>

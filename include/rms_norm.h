@@ -333,8 +333,9 @@ int group_norm_bwd(const void* dy, const void* x, const void* gamma,
  *   r = residual_scale * residual + branch_scale * gate * z
  *   y = r * rstd_next * gain(gamma_next)        (no y if gamma_next is NULL)
  *
- * with rstd_post and rstd_next as rstd of rms_norm_fwd, of x and of r, and
- * gain(g) = g or 1 + g (offset 1).  At least one of the two norms is given.
+ * with rstd_post and rstd_next as rstd of rms_norm_fwd, of x and of r (to a few
+ * units of fp32's last place, not to the bit), and gain(g) = g or 1 + g (offset
+ * 1).  At least one of the two norms is given.
  * `gate` (may be NULL: ones) is [gate_rows, hidden]: gate_rows divides rows,
  * and each run of rows / gate_rows consecutive rows uses one of its rows
  * (gate_rows 1: a gate for each channel; the batch size: one for each
