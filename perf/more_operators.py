@@ -232,11 +232,11 @@ def _run_own(s, op):
             s["rstd_k"], s["inv_freq"], s["positions"], offset=s["offset"],
             interleaved=s["interleaved"])
     if op == "embed_fwd":
-        return rmsn.embedding_fwd(s["ids"], s["weight"], scale=s["scale"], dtype=DTYPES[s["out"]])
+        return rmsn.rms_norm_embedding_fwd(s["ids"], s["weight"], scale=s["scale"], dtype=DTYPES[s["out"]])
     if s["accumulate"]:
-        return rmsn.embedding_bwd(s["dy"], s["ids"], s["vocab"], scale=s["scale"],
+        return rmsn.rms_norm_embedding_bwd(s["dy"], s["ids"], s["vocab"], scale=s["scale"],
                                   dweight=s["dweight"], accumulate=True)
-    return rmsn.embedding_bwd(s["dy"], s["ids"], s["vocab"], scale=s["scale"],
+    return rmsn.rms_norm_embedding_bwd(s["dy"], s["ids"], s["vocab"], scale=s["scale"],
                               dtype=DTYPES[s["out"]])
 
 
