@@ -40,12 +40,24 @@ The functions carry the names of the C entry points declared in
 * ``rms_norm_grad_norm(grads)`` -> ``norm``; ``rms_norm_grad_clip(grads,
   max_norm, ...)`` -> ``norm`` (the 2-norm over a list of gradients, and the
   list scaled down to a largest norm); ``rms_norm_grad_workspace_size(count)``
+* ``rms_norm_rotary_fwd(q, k, q_gamma, k_gamma, inv_freq, positions, ...)``
+  -> ``(q_out, k_out, rstd_q, rstd_k)``; ``rms_norm_rotary_bwd(dq_out, dk_out,
+  q, k, q_gamma, k_gamma, rstd_q, rstd_k, inv_freq, positions, ...)`` ->
+  ``(dq, dk, dq_gamma, dk_gamma)``; ``rms_norm_rotary_bwd_workspace_size(batch,
+  tokens, q_heads, k_heads, head_dim)`` (the norms of queries and keys over
+  each head, with the rotation by the token's position)
+* ``rms_norm_embedding_fwd(ids, weight, scale)`` -> ``y``;
+  ``rms_norm_embedding_bwd(dy, ids, vocab, scale, ...)`` -> ``dweight``;
+  ``rms_norm_embedding_bwd_workspace_size(tokens, vocab, hidden)`` (the rows of
+  a table for a batch of tokens, and its gradient)
 
 For autograd: ``rms_norm(x, weight, eps, offset=0, cast_mode="round_once")``
 (a ``torch.autograd.Function`` over rms_norm_fwd / rms_norm_bwd) and the
 module ``RMSNorm(hidden, eps, offset=0, cast_mode="round_once")``; likewise
 ``rms_norm_block`` and the module ``RMSNormBlock`` over rms_norm_block_fwd /
-rms_norm_block_bwd.
+rms_norm_block_bwd, ``rms_norm_rotary`` and ``RMSNormRotary`` over
+rms_norm_rotary_fwd / rms_norm_rotary_bwd, ``rms_norm_embedding`` and
+``RMSNormEmbedding`` over rms_norm_embedding_fwd / rms_norm_embedding_bwd.
 """
 from __future__ import annotations
 
@@ -71,6 +83,8 @@ RMSN_MAX_HIDDEN = 65536
 RMSN_MAX_PARTIALS = 1024
 RMSN_DW_CHUNK_BLOCKS = 32
 RMSN_BLOCK_MAX_PARTIALS = 608
+RMSN_ROTARY_MAX_DIM = 1024
+RMSN_EMBEDDING_MAX_VOCAB = 1 << 30
 
 DTYPE_CODES = {torch.float32: RMSN_F32, torch.bfloat16: RMSN_BF16, torch.float16: RMSN_F16}
 CAST_MODES = {"round_once": RMSN_ROUND_ONCE, "round_twice": RMSN_ROUND_TWICE}
@@ -108,6 +122,12 @@ EXPORTED = (
     "rms_norm_grad_workspace_size",
     "rms_norm_grad_norm",
     "rms_norm_grad_clip",
+    "rms_norm_rotary_fwd",
+    "rms_norm_rotary_bwd_workspace_size",
+    "rms_norm_rotary_bwd",
+    "rms_norm_embedding_fwd",
+    "rms_norm_embedding_bwd_workspace_size",
+    "rms_norm_embedding_bwd",
 )
 
 
@@ -117,6 +137,13 @@ class RMSNormError(RuntimeError):
     def __init__(self, fn: str, status: int):
         self.status = status
         super().__init__(f"{fn}: status {status} ({rms_norm_status_string(status)})")
+
+
+class _Heads(ctypes.Structure):
+    """rmsn_heads: a tensor of heads and its strides in elements."""
+
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -221,6 +248,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.rms_norm_grad_norm.restype = I
     lib.rms_norm_grad_clip.argtypes = [P, P, P, P, P, I64, F, F, P, P, P, SZ, P]
     lib.rms_norm_grad_clip.restype = I
+    H = ctypes.POINTER(_Heads)
+    lib.rms_norm_rotary_fwd.argtypes = [H, H, P, P, P, I, P, I, I64, H, H, P, P, I64, I64, I64,
+                                        I64, I64, I64, I, F, I, I, P]
+    lib.rms_norm_rotary_fwd.restype = I
+    lib.rms_norm_rotary_bwd_workspace_size.argtypes = [I64, I64, I64, I64, I64]
+    lib.rms_norm_rotary_bwd_workspace_size.restype = SZ
+    lib.rms_norm_rotary_bwd.argtypes = [H, H, H, H, P, P, P, P, P, I, P, I, I64, H, H, P, P, I64,
+                                        I64, I64, I64, I64, I64, I, I, I, P, SZ, P]
+    lib.rms_norm_rotary_bwd.restype = I
+    lib.rms_norm_embedding_fwd.argtypes = [P, I, P, P, I64, I64, I64, F, I, I, P]
+    lib.rms_norm_embedding_fwd.restype = I
+    lib.rms_norm_embedding_bwd_workspace_size.argtypes = [I64, I64, I64]
+    lib.rms_norm_embedding_bwd_workspace_size.restype = SZ
+    lib.rms_norm_embedding_bwd.argtypes = [P, P, I, P, I64, I64, I64, F, I64, I, I, I, P, SZ, P]
+    lib.rms_norm_embedding_bwd.restype = I
     _load_binding(lib)
     _lib = lib
     return lib
@@ -1160,6 +1202,328 @@ def rms_norm_grad_clip(grads, max_norm: float, eps: float = 1e-6, out=None,
     return norm
 
 
+def _check_strided(name: str, t: torch.Tensor, device: torch.device) -> None:
+    if not t.is_cuda:
+        raise RuntimeError(f"{name} must be a CUDA tensor (this library has no CPU path)")
+    if t.device != device:
+        raise RuntimeError(f"{name} is on {t.device}, the other tensors on {device}")
+
+
+def _check_heads(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape,
+                 device: torch.device) -> None:
+    """A tensor of heads: of any strides but the last dimension's."""
+    if t is None:
+        raise RuntimeError(f"{name} is missing")
+    if t.dtype != dtype:
+        raise RuntimeError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise RuntimeError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    _check_strided(name, t, device)
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise RuntimeError(f"{name} must be contiguous in its last dimension")
+
+
+def _heads_of(t: Optional[torch.Tensor]):
+    """The C call's view of a tensor of heads."""
+    if t is None:
+        return None
+    st = t.stride()
+    return _Heads(t.data_ptr(), st[0] if t.dim() == 4 else 0, st[-3], st[-2])
+
+
+class _RotaryCall:
+    """Sizes of a head-norm call, with the checks its two directions share."""
+
+    __slots__ = ("batch", "tokens", "q_heads", "k_heads", "dim", "rotary", "pos_stride")
+
+    def __init__(self, q, k, q_gamma, k_gamma, inv_freq, positions):
+        dev = q.device
+        if q.dtype not in DTYPE_CODES:
+            raise RuntimeError(f"q must be float32, bfloat16 or float16, not {q.dtype}")
+        if q.dim() not in (3, 4):
+            raise RuntimeError("q must be [tokens, heads, head_dim] or [batch, tokens, heads, "
+                               f"head_dim], not of shape {tuple(q.shape)}")
+        _check_heads("q", q, q.dtype, q.shape, dev)
+        self.dim, self.q_heads, self.tokens = q.shape[-1], q.shape[-2], q.shape[-3]
+        self.batch = q.shape[0] if q.dim() == 4 else 1
+        self.k_heads = 0
+        if k is not None:
+            if k.dim() != q.dim():
+                raise RuntimeError(f"k must have {q.dim()} dimensions, not {k.dim()}")
+            self.k_heads = k.shape[-2]
+            _check_heads("k", k, q.dtype, (*q.shape[:-2], self.k_heads, self.dim), dev)
+            if self.k_heads < 1:
+                raise RuntimeError("k has no heads: leave it out")
+        if (k is None) != (k_gamma is None):
+            raise RuntimeError("k and k_gamma belong together")
+        for name, g in (("q_gamma", q_gamma), ("k_gamma", k_gamma)):
+            if g is not None:
+                _check_like(name, g, q.dtype, self.dim, (self.dim,))
+                _check_cuda(name, g, dev)
+        self.rotary = 0
+        if inv_freq is not None:
+            if inv_freq.dtype not in (torch.float32, torch.float64):
+                raise RuntimeError(f"inv_freq must be float32 or float64, not {inv_freq.dtype}")
+            if inv_freq.dim() != 1 or 2 * inv_freq.numel() > self.dim:
+                raise RuntimeError(f"inv_freq must be one value a pair, at most {self.dim // 2}, "
+                                   f"not of shape {tuple(inv_freq.shape)}")
+            _check_cuda("inv_freq", inv_freq, dev)
+            self.rotary = 2 * inv_freq.numel()
+        self.pos_stride = 0
+        if positions is not None:
+            if positions.dtype not in (torch.int32, torch.int64):
+                raise RuntimeError(f"positions must be int32 or int64, not {positions.dtype}")
+            if tuple(positions.shape) not in ((self.tokens,), tuple(q.shape[:-2])):
+                raise RuntimeError(f"positions must have shape {tuple(q.shape[:-2])} or "
+                                   f"{(self.tokens,)}, not {tuple(positions.shape)}")
+            _check_strided("positions", positions, dev)
+            if self.tokens > 1 and positions.stride(-1) != 1:
+                raise RuntimeError("positions must be contiguous in their last dimension")
+            self.pos_stride = positions.stride(0) if positions.dim() == 2 else 0
+
+    def turn(self, inv_freq, positions):
+        """The C call's arguments of the rotation."""
+        return (_address(inv_freq) if self.rotary else None,
+                int(inv_freq is not None and inv_freq.dtype == torch.float64),
+                _address(positions),
+                int(positions is not None and positions.dtype == torch.int64), self.pos_stride)
+
+    def sizes(self):
+        return self.batch, self.tokens, self.q_heads, self.k_heads, self.dim, self.rotary
+
+
+def _flag(fn: str, value) -> int:
+    if value not in (False, True):
+        raise RMSNormError(fn, RMSN_ERR_ARG)
+    return int(value)
+
+
+def rms_norm_rotary_fwd(q: torch.Tensor, k: Optional[torch.Tensor], q_gamma: torch.Tensor,
+                        k_gamma: Optional[torch.Tensor], inv_freq: Optional[torch.Tensor],
+                        positions: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                        offset: int = 0, interleaved: bool = False,
+                        q_out: Optional[torch.Tensor] = None,
+                        k_out: Optional[torch.Tensor] = None,
+                        rstd_q: Optional[torch.Tensor] = None,
+                        rstd_k: Optional[torch.Tensor] = None, with_rstd: bool = True,
+                        stream: Optional[torch.cuda.Stream] = None):
+    """The norms of queries and keys over each head, and the rotation by the
+    token's position.  ``q`` is [tokens, heads, head_dim] or [batch, tokens,
+    heads, head_dim], of any strides but the last dimension's (a view of the
+    packed product, a head's tokens next to one another); ``k``, with heads of
+    its own number, alike, or None together with ``k_gamma``.  ``inv_freq``
+    [pairs] (fp32 or fp64) holds the angle a position for each pair of the
+    head's first ``2 * pairs`` columns, halves of them paired, or neighbours
+    where ``interleaved``; None rotates nothing.  ``positions`` (int32 or
+    int64) is [tokens] or q's leading dimensions; None: 0, 1, ... in every
+    batch entry.  Returns ``(q_out, k_out, rstd_q, rstd_k)``: outputs like
+    ``torch.empty_like`` of the inputs, or those given (any strides; the inputs
+    themselves for a call in place), and the fp32 statistics that the backward
+    reads (None without ``with_rstd``, as in serving)."""
+    lib = load_library()
+    fn = "rms_norm_rotary_fwd"
+    _check_offset(fn, offset)
+    interleaved = _flag(fn, interleaved)
+    call = _RotaryCall(q, k, q_gamma, k_gamma, inv_freq, positions)
+    dev, dtype = q.device, q.dtype
+    given = []
+    for name, t, like in (("q_out", q_out, q), ("k_out", k_out, k)):
+        if t is not None:
+            if like is None:
+                raise RuntimeError(f"{name} is given without k")
+            _check_heads(name, t, dtype, like.shape, dev)
+            given.append(t)
+    for name, t, like in (("rstd_q", rstd_q, q), ("rstd_k", rstd_k, k)):
+        if t is not None:
+            if like is None or not with_rstd:
+                raise RuntimeError(f"{name} is given, but not wanted")
+            _check_like(name, t, torch.float32, like.numel() // call.dim, like.shape[:-1])
+            _check_cuda(name, t, dev)
+            given.append(t)
+    with _On(dev, stream) as handle:
+        q_out = torch.empty_like(q) if q_out is None else q_out
+        k_out = torch.empty_like(k) if k_out is None and k is not None else k_out
+        if with_rstd and rstd_q is None:
+            rstd_q = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+        if with_rstd and rstd_k is None and k is not None:
+            rstd_k = torch.empty(k.shape[:-1], dtype=torch.float32, device=dev)
+        st = lib.rms_norm_rotary_fwd(
+            _heads_of(q), _heads_of(k), _address(q_gamma), _address(k_gamma),
+            *call.turn(inv_freq, positions), _heads_of(q_out), _heads_of(k_out),
+            _address(rstd_q), _address(rstd_k), *call.sizes(), interleaved, float(eps),
+            int(offset), DTYPE_CODES[dtype], handle)
+    if st != RMSN_OK:
+        raise RMSNormError(fn, st)
+    _written(*given)
+    return q_out, k_out, rstd_q, rstd_k
+
+
+def rms_norm_rotary_bwd_workspace_size(batch: int, tokens: int, q_heads: int, k_heads: int,
+                                       head_dim: int) -> int:
+    """Bytes of workspace ``rms_norm_rotary_bwd`` needs."""
+    return int(load_library().rms_norm_rotary_bwd_workspace_size(
+        int(batch), int(tokens), int(q_heads), int(k_heads), int(head_dim)))
+
+
+def rms_norm_rotary_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], q: torch.Tensor,
+                        k: Optional[torch.Tensor], q_gamma: torch.Tensor,
+                        k_gamma: Optional[torch.Tensor], rstd_q: torch.Tensor,
+                        rstd_k: Optional[torch.Tensor], inv_freq: Optional[torch.Tensor],
+                        positions: Optional[torch.Tensor] = None, offset: int = 0,
+                        interleaved: bool = False, dq: Optional[torch.Tensor] = None,
+                        dk: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None):
+    """Backward of ``rms_norm_rotary_fwd`` from the gradients of its outputs, of
+    any strides but the last dimension's.  ``dq`` and ``dk`` may be views of the
+    packed product's gradient, or ``dq_out`` and ``dk_out`` themselves.  Returns
+    ``(dq, dk, dq_gamma, dk_gamma)``, the gammas' gradients fp32 sums."""
+    lib = load_library()
+    fn = "rms_norm_rotary_bwd"
+    _check_offset(fn, offset)
+    interleaved = _flag(fn, interleaved)
+    call = _RotaryCall(q, k, q_gamma, k_gamma, inv_freq, positions)
+    dev, dtype = q.device, q.dtype
+    given = []
+    for names, dy, x, rstd, dx in ((("dq_out", "rstd_q", "dq"), dq_out, q, rstd_q, dq),
+                                   (("dk_out", "rstd_k", "dk"), dk_out, k, rstd_k, dk)):
+        if x is None:
+            for name, t in zip(names, (dy, rstd, dx)):
+                if t is not None:
+                    raise RuntimeError(f"{name} is given without k")
+            continue
+        _check_heads(names[0], dy, dtype, x.shape, dev)
+        if rstd is None:
+            raise RuntimeError(f"{names[1]} is missing")
+        _check_like(names[1], rstd, torch.float32, x.numel() // call.dim, x.shape[:-1])
+        _check_cuda(names[1], rstd, dev)
+        if dx is not None:
+            _check_heads(names[2], dx, dtype, x.shape, dev)
+            given.append(dx)
+    if workspace is not None:
+        _check_cuda("workspace", workspace, dev)
+    with _On(dev, stream) as handle:
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None and k is not None else dk
+        dq_gamma = torch.empty(call.dim, dtype=torch.float32, device=dev)
+        dk_gamma = None if k is None else torch.empty(call.dim, dtype=torch.float32, device=dev)
+        if workspace is None:
+            need = int(lib.rms_norm_rotary_bwd_workspace_size(*call.sizes()[:5]))
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        st = lib.rms_norm_rotary_bwd(
+            _heads_of(dq_out), _heads_of(dk_out), _heads_of(q), _heads_of(k), _address(q_gamma),
+            _address(k_gamma), _address(rstd_q), _address(rstd_k),
+            *call.turn(inv_freq, positions), _heads_of(dq), _heads_of(dk), _address(dq_gamma),
+            _address(dk_gamma), *call.sizes(), interleaved, int(offset), DTYPE_CODES[dtype],
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle)
+    if st != RMSN_OK:
+        raise RMSNormError(fn, st)
+    _written(*given)
+    return dq, dk, dq_gamma, dk_gamma
+
+
+def _check_ids(ids: torch.Tensor) -> None:
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise RuntimeError(f"ids must be int32 or int64, not {ids.dtype}")
+    _check_cuda("ids", ids)
+
+
+def _embedding_dtype(name: str, dtype: torch.dtype, other: torch.dtype) -> None:
+    if dtype not in DTYPE_CODES:
+        raise RuntimeError(f"{name} must be float32, bfloat16 or float16, not {dtype}")
+    if dtype != other and torch.float32 not in (dtype, other):
+        raise RuntimeError(f"{name} is {dtype} beside {other}: one of the two must be float32")
+
+
+def rms_norm_embedding_fwd(ids: torch.Tensor, weight: torch.Tensor, scale: float = 1.0,
+                           dtype: Optional[torch.dtype] = None, y: Optional[torch.Tensor] = None,
+                           stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The rows of ``weight`` [vocab, hidden] at ``ids`` (int32 or int64, any
+    shape), times ``scale``: ``y`` of shape [*ids.shape, hidden] in ``dtype`` (the
+    weight's, or float32 from or to a 16-bit one).  An id outside [0, vocab), as a
+    batch's padding, gives a row of zeros."""
+    lib = load_library()
+    if weight.dim() != 2 or 0 in weight.shape:
+        raise RuntimeError(f"weight must be [vocab, hidden], not of shape {tuple(weight.shape)}")
+    dev, (vocab, hidden) = weight.device, weight.shape
+    shape = (*ids.shape, hidden)
+    dtype = (weight.dtype if y is None else y.dtype) if dtype is None else dtype
+    _embedding_dtype("weight", weight.dtype, weight.dtype)
+    _embedding_dtype("y", dtype, weight.dtype)
+    _check_like("y", y, dtype, ids.numel() * hidden, shape)
+    _check_ids(ids)
+    _check_cuda("weight", weight, ids.device)
+    if y is not None:
+        _check_cuda("y", y, dev)
+    given = y
+    with _On(dev, stream) as handle:
+        y = torch.empty(shape, dtype=dtype, device=dev) if y is None else y
+        st = lib.rms_norm_embedding_fwd(
+            _address(ids), int(ids.dtype == torch.int64), _address(weight), _address(y),
+            ids.numel(), vocab, hidden, float(scale), DTYPE_CODES[weight.dtype],
+            DTYPE_CODES[dtype], handle)
+    if st != RMSN_OK:
+        raise RMSNormError("rms_norm_embedding_fwd", st)
+    _written(given)
+    return y
+
+
+def rms_norm_embedding_bwd_workspace_size(tokens: int, vocab: int, hidden: int) -> int:
+    """Bytes of workspace ``rms_norm_embedding_bwd`` needs."""
+    return int(load_library().rms_norm_embedding_bwd_workspace_size(int(tokens), int(vocab),
+                                                                    int(hidden)))
+
+
+def rms_norm_embedding_bwd(dy: torch.Tensor, ids: torch.Tensor, vocab: int, scale: float = 1.0,
+                           padding_idx: Optional[int] = None,
+                           dtype: Optional[torch.dtype] = None,
+                           dweight: Optional[torch.Tensor] = None, accumulate: bool = False,
+                           workspace: Optional[torch.Tensor] = None,
+                           stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Backward of ``rms_norm_embedding_fwd``: ``dweight`` [vocab, hidden], the
+    sums of ``scale * dy`` over each id's tokens, in ``dtype`` (float32 where it is
+    not given, or dy's, or any under a float32 ``dy``).  Tokens of ``padding_idx``,
+    and of ids outside the table, have no part.  With ``accumulate`` the sums are
+    added to the ``dweight`` given, of which the tokens' rows alone are touched."""
+    lib = load_library()
+    fn = "rms_norm_embedding_bwd"
+    accumulate = _flag(fn, accumulate)
+    if accumulate and dweight is None:
+        raise RuntimeError("accumulate needs the dweight to add to")
+    if dy.dim() < 1 or tuple(dy.shape[:-1]) != tuple(ids.shape):
+        raise RuntimeError(f"dy must have shape {tuple(ids.shape)} + (hidden,), not "
+                           f"{tuple(dy.shape)}")
+    dev, hidden, vocab = dy.device, dy.shape[-1], int(vocab)
+    if dtype is None:
+        dtype = torch.float32 if dweight is None else dweight.dtype
+    _embedding_dtype("dy", dy.dtype, dy.dtype)
+    _embedding_dtype("dweight", dtype, dy.dtype)
+    if padding_idx is not None and not 0 <= padding_idx < vocab:
+        raise RMSNormError(fn, RMSN_ERR_ARG)
+    _check_like("dweight", dweight, dtype, vocab * hidden, (vocab, hidden))
+    _check_ids(ids)
+    _check_cuda("dy", dy, ids.device)
+    for name, t in (("dweight", dweight), ("workspace", workspace)):
+        if t is not None:
+            _check_cuda(name, t, dev)
+    given = dweight
+    with _On(dev, stream) as handle:
+        if dweight is None:
+            dweight = torch.empty((max(vocab, 0), hidden), dtype=dtype, device=dev)
+        if workspace is None:
+            need = int(lib.rms_norm_embedding_bwd_workspace_size(ids.numel(), vocab, hidden))
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        st = lib.rms_norm_embedding_bwd(
+            _address(dy), _address(ids), int(ids.dtype == torch.int64), _address(dweight),
+            ids.numel(), vocab, hidden, float(scale), -1 if padding_idx is None else padding_idx,
+            accumulate, DTYPE_CODES[dy.dtype], DTYPE_CODES[dtype], workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), handle)
+    if st != RMSN_OK:
+        raise RMSNormError(fn, st)
+    _written(given)
+    return dweight
+
+
 class RMSNormFunction(torch.autograd.Function):
     """RMSNorm over the last dimension with this library's forward and
     backward.  The backward's weight gradient, summed in fp32 by the library,
@@ -1295,3 +1659,150 @@ class RMSNormBlock(torch.nn.Module):
         return (f"post={self.post_weight is not None}, gate={self.gate is not None}, "
                 f"next={self.next_weight is not None}, eps={self.eps}, offset={self.offset}, "
                 f"residual_scale={self.residual_scale}, branch_scale={self.branch_scale}")
+
+
+def _rows_contiguous(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """The tensor where its last dimension is contiguous, else a copy."""
+    if t is None or t.shape[-1] <= 1 or t.stride(-1) == 1:
+        return t
+    return t.contiguous()
+
+
+class RMSNormRotaryFunction(torch.autograd.Function):
+    """The head norm and rotation with this library's forward and backward.  The
+    fp32 sums of the backward are cast to the weights' dtype."""
+
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, inv_freq, positions, eps, offset, interleaved):
+        q, k = _rows_contiguous(q), _rows_contiguous(k)
+        q_weight = q_weight.contiguous()
+        k_weight = None if k_weight is None else k_weight.contiguous()
+        q_out, k_out, rstd_q, rstd_k = rms_norm_rotary_fwd(
+            q, k, q_weight, k_weight, inv_freq, positions, eps, offset, interleaved)
+        ctx.save_for_backward(q, k, q_weight, k_weight, rstd_q, rstd_k, inv_freq, positions)
+        ctx.kind = offset, interleaved
+        return q_out if k is None else (q_out, k_out)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq_out, dk_out=None):
+        q, k, q_weight, k_weight, rstd_q, rstd_k, inv_freq, positions = ctx.saved_tensors
+        dq, dk, dwq, dwk = rms_norm_rotary_bwd(
+            _rows_contiguous(dq_out), _rows_contiguous(dk_out), q, k, q_weight, k_weight, rstd_q,
+            rstd_k, inv_freq, positions, *ctx.kind)
+        dwk = None if dwk is None else dwk.to(q.dtype)
+        return dq, dk, dwq.to(q.dtype), dwk, None, None, None, None, None
+
+
+def rms_norm_rotary(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: torch.Tensor,
+                    k_weight: Optional[torch.Tensor], inv_freq: Optional[torch.Tensor],
+                    positions: Optional[torch.Tensor] = None, eps: float = 1e-6, offset: int = 0,
+                    interleaved: bool = False):
+    """Differentiable ``rms_norm_rotary_fwd``: returns ``(q_out, k_out)``, or
+    ``q_out`` alone without ``k``.  Differentiable in q, k and both weights.  A
+    training step captured into a CUDA graph is, as any with autograd, warmed up
+    on a side stream, with no eager graph of the same leaves alive during the
+    capture."""
+    return RMSNormRotaryFunction.apply(q, k, q_weight, k_weight, inv_freq, positions, eps, offset,
+                                       interleaved)
+
+
+class RMSNormRotary(torch.nn.Module):
+    """The norms of an attention's queries and keys over each head, with their
+    rotation: ``rotary_dim`` columns (all of them where it is not given) turn by
+    ``position * base ** (-2 p / rotary_dim)`` for the pair p.  The weights start
+    at 1, or at 0 with ``offset=1``."""
+
+    def __init__(self, head_dim: int, eps: float = 1e-6, offset: int = 0, base: float = 10000.0,
+                 rotary_dim: Optional[int] = None, interleaved: bool = False, device=None,
+                 dtype=None):
+        super().__init__()
+        if offset not in (0, 1):
+            raise ValueError("offset must be 0 or 1")
+        rotary_dim = head_dim // 2 * 2 if rotary_dim is None else rotary_dim
+        if rotary_dim % 2 or not 0 <= rotary_dim <= head_dim:
+            raise ValueError(f"rotary_dim must be even and at most {head_dim}")
+
+        def weight():
+            return torch.nn.Parameter(torch.full((head_dim,), 0.0 if offset else 1.0,
+                                                 device=device, dtype=dtype))
+
+        self.q_weight, self.k_weight = weight(), weight()
+        self.eps, self.offset, self.interleaved = eps, offset, interleaved
+        self.base, self.rotary_dim = base, rotary_dim
+        self.register_buffer("inv_freq", self._frequencies(self.q_weight.device),
+                             persistent=False)
+
+    def _frequencies(self, device) -> torch.Tensor:
+        p = torch.arange(self.rotary_dim // 2, dtype=torch.float64, device=device)
+        return float(self.base) ** (p * (-2.0 / max(self.rotary_dim, 1)))
+
+    def _apply(self, fn, *args, **kwargs):
+        super()._apply(fn, *args, **kwargs)
+        # a change of the weights' dtype leaves the frequencies what they are
+        self.inv_freq = self._frequencies(self.q_weight.device)
+        return self
+
+    def forward(self, q: torch.Tensor, k: torch.Tensor,
+                positions: Optional[torch.Tensor] = None):
+        return rms_norm_rotary(q, k, self.q_weight, self.k_weight, self.inv_freq, positions,
+                               self.eps, self.offset, self.interleaved)
+
+    def extra_repr(self) -> str:
+        return (f"{self.q_weight.numel()}, eps={self.eps}, offset={self.offset}, "
+                f"base={self.base}, rotary_dim={self.rotary_dim}, "
+                f"interleaved={self.interleaved}")
+
+
+class RMSNormEmbeddingFunction(torch.autograd.Function):
+    """The embedding with this library's forward and backward; the weight's
+    gradient, summed in fp32, is written in the weight's dtype."""
+
+    @staticmethod
+    def forward(ctx, ids, weight, scale, padding_idx, dtype):
+        ids, weight = ids.contiguous(), weight.contiguous()
+        ctx.save_for_backward(ids)
+        ctx.table = weight.shape[0], weight.dtype, scale, padding_idx
+        return rms_norm_embedding_fwd(ids, weight, scale, dtype)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        (ids,) = ctx.saved_tensors
+        vocab, dtype, scale, padding_idx = ctx.table
+        dweight = rms_norm_embedding_bwd(dy.contiguous(), ids, vocab, scale, padding_idx, dtype)
+        return None, dweight, None, None, None
+
+
+def rms_norm_embedding(ids: torch.Tensor, weight: torch.Tensor, scale: float = 1.0,
+                       padding_idx: Optional[int] = None,
+                       dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """Differentiable ``rms_norm_embedding_fwd``, in the weight.  Tokens of
+    ``padding_idx`` take their row, and give it no gradient."""
+    return RMSNormEmbeddingFunction.apply(ids, weight, scale, padding_idx, dtype)
+
+
+class RMSNormEmbedding(torch.nn.Module):
+    """A table of ``vocab`` rows, of which a batch of tokens takes its own, times
+    ``scale``; ``out_dtype`` float32 begins an fp32 residual stream under 16-bit
+    weights (as ``RMSNormBlock`` carries it)."""
+
+    def __init__(self, vocab: int, hidden: int, scale: float = 1.0,
+                 padding_idx: Optional[int] = None, out_dtype: Optional[torch.dtype] = None,
+                 init_std: float = 0.02, device=None, dtype=None):
+        super().__init__()
+        if padding_idx is not None and not 0 <= padding_idx < vocab:
+            raise ValueError(f"padding_idx must be in the table, not {padding_idx}")
+        self.weight = torch.nn.Parameter(torch.empty((vocab, hidden), device=device, dtype=dtype))
+        with torch.no_grad():
+            self.weight.normal_(0.0, init_std)
+            if padding_idx is not None:
+                self.weight[padding_idx] = 0.0
+        self.scale, self.padding_idx, self.out_dtype = scale, padding_idx, out_dtype
+
+    def forward(self, ids: torch.Tensor) -> torch.Tensor:
+        return rms_norm_embedding(ids, self.weight, self.scale, self.padding_idx, self.out_dtype)
+
+    def extra_repr(self) -> str:
+        return (f"{self.weight.shape[0]}, {self.weight.shape[1]}, scale={self.scale}, "
+                f"padding_idx={self.padding_idx}, out_dtype={self.out_dtype}")

@@ -1,0 +1,69 @@
+// The head norm and rotation's arguments, and what its kernels share: a
+// token's angles.
+#pragma once
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace rmsn {
+
+// A tensor of heads [batch, tokens, heads, dim], strides in elements.
+struct HeadView {
+  char* p;
+  int64_t sb, st, sh;
+};
+
+// One of the two tensors of a call, queries or keys.
+struct RotarySide {
+  HeadView in, out;      // forward: v and y; backward: v and dv
+  HeadView dy;           // backward
+  const void* gamma;
+  float* rstd;           // [batch * tokens, heads]
+  float* dgamma;         // backward
+  float* partial;        // backward: [CTAs of this side, dim]
+  int heads;
+  int ctas;              // backward: CTAs that take this side
+};
+
+struct RotaryParams {
+  RotarySide side[2];    // queries, keys (heads 0: none)
+  const void* inv_freq;
+  const void* positions; // NULL: the token's index
+  int64_t pos_stride;    // between batch entries
+  int freq64, pos64;
+  int all, tokens;       // batch * tokens, tokens of a batch entry
+  int dim, half;         // half: pairs
+  int interleaved;
+  float eps, off;
+  bool vec_ok;           // 16-byte aligned rows in every tensor of heads
+};
+
+// inv_freq in turns a position, as a fraction of 2^64: the product with a
+// position, modulo 2^64, is the angle modulo a turn, exactly.  1 / (2 pi) is
+// rounded to 53 bits, which is off by a turn * 2^-53 * position * inv_freq / 2 pi.
+__device__ __forceinline__ uint64_t fixed_turns(const RotaryParams& p, int i) {
+  const double f = p.freq64 ? static_cast<const double*>(p.inv_freq)[i]
+                            : (double)static_cast<const float*>(p.inv_freq)[i];
+  double t = f * 0.15915494309189533577;
+  t -= floor(t);
+  if (!(t < 1.0)) t = 0.0;      // a negative t that 1 + t rounds up
+  return (uint64_t)(t * 18446744073709551616.0);
+}
+
+// (cos, sin) of a position's angle, from 32 bits of its turn (2^-33 turns off)
+// as an fp32 part of a half turn (2^-25).
+__device__ __forceinline__ float2 turn_of(uint64_t fixed, int64_t position) {
+  const int part = (int)((fixed * (uint64_t)position) >> 32);
+  float2 cs;
+  sincospif((float)part * 0x1p-31f, &cs.y, &cs.x);
+  return cs;
+}
+
+__device__ __forceinline__ int64_t position_of(const RotaryParams& p, int b, int t) {
+  if (!p.positions) return t;
+  const int64_t at = b * p.pos_stride + t;
+  return p.pos64 ? static_cast<const int64_t*>(p.positions)[at]
+                 : static_cast<const int32_t*>(p.positions)[at];
+}
+
+}  // namespace rmsn

@@ -448,6 +448,107 @@ int rms_norm_grad_clip(const void* const* grads, const int64_t* numels, const in
                        void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Head norm and rotation -- the norms of a transformer's queries and keys,
+ * each head's row by itself, with the rotation by the token's position, in one
+ * pass over both:
+ *
+ *   u[j]  = v[j] * rstd * gain_j,  rstd = 1 / sqrt(mean(v^2) + eps) of the head's
+ *           row v of head_dim values, gain_j = gamma_j + offset
+ *   a     = position * inv_freq[p]   for the pairs p < rotary_dim / 2
+ *   y[i]  = u[i] cos a - u[j] sin a,  y[j] = u[j] cos a + u[i] sin a
+ *           of the pair's columns (i, j) = (p, p + rotary_dim / 2), or
+ *           (2 p, 2 p + 1) where `interleaved`;  y = u in the other columns
+ *
+ * rounded once, as stored.  The angle is exact modulo a turn: fixed-point
+ * turns of 64 bits, so positions up to 2^31 and beyond lose nothing.
+ *
+ * The backward, from the gradients dy of both outputs: du = dy rotated back,
+ *   dv = rstd * (g - vh * mean(g vh)),  g = du * gain,  vh = v * rstd
+ *   dgamma[j] = sum over batch, tokens and heads of du[j] vh[j]   (fp32)
+ *
+ * A tensor of heads is [batch, tokens, heads, head_dim] with strides of its own
+ * in elements (not negative; head_dim is contiguous): queries and keys inside
+ * the packed product, or a head's tokens next to one another, are taken as they
+ * lie.  Queries and keys share batch, tokens, head_dim and dtype, gammas their
+ * dtype; k (and all that goes with it) is NULL with k_heads 0.  rstd_q / rstd_k
+ * are [batch, tokens, heads] fp32, contiguous; the forward's may be NULL (not
+ * wanted).  inv_freq: rotary_dim / 2 finite fp32 values, or fp64 with
+ * inv_freq_64 (NULL with rotary_dim 0).  positions: [tokens] for every batch
+ * entry with positions_batch_stride 0, or a row of tokens for each; int32, or
+ * int64 with positions_64; NULL: 0, 1, ... in each batch entry.
+ *
+ * An output may be its own input, element for element (q_out = q; dq = dq_out
+ * or dq = q); other overlaps of an output with an input or an output are
+ * refused (RMSN_ERR_ARG), as are outputs that overlap themselves.  Views that
+ * share a buffer without sharing an element, as the parts of a packed product
+ * do, are told apart by their strides.
+ *
+ * The sums are taken in an order fixed by the sizes, the GPU's SM count and the
+ * SM budget.  Workspace as in rms_norm_bwd.  batch * tokens * heads is at most
+ * RMSN_MAX_ROWS, head_dim at most RMSN_ROTARY_MAX_DIM; rotary_dim is even and at
+ * most head_dim.  Nothing to do (no tokens) zero-fills the gammas' gradients.
+ */
+#define RMSN_ROTARY_MAX_DIM 1024
+#define RMSN_ROTARY_MAX_PARTIALS 1216
+typedef struct rmsn_heads {
+  void* data;
+  int64_t batch_stride, token_stride, head_stride; /* in elements */
+} rmsn_heads;
+int rms_norm_rotary_fwd(const rmsn_heads* q, const rmsn_heads* k, const void* q_gamma,
+                        const void* k_gamma, const void* inv_freq, int inv_freq_64,
+                        const void* positions, int positions_64,
+                        int64_t positions_batch_stride, const rmsn_heads* q_out,
+                        const rmsn_heads* k_out, float* rstd_q, float* rstd_k, int64_t batch,
+                        int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t head_dim,
+                        int64_t rotary_dim, int interleaved, float eps, int offset, int dtype,
+                        void* stream);
+size_t rms_norm_rotary_bwd_workspace_size(int64_t batch, int64_t tokens, int64_t q_heads,
+                                          int64_t k_heads, int64_t head_dim);
+int rms_norm_rotary_bwd(const rmsn_heads* dq_out, const rmsn_heads* dk_out, const rmsn_heads* q,
+                        const rmsn_heads* k, const void* q_gamma, const void* k_gamma,
+                        const float* rstd_q, const float* rstd_k, const void* inv_freq,
+                        int inv_freq_64, const void* positions, int positions_64,
+                        int64_t positions_batch_stride, const rmsn_heads* dq,
+                        const rmsn_heads* dk, float* dq_gamma, float* dk_gamma, int64_t batch,
+                        int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t head_dim,
+                        int64_t rotary_dim, int interleaved, int offset, int dtype,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Embedding -- the rows that a batch of tokens takes from a table, scaled, and
+ * the table's gradient.
+ *
+ *   y[t]       = round(scale * weight[ids[t]])
+ *   dweight[v] = round(scale * sum over the tokens t with ids[t] == v of dy[t])
+ *                (+ dweight[v] before the rounding, where `accumulate`)
+ *
+ * An id outside [0, vocab) -- the padding of a batch, or a token of another
+ * rank's part of the table -- takes a row of zeros and has no part in the
+ * gradient; neither has a token of id `padding_idx` (negative: none), whose
+ * row the forward takes like any other.
+ *
+ * ids: `tokens` int32, or int64 with ids_64.  weight [vocab, hidden] and y
+ * [tokens, hidden] are contiguous, of the same dtype or one of them fp32; so
+ * are dy [tokens, hidden] and dweight [vocab, hidden].  Without `accumulate`
+ * the whole of dweight is written, zeros where no token is; with it the rows of
+ * the tokens alone are read and written.  A row's terms are added in fp32 in
+ * the order of the tokens, in pieces whose ends are fixed by the tokens' ids,
+ * so that repeated calls give bit-identical results.  hidden is at most
+ * RMSN_MAX_HIDDEN, tokens at most RMSN_MAX_ROWS, vocab at most
+ * RMSN_EMBEDDING_MAX_VOCAB.  Outputs and workspace must not overlap an input or
+ * each other (RMSN_ERR_ARG).  `workspace` as in rms_norm_bwd.
+ */
+#define RMSN_EMBEDDING_MAX_VOCAB (1 << 30)
+int rms_norm_embedding_fwd(const void* ids, int ids_64, const void* weight, void* y,
+                           int64_t tokens, int64_t vocab, int64_t hidden, float scale,
+                           int weight_dtype, int y_dtype, void* stream);
+size_t rms_norm_embedding_bwd_workspace_size(int64_t tokens, int64_t vocab, int64_t hidden);
+int rms_norm_embedding_bwd(const void* dy, const void* ids, int ids_64, void* dweight,
+                           int64_t tokens, int64_t vocab, int64_t hidden, float scale,
+                           int64_t padding_idx, int accumulate, int dy_dtype, int dweight_dtype,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Introspection: the device kernels that the last call of any entry point
  * of this library on the calling thread launched, in launch order (at most
  * four are recorded).  names[i] receives a static, NUL-terminated string
