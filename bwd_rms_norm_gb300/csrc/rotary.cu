@@ -2,7 +2,6 @@
 // row and the rotation by the token's position, one pass over both.
 #include <math.h>
 
-#include "rms_norm.h"
 #include "rotary.cuh"
 
 namespace rmsn {
@@ -15,10 +14,6 @@ constexpr int kMaxHalf = RMSN_ROTARY_MAX_DIM / 2;
 // The columns of pair i.
 __device__ __forceinline__ int2 columns(const RotaryParams& p, int i) {
   return p.interleaved ? make_int2(2 * i, 2 * i + 1) : make_int2(i, i + p.half);
-}
-
-__device__ __forceinline__ int64_t row_at(const HeadView& v, int b, int t, int h) {
-  return b * v.sb + t * v.st + h * v.sh;
 }
 
 // rstd of a row of which this lane has the columns lane, lane + 32, ...
@@ -169,9 +164,11 @@ __global__ void __launch_bounds__(32 * kSumLanes) rotary_sums(const RotaryParams
 int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
 
 template <typename T>
-cudaError_t launch_fwd_t(const RotaryParams& p, cudaStream_t s) {
+cudaError_t launch_fwd_t(int dtype, const RotaryParams& p, cudaStream_t s) {
   int dev = 0;
-  const cudaError_t e = cudaGetDevice(&dev);
+  cudaError_t e = cudaSuccess;
+  if (try_launch_rotary_fwd_vec(dtype, p, s, &e)) return e;
+  e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   auto kern = rotary_fwd_any<T>;
   const int64_t rows = (int64_t)p.all * (p.side[0].heads + p.side[1].heads);
@@ -180,34 +177,20 @@ cudaError_t launch_fwd_t(const RotaryParams& p, cudaStream_t s) {
                        dim3(kThreads), 0, s, 1, p);
 }
 
-// Shares `most` CTAs between queries and keys by their rows; at least one each.
-void share_ctas(RotaryParams& p, int64_t most, int64_t rows_a_cta) {
-  const int64_t all = p.side[0].heads + p.side[1].heads;
-  most = most < 2 ? 2 : least(most, RMSN_ROTARY_MAX_PARTIALS);
-  int64_t left = most;
-  for (int i = 1; i >= 0; --i) {
-    RotarySide& s = p.side[i];
-    if (s.heads == 0) continue;
-    int64_t n = i == 1 ? (most * s.heads + all / 2) / all : left;
-    if (n < 1) n = 1;
-    if (i == 1 && n >= most) n = most - 1;
-    left -= n;
-    s.ctas = (int)least(n, ((int64_t)p.all * s.heads + rows_a_cta - 1) / rows_a_cta);
-  }
-  p.side[1].partial = p.side[0].partial + (int64_t)p.side[0].ctas * p.dim;
-}
-
 template <typename T>
-cudaError_t launch_bwd_t(RotaryParams& p, cudaStream_t s, int* launches) {
+cudaError_t launch_bwd_t(int dtype, RotaryParams& p, cudaStream_t s, int* launches) {
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  auto kern = rotary_bwd_any<T>;
-  const size_t smem = (size_t)kWarps * p.dim * sizeof(float);
-  share_ctas(p, (int64_t)sm_count(dev) * max_blocks_per_sm((const void*)kern, kThreads, smem),
-             kWarps);
-  e = launch_kernel(kern, dim3((unsigned)(p.side[0].ctas + p.side[1].ctas)), dim3(kThreads), smem,
-                    s, 1, p);
+  cudaError_t e = cudaSuccess;
+  if (!try_launch_rotary_bwd_vec(dtype, p, s, &e)) {
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    auto kern = rotary_bwd_any<T>;
+    const size_t smem = (size_t)kWarps * p.dim * sizeof(float);
+    share_ctas(p, (int64_t)sm_count(dev) * max_blocks_per_sm((const void*)kern, kThreads, smem),
+               kWarps);
+    e = launch_kernel(kern, dim3((unsigned)(p.side[0].ctas + p.side[1].ctas)), dim3(kThreads),
+                      smem, s, 1, p);
+  }
   if (e != cudaSuccess) return e;
   *launches += 1;
   e = launch_kernel(rotary_sums, dim3((unsigned)((p.dim + 31) / 32), p.side[1].heads ? 2 : 1),
@@ -421,9 +404,9 @@ int rms_norm_rotary_fwd(const rmsn_heads* q, const rmsn_heads* k, const void* q_
       if (meet(to[i], to[j])) return RMSN_ERR_ARG;
   }
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == RMSN_F32    ? launch_fwd_t<float>(p, cs)
-                        : dtype == RMSN_BF16 ? launch_fwd_t<__nv_bfloat16>(p, cs)
-                                             : launch_fwd_t<__half>(p, cs);
+  const cudaError_t e = dtype == RMSN_F32    ? launch_fwd_t<float>(dtype, p, cs)
+                        : dtype == RMSN_BF16 ? launch_fwd_t<__nv_bfloat16>(dtype, p, cs)
+                                             : launch_fwd_t<__half>(dtype, p, cs);
   if (e != cudaSuccess) return cuda_fail(e);
   set_last_launches(1);
   return RMSN_OK;
@@ -513,9 +496,9 @@ int rms_norm_rotary_bwd(const rmsn_heads* dq_out, const rmsn_heads* dk_out, cons
   }
   p.side[0].partial = static_cast<float*>(workspace);
   int launches = 0;
-  const cudaError_t e = dtype == RMSN_F32    ? launch_bwd_t<float>(p, cs, &launches)
-                        : dtype == RMSN_BF16 ? launch_bwd_t<__nv_bfloat16>(p, cs, &launches)
-                                             : launch_bwd_t<__half>(p, cs, &launches);
+  const cudaError_t e = dtype == RMSN_F32    ? launch_bwd_t<float>(dtype, p, cs, &launches)
+                        : dtype == RMSN_BF16 ? launch_bwd_t<__nv_bfloat16>(dtype, p, cs, &launches)
+                                             : launch_bwd_t<__half>(dtype, p, cs, &launches);
   if (e != cudaSuccess) return cuda_fail(e);
   set_last_launches(launches);
   return RMSN_OK;

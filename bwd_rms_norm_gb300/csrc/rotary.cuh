@@ -4,6 +4,7 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "rms_norm.h"
 
 namespace rmsn {
 
@@ -65,5 +66,35 @@ __device__ __forceinline__ int64_t position_of(const RotaryParams& p, int b, int
   return p.pos64 ? static_cast<const int64_t*>(p.positions)[at]
                  : static_cast<const int32_t*>(p.positions)[at];
 }
+
+__device__ __forceinline__ int64_t row_at(const HeadView& v, int b, int t, int h) {
+  return b * v.sb + t * v.st + h * v.sh;
+}
+
+// Shares `most` CTAs between queries and keys by their heads, at least one
+// each, and places their partial rows; a CTA has `rows_a_cta` rows at least.
+inline void share_ctas(RotaryParams& p, int64_t most, int64_t rows_a_cta) {
+  const int64_t all = p.side[0].heads + p.side[1].heads;
+  if (most > RMSN_ROTARY_MAX_PARTIALS) most = RMSN_ROTARY_MAX_PARTIALS;
+  if (most < 2) most = 2;
+  int64_t left = most;
+  for (int i = 1; i >= 0; --i) {
+    RotarySide& s = p.side[i];
+    if (s.heads == 0) continue;
+    int64_t n = i == 1 ? (most * s.heads + all / 2) / all : left;
+    if (n < 1) n = 1;
+    if (i == 1 && n >= most) n = most - 1;
+    left -= n;
+    const int64_t useful = ((int64_t)p.all * s.heads + rows_a_cta - 1) / rows_a_cta;
+    s.ctas = (int)(n < useful ? n : useful);
+  }
+  p.side[1].partial = p.side[0].partial + (int64_t)p.side[0].ctas * p.dim;
+}
+
+// Kernels of rows of 16-byte vectors (rotary_vec.cu).  Each returns false,
+// having enqueued nothing, where the sizes or the alignment do not suit it;
+// otherwise true with the launch status in *err.
+bool try_launch_rotary_fwd_vec(int dtype, const RotaryParams& p, cudaStream_t s, cudaError_t* err);
+bool try_launch_rotary_bwd_vec(int dtype, RotaryParams& p, cudaStream_t s, cudaError_t* err);
 
 }  // namespace rmsn

@@ -1,0 +1,419 @@
+// Head norm and rotation of rows of 16-byte vectors: a group of G lanes has a
+// head's row, two vectors a lane, 32 / G heads a warp at a time.
+#include <type_traits>
+
+#include "rotary.cuh"
+
+namespace rmsn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+// Where a pair's columns are.
+enum Mode {
+  kHalves = 0,      // (i, i + half) of whole vectors: a lane's first vector is paired with its second
+  kNeighbours = 1,  // (2 i, 2 i + 1): inside a vector
+  kApart = 2        // (i, i + half), half not of whole vectors: through shared memory
+};
+
+// The columns of a lane's two vectors; dim where it has none.
+template <int V, int MODE>
+struct Lane {
+  int a, b;
+  __device__ __forceinline__ Lane(const RotaryParams& p, int l) {
+    const int n = p.dim / V;
+    int va, vb;
+    if constexpr (MODE == kHalves) {
+      const int paired = p.half / V;
+      va = l < paired ? l : 2 * l;            // 2 paired + 2 (l - paired)
+      vb = l < paired ? l + paired : 2 * l + 1;
+    } else {
+      const int per = (n + 1) / 2;
+      va = l < per ? l : n;
+      vb = l < per ? l + per : n;
+    }
+    a = va < n ? va * V : p.dim;
+    b = vb < n ? vb * V : p.dim;
+  }
+};
+
+// Lanes that a row takes.
+int lanes_of(const RotaryParams& p, int v, int mode) {
+  const int n = p.dim / v;
+  if (mode != kHalves) return (n + 1) / 2;
+  const int paired = p.half / v;
+  return paired + (n - 2 * paired + 1) / 2;
+}
+
+// A token's angles: every pair's (cos, sin) in the warp's shared memory, and
+// those of this lane's columns in registers.
+template <int V, int MODE>
+struct Angles {
+  float c[V], s[V];  // kHalves: of the pairs a ..; kNeighbours: a / 2 .., b / 2 ..
+  __device__ __forceinline__ void take(const RotaryParams& p, const uint64_t* turns, float2* cs,
+                                       int64_t position, const Lane<V, MODE>& at, int lane) {
+    __syncwarp();
+    for (int i = lane; i < p.half; i += 32) cs[i] = turn_of(turns[i], position);
+    __syncwarp();
+    if constexpr (MODE != kApart) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        int i;
+        if constexpr (MODE == kHalves) i = at.a + k;
+        else i = k < V / 2 ? at.a / 2 + k : at.b / 2 + k - V / 2;
+        const float2 v = i < p.half ? cs[i] : make_float2(1.f, 0.f);
+        c[k] = v.x;
+        s[k] = v.y;
+      }
+    }
+  }
+  // The lane's columns turned, by SIGN times the angle.
+  template <int SIGN>
+  __device__ __forceinline__ void turn(const RotaryParams& p, const float2* cs, float* row,
+                                       const Lane<V, MODE>& at, float (&x)[V], float (&y)[V]) const {
+    if constexpr (MODE == kHalves) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const float u = x[k], w = y[k], t = SIGN * s[k];
+        x[k] = u * c[k] - w * t;
+        y[k] = w * c[k] + u * t;
+      }
+    } else if constexpr (MODE == kNeighbours) {
+#pragma unroll
+      for (int k = 0; k < V; k += 2) {
+        const float u = x[k], w = x[k + 1], t = SIGN * s[k / 2];
+        x[k] = u * c[k / 2] - w * t;
+        x[k + 1] = w * c[k / 2] + u * t;
+        const float d = y[k], e = y[k + 1], r = SIGN * s[(V + k) / 2];
+        y[k] = d * c[(V + k) / 2] - e * r;
+        y[k + 1] = e * c[(V + k) / 2] + d * r;
+      }
+    } else {
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        if (at.a < p.dim) row[at.a + k] = x[k];
+        if (at.b < p.dim) row[at.b + k] = y[k];
+      }
+      __syncwarp();
+      auto one = [&](int j, float v) {  // column j, of value v
+        if (j >= 2 * p.half) return v;
+        const bool first = j < p.half;
+        const int i = first ? j : j - p.half;
+        const float other = row[first ? j + p.half : i], t = SIGN * cs[i].y;
+        return first ? v * cs[i].x - other * t : v * cs[i].x + other * t;
+      };
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        x[k] = one(at.a + k, x[k]);
+        y[k] = one(at.b + k, y[k]);
+      }
+    }
+  }
+};
+
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int m = G / 2; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  return v;
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 load_at(const T* row, int c, int dim, bool in) {
+  return in && c < dim ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void gains(const RotarySide& s, int c, int dim, float off,
+                                      float (&g)[V]) {
+  unpack<T>(load_at(static_cast<const T*>(s.gamma), c, dim, true), g);
+#pragma unroll
+  for (int k = 0; k < V; ++k) g[k] += off;
+}
+
+// Shared memory of a CTA.
+template <int V, int G, int MODE>
+struct Shared {
+  uint64_t turns[G * V];
+  float2 cs[kWarps][G * V];
+  float row[MODE == kApart ? kWarps : 1][MODE == kApart ? 32 / G : 1][MODE == kApart ? 2 * G * V : 1];
+};
+
+// A warp takes a token's heads [h0, h0 + per_unit) of one side, `kSteps` times
+// 32 / G of them at a time: their loads are under way together, and while the
+// token's angles are found.
+constexpr int kSteps = 4;
+
+template <typename T, int G, int MODE>
+__global__ void __launch_bounds__(kThreads, 2)
+    rotary_fwd_vec(const __grid_constant__ RotaryParams p, int per_unit) {
+  constexpr int V = Traits<T>::kVec, HPS = 32 / G;
+  __shared__ Shared<V, G, MODE> sh;
+  pdl_wait();
+  pdl_trigger();
+  for (int i = threadIdx.x; i < p.half; i += kThreads) sh.turns[i] = fixed_turns(p, i);
+  __syncthreads();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = lane / G;
+  const Lane<V, MODE> at(p, lane % G);
+  float* row = sh.row[MODE == kApart ? warp : 0][MODE == kApart ? group : 0];
+  const int uq = (p.side[0].heads + per_unit - 1) / per_unit;
+  const int ut = uq + (p.side[1].heads + per_unit - 1) / per_unit;
+  const float inv_n = 1.f / (float)p.dim;
+  // units are fewer than rows, and those fewer than 2^31
+  for (uint32_t u = blockIdx.x * kWarps + warp; u < (uint32_t)p.all * ut;
+       u += gridDim.x * kWarps) {
+    const int token = u / (uint32_t)ut, b = token / p.tokens, t = token - b * p.tokens;
+    const int part = u - (uint32_t)token * ut;
+    const RotarySide& s = p.side[part >= uq];
+    const int first = (part >= uq ? part - uq : part) * per_unit;
+    const int end = first + per_unit < s.heads ? first + per_unit : s.heads;
+    const T* in = reinterpret_cast<const T*>(s.in.p) + row_at(s.in, b, t, 0);
+    T* out = reinterpret_cast<T*>(s.out.p) + row_at(s.out, b, t, 0);
+    float* rstd = s.rstd ? s.rstd + (int64_t)token * s.heads : nullptr;
+    Angles<V, MODE> angles;
+    float ga[V], gb[V];
+    for (int h0 = first; h0 < end; h0 += kSteps * HPS) {
+      uint4 va[kSteps], vb[kSteps];
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int h = h0 + i * HPS + group;
+        va[i] = load_at(in + h * s.in.sh, at.a, p.dim, h < end);
+        vb[i] = load_at(in + h * s.in.sh, at.b, p.dim, h < end);
+      }
+      if (h0 == first) {
+        angles.take(p, sh.turns, sh.cs[warp], position_of(p, b, t), at, lane);
+        gains<T>(s, at.a, p.dim, p.off, ga);
+        gains<T>(s, at.b, p.dim, p.off, gb);
+      }
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        if (h0 + i * HPS >= end) break;
+        const int h = h0 + i * HPS + group;
+        float x[V], y[V];
+        unpack<T>(va[i], x);
+        unpack<T>(vb[i], y);
+        float ss = 0.f;
+#pragma unroll
+        for (int k = 0; k < V; ++k) ss = fmaf(x[k], x[k], fmaf(y[k], y[k], ss));
+        ss = group_sum<G>(ss);
+        float rs = __frsqrt_rn(fmaf(ss, inv_n, p.eps));
+        if (__any_sync(0xffffffffu, isinf(ss))) {  // the squares are beyond fp32
+          float s2 = 0.f;
+#pragma unroll
+          for (int k = 0; k < V; ++k) {
+            const float c = x[k] * kOverflowScale, d = y[k] * kOverflowScale;
+            s2 = fmaf(c, c, fmaf(d, d, s2));
+          }
+          s2 = group_sum<G>(s2);
+          if (isinf(ss)) rs = rstd_rescaled(s2, p.dim, p.eps);
+        }
+        if (rstd && lane % G == 0 && h < end) rstd[h] = rs;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          x[k] = x[k] * rs * ga[k];
+          y[k] = y[k] * rs * gb[k];
+        }
+        angles.template turn<1>(p, sh.cs[warp], row, at, x, y);
+        if (h < end && at.a < p.dim) st_vec(out + h * s.out.sh + at.a, pack<T>(x));
+        if (h < end && at.b < p.dim) st_vec(out + h * s.out.sh + at.b, pack<T>(y));
+      }
+    }
+  }
+}
+
+// The backward: a CTA has one side, so that its sums of du vh stay in registers.
+constexpr int kBwdSteps = 2;
+
+template <typename T, int G, int MODE>
+__global__ void __launch_bounds__(kThreads, 2)
+    rotary_bwd_vec(const __grid_constant__ RotaryParams p, int per_unit) {
+  constexpr int V = Traits<T>::kVec, HPS = 32 / G;
+  __shared__ Shared<V, G, MODE> sh;
+  pdl_wait();
+  pdl_trigger();
+  for (int i = threadIdx.x; i < p.half; i += kThreads) sh.turns[i] = fixed_turns(p, i);
+  __syncthreads();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = lane / G;
+  const Lane<V, MODE> at(p, lane % G);
+  float* row = sh.row[MODE == kApart ? warp : 0][MODE == kApart ? group : 0];
+  const bool keys = (int)blockIdx.x >= p.side[0].ctas;
+  const RotarySide& s = p.side[keys];
+  const int cta = blockIdx.x - (keys ? p.side[0].ctas : 0);
+  const int ut = (s.heads + per_unit - 1) / per_unit;
+  const float inv_n = 1.f / (float)p.dim;
+  float ga[V], gb[V], da[V] = {}, db[V] = {};
+  gains<T>(s, at.a, p.dim, p.off, ga);
+  gains<T>(s, at.b, p.dim, p.off, gb);
+  for (uint32_t u = cta * kWarps + warp; u < (uint32_t)p.all * ut; u += s.ctas * kWarps) {
+    const int token = u / (uint32_t)ut, b = token / p.tokens, t = token - b * p.tokens;
+    const int first = (u - (uint32_t)token * ut) * per_unit;
+    const int end = first + per_unit < s.heads ? first + per_unit : s.heads;
+    const T* in = reinterpret_cast<const T*>(s.in.p) + row_at(s.in, b, t, 0);
+    const T* dy = reinterpret_cast<const T*>(s.dy.p) + row_at(s.dy, b, t, 0);
+    T* out = reinterpret_cast<T*>(s.out.p) + row_at(s.out, b, t, 0);
+    const float* rstd = s.rstd + (int64_t)token * s.heads;
+    Angles<V, MODE> angles;
+    for (int h0 = first; h0 < end; h0 += kBwdSteps * HPS) {
+      uint4 va[kBwdSteps], vb[kBwdSteps], wa[kBwdSteps], wb[kBwdSteps];
+      float rs[kBwdSteps];
+#pragma unroll
+      for (int i = 0; i < kBwdSteps; ++i) {
+        const int h = h0 + i * HPS + group;
+        va[i] = load_at(in + h * s.in.sh, at.a, p.dim, h < end);
+        vb[i] = load_at(in + h * s.in.sh, at.b, p.dim, h < end);
+        wa[i] = load_at(dy + h * s.dy.sh, at.a, p.dim, h < end);
+        wb[i] = load_at(dy + h * s.dy.sh, at.b, p.dim, h < end);
+        rs[i] = h < end ? rstd[h] : 0.f;
+      }
+      if (h0 == first) angles.take(p, sh.turns, sh.cs[warp], position_of(p, b, t), at, lane);
+#pragma unroll
+      for (int i = 0; i < kBwdSteps; ++i) {
+        if (h0 + i * HPS >= end) break;
+        const int h = h0 + i * HPS + group;
+        float x[V], y[V], dx[V], dz[V];
+        unpack<T>(wa[i], dx);
+        unpack<T>(wb[i], dz);
+        angles.template turn<-1>(p, sh.cs[warp], row, at, dx, dz);
+        unpack<T>(va[i], x);
+        unpack<T>(vb[i], y);
+        float dot = 0.f;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          x[k] *= rs[i];
+          y[k] *= rs[i];
+          da[k] = fmaf(dx[k], x[k], da[k]);
+          db[k] = fmaf(dz[k], y[k], db[k]);
+          dx[k] *= ga[k];
+          dz[k] *= gb[k];
+          dot = fmaf(dx[k], x[k], fmaf(dz[k], y[k], dot));
+        }
+        const float mean = group_sum<G>(dot) * inv_n;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          dx[k] = rs[i] * (dx[k] - x[k] * mean);
+          dz[k] = rs[i] * (dz[k] - y[k] * mean);
+        }
+        if (h < end && at.a < p.dim) st_vec(out + h * s.out.sh + at.a, pack<T>(dx));
+        if (h < end && at.b < p.dim) st_vec(out + h * s.out.sh + at.b, pack<T>(dz));
+      }
+    }
+  }
+  // the groups of a warp, then the warps of the CTA
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+#pragma unroll
+    for (int m = G; m < 32; m <<= 1) {
+      da[k] += __shfl_xor_sync(0xffffffffu, da[k], m);
+      db[k] += __shfl_xor_sync(0xffffffffu, db[k], m);
+    }
+  __syncthreads();  // the angles give way to the sums
+  auto sums = reinterpret_cast<float(*)[2 * G * V]>(sh.cs);
+  static_assert(sizeof(sh.cs) == kWarps * 2 * G * V * sizeof(float), "a warp's sums");
+  if (group == 0) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      if (at.a < p.dim) sums[warp][at.a + k] = da[k];
+      if (at.b < p.dim) sums[warp][at.b + k] = db[k];
+    }
+  }
+  __syncthreads();
+  for (int j = threadIdx.x; j < p.dim; j += kThreads) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v += sums[w][j];
+    s.partial[(int64_t)cta * p.dim + j] = v;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+template <typename T>
+int mode_of(const RotaryParams& p) {
+  if (p.interleaved || p.half == 0) return kNeighbours;
+  return p.half % Traits<T>::kVec == 0 ? kHalves : kApart;
+}
+
+// Heads of a unit: all of a side's `heads`, unless that leaves warps without one.
+int heads_per_unit(int64_t tokens, int heads, int hps, int steps, int64_t warps) {
+  int n = (heads + hps - 1) / hps;               // steps
+  while (n > 1 && tokens * ((heads + n * hps - 1) / (n * hps)) < 2 * warps) n = (n + 1) / 2;
+  if (n > steps) n = (n + steps - 1) / steps * steps;
+  return n * hps;
+}
+
+template <typename T, int G, int MODE>
+cudaError_t launch_fwd_g(const RotaryParams& p, cudaStream_t s) {
+  auto kern = rotary_fwd_vec<T, G, MODE>;
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int64_t most = (int64_t)sm_count(dev) * max_blocks_per_sm((const void*)kern, kThreads, 0);
+  const int per = heads_per_unit(p.all, p.side[0].heads, 32 / G, kSteps, most * kWarps);
+  const int64_t units = (int64_t)p.all * ((p.side[0].heads + per - 1) / per +
+                                          (p.side[1].heads + per - 1) / per);
+  const int64_t ctas = (units + kWarps - 1) / kWarps;
+  return launch_kernel(kern, dim3((unsigned)(ctas < most ? ctas : most)), dim3(kThreads), 0, s, 1,
+                       p, per);
+}
+
+template <typename T, int G, int MODE>
+cudaError_t launch_bwd_g(RotaryParams& p, cudaStream_t s) {
+  auto kern = rotary_bwd_vec<T, G, MODE>;
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int64_t most = (int64_t)sm_count(dev) * max_blocks_per_sm((const void*)kern, kThreads, 0);
+  const int per = heads_per_unit(p.all, p.side[0].heads, 32 / G, kBwdSteps, most * kWarps);
+  share_ctas(p, most, kWarps * (32 / G));
+  return launch_kernel(kern, dim3((unsigned)(p.side[0].ctas + p.side[1].ctas)), dim3(kThreads), 0,
+                       s, 1, p, per);
+}
+
+// f(G, MODE) of the kernel for a row's lanes.
+template <typename T, typename F>
+bool with_kernel(const RotaryParams& p, F f) {
+  const int mode = mode_of<T>(p), lanes = lanes_of(p, Traits<T>::kVec, mode);
+  auto by_mode = [&](auto g) {
+    if (mode == kHalves) f(g, std::integral_constant<int, kHalves>{});
+    else if (mode == kNeighbours) f(g, std::integral_constant<int, kNeighbours>{});
+    else f(g, std::integral_constant<int, kApart>{});
+    return true;
+  };
+  if (lanes <= 4) return by_mode(std::integral_constant<int, 4>{});
+  if (lanes <= 8) return by_mode(std::integral_constant<int, 8>{});
+  if (lanes <= 16) return by_mode(std::integral_constant<int, 16>{});
+  if (lanes <= 32) return by_mode(std::integral_constant<int, 32>{});
+  return false;
+}
+
+template <typename F>
+bool with_type(int dtype, F f) {
+  if (dtype == RMSN_F32) return f(float{});
+  if (dtype == RMSN_BF16) return f(__nv_bfloat16{});
+  return f(__half{});
+}
+
+}  // namespace
+
+bool try_launch_rotary_fwd_vec(int dtype, const RotaryParams& p, cudaStream_t s, cudaError_t* err) {
+  return p.vec_ok && with_type(dtype, [&](auto t) {
+    using T = decltype(t);
+    return with_kernel<T>(p, [&](auto g, auto m) {
+      *err = launch_fwd_g<T, decltype(g)::value, decltype(m)::value>(p, s);
+    });
+  });
+}
+
+bool try_launch_rotary_bwd_vec(int dtype, RotaryParams& p, cudaStream_t s, cudaError_t* err) {
+  return p.vec_ok && with_type(dtype, [&](auto t) {
+    using T = decltype(t);
+    return with_kernel<T>(p, [&](auto g, auto m) {
+      *err = launch_bwd_g<T, decltype(g)::value, decltype(m)::value>(p, s);
+    });
+  });
+}
+
+}  // namespace rmsn
