@@ -168,6 +168,10 @@ def _load_binding(lib: ctypes.CDLL) -> None:
     module.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.rms_norm_block_fwd, lib.rms_norm_block_bwd, lib.rms_norm_block_bwd_workspace_size,
         lib.rms_norm_grad_norm, lib.rms_norm_grad_clip, lib.rms_norm_grad_workspace_size)))
+    module.init_more(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.rms_norm_rotary_fwd, lib.rms_norm_rotary_bwd, lib.rms_norm_rotary_bwd_workspace_size,
+        lib.rms_norm_embedding_fwd, lib.rms_norm_embedding_bwd,
+        lib.rms_norm_embedding_bwd_workspace_size)))
     _binding = module
 
 
@@ -1321,6 +1325,11 @@ def rms_norm_rotary_fwd(q: torch.Tensor, k: Optional[torch.Tensor], q_gamma: tor
     themselves for a call in place), and the fp32 statistics that the backward
     reads (None without ``with_rstd``, as in serving)."""
     lib = load_library()
+    if _binding is not None and stream is None:
+        got = _binding.rotary_fwd(q, k, q_gamma, k_gamma, inv_freq, positions, eps, offset,
+                                  interleaved, with_rstd, q_out, k_out, rstd_q, rstd_k)
+        if got is not None:
+            return got
     fn = "rms_norm_rotary_fwd"
     _check_offset(fn, offset)
     interleaved = _flag(fn, interleaved)
@@ -1379,6 +1388,11 @@ def rms_norm_rotary_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], q:
     packed product's gradient, or ``dq_out`` and ``dk_out`` themselves.  Returns
     ``(dq, dk, dq_gamma, dk_gamma)``, the gammas' gradients fp32 sums."""
     lib = load_library()
+    if _binding is not None and stream is None:
+        got = _binding.rotary_bwd(dq_out, dk_out, q, k, q_gamma, k_gamma, rstd_q, rstd_k, inv_freq,
+                                  positions, offset, interleaved, dq, dk, workspace)
+        if got is not None:
+            return got
     fn = "rms_norm_rotary_bwd"
     _check_offset(fn, offset)
     interleaved = _flag(fn, interleaved)
@@ -1443,6 +1457,10 @@ def rms_norm_embedding_fwd(ids: torch.Tensor, weight: torch.Tensor, scale: float
     weight's, or float32 from or to a 16-bit one).  An id outside [0, vocab), as a
     batch's padding, gives a row of zeros."""
     lib = load_library()
+    if _binding is not None and stream is None:
+        got = _binding.embedding_fwd(ids, weight, scale, dtype, y)
+        if got is not None:
+            return got
     if weight.dim() != 2 or 0 in weight.shape:
         raise RuntimeError(f"weight must be [vocab, hidden], not of shape {tuple(weight.shape)}")
     dev, (vocab, hidden) = weight.device, weight.shape
@@ -1486,6 +1504,11 @@ def rms_norm_embedding_bwd(dy: torch.Tensor, ids: torch.Tensor, vocab: int, scal
     and of ids outside the table, have no part.  With ``accumulate`` the sums are
     added to the ``dweight`` given, of which the tokens' rows alone are touched."""
     lib = load_library()
+    if _binding is not None and stream is None:
+        got = _binding.embedding_bwd(dy, ids, vocab, scale, padding_idx, dtype, dweight,
+                                     accumulate, workspace)
+        if got is not None:
+            return got
     fn = "rms_norm_embedding_bwd"
     accumulate = _flag(fn, accumulate)
     if accumulate and dweight is None:
