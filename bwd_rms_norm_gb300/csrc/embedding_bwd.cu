@@ -1,0 +1,731 @@
+// Embedding, backward: the table's gradient, summed over the tokens of each id
+// in their order.
+//
+// Up to kFew tokens one kernel does it all: every CTA has the ids in shared
+// memory, and the warp of an id's first token looks the others up.  Beyond, a
+// cluster of CTAs sorts the tokens by id (embedding_sort); warps then sum pieces
+// of 32 sorted entries (embedding_sums): an id whose entries all lie in a piece
+// is done, of one that goes on the piece's part is kept as an open sum, and a
+// third kernel adds those (embedding_joins).  No atomics: an element's order of
+// additions is fixed by the ids.
+//
+// What bounds it is memory: dy is read once, and, unless the caller accumulates,
+// every row of the table is written.  The rows without a token are cleared by
+// warps of their own beside the sort, the sums and the joins, whose latencies
+// this hides.
+#include "cluster.cuh"
+#include "embedding.cuh"
+
+namespace rmsn {
+namespace {
+
+// A lane's E elements of a row from column c on, as they were loaded.
+template <typename T, int E, bool VEC>
+struct Slice {
+  static constexpr int N = VEC ? E * sizeof(T) / 8 : E;
+  uint2 v[VEC ? N : 1];
+  T e[VEC ? 1 : E];
+  __device__ __forceinline__ void load(const T* row, int c, int hidden) {
+    if constexpr (VEC) {
+      if constexpr (N == 1) {
+        v[0] = c < hidden ? *reinterpret_cast<const uint2*>(row + c) : make_uint2(0, 0);
+      } else {
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) {
+          const uint4 q = c < hidden ? *(reinterpret_cast<const uint4*>(row + c) + k)
+                                     : make_uint4(0, 0, 0, 0);
+          v[2 * k] = make_uint2(q.x, q.y);
+          v[2 * k + 1] = make_uint2(q.z, q.w);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) e[i] = c + 32 * i < hidden ? row[c + 32 * i] : Traits<T>::from_f(0.f);
+    }
+  }
+  __device__ __forceinline__ void clear() {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] = make_uint2(0, 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) e[i] = Traits<T>::from_f(0.f);
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[E]) const {
+    if constexpr (VEC) {
+      constexpr int H = 8 / sizeof(T);
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        float g[H];
+        unpack_h<T>(v[k], g);
+#pragma unroll
+        for (int i = 0; i < H; ++i) f[k * H + i] = g[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) f[i] = Traits<T>::to_f(e[i]);
+    }
+  }
+};
+
+template <bool VEC, int E, typename U>
+__device__ __forceinline__ void store_slice(U* row, int c, int hidden, const float (&f)[E]) {
+  if constexpr (VEC && E * sizeof(U) == 8) {
+    if (c < hidden) *reinterpret_cast<uint2*>(row + c) = pack_h<U>(f);
+  } else {
+    store_row<VEC, E>(row, c, hidden, f);
+  }
+}
+
+struct SumParams {
+  const void* dy;
+  Ids ids;
+  const uint32_t* key;    // the tokens' ids in order, `vocab` for those without a part
+  const uint32_t* token;  // the tokens in that order
+  float* open;            // [pieces][2][hidden]: sums of ids that go on before / behind a piece
+  void* dweight;
+  int64_t tokens, vocab, padding_idx;
+  int64_t clear0, clear1; // rows of the table that this kernel's clearing warps look after
+  int hidden, accumulate;
+  float scale;
+};
+
+// A sum as the row of its id; `was`: that row, where the caller accumulates.
+template <bool VEC, int E, typename U>
+__device__ __forceinline__ void finish(const SumParams& p, uint32_t id, int c,
+                                       const Slice<U, E, VEC>& was, float (&f)[E]) {
+  if (p.accumulate) {
+    float g[E];
+    was.get(g);
+#pragma unroll
+    for (int i = 0; i < E; ++i) f[i] = fmaf(f[i], p.scale, g[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) f[i] *= p.scale;
+  }
+  store_slice<VEC, E>(static_cast<U*>(p.dweight) + (int64_t)id * p.hidden, c, p.hidden, f);
+}
+
+// ---------------------------------------------------------------------------
+// few tokens
+// ---------------------------------------------------------------------------
+constexpr int kFew = 512;
+constexpr int kBits = 32768;  // rows whose tokens are looked at together
+
+template <typename T, typename U, bool VEC>
+__global__ void __launch_bounds__(kThreads) embedding_few(const SumParams p) {
+  constexpr int E = kElems<T, U>, A = 8;
+  __shared__ int id[kFew];
+  __shared__ unsigned short list[kWarps][kFew];
+  __shared__ uint32_t bits[kBits / 32];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = (int)p.tokens;
+  for (int i = threadIdx.x; i < kFew; i += kThreads) {
+    const int k = i < n ? p.ids.get(i, p.vocab) : -1;
+    id[i] = k == p.padding_idx ? -1 : k;
+  }
+  U* table = static_cast<U*>(p.dweight);
+  if (!p.accumulate) {  // this CTA's rows without a token
+    const int64_t r0 = p.vocab * blockIdx.x / gridDim.x, r1 = p.vocab * (blockIdx.x + 1) / gridDim.x;
+    constexpr int W = VEC ? 16 / sizeof(U) : 1;  // elements of a store
+    const int units = (p.hidden + W - 1) / W;
+    int g = 1;                                   // lanes a row
+    while (g < 32 && g < units) g *= 2;
+    for (int64_t base = r0; base < r1; base += kBits) {
+      const int rows = (int)(r1 - base < kBits ? r1 - base : kBits);
+      for (int i = threadIdx.x; i < (rows + 31) / 32; i += kThreads) bits[i] = 0;
+      __syncthreads();
+      for (int i = threadIdx.x; i < n; i += kThreads) {
+        const int64_t at = id[i] - base;
+        if (id[i] >= 0 && at >= 0 && at < rows) atomicOr(&bits[at >> 5], 1u << (at & 31));
+      }
+      __syncthreads();
+      for (int r = threadIdx.x / g; r < rows; r += kThreads / g) {
+        if (bits[r >> 5] >> (r & 31) & 1) continue;
+        U* row = table + (base + r) * p.hidden;
+        for (int j = threadIdx.x % g; j < units; j += g) {
+          if constexpr (VEC) st_vec(row + j * W, make_uint4(0, 0, 0, 0));
+          else row[j] = Traits<U>::from_f(0.f);
+        }
+      }
+      __syncthreads();
+    }
+  }
+  __syncthreads();
+  const T* dy = static_cast<const T*>(p.dy);
+  const int slabs = (p.hidden + 32 * E - 1) / (32 * E);
+  for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < (int64_t)n * slabs;
+       u += (int64_t)gridDim.x * kWarps) {
+    const int t = (int)(u / slabs), k = id[t];
+    if (k < 0) continue;
+    bool first = true;
+    for (int j = 0; j < t && first; j += 32)
+      first = !__any_sync(0xffffffffu, j + lane < t && id[j + lane] == k);
+    if (!first) continue;
+    int count = 0;
+    for (int j = t / 32 * 32; j < n; j += 32) {
+      const bool mine = id[j + lane] == k;  // -1 behind the tokens
+      const uint32_t m = __ballot_sync(0xffffffffu, mine);
+      if (mine) list[warp][count + __popc(m & ((1u << lane) - 1))] = (unsigned short)(j + lane);
+      count += __popc(m);
+    }
+    __syncwarp();
+    const int c = first_column<VEC, E>((int)(u % slabs), lane);
+    Slice<U, E, VEC> was;
+    if (p.accumulate) was.load(table + (int64_t)k * p.hidden, c, p.hidden);
+    float sum[E] = {};
+    for (int i0 = 0; i0 < count; i0 += A) {
+      Slice<T, E, VEC> s[A];
+#pragma unroll
+      for (int i = 0; i < A; ++i)
+        if (i0 + i < count) s[i].load(dy + (int64_t)list[warp][i0 + i] * p.hidden, c, p.hidden);
+        else s[i].clear();
+#pragma unroll
+      for (int i = 0; i < A; ++i) {
+        float f[E];
+        s[i].get(f);
+        if (i0 + i < count)
+#pragma unroll
+          for (int j = 0; j < E; ++j) sum[j] += f[j];
+      }
+    }
+    finish<VEC, E, U>(p, k, c, was, sum);
+    __syncwarp();  // the list gives way to the next
+  }
+}
+
+// ---------------------------------------------------------------------------
+// tokens sorted by id
+// ---------------------------------------------------------------------------
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kMaxBits = 9;   // of a digit
+constexpr int kHeld = 8;      // entries of a lane loaded at a time
+
+struct SortParams {
+  Ids ids;
+  int64_t tokens, vocab, padding_idx;
+  uint32_t* key[2];    // ids and tokens, in turn the source and the target of a pass
+  uint32_t* token[2];
+  int passes, bits;    // digits, and bits of each
+  int cluster;
+  char* zero;          // the rows of the table that this kernel clears: `zeros` bytes
+  int64_t zeros;
+};
+
+__device__ __forceinline__ uint32_t ld_peer(const uint32_t* local, uint32_t peer) {
+  const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(local));
+  uint32_t remote, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(a), "r"(peer));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
+  return v;
+}
+
+// Clears [p, p + n), over `ctas` CTAs of which this is number `cta`.
+__device__ __forceinline__ void clear(char* p, int64_t n, int64_t cta, int64_t ctas) {
+  const int64_t edge = (16 - (int64_t)(reinterpret_cast<uintptr_t>(p) & 15)) & 15;
+  const int64_t head = edge < n ? edge : n, vecs = (n - head) / 16, tail = head + vecs * 16;
+  if (cta == 0) {
+    for (int64_t i = threadIdx.x; i < head; i += blockDim.x) p[i] = 0;
+    for (int64_t i = tail + threadIdx.x; i < n; i += blockDim.x) p[i] = 0;
+  }
+  for (int64_t i = cta * blockDim.x + threadIdx.x; i < vecs; i += ctas * blockDim.x)
+    st_vec(p + head + i * 16, make_uint4(0, 0, 0, 0));
+}
+
+// A stable radix sort of the tokens by id, by one cluster of CTAs: each of its
+// warps has a run of consecutive entries, counts its digits, and, once the
+// counts of the warps before it are known, puts its entries in their order
+// behind theirs.  The launch's other clusters clear rows of the table meanwhile.
+__global__ void __launch_bounds__(kSortThreads) embedding_sort(const SortParams p) {
+  extern __shared__ uint32_t smem[];
+  __shared__ uint32_t sums[32];
+  pdl_wait();
+  pdl_trigger();
+  if ((int)blockIdx.x >= p.cluster) {
+    clear(p.zero, p.zeros, blockIdx.x - p.cluster, gridDim.x - p.cluster);
+    return;
+  }
+  const int bins = 1 << p.bits, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t* count = smem + warp * bins;           // this warp's
+  uint32_t* total = smem + kSortWarps * bins;     // the CTA's, read by its peers
+  uint32_t* base = total + bins;
+  const int rank = (int)cta_rank(), d = threadIdx.x;
+  const int64_t share = ((p.tokens + p.cluster * kSortWarps - 1) / (p.cluster * kSortWarps) + 31)
+                        / 32 * 32;
+  const int64_t lo = (rank * kSortWarps + warp) * share;
+  const int64_t hi = lo + share < p.tokens ? lo + share : p.tokens;
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const int shift = pass * p.bits;
+    const bool odd = pass & 1;
+    const uint32_t* key_in = odd ? p.key[0] : p.key[1];
+    const uint32_t* token_in = odd ? p.token[0] : p.token[1];
+    // This lane's next entries, all of their loads under way together.
+    uint32_t key[kHeld], token[kHeld];
+    auto take = [&](int64_t from) {
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) {
+        const int64_t i = from + 32 * k + lane;
+        key[k] = token[k] = 0;
+        if (i >= hi) continue;
+        if (pass > 0) {
+          key[k] = __ldcg(key_in + i);  // another CTA's: not through this SM's L1
+          token[k] = __ldcg(token_in + i);
+        } else {
+          const int id = p.ids.get(i, p.vocab);
+          key[k] = id < 0 || id == p.padding_idx ? (uint32_t)p.vocab : (uint32_t)id;
+          token[k] = (uint32_t)i;
+        }
+      }
+    };
+    // The lanes with this lane's digit; a lane behind the end has none.
+    auto same = [&](bool in, uint32_t digit) {
+      return __match_any_sync(0xffffffffu, in ? digit : 0xffffffffu);
+    };
+    for (int i = lane; i < bins; i += 32) count[i] = 0;
+    __syncwarp();
+    for (int64_t from = lo; from < hi; from += 32 * kHeld) {
+      take(from);
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) {
+        if (from + 32 * k >= hi) break;
+        const bool in = from + 32 * k + lane < hi;
+        const uint32_t digit = (key[k] >> shift) & (bins - 1), m = same(in, digit);
+        if (in && lane == __ffs(m) - 1) count[digit] += __popc(m);
+        __syncwarp();
+      }
+    }
+    __syncthreads();
+    if (d < bins) {
+      uint32_t run = 0;
+#pragma unroll 8
+      for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t n = smem[w * bins + d];
+        smem[w * bins + d] = run;
+        run += n;
+      }
+      total[d] = run;
+    }
+    cluster_sync();
+    uint32_t before = 0, all = 0;
+    if (d < bins)
+#pragma unroll 8
+      for (int c = 0; c < p.cluster; ++c) {
+        const uint32_t n = ld_peer(total + d, c);
+        before += c < rank ? n : 0;
+        all += n;
+      }
+    // entries of smaller digits: an exclusive sum over the threads
+    uint32_t sum = all;
+    for (int k = 1; k < 32; k <<= 1) {
+      const uint32_t n = __shfl_up_sync(0xffffffffu, sum, k);
+      if (lane >= k) sum += n;
+    }
+    if (lane == 31) sums[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+      uint32_t s = sums[lane], own = s;
+      for (int k = 1; k < 32; k <<= 1) {
+        const uint32_t n = __shfl_up_sync(0xffffffffu, s, k);
+        if (lane >= k) s += n;
+      }
+      sums[lane] = s - own;
+    }
+    __syncthreads();
+    if (d < bins) base[d] = sums[warp] + sum - all + before;
+    __syncthreads();
+    uint32_t* key_out = odd ? p.key[1] : p.key[0];
+    uint32_t* token_out = odd ? p.token[1] : p.token[0];
+    for (int64_t from = lo; from < hi; from += 32 * kHeld) {
+      if (share > 32 * kHeld) take(from);  // else they are there
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) {
+        if (from + 32 * k >= hi) break;
+        const bool in = from + 32 * k + lane < hi;
+        const uint32_t digit = (key[k] >> shift) & (bins - 1), m = same(in, digit);
+        const uint32_t at = in ? base[digit] + count[digit] + __popc(m & ((1u << lane) - 1)) : 0;
+        __syncwarp();
+        if (in) {
+          if (lane == __ffs(m) - 1) count[digit] += __popc(m);
+          key_out[at] = key[k];
+          token_out[at] = token[k];
+        }
+        __syncwarp();
+      }
+    }
+    // the target is complete before it is read; the totals, before they change
+    cluster_sync();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// rows without a token
+// ---------------------------------------------------------------------------
+// The first of the sorted keys that is not below `id`, by a whole warp.
+__device__ __forceinline__ int64_t first_not_below(const SumParams& p, uint32_t id, int lane) {
+  int64_t lo = 0, hi = p.tokens;
+  while (lo < hi) {
+    const int64_t at = lo + (hi - lo) * (lane + 1) / 33;
+    const int below = __popc(__ballot_sync(0xffffffffu, p.key[at] < id));
+    const int64_t next = __shfl_sync(0xffffffffu, at, below < 32 ? below : 31);
+    const int64_t prev = __shfl_sync(0xffffffffu, at, below > 0 ? below - 1 : 0);
+    if (below > 0) lo = prev + 1;
+    if (below < 32) hi = next;
+  }
+  return lo;
+}
+
+// One of `warps` warps clears its part of the rows [clear0, clear1) that no
+// token has; rows are of whole 16-byte vectors.  bits: kBits / 32 words of
+// shared memory.
+template <typename U>
+__device__ __forceinline__ void clear_rows(const SumParams& p, uint32_t* bits, int64_t number,
+                                           int64_t warps, int lane) {
+  const int64_t all = p.clear1 - p.clear0;
+  const int64_t r0 = p.clear0 + all * number / warps, r1 = p.clear0 + all * (number + 1) / warps;
+  const int64_t row_bytes = (int64_t)p.hidden * sizeof(U);
+  for (int64_t base = r0; base < r1; base += kBits) {
+    const int rows = (int)(r1 - base < kBits ? r1 - base : kBits);
+    const uint32_t end = (uint32_t)(base + rows);
+    for (int i = lane; i < (rows + 31) / 32; i += 32) bits[i] = 0;
+    __syncwarp();
+    for (int64_t i = first_not_below(p, (uint32_t)base, lane) + lane;; i += 32) {
+      const uint32_t key = i < p.tokens ? p.key[i] : 0xffffffffu;
+      if (key < end) atomicOr(&bits[(key - (uint32_t)base) >> 5], 1u << ((key - (uint32_t)base) & 31));
+      if (!__all_sync(0xffffffffu, key < end)) break;
+    }
+    __syncwarp();
+    for (int r = 0; r < rows;) {
+      const uint32_t w = bits[r >> 5] >> (r & 31);
+      if (w & 1) {  // rows with tokens
+        r += w == 0xffffffffu ? 32 : __ffs(~w) - 1;
+        continue;
+      }
+      int e = r;    // rows without, up to e
+      while (e < rows) {
+        const uint32_t v = bits[e >> 5] >> (e & 31);
+        if (v) {
+          e += __ffs(v) - 1;
+          break;
+        }
+        e = (e | 31) + 1;
+      }
+      if (e > rows) e = rows;
+      char* to = static_cast<char*>(p.dweight) + (base + r) * row_bytes;
+      const int64_t n = (e - r) * row_bytes;
+#pragma unroll 4
+      for (int64_t i = lane * 16; i < n; i += 512) st_vec(to + i, make_uint4(0, 0, 0, 0));
+      r = e;
+    }
+    __syncwarp();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// sums over the tokens of an id
+// ---------------------------------------------------------------------------
+constexpr int kPiece = 32;                 // sorted entries that a warp takes
+constexpr int kSumThreads = kThreads + 32; // and a warp that clears
+constexpr int kSumCtas = 2;                // an SM
+
+// A warp takes 32 E columns of a piece's rows: the sum of an id whose entries
+// all are in the piece goes to the table, that of one that goes on before or
+// behind it to the piece's open sums.
+template <typename T, typename U, bool VEC, bool ACC>
+__global__ void __launch_bounds__(kSumThreads, kSumCtas) embedding_sums(const SumParams p) {
+  constexpr int E = kElems<T, U>, A = ACC ? 4 : 8;  // rows loaded at a time
+  __shared__ uint32_t bits[kBits / 32];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp == kWarps) {
+    if constexpr (VEC && !ACC) clear_rows<U>(p, bits, blockIdx.x, gridDim.x, lane);
+    return;
+  }
+  const T* dy = static_cast<const T*>(p.dy);
+  const U* table = static_cast<const U*>(p.dweight);
+  const int slabs = (p.hidden + 32 * E - 1) / (32 * E);
+  const int64_t pieces = (p.tokens + kPiece - 1) / kPiece;
+  for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < pieces * slabs;
+       u += (int64_t)gridDim.x * kWarps) {
+    const int64_t piece = u / slabs, at = piece * kPiece;
+    const int c = first_column<VEC, E>((int)(u - piece * slabs), lane);
+    const uint32_t none = (uint32_t)p.vocab;
+    const uint32_t key = at + lane < p.tokens ? p.key[at + lane] : none;
+    const uint32_t token = at + lane < p.tokens ? p.token[at + lane] : 0;
+    const uint32_t before = at > 0 ? p.key[at - 1] : none;
+    const uint32_t behind = at + kPiece < p.tokens ? p.key[at + kPiece] : none;
+    uint32_t next = __shfl_down_sync(0xffffffffu, key, 1);
+    if (lane == 31) next = behind;
+    const int n = __popc(__ballot_sync(0xffffffffu, key < none));  // they come first
+    const uint32_t ends = __ballot_sync(0xffffffffu, key != next);
+    const bool open_left = n > 0 && before == __shfl_sync(0xffffffffu, key, 0);
+    // entries whose id is done with them: ends, but of the id that began before
+    const uint32_t done = open_left ? ends & (ends - 1) : ends;
+    bool left = open_left;
+    float sum[E] = {};
+    for (int i0 = 0; i0 < n; i0 += A) {
+      Slice<T, E, VEC> s[A];
+      Slice<U, E, VEC> was[ACC ? A : 1];
+#pragma unroll
+      for (int k = 0; k < A; ++k) {
+        const int64_t t = __shfl_sync(0xffffffffu, token, i0 + k);
+        if (i0 + k < n) s[k].load(dy + t * p.hidden, c, p.hidden);
+        if constexpr (ACC) {
+          const int64_t id = __shfl_sync(0xffffffffu, key, i0 + k);
+          if (i0 + k < n && (done >> (i0 + k) & 1)) was[k].load(table + id * p.hidden, c, p.hidden);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < A; ++k) {
+        const int i = i0 + k;
+        if (i >= n) break;
+        float f[E];
+        s[k].get(f);
+#pragma unroll
+        for (int j = 0; j < E; ++j) sum[j] += f[j];
+        const bool end = ends >> i & 1;
+        if (!end && i + 1 < kPiece) continue;
+        if (left || !end)
+          store_slice<VEC, E>(p.open + (piece * 2 + (left ? 0 : 1)) * p.hidden, c, p.hidden, sum);
+        else
+          finish<VEC, E, U>(p, __shfl_sync(0xffffffffu, key, i), c, was[ACC ? k : 0], sum);
+        left = false;
+#pragma unroll
+        for (int j = 0; j < E; ++j) sum[j] = 0.f;
+      }
+    }
+  }
+}
+
+// The ids that go on over several pieces: a warp looks at kLook pieces, takes
+// 128 columns of each one that begins in a piece and goes on behind it, and
+// adds the pieces' open sums in order.
+constexpr int kLook = 4;
+
+template <typename U, bool VEC>
+__global__ void __launch_bounds__(kSumThreads, 2) embedding_joins(const SumParams p) {
+  constexpr int E = 4, A = 16;
+  __shared__ uint32_t bits[kBits / 32];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp == kWarps) {
+    if constexpr (VEC)
+      if (!p.accumulate) clear_rows<U>(p, bits, blockIdx.x, gridDim.x, lane);
+    return;
+  }
+  const U* table = static_cast<const U*>(p.dweight);
+  const int slabs = (p.hidden + 32 * E - 1) / (32 * E);
+  const int64_t pieces = (p.tokens + kPiece - 1) / kPiece;
+  const int64_t looks = (pieces - 1 + kLook - 1) / kLook;
+  for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < looks * slabs;
+       u += (int64_t)gridDim.x * kWarps) {
+    const int64_t look = u / slabs, mine = look * kLook + lane;
+    const int c = first_column<VEC, E>((int)(u - look * slabs), lane);
+    uint32_t key = (uint32_t)p.vocab;  // of the id that begins in piece `mine` and goes on
+    if (lane < kLook && mine + 1 < pieces) {
+      const int64_t at = mine * kPiece;
+      const uint32_t id = p.key[at + kPiece], end = p.key[at + kPiece - 1], first = p.key[at];
+      const uint32_t before = at > 0 ? p.key[at - 1] : (uint32_t)p.vocab;
+      if (end == id && !(first == id && before == id)) key = id;
+    }
+    uint32_t todo = __ballot_sync(0xffffffffu, key < (uint32_t)p.vocab);
+    for (; todo; todo &= todo - 1) {
+      const int who = __ffs(todo) - 1;
+      const int64_t piece = look * kLook + who;
+      const uint32_t id = __shfl_sync(0xffffffffu, key, who);
+      Slice<U, E, VEC> was;
+      if (p.accumulate) was.load(table + (int64_t)id * p.hidden, c, p.hidden);
+      // the last piece that begins with the id: first a look at the next ones, then halving
+      int64_t last = piece + 1, out = pieces;
+      const int64_t ahead = piece + 2 + lane;
+      const bool goes_on = ahead < pieces && p.key[ahead * kPiece] == id;
+      const int more = __popc(__ballot_sync(0xffffffffu, goes_on));
+      last += more;
+      if (more < 32) out = last + 1;
+      while (out - last > 1) {
+        const int64_t mid = last + (out - last) / 2;
+        if (p.key[mid * kPiece] == id) last = mid;
+        else out = mid;
+      }
+      float sum[E];
+      Slice<float, E, VEC> s[A];
+      s[0].load(p.open + (piece * 2 + 1) * p.hidden, c, p.hidden);
+      s[0].get(sum);
+      for (int64_t q = piece + 1; q <= last; q += A) {
+#pragma unroll
+        for (int k = 0; k < A; ++k)
+          if (q + k <= last) s[k].load(p.open + (q + k) * 2 * p.hidden, c, p.hidden);
+#pragma unroll
+        for (int k = 0; k < A; ++k) {
+          if (q + k > last) break;
+          float f[E];
+          s[k].get(f);
+#pragma unroll
+          for (int j = 0; j < E; ++j) sum[j] += f[j];
+        }
+      }
+      finish<VEC, E, U>(p, id, c, was, sum);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+int64_t padded(int64_t tokens) { return (tokens + 3) / 4 * 4; }
+
+size_t workspace_of(int64_t tokens, int64_t hidden) {
+  return 4 * (size_t)padded(tokens) * sizeof(uint32_t) +
+         2 * (size_t)ceil_div(tokens, kPiece) * (size_t)hidden * sizeof(float);
+}
+
+// Bits of the ids and of `vocab` itself.
+int bits_of(int64_t vocab) {
+  int bits = 1;
+  while (((int64_t)1 << bits) <= vocab) ++bits;
+  return bits;
+}
+
+cudaError_t launch_sort(SortParams& p, int sms, cudaStream_t s) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  p.cluster = 1;
+  while (p.cluster < 8 && p.cluster * 2 <= sms &&
+         p.cluster * kSortThreads < p.tokens)  // a token a thread, where there are few
+    p.cluster *= 2;
+  const int bits = bits_of(p.vocab);
+  p.passes = (bits + kMaxBits - 1) / kMaxBits;
+  p.bits = (bits + p.passes - 1) / p.passes;
+  const size_t smem = (size_t)(kSortWarps + 2) * sizeof(uint32_t) << p.bits;
+  const size_t most = (size_t)(kSortWarps + 2) * sizeof(uint32_t) << kMaxBits;
+  if (e == cudaSuccess) e = allow_smem<embedding_sort>(dev, most);
+  if (e != cudaSuccess) return e;
+  int64_t clear = p.zeros > 0 ? least(ceil_div(p.zeros, 64 << 10), sms) : 0;
+  clear = ceil_div(clear, p.cluster) * p.cluster;
+  return launch_kernel(embedding_sort, dim3((unsigned)(p.cluster + clear)), dim3(kSortThreads),
+                       smem, s, p.cluster, p);
+}
+
+// Where the rows are cleared: as many bytes beside the sort and beside the joins
+// as those take time, the rest beside the sums.
+constexpr int64_t kClearSort = 48 << 20, kClearJoins = 40 << 20;
+
+template <typename T, typename U, bool VEC>
+cudaError_t launch_sums(SortParams& sort, SumParams& p, cudaStream_t s, int* launches) {
+  constexpr int E = kElems<T, U>;
+  const int64_t pieces = ceil_div(p.tokens, kPiece), row = (int64_t)p.hidden * sizeof(U);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int sms = sm_count(dev);
+  if (p.tokens <= kFew) {
+    auto kern = embedding_few<T, U, VEC>;
+    const int64_t work = ceil_div(p.tokens * ceil_div(p.hidden, 32 * E), kWarps);
+    const int64_t rows = p.accumulate ? 0 : ceil_div(p.vocab * row, 32 << 10);
+    const int64_t ctas = work > rows ? work : rows;
+    const int64_t most = (int64_t)sms * max_blocks_per_sm((const void*)kern, kThreads, 0);
+    e = launch_kernel(kern, dim3((unsigned)least(ctas, most)), dim3(kThreads), 0, s, 1, p);
+    if (e == cudaSuccess) ++*launches;
+    return e;
+  }
+  int64_t first = p.vocab, last = p.vocab;  // rows cleared beside the sort, and before the joins
+  if (VEC) {
+    first = least(kClearSort / row, p.vocab);
+    const int64_t joins = pieces > 1 ? kClearJoins / row : 0;
+    last = p.vocab - joins > first ? p.vocab - joins : first;
+  }
+  sort.zeros = p.accumulate ? 0 : first * row;
+  e = launch_sort(sort, sms, s);
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  const int at = (sort.passes - 1) & 1;  // where the last pass wrote
+  p.key = sort.key[at];
+  p.token = sort.token[at];
+  p.clear0 = first;
+  p.clear1 = last;
+  auto sums = p.accumulate ? embedding_sums<T, U, VEC, true> : embedding_sums<T, U, VEC, false>;
+  auto launch = [&](auto kern, int64_t units, int64_t clears) {
+    const int64_t most = (int64_t)sms * max_blocks_per_sm((const void*)kern, kSumThreads, 0);
+    int64_t ctas = ceil_div(units, kWarps);
+    if (clears > ctas) ctas = clears;
+    return launch_kernel(kern, dim3((unsigned)least(ctas, most)), dim3(kSumThreads), 0, s, 1, p);
+  };
+  auto clears = [&]() {
+    return p.accumulate ? 0 : ceil_div((p.clear1 - p.clear0) * row, 64 << 10);
+  };
+  e = launch(sums, pieces * ceil_div(p.hidden, 32 * E), clears());
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  p.clear0 = last;
+  p.clear1 = p.vocab;
+  if (pieces > 1) {
+    e = launch(embedding_joins<U, VEC>, ceil_div(pieces - 1, kLook) * ceil_div(p.hidden, 128),
+               clears());
+    if (e == cudaSuccess) ++*launches;
+  }
+  return e;
+}
+
+}  // namespace
+}  // namespace rmsn
+
+extern "C" {
+
+size_t rms_norm_embedding_bwd_workspace_size(int64_t tokens, int64_t vocab, int64_t hidden) {
+  using namespace rmsn;
+  if (tokens == 0 || check(tokens, vocab, hidden, 1.f, 0, RMSN_F32, RMSN_F32) != RMSN_OK) return 0;
+  return workspace_of(tokens, hidden);
+}
+
+int rms_norm_embedding_bwd(const void* dy, const void* ids, int ids_64, void* dweight,
+                           int64_t tokens, int64_t vocab, int64_t hidden, float scale,
+                           int64_t padding_idx, int accumulate, int dy_dtype, int dweight_dtype,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace rmsn;
+  const int st = check(tokens, vocab, hidden, scale, ids_64, dy_dtype, dweight_dtype);
+  if (st != RMSN_OK) return st;
+  if (accumulate != 0 && accumulate != 1) return RMSN_ERR_ARG;
+  begin_call();
+  if (!dweight) return RMSN_ERR_NULL;
+  const int tb = bytes_of(dy_dtype), ub = bytes_of(dweight_dtype), ib = ids_64 ? 8 : 4;
+  if ((uintptr_t)dweight % ub != 0) return RMSN_ERR_ALIGN;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const size_t table = (size_t)vocab * hidden * ub;
+  if (tokens == 0) {
+    const cudaError_t e = accumulate ? cudaSuccess : cudaMemsetAsync(dweight, 0, table, cs);
+    return e == cudaSuccess ? RMSN_OK : cuda_fail(e);
+  }
+  if (!dy || !ids || !workspace) return RMSN_ERR_NULL;
+  if ((uintptr_t)workspace % 16 != 0 || (uintptr_t)ids % ib != 0 || (uintptr_t)dy % tb != 0)
+    return RMSN_ERR_ALIGN;
+  if (workspace_bytes < workspace_of(tokens, hidden)) return RMSN_ERR_WORKSPACE;
+  const Span out(dweight, table), ws(workspace, workspace_bytes);
+  const Span ins[] = {{dy, (size_t)tokens * hidden * tb}, {ids, (size_t)tokens * ib}};
+  if (out.meets(ws)) return RMSN_ERR_ARG;
+  for (const Span& i : ins)
+    if (out.meets(i) || ws.meets(i)) return RMSN_ERR_ARG;
+  uint32_t* w = static_cast<uint32_t*>(workspace);
+  const int64_t n = padded(tokens);
+  SortParams sort = {{ids, ids_64}, tokens, vocab, padding_idx, {w, w + n}, {w + 2 * n, w + 3 * n},
+                     0, 0, 1, static_cast<char*>(dweight), 0};
+  SumParams sum = {dy, {ids, ids_64}, nullptr, nullptr, reinterpret_cast<float*>(w + 4 * n),
+                   dweight, tokens, vocab, padding_idx, 0, 0, (int)hidden, accumulate, scale};
+  int launches = 0;
+  const cudaError_t e = with_types(dy_dtype, dweight_dtype, [&](auto t, auto u) {
+    using T = decltype(t);
+    using U = decltype(u);
+    const bool vec =
+        rows_ok(dy, hidden, tb) && rows_ok(dweight, hidden, ub) && hidden % kElems<T, U> == 0;
+    return vec ? launch_sums<T, U, true>(sort, sum, cs, &launches)
+               : launch_sums<T, U, false>(sort, sum, cs, &launches);
+  });
+  if (e != cudaSuccess) return cuda_fail(e);
+  set_last_launches(launches);
+  return RMSN_OK;
+}
+
+}  // extern "C"
