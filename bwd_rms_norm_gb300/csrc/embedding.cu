@@ -4,25 +4,34 @@
 namespace rmsn {
 namespace {
 
-// A warp takes 32 E columns of a token's row.
-template <typename T, typename U, bool VEC>
+constexpr int kWide = 4;
+
+// A warp takes K times 32 E columns of a token's row, all loads under way together.
+template <typename T, typename U, bool VEC, int K>
 __global__ void __launch_bounds__(kThreads) embedding_rows(Ids ids, const T* __restrict__ weight,
                                                            U* __restrict__ y, int64_t tokens,
                                                            int64_t vocab, int hidden, float scale) {
   constexpr int E = kElems<T, U>;
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, slabs = (hidden + 32 * E - 1) / (32 * E);
+  const int lane = threadIdx.x & 31, slabs = (hidden + 32 * E * K - 1) / (32 * E * K);
   for (int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); u < tokens * slabs;
        u += (int64_t)gridDim.x * kWarps) {
     const int64_t t = u / slabs;
-    const int c = first_column<VEC, E>((int)(u % slabs), lane);
+    const int c = first_column<VEC, E>((int)(u - t * slabs) * K, lane);
     const int id = ids.get(t, vocab);
-    float f[E] = {};
-    if (id >= 0) load_row<VEC, E>(weight + (int64_t)id * hidden, c, hidden, f);
+    float f[K][E] = {};
+    if (id >= 0) {
+      const T* row = weight + (int64_t)id * hidden;
 #pragma unroll
-    for (int i = 0; i < E; ++i) f[i] = id >= 0 ? f[i] * scale : 0.f;
-    store_row<VEC, E>(y + t * hidden, c, hidden, f);
+      for (int k = 0; k < K; ++k) load_row<VEC, E>(row, c + k * 32 * E, hidden, f[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) f[k][i] = id >= 0 ? f[k][i] * scale : 0.f;
+      store_row<VEC, E>(y + t * hidden, c + k * 32 * E, hidden, f[k]);
+    }
   }
 }
 
@@ -53,10 +62,16 @@ int rms_norm_embedding_fwd(const void* ids, int ids_64, const void* weight, void
     using U = decltype(u);
     constexpr int E = kElems<T, U>;
     const bool vec = rows_ok(weight, hidden, wb) && rows_ok(y, hidden, yb) && hidden % E == 0;
-    return launch_units(vec ? embedding_rows<T, U, true> : embedding_rows<T, U, false>,
-                        tokens * ceil_div(hidden, 32 * E), static_cast<cudaStream_t>(stream), of,
-                        static_cast<const T*>(weight), static_cast<U*>(y), tokens, vocab,
-                        (int)hidden, scale);
+    const auto launch = [&](auto kern, int k) {
+      return launch_units(kern, tokens * ceil_div(hidden, 32 * E * k),
+                          static_cast<cudaStream_t>(stream), of, static_cast<const T*>(weight),
+                          static_cast<U*>(y), tokens, vocab, (int)hidden, scale);
+    };
+    constexpr int K = kWide;
+    if (vec && tokens * (hidden / (32 * E * K)) >= 4864)
+      return launch(embedding_rows<T, U, true, K>, K);
+    return vec ? launch(embedding_rows<T, U, true, 1>, 1)
+               : launch(embedding_rows<T, U, false, 1>, 1);
   });
   if (e != cudaSuccess) return cuda_fail(e);
   set_last_launches(1);

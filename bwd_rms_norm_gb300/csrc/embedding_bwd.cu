@@ -15,27 +15,35 @@
 // this hides.
 #include "cluster.cuh"
 #include "embedding.cuh"
+#include "pairs.cuh"
 
 namespace rmsn {
 namespace {
 
-// A lane's E elements of a row from column c on, as they were loaded.
-template <typename T, int E, bool VEC>
+// A lane's E elements of a row, as they were loaded.  VEC: runs of R elements, 8
+// or 16 bytes of the narrower type, that lie 32 R columns apart, from column c
+// on; else every 32nd one.
+template <typename T, int E, int R, bool VEC>
 struct Slice {
-  static constexpr int N = VEC ? E * sizeof(T) / 8 : E;
+  static constexpr int N = E * sizeof(T) / 8;  // 8-byte words
   uint2 v[VEC ? N : 1];
   T e[VEC ? 1 : E];
   __device__ __forceinline__ void load(const T* row, int c, int hidden) {
     if constexpr (VEC) {
-      if constexpr (N == 1) {
-        v[0] = c < hidden ? *reinterpret_cast<const uint2*>(row + c) : make_uint2(0, 0);
-      } else {
+      constexpr int M = R * sizeof(T) / 8;     // words of a run
 #pragma unroll
-        for (int k = 0; k < N / 2; ++k) {
-          const uint4 q = c < hidden ? *(reinterpret_cast<const uint4*>(row + c) + k)
-                                     : make_uint4(0, 0, 0, 0);
-          v[2 * k] = make_uint2(q.x, q.y);
-          v[2 * k + 1] = make_uint2(q.z, q.w);
+      for (int r = 0; r < E / R; ++r) {
+        const int at = c + 32 * R * r;
+        if constexpr (M == 1) {
+          v[r] = at < hidden ? *reinterpret_cast<const uint2*>(row + at) : make_uint2(0, 0);
+        } else {
+#pragma unroll
+          for (int k = 0; k < M / 2; ++k) {
+            const uint4 q = at < hidden ? *(reinterpret_cast<const uint4*>(row + at) + k)
+                                        : make_uint4(0, 0, 0, 0);
+            v[r * M + 2 * k] = make_uint2(q.x, q.y);
+            v[r * M + 2 * k + 1] = make_uint2(q.z, q.w);
+          }
         }
       }
     } else {
@@ -43,39 +51,59 @@ struct Slice {
       for (int i = 0; i < E; ++i) e[i] = c + 32 * i < hidden ? row[c + 32 * i] : Traits<T>::from_f(0.f);
     }
   }
-  __device__ __forceinline__ void clear() {
-    if constexpr (VEC) {
+  __device__ __forceinline__ void get(f32x2 (&f)[E / 2]) const {
+    if constexpr (!VEC) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) v[k] = make_uint2(0, 0);
+      for (int i = 0; i < E / 2; ++i) f[i] = pair(Traits<T>::to_f(e[2 * i]), Traits<T>::to_f(e[2 * i + 1]));
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) f[k] = pair(__uint_as_float(v[k].x), __uint_as_float(v[k].y));
     } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) e[i] = Traits<T>::from_f(0.f);
-    }
-  }
-  __device__ __forceinline__ void get(float (&f)[E]) const {
-    if constexpr (VEC) {
-      constexpr int H = 8 / sizeof(T);
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        float g[H];
-        unpack_h<T>(v[k], g);
-#pragma unroll
-        for (int i = 0; i < H; ++i) f[k * H + i] = g[i];
+        f[2 * k] = widen<T>(v[k].x);
+        f[2 * k + 1] = widen<T>(v[k].y);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) f[i] = Traits<T>::to_f(e[i]);
     }
   }
 };
 
-template <bool VEC, int E, typename U>
-__device__ __forceinline__ void store_slice(U* row, int c, int hidden, const float (&f)[E]) {
-  if constexpr (VEC && E * sizeof(U) == 8) {
-    if (c < hidden) *reinterpret_cast<uint2*>(row + c) = pack_h<U>(f);
+template <bool VEC, int E, int R, typename U>
+__device__ __forceinline__ void store_slice(U* row, int c, int hidden, const f32x2 (&f)[E / 2]) {
+  if constexpr (VEC) {
+    constexpr int P = R / 2;                   // pairs of a run
+#pragma unroll
+    for (int r = 0; r < E / R; ++r) {
+      const int at = c + 32 * R * r;
+      if (at >= hidden) continue;
+      if constexpr (sizeof(U) == 4) {
+#pragma unroll
+        for (int k = 0; k < P; k += 2) {
+          const float2 a = split(f[r * P + k]), b = split(f[r * P + k + 1]);
+          st_vec(row + at + 2 * k, make_uint4(__float_as_uint(a.x), __float_as_uint(a.y),
+                                              __float_as_uint(b.x), __float_as_uint(b.y)));
+        }
+      } else if constexpr (P == 4) {
+        st_vec(row + at, make_uint4(narrow<U>(f[r * P]), narrow<U>(f[r * P + 1]),
+                                    narrow<U>(f[r * P + 2]), narrow<U>(f[r * P + 3])));
+      } else {
+        *reinterpret_cast<uint2*>(row + at) = make_uint2(narrow<U>(f[r * P]), narrow<U>(f[r * P + 1]));
+      }
+    }
   } else {
-    store_row<VEC, E>(row, c, hidden, f);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      const float2 v = split(f[i]);
+      if (c + 64 * i < hidden) row[c + 64 * i] = Traits<U>::from_f(v.x);
+      if (c + 64 * i + 32 < hidden) row[c + 64 * i + 32] = Traits<U>::from_f(v.y);
+    }
   }
+}
+
+// The first of a lane's columns in slab `slab` of 32 E columns.
+template <int E, int R, bool VEC>
+__device__ __forceinline__ int column(int slab, int lane) {
+  return slab * 32 * E + (VEC ? lane * R : lane);
 }
 
 struct SumParams {
@@ -83,6 +111,8 @@ struct SumParams {
   Ids ids;
   const uint32_t* key;    // the tokens' ids in order, `vocab` for those without a part
   const uint32_t* token;  // the tokens in that order
+  int piece;              // sorted entries that a warp takes
+  int look;               // pieces that a warp of the joins looks at
   float* open;            // [pieces][2][hidden]: sums of ids that go on before / behind a piece
   void* dweight;
   int64_t tokens, vocab, padding_idx;
@@ -92,19 +122,20 @@ struct SumParams {
 };
 
 // A sum as the row of its id; `was`: that row, where the caller accumulates.
-template <bool VEC, int E, typename U>
+template <bool VEC, int E, int R, typename U>
 __device__ __forceinline__ void finish(const SumParams& p, uint32_t id, int c,
-                                       const Slice<U, E, VEC>& was, float (&f)[E]) {
+                                       const Slice<U, E, R, VEC>& was, f32x2 (&f)[E / 2]) {
+  const f32x2 scale = pair(p.scale, p.scale);
   if (p.accumulate) {
-    float g[E];
+    f32x2 g[E / 2];
     was.get(g);
 #pragma unroll
-    for (int i = 0; i < E; ++i) f[i] = fmaf(f[i], p.scale, g[i]);
+    for (int i = 0; i < E / 2; ++i) f[i] = fma2(f[i], scale, g[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < E; ++i) f[i] *= p.scale;
+    for (int i = 0; i < E / 2; ++i) f[i] = mul2(f[i], scale);
   }
-  store_slice<VEC, E>(static_cast<U*>(p.dweight) + (int64_t)id * p.hidden, c, p.hidden, f);
+  store_slice<VEC, E, R>(static_cast<U*>(p.dweight) + (int64_t)id * p.hidden, c, p.hidden, f);
 }
 
 // ---------------------------------------------------------------------------
@@ -172,26 +203,25 @@ __global__ void __launch_bounds__(kThreads) embedding_few(const SumParams p) {
       count += __popc(m);
     }
     __syncwarp();
-    const int c = first_column<VEC, E>((int)(u % slabs), lane);
-    Slice<U, E, VEC> was;
+    const int c = column<E, E, VEC>((int)(u % slabs), lane);
+    Slice<U, E, E, VEC> was;
     if (p.accumulate) was.load(table + (int64_t)k * p.hidden, c, p.hidden);
-    float sum[E] = {};
+    f32x2 sum[E / 2] = {};
     for (int i0 = 0; i0 < count; i0 += A) {
-      Slice<T, E, VEC> s[A];
+      Slice<T, E, E, VEC> s[A];
 #pragma unroll
       for (int i = 0; i < A; ++i)
         if (i0 + i < count) s[i].load(dy + (int64_t)list[warp][i0 + i] * p.hidden, c, p.hidden);
-        else s[i].clear();
 #pragma unroll
       for (int i = 0; i < A; ++i) {
-        float f[E];
+        if (i0 + i >= count) break;
+        f32x2 f[E / 2];
         s[i].get(f);
-        if (i0 + i < count)
 #pragma unroll
-          for (int j = 0; j < E; ++j) sum[j] += f[j];
+        for (int j = 0; j < E / 2; ++j) sum[j] = add2(sum[j], f[j]);
       }
     }
-    finish<VEC, E, U>(p, k, c, was, sum);
+    finish<VEC, E, E, U>(p, k, c, was, sum);
     __syncwarp();  // the list gives way to the next
   }
 }
@@ -199,7 +229,8 @@ __global__ void __launch_bounds__(kThreads) embedding_few(const SumParams p) {
 // ---------------------------------------------------------------------------
 // tokens sorted by id
 // ---------------------------------------------------------------------------
-constexpr int kSortThreads = 1024;
+constexpr int kSortThreads = 512;
+constexpr int kSortCluster = 16;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxBits = 9;   // of a digit
 constexpr int kHeld = 8;      // entries of a lane loaded at a time
@@ -263,10 +294,11 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort(const SortParams 
     const uint32_t* key_in = odd ? p.key[0] : p.key[1];
     const uint32_t* token_in = odd ? p.token[0] : p.token[1];
     // This lane's next entries, all of their loads under way together.
-    uint32_t key[kHeld], token[kHeld];
+    uint32_t key[kHeld], token[kHeld], peers[kHeld];
     auto take = [&](int64_t from) {
 #pragma unroll
       for (int k = 0; k < kHeld; ++k) {
+        if (from + 32 * k >= hi) break;
         const int64_t i = from + 32 * k + lane;
         key[k] = token[k] = 0;
         if (i >= hi) continue;
@@ -280,9 +312,17 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort(const SortParams 
         }
       }
     };
-    // The lanes with this lane's digit; a lane behind the end has none.
+    // The lanes with this lane's digit, bit by bit (__match_any_sync takes some
+    // 30 cycles of the SM: 32768 tokens 26 us, xx so).
     auto same = [&](bool in, uint32_t digit) {
-      return __match_any_sync(0xffffffffu, in ? digit : 0xffffffffu);
+      uint32_t m = __ballot_sync(0xffffffffu, in);
+#pragma unroll
+      for (int b = 0; b < kMaxBits; ++b) {
+        if (b >= p.bits) break;
+        const uint32_t set = __ballot_sync(0xffffffffu, digit >> b & 1);
+        m &= digit >> b & 1 ? set : ~set;
+      }
+      return m;
     };
     for (int i = lane; i < bins; i += 32) count[i] = 0;
     __syncwarp();
@@ -294,6 +334,7 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort(const SortParams 
         const bool in = from + 32 * k + lane < hi;
         const uint32_t digit = (key[k] >> shift) & (bins - 1), m = same(in, digit);
         if (in && lane == __ffs(m) - 1) count[digit] += __popc(m);
+        peers[k] = m;
         __syncwarp();
       }
     }
@@ -310,13 +351,16 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort(const SortParams 
     }
     cluster_sync();
     uint32_t before = 0, all = 0;
-    if (d < bins)
-#pragma unroll 8
-      for (int c = 0; c < p.cluster; ++c) {
-        const uint32_t n = ld_peer(total + d, c);
-        before += c < rank ? n : 0;
-        all += n;
+    if (d < bins) {
+      uint32_t n[kSortCluster];
+#pragma unroll
+      for (int c = 0; c < kSortCluster; ++c) n[c] = c < p.cluster ? ld_peer(total + d, c) : 0;
+#pragma unroll
+      for (int c = 0; c < kSortCluster; ++c) {
+        before += c < rank ? n[c] : 0;
+        all += n[c];
       }
+    }
     // entries of smaller digits: an exclusive sum over the threads
     uint32_t sum = all;
     for (int k = 1; k < 32; k <<= 1) {
@@ -326,7 +370,7 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort(const SortParams 
     if (lane == 31) sums[warp] = sum;
     __syncthreads();
     if (warp == 0) {
-      uint32_t s = sums[lane], own = s;
+      uint32_t s = lane < kSortWarps ? sums[lane] : 0, own = s;
       for (int k = 1; k < 32; k <<= 1) {
         const uint32_t n = __shfl_up_sync(0xffffffffu, s, k);
         if (lane >= k) s += n;
@@ -339,12 +383,14 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort(const SortParams 
     uint32_t* key_out = odd ? p.key[1] : p.key[0];
     uint32_t* token_out = odd ? p.token[1] : p.token[0];
     for (int64_t from = lo; from < hi; from += 32 * kHeld) {
-      if (share > 32 * kHeld) take(from);  // else they are there
+      const bool held = share <= 32 * kHeld;  // they are there
+      if (!held) take(from);
 #pragma unroll
       for (int k = 0; k < kHeld; ++k) {
         if (from + 32 * k >= hi) break;
         const bool in = from + 32 * k + lane < hi;
-        const uint32_t digit = (key[k] >> shift) & (bins - 1), m = same(in, digit);
+        const uint32_t digit = (key[k] >> shift) & (bins - 1);
+        const uint32_t m = held ? peers[k] : same(in, digit);
         const uint32_t at = in ? base[digit] + count[digit] + __popc(m & ((1u << lane) - 1)) : 0;
         __syncwarp();
         if (in) {
@@ -426,16 +472,16 @@ __device__ __forceinline__ void clear_rows(const SumParams& p, uint32_t* bits, i
 // ---------------------------------------------------------------------------
 // sums over the tokens of an id
 // ---------------------------------------------------------------------------
-constexpr int kPiece = 32;                 // sorted entries that a warp takes
+constexpr int kPiece = 32;                 // sorted entries that a warp takes at most
 constexpr int kSumThreads = kThreads + 32; // and a warp that clears
 constexpr int kSumCtas = 2;                // an SM
 
 // A warp takes 32 E columns of a piece's rows: the sum of an id whose entries
 // all are in the piece goes to the table, that of one that goes on before or
 // behind it to the piece's open sums.
-template <typename T, typename U, bool VEC, bool ACC>
+template <typename T, typename U, int E, bool VEC, bool ACC>
 __global__ void __launch_bounds__(kSumThreads, kSumCtas) embedding_sums(const SumParams p) {
-  constexpr int E = kElems<T, U>, A = ACC ? 4 : 8;  // rows loaded at a time
+  constexpr int R = kElems<T, U>, A = (ACC ? 32 : 64) / E;  // rows loaded at a time
   __shared__ uint32_t bits[kBits / 32];
   pdl_wait();
   pdl_trigger();
@@ -447,28 +493,29 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) embedding_sums(const Su
   const T* dy = static_cast<const T*>(p.dy);
   const U* table = static_cast<const U*>(p.dweight);
   const int slabs = (p.hidden + 32 * E - 1) / (32 * E);
-  const int64_t pieces = (p.tokens + kPiece - 1) / kPiece;
+  const int64_t pieces = (p.tokens + p.piece - 1) / p.piece;
   for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < pieces * slabs;
        u += (int64_t)gridDim.x * kWarps) {
-    const int64_t piece = u / slabs, at = piece * kPiece;
-    const int c = first_column<VEC, E>((int)(u - piece * slabs), lane);
+    const int64_t piece = u / slabs, at = piece * p.piece;
+    const int c = column<E, R, VEC>((int)(u - piece * slabs), lane);
     const uint32_t none = (uint32_t)p.vocab;
-    const uint32_t key = at + lane < p.tokens ? p.key[at + lane] : none;
-    const uint32_t token = at + lane < p.tokens ? p.token[at + lane] : 0;
+    const bool in = lane < p.piece && at + lane < p.tokens;
+    const uint32_t key = in ? p.key[at + lane] : none;
+    const uint32_t token = in ? p.token[at + lane] : 0;
     const uint32_t before = at > 0 ? p.key[at - 1] : none;
-    const uint32_t behind = at + kPiece < p.tokens ? p.key[at + kPiece] : none;
+    const uint32_t behind = at + p.piece < p.tokens ? p.key[at + p.piece] : none;
     uint32_t next = __shfl_down_sync(0xffffffffu, key, 1);
-    if (lane == 31) next = behind;
+    if (lane == p.piece - 1) next = behind;
     const int n = __popc(__ballot_sync(0xffffffffu, key < none));  // they come first
     const uint32_t ends = __ballot_sync(0xffffffffu, key != next);
     const bool open_left = n > 0 && before == __shfl_sync(0xffffffffu, key, 0);
     // entries whose id is done with them: ends, but of the id that began before
     const uint32_t done = open_left ? ends & (ends - 1) : ends;
     bool left = open_left;
-    float sum[E] = {};
+    f32x2 sum[E / 2] = {};
     for (int i0 = 0; i0 < n; i0 += A) {
-      Slice<T, E, VEC> s[A];
-      Slice<U, E, VEC> was[ACC ? A : 1];
+      Slice<T, E, R, VEC> s[A];
+      Slice<U, E, R, VEC> was[ACC ? A : 1];
 #pragma unroll
       for (int k = 0; k < A; ++k) {
         const int64_t t = __shfl_sync(0xffffffffu, token, i0 + k);
@@ -482,32 +529,34 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) embedding_sums(const Su
       for (int k = 0; k < A; ++k) {
         const int i = i0 + k;
         if (i >= n) break;
-        float f[E];
+        f32x2 f[E / 2];
         s[k].get(f);
 #pragma unroll
-        for (int j = 0; j < E; ++j) sum[j] += f[j];
+        for (int j = 0; j < E / 2; ++j) sum[j] = add2(sum[j], f[j]);
         const bool end = ends >> i & 1;
-        if (!end && i + 1 < kPiece) continue;
+        if (!end && i + 1 < p.piece) continue;
         if (left || !end)
-          store_slice<VEC, E>(p.open + (piece * 2 + (left ? 0 : 1)) * p.hidden, c, p.hidden, sum);
+          store_slice<VEC, E, R>(p.open + (piece * 2 + (left ? 0 : 1)) * p.hidden, c, p.hidden,
+                                 sum);
         else
-          finish<VEC, E, U>(p, __shfl_sync(0xffffffffu, key, i), c, was[ACC ? k : 0], sum);
+          finish<VEC, E, R, U>(p, __shfl_sync(0xffffffffu, key, i), c, was[ACC ? k : 0], sum);
         left = false;
 #pragma unroll
-        for (int j = 0; j < E; ++j) sum[j] = 0.f;
+        for (int j = 0; j < E / 2; ++j) sum[j] = 0;
       }
     }
   }
 }
 
-// The ids that go on over several pieces: a warp looks at kLook pieces, takes
-// 128 columns of each one that begins in a piece and goes on behind it, and
-// adds the pieces' open sums in order.
-constexpr int kLook = 4;
+constexpr int kJoinCtas = 3, kJoinAhead = 8;  // CTAs an SM, open sums loaded at a time
+
+// The ids that go on over several pieces: a warp looks at p.look pieces (32 at
+// most), takes 128 columns of each id that begins in one and goes on behind it,
+// and adds the pieces' open sums in order.
 
 template <typename U, bool VEC>
-__global__ void __launch_bounds__(kSumThreads, 2) embedding_joins(const SumParams p) {
-  constexpr int E = 4, A = 16;
+__global__ void __launch_bounds__(kSumThreads, kJoinCtas) embedding_joins(const SumParams p) {
+  constexpr int E = 4, A = kJoinAhead;
   __shared__ uint32_t bits[kBits / 32];
   pdl_wait();
   pdl_trigger();
@@ -519,40 +568,40 @@ __global__ void __launch_bounds__(kSumThreads, 2) embedding_joins(const SumParam
   }
   const U* table = static_cast<const U*>(p.dweight);
   const int slabs = (p.hidden + 32 * E - 1) / (32 * E);
-  const int64_t pieces = (p.tokens + kPiece - 1) / kPiece;
-  const int64_t looks = (pieces - 1 + kLook - 1) / kLook;
+  const int64_t pieces = (p.tokens + p.piece - 1) / p.piece;
+  const int64_t looks = (pieces - 1 + p.look - 1) / p.look;
   for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < looks * slabs;
        u += (int64_t)gridDim.x * kWarps) {
-    const int64_t look = u / slabs, mine = look * kLook + lane;
-    const int c = first_column<VEC, E>((int)(u - look * slabs), lane);
+    const int64_t look = u / slabs, mine = look * p.look + lane;
+    const int c = column<E, E, VEC>((int)(u - look * slabs), lane);
     uint32_t key = (uint32_t)p.vocab;  // of the id that begins in piece `mine` and goes on
-    if (lane < kLook && mine + 1 < pieces) {
-      const int64_t at = mine * kPiece;
-      const uint32_t id = p.key[at + kPiece], end = p.key[at + kPiece - 1], first = p.key[at];
+    if (lane < p.look && mine + 1 < pieces) {
+      const int64_t at = mine * p.piece;
+      const uint32_t id = p.key[at + p.piece], end = p.key[at + p.piece - 1], first = p.key[at];
       const uint32_t before = at > 0 ? p.key[at - 1] : (uint32_t)p.vocab;
       if (end == id && !(first == id && before == id)) key = id;
     }
     uint32_t todo = __ballot_sync(0xffffffffu, key < (uint32_t)p.vocab);
     for (; todo; todo &= todo - 1) {
       const int who = __ffs(todo) - 1;
-      const int64_t piece = look * kLook + who;
+      const int64_t piece = look * p.look + who;
       const uint32_t id = __shfl_sync(0xffffffffu, key, who);
-      Slice<U, E, VEC> was;
+      Slice<U, E, E, VEC> was;
       if (p.accumulate) was.load(table + (int64_t)id * p.hidden, c, p.hidden);
       // the last piece that begins with the id: first a look at the next ones, then halving
       int64_t last = piece + 1, out = pieces;
       const int64_t ahead = piece + 2 + lane;
-      const bool goes_on = ahead < pieces && p.key[ahead * kPiece] == id;
+      const bool goes_on = ahead < pieces && p.key[ahead * p.piece] == id;
       const int more = __popc(__ballot_sync(0xffffffffu, goes_on));
       last += more;
       if (more < 32) out = last + 1;
       while (out - last > 1) {
         const int64_t mid = last + (out - last) / 2;
-        if (p.key[mid * kPiece] == id) last = mid;
+        if (p.key[mid * p.piece] == id) last = mid;
         else out = mid;
       }
-      float sum[E];
-      Slice<float, E, VEC> s[A];
+      f32x2 sum[E / 2];
+      Slice<float, E, E, VEC> s[A];
       s[0].load(p.open + (piece * 2 + 1) * p.hidden, c, p.hidden);
       s[0].get(sum);
       for (int64_t q = piece + 1; q <= last; q += A) {
@@ -562,13 +611,13 @@ __global__ void __launch_bounds__(kSumThreads, 2) embedding_joins(const SumParam
 #pragma unroll
         for (int k = 0; k < A; ++k) {
           if (q + k > last) break;
-          float f[E];
+          f32x2 f[E / 2];
           s[k].get(f);
 #pragma unroll
-          for (int j = 0; j < E; ++j) sum[j] += f[j];
+          for (int j = 0; j < E / 2; ++j) sum[j] = add2(sum[j], f[j]);
         }
       }
-      finish<VEC, E, U>(p, id, c, was, sum);
+      finish<VEC, E, E, U>(p, id, c, was, sum);
     }
   }
 }
@@ -578,9 +627,21 @@ __global__ void __launch_bounds__(kSumThreads, 2) embedding_joins(const SumParam
 // ---------------------------------------------------------------------------
 int64_t padded(int64_t tokens) { return (tokens + 3) / 4 * 4; }
 
+// Elements of a row that a lane of the sums takes: two vectors of a wide row.
+bool wide(int64_t hidden) { return hidden >= 1024; }
+
+// Entries of a piece: fewer where there would be fewer pieces than warps.
+int piece_of(int64_t tokens, int64_t hidden) {
+  const int64_t slabs = ceil_div(hidden, wide(hidden) ? 512 : 256);
+  int piece = kPiece;
+  while (piece > 8 && ceil_div(tokens, piece) < 512 && ceil_div(tokens, piece) * slabs < 2432)
+    piece /= 2;
+  return piece;
+}
+
 size_t workspace_of(int64_t tokens, int64_t hidden) {
   return 4 * (size_t)padded(tokens) * sizeof(uint32_t) +
-         2 * (size_t)ceil_div(tokens, kPiece) * (size_t)hidden * sizeof(float);
+         2 * (size_t)ceil_div(tokens, piece_of(tokens, hidden)) * (size_t)hidden * sizeof(float);
 }
 
 // Bits of the ids and of `vocab` itself.
@@ -594,7 +655,7 @@ cudaError_t launch_sort(SortParams& p, int sms, cudaStream_t s) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   p.cluster = 1;
-  while (p.cluster < 8 && p.cluster * 2 <= sms &&
+  while (p.cluster < kSortCluster && p.cluster * 2 <= sms &&
          p.cluster * kSortThreads < p.tokens)  // a token a thread, where there are few
     p.cluster *= 2;
   const int bits = bits_of(p.vocab);
@@ -603,6 +664,7 @@ cudaError_t launch_sort(SortParams& p, int sms, cudaStream_t s) {
   const size_t smem = (size_t)(kSortWarps + 2) * sizeof(uint32_t) << p.bits;
   const size_t most = (size_t)(kSortWarps + 2) * sizeof(uint32_t) << kMaxBits;
   if (e == cudaSuccess) e = allow_smem<embedding_sort>(dev, most);
+  if (e == cudaSuccess) e = allow_cluster((const void*)embedding_sort, kSortCluster);
   if (e != cudaSuccess) return e;
   int64_t clear = p.zeros > 0 ? least(ceil_div(p.zeros, 64 << 10), sms) : 0;
   clear = ceil_div(clear, p.cluster) * p.cluster;
@@ -612,12 +674,13 @@ cudaError_t launch_sort(SortParams& p, int sms, cudaStream_t s) {
 
 // Where the rows are cleared: as many bytes beside the sort and beside the joins
 // as those take time, the rest beside the sums.
-constexpr int64_t kClearSort = 48 << 20, kClearJoins = 40 << 20;
+constexpr int64_t kClearSort = 64 << 20, kClearJoins = 100 << 20;
 
 template <typename T, typename U, bool VEC>
 cudaError_t launch_sums(SortParams& sort, SumParams& p, cudaStream_t s, int* launches) {
   constexpr int E = kElems<T, U>;
-  const int64_t pieces = ceil_div(p.tokens, kPiece), row = (int64_t)p.hidden * sizeof(U);
+  p.piece = piece_of(p.tokens, p.hidden);
+  const int64_t pieces = ceil_div(p.tokens, p.piece), row = (int64_t)p.hidden * sizeof(U);
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -647,7 +710,12 @@ cudaError_t launch_sums(SortParams& sort, SumParams& p, cudaStream_t s, int* lau
   p.token = sort.token[at];
   p.clear0 = first;
   p.clear1 = last;
-  auto sums = p.accumulate ? embedding_sums<T, U, VEC, true> : embedding_sums<T, U, VEC, false>;
+  constexpr int W = VEC ? 2 * E : E;
+  const bool two = VEC && wide(p.hidden);
+  auto sums = p.accumulate ? two ? embedding_sums<T, U, W, VEC, true>
+                                 : embedding_sums<T, U, E, VEC, true>
+                           : two ? embedding_sums<T, U, W, VEC, false>
+                                 : embedding_sums<T, U, E, VEC, false>;
   auto launch = [&](auto kern, int64_t units, int64_t clears) {
     const int64_t most = (int64_t)sms * max_blocks_per_sm((const void*)kern, kSumThreads, 0);
     int64_t ctas = ceil_div(units, kWarps);
@@ -657,14 +725,16 @@ cudaError_t launch_sums(SortParams& sort, SumParams& p, cudaStream_t s, int* lau
   auto clears = [&]() {
     return p.accumulate ? 0 : ceil_div((p.clear1 - p.clear0) * row, 64 << 10);
   };
-  e = launch(sums, pieces * ceil_div(p.hidden, 32 * E), clears());
+  e = launch(sums, pieces * ceil_div(p.hidden, 32 * (two ? W : E)), clears());
   if (e != cudaSuccess) return e;
   ++*launches;
   p.clear0 = last;
   p.clear1 = p.vocab;
   if (pieces > 1) {
-    e = launch(embedding_joins<U, VEC>, ceil_div(pieces - 1, kLook) * ceil_div(p.hidden, 128),
-               clears());
+    const int64_t slabs = ceil_div(p.hidden, 128), warps = (int64_t)sms * kJoinCtas * kWarps;
+    const int64_t look = ceil_div((pieces - 1) * slabs, warps);
+    p.look = (int)least(look, 32);
+    e = launch(embedding_joins<U, VEC>, ceil_div(pieces - 1, p.look) * slabs, clears());
     if (e == cudaSuccess) ++*launches;
   }
   return e;
@@ -712,7 +782,7 @@ int rms_norm_embedding_bwd(const void* dy, const void* ids, int ids_64, void* dw
   const int64_t n = padded(tokens);
   SortParams sort = {{ids, ids_64}, tokens, vocab, padding_idx, {w, w + n}, {w + 2 * n, w + 3 * n},
                      0, 0, 1, static_cast<char*>(dweight), 0};
-  SumParams sum = {dy, {ids, ids_64}, nullptr, nullptr, reinterpret_cast<float*>(w + 4 * n),
+  SumParams sum = {dy, {ids, ids_64}, nullptr, nullptr, 0, 0, reinterpret_cast<float*>(w + 4 * n),
                    dweight, tokens, vocab, padding_idx, 0, 0, (int)hidden, accumulate, scale};
   int launches = 0;
   const cudaError_t e = with_types(dy_dtype, dweight_dtype, [&](auto t, auto u) {
