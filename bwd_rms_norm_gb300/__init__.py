@@ -1369,7 +1369,7 @@ def rms_norm_rotary_fwd(q: torch.Tensor, k: Optional[torch.Tensor], q_gamma: tor
 
 def rms_norm_rotary_bwd_workspace_size(batch: int, tokens: int, q_heads: int, k_heads: int,
                                        head_dim: int) -> int:
-    """Bytes of workspace ``rms_norm_rotary_bwd`` needs."""
+    """Bytes of workspace ``rms_norm_rotary_bwd`` needs: none for few rows."""
     return int(load_library().rms_norm_rotary_bwd_workspace_size(
         int(batch), int(tokens), int(q_heads), int(k_heads), int(head_dim)))
 
@@ -1423,13 +1423,13 @@ def rms_norm_rotary_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], q:
         dk_gamma = None if k is None else torch.empty(call.dim, dtype=torch.float32, device=dev)
         if workspace is None:
             need = int(lib.rms_norm_rotary_bwd_workspace_size(*call.sizes()[:5]))
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         st = lib.rms_norm_rotary_bwd(
             _heads_of(dq_out), _heads_of(dk_out), _heads_of(q), _heads_of(k), _address(q_gamma),
             _address(k_gamma), _address(rstd_q), _address(rstd_k),
             *call.turn(inv_freq, positions), _heads_of(dq), _heads_of(dk), _address(dq_gamma),
             _address(dk_gamma), *call.sizes(), interleaved, int(offset), DTYPE_CODES[dtype],
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle)
+            _ptr(workspace), workspace.numel() * workspace.element_size(), handle)
     if st != RMSN_OK:
         raise RMSNormError(fn, st)
     _written(*given)

@@ -246,14 +246,6 @@ struct SortParams {
   int64_t zeros;
 };
 
-__device__ __forceinline__ uint32_t ld_peer(const uint32_t* local, uint32_t peer) {
-  const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(local));
-  uint32_t remote, v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(a), "r"(peer));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
-  return v;
-}
-
 // Clears [p, p + n), over `ctas` CTAs of which this is number `cta`.
 __device__ __forceinline__ void clear(char* p, int64_t n, int64_t cta, int64_t ctas) {
   const int64_t edge = (16 - (int64_t)(reinterpret_cast<uintptr_t>(p) & 15)) & 15;
@@ -313,7 +305,7 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort(const SortParams 
       }
     };
     // The lanes with this lane's digit, bit by bit (__match_any_sync takes some
-    // 30 cycles of the SM: 32768 tokens 26 us, xx so).
+    // 30 cycles of the SM each).
     auto same = [&](bool in, uint32_t digit) {
       uint32_t m = __ballot_sync(0xffffffffu, in);
 #pragma unroll
@@ -663,8 +655,7 @@ cudaError_t launch_sort(SortParams& p, int sms, cudaStream_t s) {
   p.bits = (bits + p.passes - 1) / p.passes;
   const size_t smem = (size_t)(kSortWarps + 2) * sizeof(uint32_t) << p.bits;
   const size_t most = (size_t)(kSortWarps + 2) * sizeof(uint32_t) << kMaxBits;
-  if (e == cudaSuccess) e = allow_smem<embedding_sort>(dev, most);
-  if (e == cudaSuccess) e = allow_cluster((const void*)embedding_sort, kSortCluster);
+  if (e == cudaSuccess) e = allow_launch<embedding_sort>(dev, most);
   if (e != cudaSuccess) return e;
   int64_t clear = p.zeros > 0 ? least(ceil_div(p.zeros, 64 << 10), sms) : 0;
   clear = ceil_div(clear, p.cluster) * p.cluster;

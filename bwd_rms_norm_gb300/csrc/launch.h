@@ -141,15 +141,18 @@ cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t 
   return e;
 }
 
-// Lets KERNEL use `bytes` of dynamic shared memory, once a device.
+// Lets KERNEL use `bytes` of dynamic shared memory, and clusters of more than 8
+// CTAs, once a device.
 template <auto KERNEL>
-cudaError_t allow_smem(int dev, size_t bytes) {
+cudaError_t allow_launch(int dev, size_t bytes) {
   static std::atomic<uint64_t> done{0};
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  const cudaError_t e =
-      cudaFuncSetAttribute(reinterpret_cast<const void*>(KERNEL),
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  const void* kern = reinterpret_cast<const void*>(KERNEL);
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
   return e;
 }

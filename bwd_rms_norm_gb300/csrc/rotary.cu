@@ -67,13 +67,13 @@ __global__ void __launch_bounds__(kThreads) rotary_fwd_any(const RotaryParams p)
 }
 
 // A CTA's sums of du vh, which its warps have in `acc` [kWarps][dim], as its
-// partial row.
-__device__ __forceinline__ void store_partial(const float* acc, float* partial, int dim) {
+// partial row, or in the first of acc's.
+__device__ __forceinline__ void sum_warps(float* acc, float* partial, int dim) {
   __syncthreads();
   for (int j = threadIdx.x; j < dim; j += kThreads) {
     float s = 0.f;
     for (int w = 0; w < kWarps; ++w) s += acc[w * dim + j];
-    partial[j] = s;
+    (partial ? partial : acc)[j] = s;
   }
 }
 
@@ -136,7 +136,8 @@ __global__ void __launch_bounds__(kThreads) rotary_bwd_any(const RotaryParams p)
     for (int j = 2 * p.half + lane; j < p.dim; j += 32)
       dv[j] = out(j, Traits<T>::to_f(dy[j]));
   }
-  store_partial(acc, s.partial + (int64_t)cta * p.dim, p.dim);
+  sum_warps(acc, p.direct ? nullptr : s.partial + (int64_t)cta * p.dim, p.dim);
+  if (p.direct) add_cluster(acc, s.dgamma, p.dim, s.ctas);
 }
 
 // dgamma[j] = the sum of a side's partial rows: 32 lanes a column, each over
@@ -184,15 +185,17 @@ cudaError_t launch_bwd_t(int dtype, RotaryParams& p, cudaStream_t s, int* launch
   if (!try_launch_rotary_bwd_vec(dtype, p, s, &e)) {
     e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    auto kern = rotary_bwd_any<T>;
+    constexpr auto kern = rotary_bwd_any<T>;
     const size_t smem = (size_t)kWarps * p.dim * sizeof(float);
-    share_ctas(p, (int64_t)sm_count(dev) * max_blocks_per_sm((const void*)kern, kThreads, smem),
-               kWarps);
+    e = allow_launch<kern>(dev, kWarps * RMSN_ROTARY_MAX_DIM * sizeof(float));
+    if (e != cudaSuccess) return e;
+    const int cluster = place_ctas(p, (const void*)kern, kThreads, smem, kWarps, sm_count(dev));
     e = launch_kernel(kern, dim3((unsigned)(p.side[0].ctas + p.side[1].ctas)), dim3(kThreads),
-                      smem, s, 1, p);
+                      smem, s, cluster, p);
   }
   if (e != cudaSuccess) return e;
   *launches += 1;
+  if (p.direct) return e;
   e = launch_kernel(rotary_sums, dim3((unsigned)((p.dim + 31) / 32), p.side[1].heads ? 2 : 1),
                     dim3(32, kSumLanes), 0, s, 1, p);
   if (e == cudaSuccess) *launches += 1;
@@ -416,7 +419,9 @@ size_t rms_norm_rotary_bwd_workspace_size(int64_t batch, int64_t tokens, int64_t
                                           int64_t k_heads, int64_t head_dim) {
   using namespace rmsn;
   const Sizes z = {batch, tokens, {q_heads, k_heads}, head_dim, 0};
-  if (check_sizes(z, 0, 0, RMSN_F32) != RMSN_OK || batch * tokens == 0) return 0;
+  if (check_sizes(z, 0, 0, RMSN_F32) != RMSN_OK || batch * tokens == 0 ||
+      few_rows(batch * tokens, q_heads, k_heads, head_dim))
+    return 0;
   return (size_t)least(batch * tokens * (q_heads + k_heads), RMSN_ROTARY_MAX_PARTIALS) *
          (size_t)head_dim * sizeof(float);
 }
@@ -477,12 +482,13 @@ int rms_norm_rotary_bwd(const rmsn_heads* dq_out, const rmsn_heads* dk_out, cons
                            nullptr, (int)h, 0};
     if ((uintptr_t)p.side[i].gamma % 16 != 0) p.vec_ok = false;
   }
-  if (!workspace) return RMSN_ERR_NULL;
+  const size_t need =
+      rms_norm_rotary_bwd_workspace_size(batch, tokens, q_heads, k_heads, head_dim);
+  p.direct = need == 0;
+  if (need > 0 && !workspace) return RMSN_ERR_NULL;
   if ((uintptr_t)workspace % 16 != 0) return RMSN_ERR_ALIGN;
-  if (workspace_bytes <
-      rms_norm_rotary_bwd_workspace_size(batch, tokens, q_heads, k_heads, head_dim))
-    return RMSN_ERR_WORKSPACE;
-  to[4] = Block(workspace, (int64_t)workspace_bytes);
+  if (workspace_bytes < need) return RMSN_ERR_WORKSPACE;
+  to[4] = Block(need > 0 ? workspace : nullptr, (int64_t)workspace_bytes);
   for (int i = 0; i < 5; ++i) {
     for (int j = 0; j < 2; ++j) {
       if (!(i == j && to[i] == from[j]) && meet(to[i], from[j])) return RMSN_ERR_ARG;

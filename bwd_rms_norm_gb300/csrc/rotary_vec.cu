@@ -324,12 +324,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
   __syncthreads();
+  static_assert(sizeof(sh.turns) == 2 * G * V * sizeof(float), "a CTA's sums");
+  float* to = p.direct ? reinterpret_cast<float*>(sh.turns) : s.partial + (int64_t)cta * p.dim;
   for (int j = threadIdx.x; j < p.dim; j += kThreads) {
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) v += sums[w][j];
-    s.partial[(int64_t)cta * p.dim + j] = v;
+    to[j] = v;
   }
+  if (p.direct) add_cluster(to, s.dgamma, p.dim, s.ctas);
 }
 
 // ---------------------------------------------------------------------------
@@ -366,15 +369,17 @@ cudaError_t launch_fwd_g(const RotaryParams& p, cudaStream_t s) {
 
 template <typename T, int G, int MODE>
 cudaError_t launch_bwd_g(RotaryParams& p, cudaStream_t s) {
-  auto kern = rotary_bwd_vec<T, G, MODE>;
+  constexpr auto kern = rotary_bwd_vec<T, G, MODE>;
   int dev = 0;
-  const cudaError_t e = cudaGetDevice(&dev);
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = allow_launch<kern>(dev, 0);
   if (e != cudaSuccess) return e;
-  const int64_t most = (int64_t)sm_count(dev) * max_blocks_per_sm((const void*)kern, kThreads, 0);
-  const int per = heads_per_unit(p.all, p.side[0].heads, 32 / G, kBwdSteps, most * kWarps);
-  share_ctas(p, most, kWarps * (32 / G));
+  const int cluster =
+      place_ctas(p, (const void*)kern, kThreads, 0, kWarps * (32 / G), sm_count(dev));
+  const int64_t warps = (int64_t)(p.side[0].ctas + p.side[1].ctas) * kWarps;
+  const int per = heads_per_unit(p.all, p.side[0].heads, 32 / G, kBwdSteps, warps);
   return launch_kernel(kern, dim3((unsigned)(p.side[0].ctas + p.side[1].ctas)), dim3(kThreads), 0,
-                       s, 1, p, per);
+                       s, cluster, p, per);
 }
 
 // f(G, MODE) of the kernel for a row's lanes.

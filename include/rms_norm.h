@@ -484,7 +484,8 @@ int rms_norm_grad_clip(const void* const* grads, const int64_t* numels, const in
  * do, are told apart by their strides.
  *
  * The sums are taken in an order fixed by the sizes, the GPU's SM count and the
- * SM budget.  Workspace as in rms_norm_bwd.  batch * tokens * heads is at most
+ * SM budget.  Workspace as in rms_norm_bwd; few rows need none (size 0, NULL
+ * allowed).  batch * tokens * heads is at most
  * RMSN_MAX_ROWS, head_dim at most RMSN_ROTARY_MAX_DIM; rotary_dim is even and at
  * most head_dim.  Nothing to do (no tokens) zero-fills the gammas' gradients.
  */

@@ -119,14 +119,26 @@ def test_rotary_given_outputs(L, other_way):
     back = *up, *x, *want[2:], freq, None
     grads = other_way(L.rms_norm_rotary_bwd, *back)
     dq, dk = (torch.zeros_like(t) for t in grads[:2])
-    need = L.rms_norm_rotary_bwd_workspace_size(2, 6, 4, 2, 32)
-    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
-    got = L._binding.rotary_bwd(*back, 0, False, dq, dk, ws)
+    assert L.rms_norm_rotary_bwd_workspace_size(2, 6, 4, 2, 32) == 0
+    got = L._binding.rotary_bwd(*back, 0, False, dq, dk, None)
     assert got[0] is dq and got[1] is dk
     same(got, grads)
-    assert L._binding.rotary_bwd(*back, 0, False, dq, dk, ws[:-16]) is None
+
+
+@pytest.mark.gpu
+def test_rotary_given_workspace(L, other_way):
+    q = torch.randn(600, 8, 32, device="cuda").bfloat16()
+    w, freq = torch.ones(32, device="cuda").bfloat16(), torch.rand(16, device="cuda")
+    rstd = L.rms_norm_rotary_fwd(q, None, w, None, freq)[2]
+    back = torch.randn_like(q), None, q, None, w, None, rstd, None, freq, None
+    grads = other_way(L.rms_norm_rotary_bwd, *back)
+    need = L.rms_norm_rotary_bwd_workspace_size(1, 600, 8, 0, 32)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    same(L._binding.rotary_bwd(*back, 0, False, None, None, ws), grads)
+    same(L._binding.rotary_bwd(*back, 0, False), grads)
+    assert L._binding.rotary_bwd(*back, 0, False, None, None, ws[:-16]) is None
     with pytest.raises(L.RMSNormError):
-        L.rms_norm_rotary_bwd(*back, dq=dq, dk=dk, workspace=ws[:-16])
+        L.rms_norm_rotary_bwd(*back, workspace=ws[:-16])
 
 
 @pytest.mark.gpu

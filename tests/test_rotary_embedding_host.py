@@ -45,7 +45,7 @@ def fwd(L, **k):
 def bwd(L, **k):
     g = lambda n, d: k[n] if n in k else d  # noqa: E731
     lib = L.load_library()
-    need = lib.rms_norm_rotary_bwd_workspace_size(2, 4, 4, 2, 64)
+    need = lib.rms_norm_rotary_bwd_workspace_size(2, g("tokens", 4), 4, 2, 64)
     return lib.rms_norm_rotary_bwd(
         g("dqo", plain(L, 0x700000, 4)), g("dko", plain(L, 0x710000, 2)),
         g("q", plain(L, 0x100000, 4)), g("k", plain(L, 0x200000, 2)), g("qg", 0x300000),
@@ -101,15 +101,24 @@ def test_rotary_overlaps(L, call):
 
 def test_rotary_backward_refusals(L):
     for bad in (dict(dqo=NULL), dict(dko=NULL), dict(rq=NULL), dict(rk=NULL), dict(dqg=NULL),
-                dict(dkg=NULL), dict(ws=NULL)):
+                dict(dkg=NULL)):
         assert bwd(L, **bad) == ERR_NULL, bad
-    need = L.rms_norm_rotary_bwd_workspace_size(2, 4, 4, 2, 64)
-    assert need == 2 * 4 * 6 * 64 * 4
-    assert bwd(L, ws_bytes=need - 1) == WORKSPACE
-    assert bwd(L, ws=0x900008) == ALIGN and bwd(L, dqg=0x800002) == ALIGN
-    for bad in (dict(dqg=0x300000), dict(dqg=0x810000), dict(ws=0x100000), dict(dkg=0x900000),
-                dict(qo=plain(L, 0x710000, 4)), dict(dqg=0x600000)):
+    for bad in (dict(dqg=0x300000), dict(dqg=0x810000), dict(qo=plain(L, 0x710000, 4)),
+                dict(dqg=0x600000)):
         assert bwd(L, **bad) == ARG, bad
+    assert bwd(L, dqg=0x800002) == ALIGN
+    # few rows need none; more do
+    assert L.rms_norm_rotary_bwd_workspace_size(2, 4, 4, 2, 64) == 0
+    need = L.rms_norm_rotary_bwd_workspace_size(2, 1024, 4, 2, 64)
+    assert need == 1216 * 64 * 4
+    at = lambda a, n: plain(L, a, n, tokens=1024)  # noqa: E731
+    long = dict(tokens=1024, dqo=at(0x700000, 4), dko=at(0xa00000, 2), q=at(0x100000, 4),
+                k=at(0x200000, 2), qo=at(0x400000, 4), ko=at(0x500000, 2), ps=1024)
+    assert bwd(L, ws=NULL, **long) == ERR_NULL
+    assert bwd(L, ws_bytes=need - 1, **long) == WORKSPACE
+    assert bwd(L, ws=0x900008, **long) == ALIGN
+    for bad in (dict(ws=0x100000), dict(dkg=0x900000), dict(ws=0x610000 - 16)):
+        assert bwd(L, **bad, **long) == ARG, bad
     for bad in ((-1, 4, 4, 2, 64), (2, 4, 0, 2, 64), (2, 4, 4, 2, 0), (0, 4, 4, 2, 64)):
         assert L.rms_norm_rotary_bwd_workspace_size(*bad) == 0
     assert L.rms_norm_rotary_bwd_workspace_size(8, 4096, 32, 8, 128) == 1216 * 128 * 4

@@ -271,8 +271,24 @@ def test_no_tokens(L):
     assert not back[2].any() and not back[3].any() and back[2].shape == (64,)
 
 
-def test_same_bits_every_time_and_under_a_budget(L):
-    c = make(1, 500, 8, 2, 128, 128, "bf16")
+@pytest.mark.parametrize("dim", [128, 33])
+def test_a_cluster_of_any_size_for_few_rows(L, dim):
+    for tokens in (1, 2, 9, 33, 64, 255, 256, 257):     # 8 rows a token: to 2048 rows and beyond
+        c = make(1, tokens, 8, 2, dim, 32, "f32")
+        both(L, c)
+        launches = L.last_launch_count()
+        assert launches == (1 if tokens <= 256 else 2)
+    try:
+        for sms in (1, 3, 8):
+            L.rms_norm_set_sm_budget(sms)
+            both(L, make(1, 100, 4, 1, dim, 32, "bf16"))
+    finally:
+        L.rms_norm_set_sm_budget(0)
+
+
+@pytest.mark.parametrize("tokens", [60, 500])
+def test_same_bits_every_time_and_under_a_budget(L, tokens):
+    c = make(1, tokens, 8, 2, 128, 128, "bf16")
     args = [c[k] for k in ("dq", "dk", "q", "k", "q_gamma", "k_gamma")]
     rstd = L.rms_norm_rotary_fwd(c["q"], c["k"], c["q_gamma"], c["k_gamma"], c["freq"],
                                  c["pos"])[2:]
