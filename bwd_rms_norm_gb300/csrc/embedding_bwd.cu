@@ -109,8 +109,7 @@ __device__ __forceinline__ int column(int slab, int lane) {
 struct SumParams {
   const void* dy;
   Ids ids;
-  const uint32_t* key;    // the tokens' ids in order, `vocab` for those without a part
-  const uint32_t* token;  // the tokens in that order
+  const uint2* sorted;    // (id, token) in order, id `vocab` for those without a part
   int piece;              // sorted entries that a warp takes
   int look;               // pieces that a warp of the joins looks at
   float* open;            // [pieces][2][hidden]: sums of ids that go on before / behind a piece
@@ -139,17 +138,58 @@ __device__ __forceinline__ void finish(const SumParams& p, uint32_t id, int c,
 }
 
 // ---------------------------------------------------------------------------
+// rows without a token
+// ---------------------------------------------------------------------------
+constexpr int kBits = 4096;   // rows whose tokens are looked at together
+
+// A warp clears those of `rows` rows, from `table` on, whose bit is not set, a
+// run of them at a time, in 16-byte stores but for its ends.
+template <typename U>
+__device__ __forceinline__ void clear_unmarked(U* table, int hidden, const uint32_t* bits, int rows,
+                                               int lane) {
+  for (int r = 0; r < rows;) {
+    const uint32_t w = bits[r >> 5] >> (r & 31);
+    if (w & 1) {  // rows with tokens
+      r += w == 0xffffffffu ? 32 : __ffs(~w) - 1;
+      continue;
+    }
+    int e = r;    // rows without, up to e
+    while (e < rows) {
+      const uint32_t v = bits[e >> 5] >> (e & 31);
+      if (v) {
+        e += __ffs(v) - 1;
+        break;
+      }
+      e = (e | 31) + 1;
+    }
+    if (e > rows) e = rows;
+    U* to = table + (int64_t)r * hidden;
+    int64_t n = (int64_t)(e - r) * hidden;
+    constexpr int W = 16 / sizeof(U);
+    int64_t head = ((16 - (reinterpret_cast<uintptr_t>(to) & 15)) & 15) / sizeof(U);
+    if (head > n) head = n;
+    if (lane < head) to[lane] = Traits<U>::from_f(0.f);
+    to += head;
+    n -= head;
+    const int64_t vecs = n / W;
+#pragma unroll 4
+    for (int64_t i = lane; i < vecs; i += 32) st_vec(to + i * W, make_uint4(0, 0, 0, 0));
+    if (vecs * W + lane < n) to[vecs * W + lane] = Traits<U>::from_f(0.f);
+    r = e;
+  }
+}
+
+// ---------------------------------------------------------------------------
 // few tokens
 // ---------------------------------------------------------------------------
 constexpr int kFew = 512;
-constexpr int kBits = 32768;  // rows whose tokens are looked at together
 
 template <typename T, typename U, bool VEC>
 __global__ void __launch_bounds__(kThreads) embedding_few(const SumParams p) {
   constexpr int E = kElems<T, U>, A = 8;
   __shared__ int id[kFew];
   __shared__ unsigned short list[kWarps][kFew];
-  __shared__ uint32_t bits[kBits / 32];
+  __shared__ uint32_t bits[kWarps][kBits / 32];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = (int)p.tokens;
@@ -157,34 +197,24 @@ __global__ void __launch_bounds__(kThreads) embedding_few(const SumParams p) {
     const int k = i < n ? p.ids.get(i, p.vocab) : -1;
     id[i] = k == p.padding_idx ? -1 : k;
   }
+  __syncthreads();
   U* table = static_cast<U*>(p.dweight);
-  if (!p.accumulate) {  // this CTA's rows without a token
-    const int64_t r0 = p.vocab * blockIdx.x / gridDim.x, r1 = p.vocab * (blockIdx.x + 1) / gridDim.x;
-    constexpr int W = VEC ? 16 / sizeof(U) : 1;  // elements of a store
-    const int units = (p.hidden + W - 1) / W;
-    int g = 1;                                   // lanes a row
-    while (g < 32 && g < units) g *= 2;
+  if (!p.accumulate) {  // this warp's rows without a token
+    const int64_t number = (int64_t)blockIdx.x * kWarps + warp, warps = (int64_t)gridDim.x * kWarps;
+    const int64_t r0 = p.vocab * number / warps, r1 = p.vocab * (number + 1) / warps;
     for (int64_t base = r0; base < r1; base += kBits) {
       const int rows = (int)(r1 - base < kBits ? r1 - base : kBits);
-      for (int i = threadIdx.x; i < (rows + 31) / 32; i += kThreads) bits[i] = 0;
-      __syncthreads();
-      for (int i = threadIdx.x; i < n; i += kThreads) {
+      for (int i = lane; i < (rows + 31) / 32; i += 32) bits[warp][i] = 0;
+      __syncwarp();
+      for (int i = lane; i < n; i += 32) {
         const int64_t at = id[i] - base;
-        if (id[i] >= 0 && at >= 0 && at < rows) atomicOr(&bits[at >> 5], 1u << (at & 31));
+        if (id[i] >= 0 && at >= 0 && at < rows) atomicOr(&bits[warp][at >> 5], 1u << (at & 31));
       }
-      __syncthreads();
-      for (int r = threadIdx.x / g; r < rows; r += kThreads / g) {
-        if (bits[r >> 5] >> (r & 31) & 1) continue;
-        U* row = table + (base + r) * p.hidden;
-        for (int j = threadIdx.x % g; j < units; j += g) {
-          if constexpr (VEC) st_vec(row + j * W, make_uint4(0, 0, 0, 0));
-          else row[j] = Traits<U>::from_f(0.f);
-        }
-      }
-      __syncthreads();
+      __syncwarp();
+      clear_unmarked(table + base * p.hidden, p.hidden, bits[warp], rows, lane);
+      __syncwarp();
     }
   }
-  __syncthreads();
   const T* dy = static_cast<const T*>(p.dy);
   const int slabs = (p.hidden + 32 * E - 1) / (32 * E);
   for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < (int64_t)n * slabs;
@@ -232,14 +262,13 @@ __global__ void __launch_bounds__(kThreads) embedding_few(const SumParams p) {
 constexpr int kSortThreads = 512;
 constexpr int kSortCluster = 16;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kMaxBits = 9;   // of a digit
-constexpr int kHeld = 8;      // entries of a lane loaded at a time
+constexpr int kMaxBits = 10;  // of a digit: two bins a thread
+constexpr int kHeld = 16;     // entries of a lane loaded at a time
 
 struct SortParams {
   Ids ids;
   int64_t tokens, vocab, padding_idx;
-  uint32_t* key[2];    // ids and tokens, in turn the source and the target of a pass
-  uint32_t* token[2];
+  uint2* items[2];     // (id, token), in turn the source and the target of a pass
   int passes, bits;    // digits, and bits of each
   int cluster;
   char* zero;          // the rows of the table that this kernel clears: `zeros` bytes
@@ -283,24 +312,23 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort(const SortParams 
   for (int pass = 0; pass < p.passes; ++pass) {
     const int shift = pass * p.bits;
     const bool odd = pass & 1;
-    const uint32_t* key_in = odd ? p.key[0] : p.key[1];
-    const uint32_t* token_in = odd ? p.token[0] : p.token[1];
+    const uint2* from_items = odd ? p.items[0] : p.items[1];
     // This lane's next entries, all of their loads under way together.
-    uint32_t key[kHeld], token[kHeld], peers[kHeld];
+    uint2 item[kHeld];
+    uint32_t peers[kHeld];
     auto take = [&](int64_t from) {
 #pragma unroll
       for (int k = 0; k < kHeld; ++k) {
         if (from + 32 * k >= hi) break;
         const int64_t i = from + 32 * k + lane;
-        key[k] = token[k] = 0;
+        item[k] = make_uint2(0, 0);
         if (i >= hi) continue;
         if (pass > 0) {
-          key[k] = __ldcg(key_in + i);  // another CTA's: not through this SM's L1
-          token[k] = __ldcg(token_in + i);
+          item[k] = __ldcg(from_items + i);  // another CTA's: not through this SM's L1
         } else {
           const int id = p.ids.get(i, p.vocab);
-          key[k] = id < 0 || id == p.padding_idx ? (uint32_t)p.vocab : (uint32_t)id;
-          token[k] = (uint32_t)i;
+          item[k].x = id < 0 || id == p.padding_idx ? (uint32_t)p.vocab : (uint32_t)id;
+          item[k].y = (uint32_t)i;
         }
       }
     };
@@ -324,37 +352,46 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort(const SortParams 
       for (int k = 0; k < kHeld; ++k) {
         if (from + 32 * k >= hi) break;
         const bool in = from + 32 * k + lane < hi;
-        const uint32_t digit = (key[k] >> shift) & (bins - 1), m = same(in, digit);
+        const uint32_t digit = (item[k].x >> shift) & (bins - 1), m = same(in, digit);
         if (in && lane == __ffs(m) - 1) count[digit] += __popc(m);
         peers[k] = m;
         __syncwarp();
       }
     }
     __syncthreads();
-    if (d < bins) {
-      uint32_t run = 0;
+    // the thread's two bins, 2 d and 2 d + 1, of at least two
+    uint2 before = make_uint2(0, 0), all = make_uint2(0, 0);
+    if (2 * d < bins) {
+      uint2 run = make_uint2(0, 0);
 #pragma unroll 8
       for (int w = 0; w < kSortWarps; ++w) {
-        const uint32_t n = smem[w * bins + d];
-        smem[w * bins + d] = run;
-        run += n;
+        uint2* at = reinterpret_cast<uint2*>(smem + w * bins) + d;
+        const uint2 n = *at;
+        *at = run;
+        run.x += n.x;
+        run.y += n.y;
       }
-      total[d] = run;
+      reinterpret_cast<uint2*>(total)[d] = run;
     }
     cluster_sync();
-    uint32_t before = 0, all = 0;
-    if (d < bins) {
-      uint32_t n[kSortCluster];
-#pragma unroll
-      for (int c = 0; c < kSortCluster; ++c) n[c] = c < p.cluster ? ld_peer(total + d, c) : 0;
+    if (2 * d < bins) {
+      uint32_t n[2][kSortCluster];
 #pragma unroll
       for (int c = 0; c < kSortCluster; ++c) {
-        before += c < rank ? n[c] : 0;
-        all += n[c];
+        n[0][c] = c < p.cluster ? ld_peer(total + 2 * d, c) : 0;
+        n[1][c] = c < p.cluster ? ld_peer(total + 2 * d + 1, c) : 0;
+      }
+#pragma unroll
+      for (int c = 0; c < kSortCluster; ++c) {
+        before.x += c < rank ? n[0][c] : 0;
+        before.y += c < rank ? n[1][c] : 0;
+        all.x += n[0][c];
+        all.y += n[1][c];
       }
     }
     // entries of smaller digits: an exclusive sum over the threads
-    uint32_t sum = all;
+    const uint32_t own = all.x + all.y;
+    uint32_t sum = own;
     for (int k = 1; k < 32; k <<= 1) {
       const uint32_t n = __shfl_up_sync(0xffffffffu, sum, k);
       if (lane >= k) sum += n;
@@ -362,18 +399,21 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort(const SortParams 
     if (lane == 31) sums[warp] = sum;
     __syncthreads();
     if (warp == 0) {
-      uint32_t s = lane < kSortWarps ? sums[lane] : 0, own = s;
+      uint32_t s = lane < kSortWarps ? sums[lane] : 0;
+      const uint32_t mine = s;
       for (int k = 1; k < 32; k <<= 1) {
         const uint32_t n = __shfl_up_sync(0xffffffffu, s, k);
         if (lane >= k) s += n;
       }
-      sums[lane] = s - own;
+      sums[lane] = s - mine;
     }
     __syncthreads();
-    if (d < bins) base[d] = sums[warp] + sum - all + before;
+    if (2 * d < bins) {
+      const uint32_t smaller = sums[warp] + sum - own;
+      reinterpret_cast<uint2*>(base)[d] = make_uint2(smaller + before.x, smaller + all.x + before.y);
+    }
     __syncthreads();
-    uint32_t* key_out = odd ? p.key[1] : p.key[0];
-    uint32_t* token_out = odd ? p.token[1] : p.token[0];
+    uint2* to_items = odd ? p.items[1] : p.items[0];
     for (int64_t from = lo; from < hi; from += 32 * kHeld) {
       const bool held = share <= 32 * kHeld;  // they are there
       if (!held) take(from);
@@ -381,14 +421,13 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort(const SortParams 
       for (int k = 0; k < kHeld; ++k) {
         if (from + 32 * k >= hi) break;
         const bool in = from + 32 * k + lane < hi;
-        const uint32_t digit = (key[k] >> shift) & (bins - 1);
+        const uint32_t digit = (item[k].x >> shift) & (bins - 1);
         const uint32_t m = held ? peers[k] : same(in, digit);
         const uint32_t at = in ? base[digit] + count[digit] + __popc(m & ((1u << lane) - 1)) : 0;
         __syncwarp();
         if (in) {
           if (lane == __ffs(m) - 1) count[digit] += __popc(m);
-          key_out[at] = key[k];
-          token_out[at] = token[k];
+          to_items[at] = item[k];
         }
         __syncwarp();
       }
@@ -398,15 +437,12 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort(const SortParams 
   }
 }
 
-// ---------------------------------------------------------------------------
-// rows without a token
-// ---------------------------------------------------------------------------
-// The first of the sorted keys that is not below `id`, by a whole warp.
+// The first of the sorted ids that is not below `id`, by a whole warp.
 __device__ __forceinline__ int64_t first_not_below(const SumParams& p, uint32_t id, int lane) {
   int64_t lo = 0, hi = p.tokens;
   while (lo < hi) {
     const int64_t at = lo + (hi - lo) * (lane + 1) / 33;
-    const int below = __popc(__ballot_sync(0xffffffffu, p.key[at] < id));
+    const int below = __popc(__ballot_sync(0xffffffffu, p.sorted[at].x < id));
     const int64_t next = __shfl_sync(0xffffffffu, at, below < 32 ? below : 31);
     const int64_t prev = __shfl_sync(0xffffffffu, at, below > 0 ? below - 1 : 0);
     if (below > 0) lo = prev + 1;
@@ -416,47 +452,24 @@ __device__ __forceinline__ int64_t first_not_below(const SumParams& p, uint32_t 
 }
 
 // One of `warps` warps clears its part of the rows [clear0, clear1) that no
-// token has; rows are of whole 16-byte vectors.  bits: kBits / 32 words of
-// shared memory.
+// token has.  bits: kBits / 32 words of shared memory.
 template <typename U>
 __device__ __forceinline__ void clear_rows(const SumParams& p, uint32_t* bits, int64_t number,
                                            int64_t warps, int lane) {
   const int64_t all = p.clear1 - p.clear0;
   const int64_t r0 = p.clear0 + all * number / warps, r1 = p.clear0 + all * (number + 1) / warps;
-  const int64_t row_bytes = (int64_t)p.hidden * sizeof(U);
   for (int64_t base = r0; base < r1; base += kBits) {
     const int rows = (int)(r1 - base < kBits ? r1 - base : kBits);
     const uint32_t end = (uint32_t)(base + rows);
     for (int i = lane; i < (rows + 31) / 32; i += 32) bits[i] = 0;
     __syncwarp();
     for (int64_t i = first_not_below(p, (uint32_t)base, lane) + lane;; i += 32) {
-      const uint32_t key = i < p.tokens ? p.key[i] : 0xffffffffu;
+      const uint32_t key = i < p.tokens ? p.sorted[i].x : 0xffffffffu;
       if (key < end) atomicOr(&bits[(key - (uint32_t)base) >> 5], 1u << ((key - (uint32_t)base) & 31));
       if (!__all_sync(0xffffffffu, key < end)) break;
     }
     __syncwarp();
-    for (int r = 0; r < rows;) {
-      const uint32_t w = bits[r >> 5] >> (r & 31);
-      if (w & 1) {  // rows with tokens
-        r += w == 0xffffffffu ? 32 : __ffs(~w) - 1;
-        continue;
-      }
-      int e = r;    // rows without, up to e
-      while (e < rows) {
-        const uint32_t v = bits[e >> 5] >> (e & 31);
-        if (v) {
-          e += __ffs(v) - 1;
-          break;
-        }
-        e = (e | 31) + 1;
-      }
-      if (e > rows) e = rows;
-      char* to = static_cast<char*>(p.dweight) + (base + r) * row_bytes;
-      const int64_t n = (e - r) * row_bytes;
-#pragma unroll 4
-      for (int64_t i = lane * 16; i < n; i += 512) st_vec(to + i, make_uint4(0, 0, 0, 0));
-      r = e;
-    }
+    clear_unmarked(static_cast<U*>(p.dweight) + base * p.hidden, p.hidden, bits, rows, lane);
     __syncwarp();
   }
 }
@@ -479,7 +492,7 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) embedding_sums(const Su
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (warp == kWarps) {
-    if constexpr (VEC && !ACC) clear_rows<U>(p, bits, blockIdx.x, gridDim.x, lane);
+    if constexpr (!ACC) clear_rows<U>(p, bits, blockIdx.x, gridDim.x, lane);
     return;
   }
   const T* dy = static_cast<const T*>(p.dy);
@@ -492,10 +505,10 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) embedding_sums(const Su
     const int c = column<E, R, VEC>((int)(u - piece * slabs), lane);
     const uint32_t none = (uint32_t)p.vocab;
     const bool in = lane < p.piece && at + lane < p.tokens;
-    const uint32_t key = in ? p.key[at + lane] : none;
-    const uint32_t token = in ? p.token[at + lane] : 0;
-    const uint32_t before = at > 0 ? p.key[at - 1] : none;
-    const uint32_t behind = at + p.piece < p.tokens ? p.key[at + p.piece] : none;
+    const uint2 item = in ? p.sorted[at + lane] : make_uint2(none, 0);
+    const uint32_t key = item.x, token = item.y;
+    const uint32_t before = at > 0 ? p.sorted[at - 1].x : none;
+    const uint32_t behind = at + p.piece < p.tokens ? p.sorted[at + p.piece].x : none;
     uint32_t next = __shfl_down_sync(0xffffffffu, key, 1);
     if (lane == p.piece - 1) next = behind;
     const int n = __popc(__ballot_sync(0xffffffffu, key < none));  // they come first
@@ -541,75 +554,107 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) embedding_sums(const Su
 }
 
 constexpr int kJoinCtas = 3, kJoinAhead = 8;  // CTAs an SM, open sums loaded at a time
+constexpr int kLong = 32;                     // pieces of an id that a CTA's warps share
+
+// The open sums of the pieces [from, to), added in order to sum.
+template <bool VEC>
+__device__ __forceinline__ void add_open(const SumParams& p, int64_t from, int64_t to, int c,
+                                         f32x2 (&sum)[2]) {
+  for (int64_t q = from; q < to; q += kJoinAhead) {
+    Slice<float, 4, 4, VEC> s[kJoinAhead];
+#pragma unroll
+    for (int k = 0; k < kJoinAhead; ++k)
+      if (q + k < to) s[k].load(p.open + (q + k) * 2 * p.hidden, c, p.hidden);
+#pragma unroll
+    for (int k = 0; k < kJoinAhead; ++k) {
+      if (q + k >= to) break;
+      f32x2 f[2];
+      s[k].get(f);
+      sum[0] = add2(sum[0], f[0]);
+      sum[1] = add2(sum[1], f[1]);
+    }
+  }
+}
 
 // The ids that go on over several pieces: a warp looks at p.look pieces (32 at
 // most), takes 128 columns of each id that begins in one and goes on behind it,
-// and adds the pieces' open sums in order.
-
-template <typename U, bool VEC>
+// and adds the pieces' open sums in order.  TEAM, for narrow rows: all warps of
+// a CTA look at the same pieces and share the ids; one of many pieces they add
+// together, a run of them each, and then their sums in order.
+template <typename U, bool VEC, bool TEAM>
 __global__ void __launch_bounds__(kSumThreads, kJoinCtas) embedding_joins(const SumParams p) {
-  constexpr int E = 4, A = kJoinAhead;
+  constexpr int E = 4;
   __shared__ uint32_t bits[kBits / 32];
+  __shared__ float4 part[kWarps][32];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (warp == kWarps) {
-    if constexpr (VEC)
-      if (!p.accumulate) clear_rows<U>(p, bits, blockIdx.x, gridDim.x, lane);
+    if (!p.accumulate) clear_rows<U>(p, bits, blockIdx.x, gridDim.x, lane);
     return;
   }
+  // of the warps that add, not of the one that clears
+  auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); };
   const U* table = static_cast<const U*>(p.dweight);
   const int slabs = (p.hidden + 32 * E - 1) / (32 * E);
   const int64_t pieces = (p.tokens + p.piece - 1) / p.piece;
   const int64_t looks = (pieces - 1 + p.look - 1) / p.look;
-  for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < looks * slabs;
-       u += (int64_t)gridDim.x * kWarps) {
+  for (int64_t u = TEAM ? blockIdx.x : (int64_t)blockIdx.x * kWarps + warp; u < looks * slabs;
+       u += TEAM ? gridDim.x : (int64_t)gridDim.x * kWarps) {
     const int64_t look = u / slabs, mine = look * p.look + lane;
     const int c = column<E, E, VEC>((int)(u - look * slabs), lane);
     uint32_t key = (uint32_t)p.vocab;  // of the id that begins in piece `mine` and goes on
     if (lane < p.look && mine + 1 < pieces) {
       const int64_t at = mine * p.piece;
-      const uint32_t id = p.key[at + p.piece], end = p.key[at + p.piece - 1], first = p.key[at];
-      const uint32_t before = at > 0 ? p.key[at - 1] : (uint32_t)p.vocab;
+      const uint32_t id = p.sorted[at + p.piece].x, end = p.sorted[at + p.piece - 1].x;
+      const uint32_t first = p.sorted[at].x, before = at > 0 ? p.sorted[at - 1].x : (uint32_t)p.vocab;
       if (end == id && !(first == id && before == id)) key = id;
     }
     uint32_t todo = __ballot_sync(0xffffffffu, key < (uint32_t)p.vocab);
-    for (; todo; todo &= todo - 1) {
+    for (int turn = 0; todo; todo &= todo - 1, ++turn) {
       const int who = __ffs(todo) - 1;
       const int64_t piece = look * p.look + who;
       const uint32_t id = __shfl_sync(0xffffffffu, key, who);
-      Slice<U, E, E, VEC> was;
-      if (p.accumulate) was.load(table + (int64_t)id * p.hidden, c, p.hidden);
-      // the last piece that begins with the id: first a look at the next ones, then halving
-      int64_t last = piece + 1, out = pieces;
+      // pieces behind this one that begin with the id: a look at the next ones, then halving
       const int64_t ahead = piece + 2 + lane;
-      const bool goes_on = ahead < pieces && p.key[ahead * p.piece] == id;
+      const bool goes_on = ahead < pieces && p.sorted[ahead * p.piece].x == id;
       const int more = __popc(__ballot_sync(0xffffffffu, goes_on));
-      last += more;
-      if (more < 32) out = last + 1;
-      while (out - last > 1) {
-        const int64_t mid = last + (out - last) / 2;
-        if (p.key[mid * p.piece] == id) last = mid;
-        else out = mid;
-      }
-      f32x2 sum[E / 2];
-      Slice<float, E, E, VEC> s[A];
-      s[0].load(p.open + (piece * 2 + 1) * p.hidden, c, p.hidden);
-      s[0].get(sum);
-      for (int64_t q = piece + 1; q <= last; q += A) {
-#pragma unroll
-        for (int k = 0; k < A; ++k)
-          if (q + k <= last) s[k].load(p.open + (q + k) * 2 * p.hidden, c, p.hidden);
-#pragma unroll
-        for (int k = 0; k < A; ++k) {
-          if (q + k > last) break;
-          f32x2 f[E / 2];
-          s[k].get(f);
-#pragma unroll
-          for (int j = 0; j < E / 2; ++j) sum[j] = add2(sum[j], f[j]);
+      int64_t end = piece + 2 + more;
+      if (more == 32) {
+        int64_t out = pieces + 1;  // the last such piece is end - 1, and before out - 1
+        while (out - end > 1) {
+          const int64_t mid = end + (out - end) / 2;
+          if (p.sorted[(mid - 1) * p.piece].x == id) end = mid;
+          else out = mid;
         }
       }
-      finish<VEC, E, E, U>(p, id, c, was, sum);
+      const bool together = TEAM && end - piece - 1 >= kLong;  // the same for every warp
+      if (TEAM && !together && turn % kWarps != warp) continue;
+      const bool last = !together || warp == 0;        // the warp that has the sum
+      Slice<U, E, E, VEC> was;
+      if (last && p.accumulate) was.load(table + (int64_t)id * p.hidden, c, p.hidden);
+      f32x2 sum[2] = {};
+      if (last) {
+        Slice<float, E, E, VEC> s;
+        s.load(p.open + (piece * 2 + 1) * p.hidden, c, p.hidden);
+        s.get(sum);
+      }
+      const int64_t n = end - piece - 1;
+      add_open<VEC>(p, piece + 1 + (together ? n * warp / kWarps : 0),
+                    piece + 1 + (together ? n * (warp + 1) / kWarps : n), c, sum);
+      if (together) {
+        const float2 a = split(sum[0]), b = split(sum[1]);
+        part[warp][lane] = make_float4(a.x, a.y, b.x, b.y);
+        sync();
+        if (warp == 0)
+          for (int w = 1; w < kWarps; ++w) {
+            const float4 f = part[w][lane];
+            sum[0] = add2(sum[0], pair(f.x, f.y));
+            sum[1] = add2(sum[1], pair(f.z, f.w));
+          }
+        sync();  // the sums give way to the next id's
+      }
+      if (last) finish<VEC, E, E, U>(p, id, c, was, sum);
     }
   }
 }
@@ -617,7 +662,7 @@ __global__ void __launch_bounds__(kSumThreads, kJoinCtas) embedding_joins(const 
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
-int64_t padded(int64_t tokens) { return (tokens + 3) / 4 * 4; }
+int64_t padded(int64_t tokens) { return (tokens + 1) / 2 * 2; }
 
 // Elements of a row that a lane of the sums takes: two vectors of a wide row.
 bool wide(int64_t hidden) { return hidden >= 1024; }
@@ -632,7 +677,7 @@ int piece_of(int64_t tokens, int64_t hidden) {
 }
 
 size_t workspace_of(int64_t tokens, int64_t hidden) {
-  return 4 * (size_t)padded(tokens) * sizeof(uint32_t) +
+  return 2 * (size_t)padded(tokens) * sizeof(uint2) +
          2 * (size_t)ceil_div(tokens, piece_of(tokens, hidden)) * (size_t)hidden * sizeof(float);
 }
 
@@ -686,19 +731,14 @@ cudaError_t launch_sums(SortParams& sort, SumParams& p, cudaStream_t s, int* lau
     if (e == cudaSuccess) ++*launches;
     return e;
   }
-  int64_t first = p.vocab, last = p.vocab;  // rows cleared beside the sort, and before the joins
-  if (VEC) {
-    first = least(kClearSort / row, p.vocab);
-    const int64_t joins = pieces > 1 ? kClearJoins / row : 0;
-    last = p.vocab - joins > first ? p.vocab - joins : first;
-  }
+  // rows cleared beside the sort, and before the joins
+  const int64_t first = least(kClearSort / row, p.vocab), joins = kClearJoins / row;
+  const int64_t last = p.vocab - joins > first ? p.vocab - joins : first;
   sort.zeros = p.accumulate ? 0 : first * row;
   e = launch_sort(sort, sms, s);
   if (e != cudaSuccess) return e;
   ++*launches;
-  const int at = (sort.passes - 1) & 1;  // where the last pass wrote
-  p.key = sort.key[at];
-  p.token = sort.token[at];
+  p.sorted = sort.items[(sort.passes - 1) & 1];  // where the last pass wrote
   p.clear0 = first;
   p.clear1 = last;
   constexpr int W = VEC ? 2 * E : E;
@@ -722,10 +762,13 @@ cudaError_t launch_sums(SortParams& sort, SumParams& p, cudaStream_t s, int* lau
   p.clear0 = last;
   p.clear1 = p.vocab;
   if (pieces > 1) {
-    const int64_t slabs = ceil_div(p.hidden, 128), warps = (int64_t)sms * kJoinCtas * kWarps;
-    const int64_t look = ceil_div((pieces - 1) * slabs, warps);
-    p.look = (int)least(look, 32);
-    e = launch(embedding_joins<U, VEC>, ceil_div(pieces - 1, p.look) * slabs, clears());
+    const bool team = !wide(p.hidden);
+    const int64_t slabs = ceil_div(p.hidden, 128);
+    const int64_t lookers = (int64_t)sms * kJoinCtas * (team ? 1 : kWarps);
+    p.look = (int)least(ceil_div((pieces - 1) * slabs, lookers), 32);
+    const int64_t units = ceil_div(pieces - 1, p.look) * slabs;
+    e = team ? launch(embedding_joins<U, VEC, true>, units * kWarps, clears())
+             : launch(embedding_joins<U, VEC, false>, units, clears());
     if (e == cudaSuccess) ++*launches;
   }
   return e;
@@ -769,11 +812,11 @@ int rms_norm_embedding_bwd(const void* dy, const void* ids, int ids_64, void* dw
   if (out.meets(ws)) return RMSN_ERR_ARG;
   for (const Span& i : ins)
     if (out.meets(i) || ws.meets(i)) return RMSN_ERR_ARG;
-  uint32_t* w = static_cast<uint32_t*>(workspace);
+  uint2* w = static_cast<uint2*>(workspace);
   const int64_t n = padded(tokens);
-  SortParams sort = {{ids, ids_64}, tokens, vocab, padding_idx, {w, w + n}, {w + 2 * n, w + 3 * n},
-                     0, 0, 1, static_cast<char*>(dweight), 0};
-  SumParams sum = {dy, {ids, ids_64}, nullptr, nullptr, 0, 0, reinterpret_cast<float*>(w + 4 * n),
+  SortParams sort = {{ids, ids_64}, tokens, vocab, padding_idx, {w, w + n}, 0, 0, 1,
+                     static_cast<char*>(dweight), 0};
+  SumParams sum = {dy, {ids, ids_64}, nullptr, 0, 0, reinterpret_cast<float*>(w + 2 * n),
                    dweight, tokens, vocab, padding_idx, 0, 0, (int)hidden, accumulate, scale};
   int launches = 0;
   const cudaError_t e = with_types(dy_dtype, dweight_dtype, [&](auto t, auto u) {
