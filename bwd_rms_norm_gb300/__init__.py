@@ -1487,7 +1487,7 @@ def rms_norm_embedding_fwd(ids: torch.Tensor, weight: torch.Tensor, scale: float
 
 
 def rms_norm_embedding_bwd_workspace_size(tokens: int, vocab: int, hidden: int) -> int:
-    """Bytes of workspace ``rms_norm_embedding_bwd`` needs."""
+    """Bytes of workspace ``rms_norm_embedding_bwd`` needs: none for few tokens."""
     return int(load_library().rms_norm_embedding_bwd_workspace_size(int(tokens), int(vocab),
                                                                     int(hidden)))
 
@@ -1535,11 +1535,11 @@ def rms_norm_embedding_bwd(dy: torch.Tensor, ids: torch.Tensor, vocab: int, scal
             dweight = torch.empty((max(vocab, 0), hidden), dtype=dtype, device=dev)
         if workspace is None:
             need = int(lib.rms_norm_embedding_bwd_workspace_size(ids.numel(), vocab, hidden))
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         st = lib.rms_norm_embedding_bwd(
             _address(dy), _address(ids), int(ids.dtype == torch.int64), _address(dweight),
             ids.numel(), vocab, hidden, float(scale), -1 if padding_idx is None else padding_idx,
-            accumulate, DTYPE_CODES[dy.dtype], DTYPE_CODES[dtype], workspace.data_ptr(),
+            accumulate, DTYPE_CODES[dy.dtype], DTYPE_CODES[dtype], _ptr(workspace),
             workspace.numel() * workspace.element_size(), handle)
     if st != RMSN_OK:
         raise RMSNormError(fn, st)
@@ -1801,7 +1801,8 @@ def rms_norm_embedding(ids: torch.Tensor, weight: torch.Tensor, scale: float = 1
                        padding_idx: Optional[int] = None,
                        dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """Differentiable ``rms_norm_embedding_fwd``, in the weight.  Tokens of
-    ``padding_idx`` take their row, and give it no gradient."""
+    ``padding_idx`` take their row, and give it no gradient.  Captured into a
+    CUDA graph as ``rms_norm_rotary``."""
     return RMSNormEmbeddingFunction.apply(ids, weight, scale, padding_idx, dtype)
 
 

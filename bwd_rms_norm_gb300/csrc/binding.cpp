@@ -740,11 +740,12 @@ PyObject* embedding_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     {
       const Unlocked unlocked;
       out = dw ? *dw.t : empty({vocab, hidden}, type, device);
-      if (!ws.defined()) ws = bytes(more.embedding_ws(tokens, vocab, hidden), device);
+      const size_t need = more.embedding_ws(tokens, vocab, hidden);
+      if (need > 0 && !ws.defined()) ws = bytes(need, device);
       st = more.embedding_bwd(dy.ptr(), ids->data_ptr(), ids->scalar_type() == at::kLong,
                               out.data_ptr(), tokens, vocab, hidden, (float)scale, pad,
                               (int)accumulate, code_of(*dy.t), code_of(type), ptr(ws),
-                              (size_t)ws.nbytes(),
+                              ws.defined() ? (size_t)ws.nbytes() : 0,
                               c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream());
     }
     if (st != RMSN_OK) return nullptr;

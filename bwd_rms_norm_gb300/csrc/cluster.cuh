@@ -37,15 +37,6 @@ __device__ __forceinline__ void st_peer2(float2* local, uint32_t peer, float2 v)
                : "memory");
 }
 
-// The word at `local` in the shared memory of CTA `peer` of the cluster.
-__device__ __forceinline__ uint32_t ld_peer(const void* local, uint32_t peer) {
-  const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(local));
-  uint32_t remote, v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(a), "r"(peer));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
-  return v;
-}
-
 // Sum of `v` over the cluster, the same value (and order) in every thread:
 // CTA sum (block_sum), pushed to slot[rank] of every CTA, cluster barrier,
 // slots added in rank order.  `slots` holds 2 x kMaxCluster floats; the

@@ -13,7 +13,7 @@
 // every row of the table is written.  The rows without a token are cleared by
 // warps of their own beside the sort, the sums and the joins, whose latencies
 // this hides.
-#include "cluster.cuh"
+#include "cluster_launch.cuh"
 #include "embedding.cuh"
 #include "pairs.cuh"
 
@@ -677,6 +677,7 @@ int piece_of(int64_t tokens, int64_t hidden) {
 }
 
 size_t workspace_of(int64_t tokens, int64_t hidden) {
+  if (tokens <= kFew) return 0;
   return 2 * (size_t)padded(tokens) * sizeof(uint2) +
          2 * (size_t)ceil_div(tokens, piece_of(tokens, hidden)) * (size_t)hidden * sizeof(float);
 }
@@ -702,7 +703,9 @@ cudaError_t launch_sort(SortParams& p, int sms, cudaStream_t s) {
   const size_t most = (size_t)(kSortWarps + 2) * sizeof(uint32_t) << kMaxBits;
   if (e == cudaSuccess) e = allow_launch<embedding_sort>(dev, most);
   if (e != cudaSuccess) return e;
-  int64_t clear = p.zeros > 0 ? least(ceil_div(p.zeros, 64 << 10), sms) : 0;
+  // the other SMs clear; whole clusters, one at least
+  int64_t clear = p.zeros > 0 ? least(ceil_div(p.zeros, 64 << 10), sms - p.cluster) : 0;
+  if (p.zeros > 0 && clear < 1) clear = 1;
   clear = ceil_div(clear, p.cluster) * p.cluster;
   return launch_kernel(embedding_sort, dim3((unsigned)(p.cluster + clear)), dim3(kSortThreads),
                        smem, s, p.cluster, p);
@@ -803,11 +806,12 @@ int rms_norm_embedding_bwd(const void* dy, const void* ids, int ids_64, void* dw
     const cudaError_t e = accumulate ? cudaSuccess : cudaMemsetAsync(dweight, 0, table, cs);
     return e == cudaSuccess ? RMSN_OK : cuda_fail(e);
   }
-  if (!dy || !ids || !workspace) return RMSN_ERR_NULL;
+  const size_t need = workspace_of(tokens, hidden);
+  if (!dy || !ids || (need > 0 && !workspace)) return RMSN_ERR_NULL;
   if ((uintptr_t)workspace % 16 != 0 || (uintptr_t)ids % ib != 0 || (uintptr_t)dy % tb != 0)
     return RMSN_ERR_ALIGN;
-  if (workspace_bytes < workspace_of(tokens, hidden)) return RMSN_ERR_WORKSPACE;
-  const Span out(dweight, table), ws(workspace, workspace_bytes);
+  if (workspace_bytes < need) return RMSN_ERR_WORKSPACE;
+  const Span out(dweight, table), ws(need > 0 ? workspace : nullptr, workspace_bytes);
   const Span ins[] = {{dy, (size_t)tokens * hidden * tb}, {ids, (size_t)tokens * ib}};
   if (out.meets(ws)) return RMSN_ERR_ARG;
   for (const Span& i : ins)

@@ -6,8 +6,6 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include <atomic>
-
 namespace rmsn {
 
 // Inputs of one forward call, already validated (rows >= 1).
@@ -138,22 +136,6 @@ cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t 
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
   LaunchLog& log = launch_log();
   if (e == cudaSuccess && log.n < 4) log.kern[log.n++] = reinterpret_cast<const void*>(kern);
-  return e;
-}
-
-// Lets KERNEL use `bytes` of dynamic shared memory, and clusters of more than 8
-// CTAs, once a device.
-template <auto KERNEL>
-cudaError_t allow_launch(int dev, size_t bytes) {
-  static std::atomic<uint64_t> done{0};
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  const void* kern = reinterpret_cast<const void*>(KERNEL);
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
   return e;
 }
 

@@ -2,7 +2,7 @@
 // token's angles.
 #pragma once
 
-#include "cluster.cuh"
+#include "cluster_launch.cuh"
 #include "common.cuh"
 #include "launch.h"
 #include "rms_norm.h"
@@ -41,16 +41,17 @@ struct RotaryParams {
   bool direct;           // backward: a side's CTAs are a cluster, which adds up their sums
 };
 
-// inv_freq in turns a position, as a fraction of 2^64: the product with a
-// position, modulo 2^64, is the angle modulo a turn, exactly.  1 / (2 pi) is
-// rounded to 53 bits, which is off by a turn * 2^-53 * position * inv_freq / 2 pi.
+// inv_freq in turns a position, in units of 2^-64 turns: the product with a
+// position, modulo 2^64, is the angle modulo a turn.  1 / (2 pi) goes in as two
+// doubles, so that the turns are off by 2^-63 or so a position, not by the 2^-54
+// of one product.
 __device__ __forceinline__ uint64_t fixed_turns(const RotaryParams& p, int i) {
+  constexpr double kHigh = 0x1.45f306dc9c883p-3, kLow = -0x1.6b01ec5417056p-57;
   const double f = p.freq64 ? static_cast<const double*>(p.inv_freq)[i]
                             : (double)static_cast<const float*>(p.inv_freq)[i];
-  double t = f * 0.15915494309189533577;
-  t -= floor(t);
-  if (!(t < 1.0)) t = 0.0;      // a negative t that 1 + t rounds up
-  return (uint64_t)(t * 18446744073709551616.0);
+  const double t = f * kHigh, rest = fma(f, kHigh, -t) + f * kLow;
+  const double part = t - rint(t);  // exact
+  return (uint64_t)((long long)(part * 0x1p64)) + (uint64_t)((long long)(rest * 0x1p64));
 }
 
 // (cos, sin) of a position's angle, from 32 bits of its turn (2^-33 turns off)

@@ -459,8 +459,9 @@ int rms_norm_grad_clip(const void* const* grads, const int64_t* numels, const in
  *           of the pair's columns (i, j) = (p, p + rotary_dim / 2), or
  *           (2 p, 2 p + 1) where `interleaved`;  y = u in the other columns
  *
- * rounded once, as stored.  The angle is exact modulo a turn: fixed-point
- * turns of 64 bits, so positions up to 2^31 and beyond lose nothing.
+ * rounded once, as stored.  The angle is found modulo a turn, in fixed-point
+ * turns of 64 bits: off by 2^-63 of a turn a position, nothing that fp32 shows
+ * at positions up to 2^31.
  *
  * The backward, from the gradients dy of both outputs: du = dy rotated back,
  *   dv = rstd * (g - vh * mean(g vh)),  g = du * gain,  vh = v * rstd
@@ -537,7 +538,8 @@ int rms_norm_rotary_bwd(const rmsn_heads* dq_out, const rmsn_heads* dk_out, cons
  * so that repeated calls give bit-identical results.  hidden is at most
  * RMSN_MAX_HIDDEN, tokens at most RMSN_MAX_ROWS, vocab at most
  * RMSN_EMBEDDING_MAX_VOCAB.  Outputs and workspace must not overlap an input or
- * each other (RMSN_ERR_ARG).  `workspace` as in rms_norm_bwd.
+ * each other (RMSN_ERR_ARG).  `workspace` as in rms_norm_bwd; few tokens need
+ * none (size 0, NULL allowed).
  */
 #define RMSN_EMBEDDING_MAX_VOCAB (1 << 30)
 int rms_norm_embedding_fwd(const void* ids, int ids_64, const void* weight, void* y,

@@ -126,6 +126,16 @@ def test_largest_ids(L):
     assert y[:, 0].tolist() == [6.0, 2.0, 3.0, 0.0, 6.0, 6.0, 7.0, 0.0]
 
 
+@pytest.mark.parametrize("types", PAIRS, ids="-".join)
+@pytest.mark.parametrize("hidden", [1, 64, 257, 1000, 1088])
+def test_types_of_many_tokens(L, types, hidden):
+    """The sorted tokens' way: ids of one piece, of two, and of dozens."""
+    ids = make_ids("padded", 900, 200).cuda()
+    check_bwd(L, ids, randn((900, hidden), types[0], 2), 200, types[1], 0.3, pad=0)
+    check_bwd(L, ids, randn((900, hidden), types[0], 2), 200, types[1], -2.0,
+              start=randn((200, hidden), types[1], 3))
+
+
 @pytest.mark.parametrize("kind", ["text", "same", "each", "padded"])
 def test_many_tokens(L, kind):
     # several entries a lane of the sort; ids that go on over thousands of pieces
@@ -147,13 +157,14 @@ def test_order_of_the_tokens(L):
     assert L.rms_norm_embedding_bwd(dy, ids, 5)[3].tolist() == [1.0] * 64
 
 
-def test_rows_that_are_not_touched(L):
+@pytest.mark.parametrize("tokens,hidden", [(100, 72), (3000, 72), (3000, 71)])
+def test_rows_that_are_not_touched(L, tokens, hidden):
     """Values behind the rows of the tokens stay what they are, not a number among them."""
-    ids = make_ids("padded", 100, 500).cuda()
-    start = torch.full((500, 72), float("nan"), device="cuda")
+    ids = make_ids("padded", tokens, 500).cuda()
+    start = torch.full((500, hidden), float("nan"), device="cuda")
     inside = ids[(ids >= 0) & (ids < 500)]
     start[inside] = 1.0
-    dy = randn((100, 72), "bf16", 1)
+    dy = randn((tokens, hidden), "bf16", 1)
     dy[(ids < 0) | (ids >= 500)] = float("inf")
     got = L.rms_norm_embedding_bwd(dy, ids, 500, dweight=start, accumulate=True)
     touched = torch.zeros(500, dtype=torch.bool, device="cuda")
@@ -186,12 +197,13 @@ def test_given_outputs_and_refusals(L):
     y = torch.empty((40, 64), dtype=torch.bfloat16, device="cuda")
     version = y._version
     assert L.rms_norm_embedding_fwd(ids, w, y=y) is y and y._version > version
-    ws = torch.empty(L.rms_norm_embedding_bwd_workspace_size(40, 30, 64), dtype=torch.uint8,
+    many, up = make_ids("text", 800, 30).cuda(), randn((800, 64), "bf16", 2)
+    ws = torch.empty(L.rms_norm_embedding_bwd_workspace_size(800, 30, 64), dtype=torch.uint8,
                      device="cuda")
-    assert torch.equal(L.rms_norm_embedding_bwd(dy, ids, 30, workspace=ws),
-                       L.rms_norm_embedding_bwd(dy, ids, 30))
+    assert torch.equal(L.rms_norm_embedding_bwd(up, many, 30, workspace=ws),
+                       L.rms_norm_embedding_bwd(up, many, 30))
     with pytest.raises(L.RMSNormError):
-        L.rms_norm_embedding_bwd(dy, ids, 30, workspace=ws[:-16])
+        L.rms_norm_embedding_bwd(up, many, 30, workspace=ws[:-16])
     with pytest.raises(L.RMSNormError):
         L.rms_norm_embedding_bwd(dy, ids, 30, dweight=dy[:30])
     with pytest.raises(L.RMSNormError):

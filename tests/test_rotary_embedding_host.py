@@ -160,7 +160,7 @@ def emb(L, **k):
 def emb_bwd(L, **k):
     g = lambda n, d: k[n] if n in k else d  # noqa: E731
     lib = L.load_library()
-    need = lib.rms_norm_embedding_bwd_workspace_size(8, 16, 64)
+    need = lib.rms_norm_embedding_bwd_workspace_size(g("tokens", 8), 16, 64)
     return lib.rms_norm_embedding_bwd(
         g("y", 0x200000), g("ids", 0x1000), g("i64", 1), g("w", 0x100000), g("tokens", 8),
         g("vocab", 16), g("hidden", 64), g("scale", 1.0), g("pad", -1), g("acc", 0), g("yt", 1),
@@ -189,10 +189,14 @@ def test_embedding_call_refusals(L):
     assert emb(L, y=0x1000 - 1022) == ARG and emb(L, tokens=0, y=NULL) == OK
     assert emb_bwd(L, w=0x1000 - 2046) == ARG and emb_bwd(L, acc=2) == ARG
     assert emb_bwd(L, tokens=0, acc=1) == OK
-    assert emb_bwd(L, ws=0x300008) == ALIGN and emb_bwd(L, ws=NULL) == ERR_NULL
-    assert emb_bwd(L, ws=0x100000) == ARG and emb_bwd(L, ws=0x200000) == ARG
-    need = L.rms_norm_embedding_bwd_workspace_size(8, 16, 64)
-    assert need > 0 and emb_bwd(L, ws_bytes=need - 1) == WORKSPACE
+    # few tokens need no workspace; more do
+    assert L.rms_norm_embedding_bwd_workspace_size(512, 16, 64) == 0
+    need = L.rms_norm_embedding_bwd_workspace_size(600, 16, 64)
+    many = dict(tokens=600, ids=0x20000)
+    assert emb_bwd(L, ws=0x300008, **many) == ALIGN and emb_bwd(L, ws=NULL, **many) == ERR_NULL
+    for at in (0x100000, 0x200000, 0x200000 + 600 * 128 - 16, 0x20000):
+        assert emb_bwd(L, ws=at, **many) == ARG
+    assert need > 0 and emb_bwd(L, ws_bytes=need - 1, **many) == WORKSPACE
     for bad in ((0, 16, 64), (-1, 16, 64), (8, 0, 64), (8, 16, 0), (8, 16, 65537)):
         assert L.rms_norm_embedding_bwd_workspace_size(*bad) == 0
 

@@ -173,6 +173,14 @@ def test_positions(L, pos, dim):
     both(L, dict(c, freq=c["freq"].float()))
 
 
+def test_far_positions_at_full_frequency(L):
+    """Positions to 2^31 at up to a radian each: 2^-63 of a turn a position is 1e-9 rad."""
+    c = make(1, 40, 2, 1, 64, 64, "f32")
+    at = torch.randint(0, 1 << 31, (1, 40), generator=torch.Generator().manual_seed(4))
+    both(L, dict(c, pos=at.cuda()))
+    both(L, dict(c, pos=at.int().cuda(), freq=c["freq"].float()))
+
+
 def test_frequencies_of_any_size(L):
     # above a turn a position, negative, zero, tiny
     freq = torch.tensor([7.5, -0.3, 0.0, 1e-30, 6.283185307179586, -1e-25, 100.25, 3.0],
