@@ -459,12 +459,16 @@ rmsn_heads heads_of(const at::Tensor& t) {
 // A new tensor like torch.empty_like's.
 at::Tensor heads_like(const at::Tensor& t, int device) {
   int64_t last = 0;
-  for (int64_t i = t.dim() - 1; i >= 0; --i) {
+  bool in_order = true;
+  for (int64_t i = t.dim() - 1; i >= 0 && in_order; --i) {
     if (t.size(i) == 1) continue;
-    if (t.stride(i) < last) return at::empty_like(t);  // its dimensions in another order
+    in_order = t.stride(i) >= last;
     last = t.stride(i);
   }
-  return empty(t.sizes(), t.scalar_type(), device);
+  if (in_order) return empty(t.sizes(), t.scalar_type(), device);
+  if (!t.is_non_overlapping_and_dense()) return at::empty_like(t);
+  return at::Tensor(at::detail::empty_strided_cuda(
+      t.sizes(), t.strides(), t.scalar_type(), at::Device(at::kCUDA, (c10::DeviceIndex)device)));
 }
 
 // What the head norm's calls share.
