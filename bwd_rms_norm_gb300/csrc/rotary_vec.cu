@@ -2,6 +2,7 @@
 // head's row, two vectors a lane, 32 / G heads a warp at a time.
 #include <type_traits>
 
+#include "pairs.cuh"
 #include "rotary.cuh"
 
 namespace rmsn {
@@ -46,16 +47,21 @@ int lanes_of(const RotaryParams& p, int v, int mode) {
   return paired + (n - 2 * paired + 1) / 2;
 }
 
-// A token's angles: every pair's (cos, sin) in the warp's shared memory, and
-// those of this lane's columns in registers.
+// Every pair's (cos, sin) of a token's angles, in the warp's shared memory.
+__device__ __forceinline__ void find_angles(const RotaryParams& p, const uint64_t* turns,
+                                            float2* cs, int64_t position, int lane) {
+  __syncwarp();
+  for (int i = lane; i < p.half; i += 32) cs[i] = turn_of(turns[i], position);
+  __syncwarp();
+}
+
+// A token's angles of this lane's columns.
 template <int V, int MODE>
 struct Angles {
   float c[V], s[V];  // kHalves: of the pairs a ..; kNeighbours: a / 2 .., b / 2 ..
   __device__ __forceinline__ void take(const RotaryParams& p, const uint64_t* turns, float2* cs,
                                        int64_t position, const Lane<V, MODE>& at, int lane) {
-    __syncwarp();
-    for (int i = lane; i < p.half; i += 32) cs[i] = turn_of(turns[i], position);
-    __syncwarp();
+    find_angles(p, turns, cs, position, lane);
     if constexpr (MODE != kApart) {
 #pragma unroll
       for (int k = 0; k < V; ++k) {
@@ -136,16 +142,114 @@ struct Angles {
   }
 };
 
+template <typename T>
+__device__ __forceinline__ uint4 load_at(const T* row, int c, int dim, bool in) {
+  return in && c < dim ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
+}
+
+// A vector's values by pairs.
+template <typename T, int E>
+__device__ __forceinline__ void unpack2(const uint4& v, f32x2 (&f)[E]) {
+  if constexpr (E == 2) {
+    f[0] = pair(__uint_as_float(v.x), __uint_as_float(v.y));
+    f[1] = pair(__uint_as_float(v.z), __uint_as_float(v.w));
+  } else {
+    f[0] = widen<T>(v.x);
+    f[1] = widen<T>(v.y);
+    f[2] = widen<T>(v.z);
+    f[3] = widen<T>(v.w);
+  }
+}
+
+__device__ __forceinline__ f32x2 swapped(f32x2 v) {
+  const float2 f = split(v);
+  return pair(f.y, f.x);
+}
+
+// The forward's factors of a lane's columns x (of its first vector) and y, with
+// x', y' the pairs' other columns: gain and angle in one,
+//   kHalves:     x <- x a - y b,   y <- y c + x d
+//   kNeighbours: x <- x a + x' b,  y <- y c + y' d
+//   kApart:      x <- x a,  y <- y c, and then the angle
+template <int V, int MODE>
+struct Factors {
+  static constexpr int E = V / 2;
+  f32x2 a[E], b[E], c[E], d[E];
+  template <typename T>
+  __device__ __forceinline__ void take(const RotaryParams& p, const RotarySide& s, const float2* cs,
+                                       const Lane<V, MODE>& at) {
+    const T* gamma = static_cast<const T*>(s.gamma);
+    unpack2<T>(load_at(gamma, at.a, p.dim, true), a);
+    unpack2<T>(load_at(gamma, at.b, p.dim, true), c);
+    const f32x2 off = pair(p.off, p.off);
+    const float2 none = make_float2(1.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      const f32x2 ga = add2(a[k], off), gb = add2(c[k], off);
+      if constexpr (MODE == kApart) {
+        a[k] = ga;
+        c[k] = gb;
+      } else if constexpr (MODE == kHalves) {
+        const int i = at.a + 2 * k;
+        const bool in = i < p.half;
+        const float2 u = in ? cs[i] : none, v = in ? cs[i + 1] : none;
+        const f32x2 cos = pair(u.x, v.x), sin = pair(u.y, v.y);
+        a[k] = mul2(ga, cos);
+        b[k] = mul2(gb, pair(-u.y, -v.y));
+        c[k] = mul2(gb, cos);
+        d[k] = mul2(ga, sin);
+      } else {
+        const int i = at.a / 2 + k, j = at.b / 2 + k;
+        const float2 u = i < p.half ? cs[i] : none, v = j < p.half ? cs[j] : none;
+        a[k] = mul2(ga, pair(u.x, u.x));
+        b[k] = mul2(swapped(ga), pair(-u.y, u.y));
+        c[k] = mul2(gb, pair(v.x, v.x));
+        d[k] = mul2(swapped(gb), pair(-v.y, v.y));
+      }
+    }
+  }
+  __device__ __forceinline__ void apply(f32x2 (&x)[E], f32x2 (&y)[E]) const {
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      if constexpr (MODE == kHalves) {
+        const f32x2 u = fma2(y[k], b[k], mul2(x[k], a[k]));
+        y[k] = fma2(x[k], d[k], mul2(y[k], c[k]));
+        x[k] = u;
+      } else if constexpr (MODE == kNeighbours) {
+        x[k] = fma2(swapped(x[k]), b[k], mul2(x[k], a[k]));
+        y[k] = fma2(swapped(y[k]), d[k], mul2(y[k], c[k]));
+      } else {
+        x[k] = mul2(x[k], a[k]);
+        y[k] = mul2(y[k], c[k]);
+      }
+    }
+  }
+};
+
+// A row's columns turned through shared memory (MODE kApart).
+template <int E, int MODE>
+__device__ __forceinline__ void turn_apart(const RotaryParams& p, const float2* cs, float* row,
+                                           const Lane<2 * E, MODE>& at, f32x2 (&x)[E],
+                                           f32x2 (&y)[E]) {
+  float u[2 * E], v[2 * E];
+#pragma unroll
+  for (int k = 0; k < E; ++k) {
+    const float2 a = split(x[k]), b = split(y[k]);
+    u[2 * k] = a.x, u[2 * k + 1] = a.y, v[2 * k] = b.x, v[2 * k + 1] = b.y;
+  }
+  Angles<2 * E, MODE>().template turn<1>(p, cs, row, at, u, v);
+#pragma unroll
+  for (int k = 0; k < E; ++k) {
+    x[k] = pair(u[2 * k], u[2 * k + 1]);
+    y[k] = pair(v[2 * k], v[2 * k + 1]);
+  }
+}
+
 template <int G>
 __device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
   for (int m = G / 2; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
   return v;
-}
-
-template <typename T>
-__device__ __forceinline__ uint4 load_at(const T* row, int c, int dim, bool in) {
-  return in && c < dim ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
 }
 
 template <typename T, int V>
@@ -200,8 +304,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const T* in = reinterpret_cast<const T*>(s.in.p) + row_at(s.in, b, t, 0);
     T* out = reinterpret_cast<T*>(s.out.p) + row_at(s.out, b, t, 0);
     float* rstd = s.rstd ? s.rstd + (int64_t)token * s.heads : nullptr;
-    Angles<V, MODE> angles;
-    float ga[V], gb[V];
+    Factors<V, MODE> factors;
     for (int h0 = first; h0 < end; h0 += kSteps * HPS) {
       uint4 va[kSteps], vb[kSteps];
 #pragma unroll
@@ -211,41 +314,45 @@ __global__ void __launch_bounds__(kThreads, 2)
         vb[i] = load_at(in + h * s.in.sh, at.b, p.dim, h < end);
       }
       if (h0 == first) {
-        angles.take(p, sh.turns, sh.cs[warp], position_of(p, b, t), at, lane);
-        gains<T>(s, at.a, p.dim, p.off, ga);
-        gains<T>(s, at.b, p.dim, p.off, gb);
+        find_angles(p, sh.turns, sh.cs[warp], position_of(p, b, t), lane);
+        factors.template take<T>(p, s, sh.cs[warp], at);
       }
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
         if (h0 + i * HPS >= end) break;
         const int h = h0 + i * HPS + group;
-        float x[V], y[V];
-        unpack<T>(va[i], x);
-        unpack<T>(vb[i], y);
-        float ss = 0.f;
+        f32x2 x[V / 2], y[V / 2];
+        unpack2<T>(va[i], x);
+        unpack2<T>(vb[i], y);
+        f32x2 squares = mul2(x[0], x[0]);
 #pragma unroll
-        for (int k = 0; k < V; ++k) ss = fmaf(x[k], x[k], fmaf(y[k], y[k], ss));
-        ss = group_sum<G>(ss);
+        for (int k = 1; k < V / 2; ++k) squares = fma2(x[k], x[k], squares);
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) squares = fma2(y[k], y[k], squares);
+        const float ss = group_sum<G>(sum2(squares));
         float rs = __frsqrt_rn(fmaf(ss, inv_n, p.eps));
         if (__any_sync(0xffffffffu, isinf(ss))) {  // the squares are beyond fp32
-          float s2 = 0.f;
+          const f32x2 down = pair(kOverflowScale, kOverflowScale);
+          squares = 0;
 #pragma unroll
-          for (int k = 0; k < V; ++k) {
-            const float c = x[k] * kOverflowScale, d = y[k] * kOverflowScale;
-            s2 = fmaf(c, c, fmaf(d, d, s2));
+          for (int k = 0; k < V / 2; ++k) {
+            const f32x2 c = mul2(x[k], down), d = mul2(y[k], down);
+            squares = fma2(c, c, fma2(d, d, squares));
           }
-          s2 = group_sum<G>(s2);
+          const float s2 = group_sum<G>(sum2(squares));
           if (isinf(ss)) rs = rstd_rescaled(s2, p.dim, p.eps);
         }
         if (rstd && lane % G == 0 && h < end) rstd[h] = rs;
+        const f32x2 r = pair(rs, rs);
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          x[k] = x[k] * rs * ga[k];
-          y[k] = y[k] * rs * gb[k];
+        for (int k = 0; k < V / 2; ++k) {
+          x[k] = mul2(x[k], r);
+          y[k] = mul2(y[k], r);
         }
-        angles.template turn<1>(p, sh.cs[warp], row, at, x, y);
-        if (h < end && at.a < p.dim) st_vec(out + h * s.out.sh + at.a, pack<T>(x));
-        if (h < end && at.b < p.dim) st_vec(out + h * s.out.sh + at.b, pack<T>(y));
+        factors.apply(x, y);
+        if constexpr (MODE == kApart) turn_apart(p, sh.cs[warp], row, at, x, y);
+        if (h < end && at.a < p.dim) store_pairs(out + h * s.out.sh + at.a, x);
+        if (h < end && at.b < p.dim) store_pairs(out + h * s.out.sh + at.b, y);
       }
     }
   }
