@@ -463,10 +463,20 @@ __device__ __forceinline__ void clear_rows(const SumParams& p, uint32_t* bits, i
     const uint32_t end = (uint32_t)(base + rows);
     for (int i = lane; i < (rows + 31) / 32; i += 32) bits[i] = 0;
     __syncwarp();
-    for (int64_t i = first_not_below(p, (uint32_t)base, lane) + lane;; i += 32) {
-      const uint32_t key = i < p.tokens ? p.sorted[i].x : 0xffffffffu;
-      if (key < end) atomicOr(&bits[(key - (uint32_t)base) >> 5], 1u << ((key - (uint32_t)base) & 31));
-      if (!__all_sync(0xffffffffu, key < end)) break;
+    // eight of a lane's ids under way together: frequent ones have thousands of tokens
+    for (int64_t i = first_not_below(p, (uint32_t)base, lane) + lane;; i += 256) {
+      uint32_t key[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        key[k] = i + 32 * k < p.tokens ? p.sorted[i + 32 * k].x : 0xffffffffu;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {  // of equal neighbours one
+        const uint32_t before = __shfl_up_sync(0xffffffffu, key[k], 1);
+        const uint32_t at = key[k] - (uint32_t)base;
+        if (key[k] < end && (lane == 0 || key[k] != before))
+          atomicOr(&bits[at >> 5], 1u << (at & 31));
+      }
+      if (!__all_sync(0xffffffffu, key[7] < end)) break;
     }
     __syncwarp();
     clear_unmarked(static_cast<U*>(p.dweight) + base * p.hidden, p.hidden, bits, rows, lane);
@@ -734,16 +744,19 @@ cudaError_t launch_sums(SortParams& sort, SumParams& p, cudaStream_t s, int* lau
     if (e == cudaSuccess) ++*launches;
     return e;
   }
-  // rows cleared beside the sort, and before the joins
-  const int64_t first = least(kClearSort / row, p.vocab), joins = kClearJoins / row;
-  const int64_t last = p.vocab - joins > first ? p.vocab - joins : first;
-  sort.zeros = p.accumulate ? 0 : first * row;
+  // Beside the sums the first rows are cleared, beside the joins the next ones, and
+  // beside the sort the last, with the tokens' among them: where ids go by
+  // frequency those are few there.
+  const int64_t sorts = least(kClearSort / row, p.vocab), rest = p.vocab - sorts;
+  const int64_t joins = least(kClearJoins / row, rest);
+  sort.zero = static_cast<char*>(p.dweight) + rest * row;
+  sort.zeros = p.accumulate ? 0 : sorts * row;
   e = launch_sort(sort, sms, s);
   if (e != cudaSuccess) return e;
   ++*launches;
   p.sorted = sort.items[(sort.passes - 1) & 1];  // where the last pass wrote
-  p.clear0 = first;
-  p.clear1 = last;
+  p.clear0 = 0;
+  p.clear1 = rest - joins;
   constexpr int W = VEC ? 2 * E : E;
   const bool two = VEC && wide(p.hidden);
   auto sums = p.accumulate ? two ? embedding_sums<T, U, W, VEC, true>
@@ -762,8 +775,8 @@ cudaError_t launch_sums(SortParams& sort, SumParams& p, cudaStream_t s, int* lau
   e = launch(sums, pieces * ceil_div(p.hidden, 32 * (two ? W : E)), clears());
   if (e != cudaSuccess) return e;
   ++*launches;
-  p.clear0 = last;
-  p.clear1 = p.vocab;
+  p.clear0 = rest - joins;
+  p.clear1 = rest;
   if (pieces > 1) {
     const bool team = !wide(p.hidden);
     const int64_t slabs = ceil_div(p.hidden, 128);
@@ -819,7 +832,7 @@ int rms_norm_embedding_bwd(const void* dy, const void* ids, int ids_64, void* dw
   uint2* w = static_cast<uint2*>(workspace);
   const int64_t n = padded(tokens);
   SortParams sort = {{ids, ids_64}, tokens, vocab, padding_idx, {w, w + n}, 0, 0, 1,
-                     static_cast<char*>(dweight), 0};
+                     nullptr, 0};
   SumParams sum = {dy, {ids, ids_64}, nullptr, 0, 0, reinterpret_cast<float*>(w + 2 * n),
                    dweight, tokens, vocab, padding_idx, 0, 0, (int)hidden, accumulate, scale};
   int launches = 0;
