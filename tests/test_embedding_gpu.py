@@ -263,6 +263,19 @@ def test_streams_and_graphs(L):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_two_streams_at_once(L):
+    sets = [(make_ids("text", n, 4000, n).cuda(), randn((n, 264), "bf16", n)) for n in (5000, 300)]
+    want = [L.rms_norm_embedding_bwd(dy, ids, 4000) for ids, dy in sets]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in sets], [None, None]
+    for _ in range(10):
+        for i, (s, (ids, dy)) in enumerate(zip(streams, sets)):
+            with torch.cuda.stream(s):
+                got[i] = L.rms_norm_embedding_bwd(dy, ids, 4000)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_autograd_and_module(L):
     m = L.RMSNormEmbedding(50, 64, scale=8.0, padding_idx=4, out_dtype=torch.float32,
                            device="cuda", dtype=torch.bfloat16)

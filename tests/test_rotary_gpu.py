@@ -372,6 +372,51 @@ def test_autograd(L, interleaved):
     assert leaf.grad.shape == leaf.shape and bool(leaf.grad.any())
 
 
+def test_autograd_of_queries_alone_and_of_one_output(L):
+    c = make(1, 9, 4, 2, 64, 32, "f32")
+    q, w = (c[n].detach().clone().requires_grad_() for n in ("q", "q_gamma"))
+    L.rms_norm_rotary(q, None, w, None, c["freq"], c["pos"]).backward(c["dq"])
+    both_q, both_w, k = (c[n].detach().clone().requires_grad_() for n in ("q", "q_gamma", "k"))
+    L.rms_norm_rotary(both_q, k, both_w, c["k_gamma"], c["freq"], c["pos"])[0].backward(c["dq"])
+    assert torch.equal(q.grad, both_q.grad) and torch.equal(w.grad, both_w.grad)
+    assert not k.grad.any()
+    # one head of keys for all, and one row of positions for every batch entry
+    one = torch.randn(2, 9, 1, 64, device="cuda", requires_grad=True)
+    y = L.rms_norm_rotary(one.expand(2, 9, 4, 64), None, w, None, c["freq"],
+                          torch.arange(9, device="cuda").expand(2, 9))
+    y.sum().backward()
+    assert one.grad.shape == one.shape and bool(one.grad.any())
+
+
+def test_two_streams_at_once(L):
+    cs = [make(1, 700, 8, 2, 128, 128, "bf16", seed=s) for s in (1, 2)]
+
+    def step(c):
+        y = L.rms_norm_rotary_fwd(c["q"], c["k"], c["q_gamma"], c["k_gamma"], c["freq"], c["pos"])
+        return *y, *L.rms_norm_rotary_bwd(c["dq"], c["dk"], c["q"], c["k"], c["q_gamma"],
+                                          c["k_gamma"], y[2], y[3], c["freq"], c["pos"])
+
+    want = [step(c) for c in cs]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in cs], [None, None]
+    for _ in range(10):
+        for i, (s, c) in enumerate(zip(streams, cs)):
+            with torch.cuda.stream(s):
+                got[i] = step(c)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for u, v in zip(got, want) for a, b in zip(u, v))
+
+
+def test_inference_mode(L):
+    c = make(1, 5, 4, 2, 64, 32, "bf16")
+    with torch.inference_mode():
+        q, k = c["q"].clone(), c["k"].clone()
+        L.rms_norm_rotary_fwd(q, k, c["q_gamma"], c["k_gamma"], c["freq"], c["pos"], q_out=q,
+                              k_out=k, with_rstd=False)
+    want = L.rms_norm_rotary_fwd(c["q"], c["k"], c["q_gamma"], c["k_gamma"], c["freq"], c["pos"])
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+
+
 def test_module(L):
     m = L.RMSNormRotary(64, base=500000.0, rotary_dim=32, device="cuda", dtype=torch.bfloat16)
     c = make(2, 9, 4, 2, 64, 32, "bf16", pos="none", base=500000.0)
