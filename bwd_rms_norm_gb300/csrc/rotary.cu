@@ -189,7 +189,10 @@ cudaError_t launch_bwd_t(int dtype, RotaryParams& p, cudaStream_t s, int* launch
     const size_t smem = (size_t)kWarps * p.dim * sizeof(float);
     e = allow_launch<kern>(dev, kWarps * RMSN_ROTARY_MAX_DIM * sizeof(float));
     if (e != cudaSuccess) return e;
-    const int cluster = place_ctas(p, (const void*)kern, kThreads, smem, kWarps, sm_count(dev));
+    const int sms = sm_count(dev);
+    const int64_t most = (int64_t)sms * max_blocks_per_sm((const void*)kern, kThreads, smem);
+    const int cluster =
+        place_ctas(p, most, kWarps, sms, p.side[0].heads, p.side[1].heads);
     e = launch_kernel(kern, dim3((unsigned)(p.side[0].ctas + p.side[1].ctas)), dim3(kThreads),
                       smem, s, cluster, p);
   }

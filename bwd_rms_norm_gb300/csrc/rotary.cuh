@@ -108,17 +108,17 @@ __device__ __forceinline__ void add_cluster(const float* mine, float* dgamma, in
   cluster_sync();  // no CTA leaves while its sums are read
 }
 
-// Shares `most` CTAs between queries and keys by their heads, at least one
-// each, and places their partial rows; a CTA has `rows_a_cta` rows at least.
-inline void share_ctas(RotaryParams& p, int64_t most, int64_t rows_a_cta) {
-  const int64_t all = p.side[0].heads + p.side[1].heads;
+// Shares `most` CTAs between queries and keys by their costs, at least one each,
+// and places their partial rows; a CTA has `rows_a_cta` rows at least.
+inline void share_ctas(RotaryParams& p, int64_t most, int64_t rows_a_cta, int64_t q_cost,
+                       int64_t k_cost) {
   if (most > RMSN_ROTARY_MAX_PARTIALS) most = RMSN_ROTARY_MAX_PARTIALS;
   if (most < 2) most = 2;
   int64_t left = most;
   for (int i = 1; i >= 0; --i) {
     RotarySide& s = p.side[i];
     if (s.heads == 0) continue;
-    int64_t n = i == 1 ? (most * s.heads + all / 2) / all : left;
+    int64_t n = i == 1 ? most * k_cost / (q_cost + k_cost) : left;
     if (n < 1) n = 1;
     if (i == 1 && n >= most) n = most - 1;
     left -= n;
@@ -128,11 +128,12 @@ inline void share_ctas(RotaryParams& p, int64_t most, int64_t rows_a_cta) {
   p.side[1].partial = p.side[0].partial + (int64_t)p.side[0].ctas * p.dim;
 }
 
-// The backward's CTAs; returns the size of their clusters.
-inline int place_ctas(RotaryParams& p, const void* kern, int threads, size_t smem,
-                      int64_t rows_a_cta, int sms) {
+// The backward's CTAs, of `most` at once; returns the size of their clusters.
+// q_cost, k_cost: of a token's queries and of its keys.
+inline int place_ctas(RotaryParams& p, int64_t most, int64_t rows_a_cta, int sms, int64_t q_cost,
+                      int64_t k_cost) {
   if (!p.direct) {
-    share_ctas(p, (int64_t)sms * max_blocks_per_sm(kern, threads, smem), rows_a_cta);
+    share_ctas(p, most, rows_a_cta, q_cost, k_cost);
     return 1;
   }
   const int heads = p.side[0].heads > p.side[1].heads ? p.side[0].heads : p.side[1].heads;

@@ -504,10 +504,19 @@ cudaError_t launch_bwd_g(RotaryParams& p, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = allow_launch<kern>(dev, 0);
   if (e != cudaSuccess) return e;
+  constexpr int hps = 32 / G;
+  const int sms = sm_count(dev);
+  const int64_t most = (int64_t)sms * max_blocks_per_sm((const void*)kern, kThreads, 0);
+  const int per = heads_per_unit(p.all, p.side[0].heads, hps, kBwdSteps,
+                                 (p.direct ? 2 * kMaxCluster : most) * kWarps);
+  // a unit costs its steps and about one more for its angles (shared by heads alone
+  // the keys' CTAs end last: 4096 x (32+8) x 128 bf16 30.5 us, 29.7
+  // so; 16384 x (32+8) x 64 69 and 56)
+  const auto cost = [&](int heads) {
+    return (int64_t)((heads + hps - 1) / hps + (heads + per - 1) / per);
+  };
   const int cluster =
-      place_ctas(p, (const void*)kern, kThreads, 0, kWarps * (32 / G), sm_count(dev));
-  const int64_t warps = (int64_t)(p.side[0].ctas + p.side[1].ctas) * kWarps;
-  const int per = heads_per_unit(p.all, p.side[0].heads, 32 / G, kBwdSteps, warps);
+      place_ctas(p, most, kWarps * hps, sms, cost(p.side[0].heads), cost(p.side[1].heads));
   return launch_kernel(kern, dim3((unsigned)(p.side[0].ctas + p.side[1].ctas)), dim3(kThreads), 0,
                        s, cluster, p, per);
 }
