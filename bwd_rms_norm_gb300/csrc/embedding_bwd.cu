@@ -4,7 +4,7 @@
 // Up to kFew tokens one kernel does it all: every CTA has the ids in shared
 // memory, and the warp of an id's first token looks the others up.  Beyond, a
 // cluster of CTAs sorts the tokens by id (embedding_sort); warps then sum pieces
-// of 32 sorted entries (embedding_sums): an id whose entries all lie in a piece
+// of up to 32 sorted entries (embedding_sums): an id whose entries all lie in a piece
 // is done, of one that goes on the piece's part is kept as an open sum, and a
 // third kernel adds those (embedding_joins).  No atomics: an element's order of
 // additions is fixed by the ids.
@@ -335,17 +335,9 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort(const SortParams 
         }
       }
     };
-    // The lanes with this lane's digit, bit by bit (__match_any_sync takes some
-    // 30 cycles of the SM each).
+    // The lanes with this lane's digit; a lane behind the end has none.
     auto same = [&](bool in, uint32_t digit) {
-      uint32_t m = __ballot_sync(0xffffffffu, in);
-#pragma unroll
-      for (int b = 0; b < kMaxBits; ++b) {
-        if (b >= p.bits) break;
-        const uint32_t set = __ballot_sync(0xffffffffu, digit >> b & 1);
-        m &= digit >> b & 1 ? set : ~set;
-      }
-      return m;
+      return __match_any_sync(0xffffffffu, in ? digit : 0xffffffffu);
     };
     for (int i = lane; i < bins; i += 32) count[i] = 0;
     __syncwarp();

@@ -533,9 +533,10 @@ int rms_norm_rotary_bwd(const rmsn_heads* dq_out, const rmsn_heads* dk_out, cons
  * [tokens, hidden] are contiguous, of the same dtype or one of them fp32; so
  * are dy [tokens, hidden] and dweight [vocab, hidden].  Without `accumulate`
  * the whole of dweight is written, zeros where no token is; with it the rows of
- * the tokens alone are read and written.  A row's terms are added in fp32 in
- * the order of the tokens, in pieces whose ends are fixed by the tokens' ids,
- * so that repeated calls give bit-identical results.  hidden is at most
+ * the tokens alone are read and written.  A row's terms are added in fp32, in
+ * the order of the tokens within pieces, then the pieces' sums; which these are
+ * depends on the ids and the sizes alone, so that repeated calls give
+ * bit-identical results.  hidden is at most
  * RMSN_MAX_HIDDEN, tokens at most RMSN_MAX_ROWS, vocab at most
  * RMSN_EMBEDDING_MAX_VOCAB.  Outputs and workspace must not overlap an input or
  * each other (RMSN_ERR_ARG).  `workspace` as in rms_norm_bwd; few tokens need
