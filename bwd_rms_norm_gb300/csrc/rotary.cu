@@ -224,11 +224,9 @@ struct Block {
     const int64_t st[3] = {v->batch_stride, v->token_stride, v->head_stride};
     for (int i = 0; i < 3; ++i) size[i] = n[i], step[i] = n[i] > 1 ? st[i] * bytes : 0;
   }
-  // bytes from the first to behind the last, over the steps that are no multiples of t (0: all)
-  int64_t extent(int64_t t) const {
+  int64_t extent() const {  // bytes from the first to behind the last
     int64_t n = run;
-    for (int i = 0; i < 3; ++i)
-      if (t == 0 || step[i] % t != 0) n += (size[i] - 1) * step[i];
+    for (int i = 0; i < 3; ++i) n += (size[i] - 1) * step[i];
     return n;
   }
   bool operator==(const Block& o) const {
@@ -238,22 +236,50 @@ struct Block {
   }
 };
 
-// Whether two arguments may share a byte.  They do not where their extents do
-// not meet; nor where, modulo one of their steps t, the bytes of each lie in one
-// window and the windows do not meet (the parts of a packed product).
+// How far apart two arguments' runs can be: d bytes and lo to hi times each of `n`
+// steps, the largest first.
+struct Distances {
+  int n = 0;
+  int64_t step[6], lo[6], hi[6];
+  void add(int64_t s, int64_t from, int64_t to) {
+    if (s == 0 || from == to) return;
+    int at = 0;
+    while (at < n && step[at] > s) ++at;
+    if (at == n || step[at] != s) {
+      for (int i = n++; i > at; --i) step[i] = step[i - 1], lo[i] = lo[i - 1], hi[i] = hi[i - 1];
+      step[at] = s, lo[at] = hi[at] = 0;
+    }
+    lo[at] += from, hi[at] += to;
+  }
+  // Whether one is above -below and under `above`; taken to be so where `looks` run out.
+  bool between(int64_t d, int64_t below, int64_t above, int* looks, int at = 0) const {
+    if (at == n) return -below < d && d < above;
+    if (--*looks < 0) return true;
+    int64_t least = d, most = d;  // with what the smaller steps add
+    for (int i = at + 1; i < n; ++i) least += lo[i] * step[i], most += hi[i] * step[i];
+    auto floor_div = [](int64_t a, int64_t b) { return a / b - (a % b < 0); };
+    int64_t j = floor_div(-below - most, step[at]) + 1, end = -floor_div(least - above, step[at]);
+    if (j < lo[at]) j = lo[at];
+    if (end > hi[at] + 1) end = hi[at] + 1;
+    if (at + 1 == n) return j < end;
+    for (; j < end; ++j)
+      if (between(d + j * step[at], below, above, looks, at + 1)) return true;
+    return false;
+  }
+};
+
+// Whether two arguments share a byte.  Arguments whose steps lie within one another,
+// as in any slice or transpose of contiguous memory, take a few looks.
 bool meet(const Block& a, const Block& b) {
   if (a.run == 0 || b.run == 0) return false;
-  if (a.p + (uintptr_t)a.extent(0) <= b.p || b.p + (uintptr_t)b.extent(0) <= a.p) return false;
-  for (const Block* from : {&a, &b})
-    for (int i = 0; i < 3; ++i) {
-      const int64_t t = from->step[i];
-      if (t <= 0) continue;
-      const int64_t la = a.extent(t), lb = b.extent(t);
-      int64_t d = (int64_t)(b.p - a.p) % t;
-      if (d < 0) d += t;
-      if (la <= d && d + lb <= t) return false;
-    }
-  return true;
+  if (a.p + (uintptr_t)a.extent() <= b.p || b.p + (uintptr_t)b.extent() <= a.p) return false;
+  Distances way;
+  for (int i = 0; i < 3; ++i) {
+    way.add(a.step[i], 1 - a.size[i], 0);
+    way.add(b.step[i], 0, b.size[i] - 1);
+  }
+  int looks = 4096;
+  return way.between((int64_t)(b.p - a.p), b.run, a.run, &looks);
 }
 
 // Whether every element of an output has a place of its own.

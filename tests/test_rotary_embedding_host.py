@@ -95,8 +95,36 @@ def test_rotary_overlaps(L, call):
     for qo, ko in ((heads(L, 0x400000, 4 * t, t, 64), heads(L, 0x400000 + 3 * 128, 4 * t, t, 64)),
                    (heads(L, 0x400000, 4 * t, t, 64), heads(L, 0x400000 + 7 * 128, 4 * t, t, 64)),
                    (heads(L, 0x400000, 4 * t, t, 64),
-                    heads(L, 0x400000 + 4 * 128, 4 * t + 64, t, 64))):
+                    heads(L, 0x400000 + 4 * 128, 4 * t + 256, t, 64))):
         assert call(L, qo=qo, ko=ko) == ARG
+
+
+def places(at, strides, sizes, dim):
+    """The elements of a tensor of heads, as numbers of 2-byte places."""
+    import numpy as np
+    n = np.full((1,), at // 2)
+    for s, k in zip((*strides, 1), (*sizes, dim)):
+        n = (n[:, None] + s * np.arange(k)).ravel()
+    return n
+
+
+@pytest.mark.parametrize("call", [fwd, bwd])
+def test_rotary_overlaps_of_any_strides(L, call):
+    import numpy as np
+    rng = np.random.default_rng(0)
+    met = 0
+    for _ in range(2000):
+        at, st = [0x400000, 0x400000 + 2 * int(rng.integers(0, 4000))], []
+        for _ in range(2):
+            h = 64 * int(rng.integers(1, 4)) + int(rng.integers(0, 3))
+            t = int(rng.integers(1, 1200))
+            st.append((int(rng.integers(1, 5000)), t, h))
+        elements = [places(a, s, (2, 4, n), 64) for a, s, n in zip(at, st, (4, 2))]
+        if all(len(set(e)) == len(e) for e in elements) and not set(elements[0]) & set(elements[1]):
+            continue
+        met += 1
+        assert call(L, qo=heads(L, at[0], *st[0]), ko=heads(L, at[1], *st[1])) == ARG, (at, st)
+    assert met > 500
 
 
 def test_rotary_backward_refusals(L):

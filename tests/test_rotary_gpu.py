@@ -156,6 +156,68 @@ def test_layouts(L, layout, dim, rot, dtype):
         both(L, make(2, 19, 6, 2, dim, rot, dtype, layout), interleaved=interleaved)
 
 
+def test_outputs_told_apart_from_inputs(L):
+    # outputs between inputs of other strides in one buffer: what shares no element runs
+    g = torch.Generator().manual_seed(12)
+    c = make(2, 3, 2, 1, 16, 16, "bf16")
+    number = lambda lo, hi: int(torch.randint(lo, hi, (1,), generator=g))  # noqa: E731
+    ran = refused = 0
+    for _ in range(400):
+        buf = torch.zeros(4096, dtype=torch.bfloat16, device="cuda")
+        spots = torch.arange(4096)
+        views, taken = [], []
+        row = number(200, 500)
+        for n in (2, 1, 2, 1):
+            h = number(16, 24)
+            t = row if number(0, 4) else number(16 + h, 500)
+            strides = (3 * max(row, t) if number(0, 4) else number(16 + h + 2 * t, 1600), t, h, 1)
+            at = number(0, row)
+            views.append(torch.as_strided(buf, (2, 3, n, 16), strides, at))
+            taken.append(set(torch.as_strided(spots, (2, 3, n, 16), strides, at).flatten().tolist()))
+        q, k, q_out, k_out = views
+        if taken[0] & taken[1]:
+            continue
+        q.copy_(c["q"]), k.copy_(c["k"])
+        args = q, k, c["q_gamma"], c["k_gamma"], c["freq"], c["pos"], 1e-5
+        if (taken[0] | taken[1]) & (taken[2] | taken[3]) or taken[2] & taken[3]:
+            with pytest.raises(L.RMSNormError):
+                L.rms_norm_rotary_fwd(*args, q_out=q_out, k_out=k_out)
+            refused += 1
+        else:
+            got = L.rms_norm_rotary_fwd(*args, q_out=q_out, k_out=k_out)
+            check_forward(c, got, 1e-5, 0, False)
+            ran += 1
+    assert ran > 20 and refused > 20
+
+
+@pytest.mark.parametrize("dim", [64, 33])
+def test_offsets_beyond_32_bits(L, dim):
+    # inputs and outputs side by side in one buffer of 2^32 elements and more
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("not enough free memory")
+    b, n, hq, hk = 2, 3, 4, 2
+    far = (1 << 32) + (64 if dim == 64 else 65)
+    buf = torch.empty(far + (3 << 30), dtype=torch.bfloat16, device="cuda")
+    size = hq * 128
+
+    def place(number, t):
+        if t is None:
+            return None
+        view = torch.as_strided(buf, t.shape, (far, 1 << 30, 128, 1), number * size)
+        return view.copy_(t)
+
+    c = make(b, n, hq, hk, dim, 32, "bf16")
+    c = dict(c, **{k: place(i, c[k]) for i, k in enumerate(("q", "k", "dq", "dk"))})
+    out = [place(4, torch.zeros_like(c["q"])), place(5, torch.zeros_like(c["k"]))]
+    got = L.rms_norm_rotary_fwd(c["q"], c["k"], c["q_gamma"], c["k_gamma"], c["freq"], c["pos"],
+                                eps=1e-5, q_out=out[0], k_out=out[1])
+    assert got[0] is out[0] and got[1] is out[1]
+    check_forward(c, got, 1e-5, 0, False)
+    back = L.rms_norm_rotary_bwd(c["dq"], c["dk"], c["q"], c["k"], c["q_gamma"], c["k_gamma"],
+                                 got[2], got[3], c["freq"], c["pos"], dq=out[0], dk=out[1])
+    check_backward(c, back, got[2:], 0, False)
+
+
 @pytest.mark.parametrize("pos", ["none", "far"])
 @pytest.mark.parametrize("dim", [64, 33])
 def test_positions(L, pos, dim):
