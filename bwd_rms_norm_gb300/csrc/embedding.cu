@@ -8,9 +8,9 @@ constexpr int kWide = 4;
 
 // A warp takes K times 32 E columns of a token's row, all loads under way together.
 template <typename T, typename U, bool VEC, int K>
-__global__ void __launch_bounds__(kThreads) embedding_rows(Ids ids, const T* __restrict__ weight,
-                                                           U* __restrict__ y, int64_t tokens,
-                                                           int64_t vocab, int hidden, float scale) {
+__global__ void __launch_bounds__(kThreads) embedding_rows(Ids ids, const T* weight, U* y,
+                                                           int64_t tokens, int64_t vocab,
+                                                           int hidden, float scale) {
   constexpr int E = kElems<T, U>;
   pdl_wait();
   pdl_trigger();

@@ -126,6 +126,48 @@ def test_largest_ids(L):
     assert y[:, 0].tolist() == [6.0, 2.0, 3.0, 0.0, 6.0, 6.0, 7.0, 0.0]
 
 
+@pytest.mark.parametrize("tokens", [300, 700])
+def test_tables_beyond_32_bits(L, tokens):
+    vocab, hidden = (1 << 19) + 3, 8200
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("not enough free memory")
+    # the table's first row, its last, and rows on both sides of 2^31 and 2^32 elements
+    near_ = [0, (1 << 31) // hidden, (1 << 31) // hidden + 1, (1 << 32) // hidden,
+             (1 << 32) // hidden + 1, vocab - 1]
+    ids = torch.tensor(near_).repeat(tokens // 6 + 1)[:tokens].cuda()
+    dy = torch.randint(-3, 4, (tokens, hidden), generator=torch.Generator().manual_seed(3)).cuda()
+    ref = torch.stack([dy[ids == v].sum(0) for v in near_])    # whole numbers: exact
+    assert int(ref.abs().max()) <= 256                         # in bf16 too
+    dy = dy.bfloat16()
+    table = torch.ones((vocab, hidden), dtype=torch.bfloat16, device="cuda")
+    L.rms_norm_embedding_bwd(dy, ids, vocab, dweight=table)
+    assert torch.equal(table[near_], ref.bfloat16())
+    assert sum(int(part.count_nonzero()) for part in table.split(1 << 16)) == int(
+        ref.count_nonzero())
+    assert torch.equal(L.rms_norm_embedding_fwd(ids, table), table[ids])
+    L.rms_norm_embedding_bwd(dy, ids, vocab, scale=-1.0, dweight=table, accumulate=True)
+    assert not any(bool(part.any()) for part in table.split(1 << 16))
+
+
+def test_tokens_beyond_32_bits(L):
+    tokens, vocab, hidden = (1 << 19) + 5, 50, 8200
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("not enough free memory")
+    ids = make_ids("padded", tokens, vocab, 7).cuda()
+    weight = randn((vocab, hidden), "bf16", 8)
+    y = L.rms_norm_embedding_fwd(ids, weight)
+    zero = torch.cat((weight, torch.zeros_like(weight[:1])))
+    where = torch.where((ids >= 0) & (ids < vocab), ids, vocab)
+    for a in range(0, tokens, 1 << 16):
+        assert torch.equal(y[a:a + (1 << 16)], zero[where[a:a + (1 << 16)]])
+    dy = y.fill_(0.0)                     # whole numbers below 2^24 in sum: exact
+    dy[:] = (torch.arange(tokens, device="cuda") % 8)[:, None]
+    got = L.rms_norm_embedding_bwd(dy, ids, vocab)
+    ref = torch.zeros(vocab + 1, dtype=torch.float64, device="cuda").index_add_(
+        0, where, (torch.arange(tokens, device="cuda") % 8).double())
+    assert torch.equal(got, ref[:vocab, None].float().expand(vocab, hidden))
+
+
 @pytest.mark.parametrize("types", PAIRS, ids="-".join)
 @pytest.mark.parametrize("hidden", [1, 64, 257, 1000, 1088])
 def test_types_of_many_tokens(L, types, hidden):
