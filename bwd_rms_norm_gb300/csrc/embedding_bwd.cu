@@ -736,9 +736,12 @@ cudaError_t launch_sort(SortParams& p, int sms, cudaStream_t s) {
                        smem, s, p.cluster, p);
 }
 
-// Where the rows are cleared: as many bytes beside the sort and beside the joins
-// as those take time, the rest beside the sums.
-constexpr int64_t kClearSort = 64 << 20, kClearJoins = 100 << 20;
+// Where the rows are cleared: as many bytes beside the sort, which takes longer
+// for more tokens, and beside the joins as those take time, the rest beside the
+// sums.  With 64 MB beside any sort and 100 beside the joins 89591 tokens of 142402
+// ids of 384 columns take 90 us, 86 so; 11826 of 23462 of 4075 111 and 107; 600 of
+// 50000 of 768 33.1 and 32.3; 32768 of 32000 of 4096 bf16 111 and 113.
+constexpr int64_t kClearSort = 40 << 20, kClearToken = 1024, kClearJoins = 64 << 20;
 
 template <typename T, typename U, bool VEC>
 cudaError_t launch_sums(SortParams& sort, SumParams& p, cudaStream_t s, int* launches) {
@@ -762,7 +765,8 @@ cudaError_t launch_sums(SortParams& sort, SumParams& p, cudaStream_t s, int* lau
   // Beside the sums the first rows are cleared, beside the joins the next ones, and
   // beside the sort the last, with the tokens' among them: where ids go by
   // frequency those are few there.
-  const int64_t sorts = least(kClearSort / row, p.vocab), rest = p.vocab - sorts;
+  const int64_t sorts = least((kClearSort + p.tokens * kClearToken) / row, p.vocab);
+  const int64_t rest = p.vocab - sorts;
   const int64_t joins = least(kClearJoins / row, rest);
   sort.zero = static_cast<char*>(p.dweight) + rest * row;
   sort.zeros = p.accumulate ? 0 : sorts * row;
