@@ -1734,7 +1734,11 @@ class RMSNormRotary(torch.nn.Module):
     """The norms of an attention's queries and keys over each head, with their
     rotation: ``rotary_dim`` columns (all of them where it is not given) turn by
     ``position * base ** (-2 p / rotary_dim)`` for the pair p.  The weights start
-    at 1, or at 0 with ``offset=1``."""
+    at 1, or at 0 with ``offset=1``.  Other frequencies, as those of a longer
+    context, are assigned to ``inv_freq`` (fp64 or fp32, one a pair); casts and
+    moves of the module keep them and their dtype.  They are not in the state
+    dict, and a module on the meta device gets those of ``base`` when it leaves
+    it."""
 
     def __init__(self, head_dim: int, eps: float = 1e-6, offset: int = 0, base: float = 10000.0,
                  rotary_dim: Optional[int] = None, interleaved: bool = False, device=None,
@@ -1761,9 +1765,14 @@ class RMSNormRotary(torch.nn.Module):
         return float(self.base) ** (p * (-2.0 / max(self.rotary_dim, 1)))
 
     def _apply(self, fn, *args, **kwargs):
+        freq = self.inv_freq
         super()._apply(fn, *args, **kwargs)
-        # a change of the weights' dtype leaves the frequencies what they are
-        self.inv_freq = self._frequencies(self.q_weight.device)
+        # the frequencies, assigned ones too, go where the weights go, and stay what
+        # they are; on the meta device they have no values to keep
+        device = self.q_weight.device
+        if freq is not None:
+            lost = freq.is_meta and device.type != "meta"
+            self.inv_freq = self._frequencies(device) if lost else freq.to(device)
         return self
 
     def forward(self, q: torch.Tensor, k: torch.Tensor,
