@@ -18,6 +18,11 @@ enum Mode {
   kApart = 2        // (i, i + half), half not of whole vectors: through shared memory
 };
 
+// PART, of a row of which some columns do not rotate: those lie beside other columns
+// all the same, and take nothing from them, not 0 times a value that may not be finite.
+// Kernels of their own, as the selects cost a row that rotates as a whole 2 to 4 %
+// (32768 x (64+8) x 128 bf16 forward 205 and 210 us, with neighbours paired 203 and 211).
+
 // The columns of a lane's two vectors; dim where it has none.
 template <int V, int MODE>
 struct Lane {
@@ -75,10 +80,11 @@ struct Angles {
     }
   }
   // The lane's columns turned, by SIGN times the angle.
-  template <int SIGN>
+  template <int SIGN, bool PART>
   __device__ __forceinline__ void turn(const RotaryParams& p, const float2* cs, float* row,
                                        const Lane<V, MODE>& at, float (&x)[V], float (&y)[V]) const {
     if constexpr (MODE == kHalves) {
+      if (PART && at.a >= p.half) return;  // all of a lane's columns rotate, or none
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         const float u = x[k], w = y[k], t = SIGN * s[k];
@@ -89,11 +95,15 @@ struct Angles {
 #pragma unroll
       for (int k = 0; k < V; k += 2) {
         const float u = x[k], w = x[k + 1], t = SIGN * s[k / 2];
-        x[k] = u * c[k / 2] - w * t;
-        x[k + 1] = w * c[k / 2] + u * t;
+        if (!PART || at.a + k < 2 * p.half) {
+          x[k] = u * c[k / 2] - w * t;
+          x[k + 1] = w * c[k / 2] + u * t;
+        }
         const float d = y[k], e = y[k + 1], r = SIGN * s[(V + k) / 2];
-        y[k] = d * c[(V + k) / 2] - e * r;
-        y[k + 1] = e * c[(V + k) / 2] + d * r;
+        if (!PART || at.b + k < 2 * p.half) {
+          y[k] = d * c[(V + k) / 2] - e * r;
+          y[k + 1] = e * c[(V + k) / 2] + d * r;
+        }
       }
     } else {
       __syncwarp();
@@ -208,19 +218,23 @@ struct Factors {
       }
     }
   }
-  __device__ __forceinline__ void apply(f32x2 (&x)[E], f32x2 (&y)[E]) const {
+  template <bool PART>
+  __device__ __forceinline__ void apply(const RotaryParams& p, const Lane<V, MODE>& at,
+                                        f32x2 (&x)[E], f32x2 (&y)[E]) const {
 #pragma unroll
     for (int k = 0; k < E; ++k) {
+      const f32x2 u = mul2(x[k], a[k]), v = mul2(y[k], c[k]);
       if constexpr (MODE == kHalves) {
-        const f32x2 u = fma2(y[k], b[k], mul2(x[k], a[k]));
-        y[k] = fma2(x[k], d[k], mul2(y[k], c[k]));
-        x[k] = u;
+        const bool in = !PART || at.a < p.half;
+        const f32x2 w = in ? fma2(y[k], b[k], u) : u;
+        y[k] = in ? fma2(x[k], d[k], v) : v;
+        x[k] = w;
       } else if constexpr (MODE == kNeighbours) {
-        x[k] = fma2(swapped(x[k]), b[k], mul2(x[k], a[k]));
-        y[k] = fma2(swapped(y[k]), d[k], mul2(y[k], c[k]));
+        x[k] = !PART || at.a + 2 * k < 2 * p.half ? fma2(swapped(x[k]), b[k], u) : u;
+        y[k] = !PART || at.b + 2 * k < 2 * p.half ? fma2(swapped(y[k]), d[k], v) : v;
       } else {
-        x[k] = mul2(x[k], a[k]);
-        y[k] = mul2(y[k], c[k]);
+        x[k] = u;
+        y[k] = v;
       }
     }
   }
@@ -237,7 +251,7 @@ __device__ __forceinline__ void turn_apart(const RotaryParams& p, const float2* 
     const float2 a = split(x[k]), b = split(y[k]);
     u[2 * k] = a.x, u[2 * k + 1] = a.y, v[2 * k] = b.x, v[2 * k + 1] = b.y;
   }
-  Angles<2 * E, MODE>().template turn<1>(p, cs, row, at, u, v);
+  Angles<2 * E, MODE>().template turn<1, false>(p, cs, row, at, u, v);
 #pragma unroll
   for (int k = 0; k < E; ++k) {
     x[k] = pair(u[2 * k], u[2 * k + 1]);
@@ -273,7 +287,7 @@ struct Shared {
 // token's angles are found.
 constexpr int kSteps = 4;
 
-template <typename T, int G, int MODE>
+template <typename T, int G, int MODE, bool PART>
 __global__ void __launch_bounds__(kThreads, 2)
     rotary_fwd_vec(const __grid_constant__ RotaryParams p, int per_unit) {
   constexpr int V = Traits<T>::kVec, HPS = 32 / G;
@@ -349,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           x[k] = mul2(x[k], r);
           y[k] = mul2(y[k], r);
         }
-        factors.apply(x, y);
+        factors.template apply<PART>(p, at, x, y);
         if constexpr (MODE == kApart) turn_apart(p, sh.cs[warp], row, at, x, y);
         if (h < end && at.a < p.dim) store_pairs(out + h * s.out.sh + at.a, x);
         if (h < end && at.b < p.dim) store_pairs(out + h * s.out.sh + at.b, y);
@@ -361,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 // The backward: a CTA has one side, so that its sums of du vh stay in registers.
 constexpr int kBwdSteps = 2;
 
-template <typename T, int G, int MODE>
+template <typename T, int G, int MODE, bool PART>
 __global__ void __launch_bounds__(kThreads, 2)
     rotary_bwd_vec(const __grid_constant__ RotaryParams p, int per_unit) {
   constexpr int V = Traits<T>::kVec, HPS = 32 / G;
@@ -410,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         float x[V], y[V], dx[V], dz[V];
         unpack<T>(wa[i], dx);
         unpack<T>(wb[i], dz);
-        angles.template turn<-1>(p, sh.cs[warp], row, at, dx, dz);
+        angles.template turn<-1, PART>(p, sh.cs[warp], row, at, dx, dz);
         unpack<T>(va[i], x);
         unpack<T>(vb[i], y);
         float dot = 0.f;
@@ -482,9 +496,9 @@ int heads_per_unit(int64_t tokens, int heads, int hps, int steps, int64_t warps)
   return n * hps;
 }
 
-template <typename T, int G, int MODE>
+template <typename T, int G, int MODE, bool PART>
 cudaError_t launch_fwd_g(const RotaryParams& p, cudaStream_t s) {
-  auto kern = rotary_fwd_vec<T, G, MODE>;
+  auto kern = rotary_fwd_vec<T, G, MODE, PART>;
   int dev = 0;
   const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -497,9 +511,9 @@ cudaError_t launch_fwd_g(const RotaryParams& p, cudaStream_t s) {
                        p, per);
 }
 
-template <typename T, int G, int MODE>
+template <typename T, int G, int MODE, bool PART>
 cudaError_t launch_bwd_g(RotaryParams& p, cudaStream_t s) {
-  constexpr auto kern = rotary_bwd_vec<T, G, MODE>;
+  constexpr auto kern = rotary_bwd_vec<T, G, MODE, PART>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = allow_launch<kern>(dev, 0);
@@ -521,14 +535,18 @@ cudaError_t launch_bwd_g(RotaryParams& p, cudaStream_t s) {
                        s, cluster, p, per);
 }
 
-// f(G, MODE) of the kernel for a row's lanes.
+// f(G, MODE, PART) of the kernel for a row's lanes.
 template <typename T, typename F>
 bool with_kernel(const RotaryParams& p, F f) {
   const int mode = mode_of<T>(p), lanes = lanes_of(p, Traits<T>::kVec, mode);
   auto by_mode = [&](auto g) {
-    if (mode == kHalves) f(g, std::integral_constant<int, kHalves>{});
-    else if (mode == kNeighbours) f(g, std::integral_constant<int, kNeighbours>{});
-    else f(g, std::integral_constant<int, kApart>{});
+    auto by_part = [&](auto m) {
+      if (2 * p.half < p.dim) f(g, m, std::true_type{});
+      else f(g, m, std::false_type{});
+    };
+    if (mode == kHalves) by_part(std::integral_constant<int, kHalves>{});
+    else if (mode == kNeighbours) by_part(std::integral_constant<int, kNeighbours>{});
+    else f(g, std::integral_constant<int, kApart>{}, std::false_type{});
     return true;
   };
   if (lanes <= 4) return by_mode(std::integral_constant<int, 4>{});
@@ -550,8 +568,8 @@ bool with_type(int dtype, F f) {
 bool try_launch_rotary_fwd_vec(int dtype, const RotaryParams& p, cudaStream_t s, cudaError_t* err) {
   return p.vec_ok && with_type(dtype, [&](auto t) {
     using T = decltype(t);
-    return with_kernel<T>(p, [&](auto g, auto m) {
-      *err = launch_fwd_g<T, decltype(g)::value, decltype(m)::value>(p, s);
+    return with_kernel<T>(p, [&](auto g, auto m, auto part) {
+      *err = launch_fwd_g<T, decltype(g)::value, decltype(m)::value, decltype(part)::value>(p, s);
     });
   });
 }
@@ -559,8 +577,8 @@ bool try_launch_rotary_fwd_vec(int dtype, const RotaryParams& p, cudaStream_t s,
 bool try_launch_rotary_bwd_vec(int dtype, RotaryParams& p, cudaStream_t s, cudaError_t* err) {
   return p.vec_ok && with_type(dtype, [&](auto t) {
     using T = decltype(t);
-    return with_kernel<T>(p, [&](auto g, auto m) {
-      *err = launch_bwd_g<T, decltype(g)::value, decltype(m)::value>(p, s);
+    return with_kernel<T>(p, [&](auto g, auto m, auto part) {
+      *err = launch_bwd_g<T, decltype(g)::value, decltype(m)::value, decltype(part)::value>(p, s);
     });
   });
 }

@@ -1,8 +1,14 @@
-"""Calls of the head norm with rotation at its edges: frequencies of the user's own."""
+"""Calls of the head norm with rotation at its edges: frequencies of the user's own,
+values that are not finite.
+
+Tolerances as in test_rotary_gpu.py: y within h |y| + 2e-6 (|u_i| + |u_j|), dgamma
+within ((n + 64) u + 2e-6) sum |vh| (|dy_i| + |dy_j|) over its n rows."""
 import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
+INF, NAN = float("inf"), float("nan")
+U = 2.0 ** -24
 
 
 @pytest.fixture(scope="module")
@@ -25,3 +31,81 @@ def test_assigned_frequencies_move_to_the_gpu(L):
     got = m(q, k)
     ref = L.rms_norm_rotary_fwd(q, k, m.q_weight, m.k_weight, want.cuda())
     assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+def partner(dim, rot, interleaved):
+    """The other column of each column's pair, -1 where it does not rotate."""
+    j = torch.arange(dim, device="cuda")
+    other = j ^ 1 if interleaved else torch.where(j < rot // 2, j + rot // 2, j - rot // 2)
+    return torch.where(j < rot, other, -1)
+
+
+def turned(t, at, freq, other, interleaved, sign):
+    """Rows t [tokens, heads, dim] with the first columns turned, element for element."""
+    rot = int((other >= 0).sum())
+    j = torch.arange(rot, device="cuda")
+    pair = j // 2 if interleaved else j % (rot // 2)
+    first = j % 2 == 0 if interleaved else j < rot // 2
+    angle = (at[:, None].double() * freq)[:, pair]
+    c, s = angle.cos()[:, None], angle.sin()[:, None] * sign
+    u, w = t[..., :rot], t[..., other[:rot]]
+    return torch.cat((torch.where(first, u * c - w * s, u * c + w * s), t[..., rot:]), -1)
+
+
+def same_kind(got, ref, most, what):
+    """Equal where ref is not finite, within `most` of it elsewhere."""
+    got = got.double()
+    fine = torch.where(ref.isfinite(), (got - ref).abs() <= most,
+                       (got == ref) | (got.isnan() & ref.isnan()))
+    assert bool(fine.all()), (what, (~fine).nonzero()[0].tolist(), got[~fine][0], ref[~fine][0])
+
+
+# whole vectors of halves, neighbours (a part of a vector), halves of no whole vectors,
+# rows of no whole vectors
+@pytest.mark.parametrize("dim,rot,interleaved", [(64, 32, False), (64, 32, True), (64, 18, True),
+                                                 (64, 64, True), (72, 36, False), (256, 128, False),
+                                                 (33, 20, False), (33, 20, True)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_columns_that_do_not_rotate_keep_what_is_not_finite(L, dim, rot, interleaved, dtype):
+    g = torch.Generator().manual_seed(3)
+    make = lambda *s: torch.randn(*s, generator=g).to(dtype).cuda()  # noqa: E731
+    n, heads, h = 2 * (dim - rot) + 2, 3, torch.finfo(dtype).eps / 2
+    q, dy, clean = make(n, heads, dim), make(n, heads, dim), make(dim) * 0.3 + 1
+    at, other = torch.arange(n, device="cuda"), partner(dim, rot, interleaved)
+    freq = 10000.0 ** (torch.arange(rot // 2, device="cuda", dtype=torch.float64) * (-2.0 / rot))
+    # of every column that does not rotate an infinity and a NaN, in rows of their own
+    bad_q, bad_dy = q.clone(), dy.clone()
+    for i, j in enumerate(range(rot, dim)):
+        bad_q[2 * i, i % heads, j], bad_q[2 * i + 1, i % heads, j] = -INF, NAN
+        bad_dy[2 * i, i % heads, j] = INF
+    gammas = [clean]
+    for j in sorted({rot, rot + 1, (rot + dim) // 2, dim - 1} & set(range(rot, dim))):
+        for value in (INF, NAN):
+            gammas.append(clean.clone())
+            gammas[-1][j] = value
+
+    def check(v, up, gamma):
+        y, _, rstd, _ = L.rms_norm_rotary_fwd(v, None, gamma, None, freq, eps=1e-6,
+                                              interleaved=interleaved)
+        x, w, d = v.double(), gamma.double(), up.double()
+        r = (x.square().mean(-1, keepdim=True) + 1e-6).rsqrt()
+        same_kind(rstd, r[..., 0], 1e-6 * r[..., 0], "rstd")
+        u = x * r * w
+        ref = turned(u, at, freq, other, interleaved, 1)
+        pair = lambda t: t.abs() + torch.where(other >= 0, t[..., other].abs(), 0.0)  # noqa: E731
+        same_kind(y, ref, h * ref.abs() + 2e-6 * pair(u) + 2.0 ** -24, "y")
+        back = L.rms_norm_rotary_bwd(up, None, v, None, gamma, None, rstd, None, freq,
+                                     interleaved=interleaved)
+        r = rstd.double()[..., None]
+        du, vh = turned(d, at, freq, other, interleaved, -1), x * r
+        ref = (du * vh).sum((0, 1))
+        same_kind(back[2], ref, ((n * heads + 64) * U + 2e-6) * (vh.abs() * pair(d)).sum((0, 1)),
+                  "dgamma")
+        fine = (r * (du * w - vh * (du * w * vh).mean(-1, keepdim=True))).isfinite()
+        assert torch.equal(back[0].isfinite(), fine)
+
+    for gamma in gammas:
+        check(q, dy, gamma)
+    check(bad_q, dy, clean)
+    check(q, bad_dy, clean)
+    check(bad_q, bad_dy, clean)
