@@ -16,7 +16,6 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty_like.h>
-#include <c10/core/TensorImpl.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -123,20 +122,6 @@ bool usual_call(const Arg& x, const Arg& res, const Arg& post, const Arg& gate, 
 at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type, int device) {
   return at::Tensor(at::detail::empty_cuda(
       sizes, type, at::Device(at::kCUDA, (c10::DeviceIndex)device), std::nullopt));
-}
-
-// Two new fp32 tensors in one allocation (1.2 us each have of a call, 0.6 the
-// second one so): for results that are kept and dropped together.
-void empty_pair(at::IntArrayRef a, at::IntArrayRef b, int device, at::Tensor* first,
-                at::Tensor* second) {
-  const int64_t na = c10::multiply_integers(a), nb = c10::multiply_integers(b);
-  *first = empty({na + nb}, at::kFloat, device);
-  auto impl = c10::make_intrusive<c10::TensorImpl>(
-      c10::TensorImpl::VIEW, c10::Storage(first->storage()), first->key_set(), first->dtype());
-  impl->set_storage_offset(na);
-  impl->set_sizes_contiguous(b);
-  *second = at::Tensor(std::move(impl));
-  first->unsafeGetTensorImpl()->set_sizes_contiguous(a);
 }
 
 at::Tensor bytes(size_t n, int device) {
@@ -565,8 +550,6 @@ PyObject* rotary_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       const Unlocked unlocked;
       if (!qo.defined()) qo = heads_like(*c.q, c.device);
       if (!ko.defined() && c.k) ko = heads_like(*c.k, c.device);
-      if (rq.wanted && rk.wanted && !rq.t.defined() && !rk.t.defined())
-        empty_pair(rq.sizes, rk.sizes, c.device, &rq.t, &rk.t);
       rq.make();
       rk.make();
       const rmsn_heads q = heads_of(*c.q), q_out = heads_of(qo);
@@ -617,8 +600,8 @@ PyObject* rotary_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       const Unlocked unlocked;
       if (!dq.defined()) dq = heads_like(*c.q, c.device);
       if (!dk.defined() && c.k) dk = heads_like(*c.k, c.device);
-      if (c.k) empty_pair({c.dim}, {c.dim}, c.device, &dgq, &dgk);
-      else dgq = empty({c.dim}, at::kFloat, c.device);
+      dgq = empty({c.dim}, at::kFloat, c.device);
+      if (c.k) dgk = empty({c.dim}, at::kFloat, c.device);
       const size_t need = more.rotary_ws(c.batch, c.tokens, c.hq, c.hk, c.dim);
       if (need > 0 && !ws.defined()) ws = bytes(need, c.device);
       const rmsn_heads q = heads_of(*c.q), up_q = heads_of(*uq), out_q = heads_of(dq);

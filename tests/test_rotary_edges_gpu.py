@@ -1,5 +1,5 @@
 """Calls of the head norm with rotation at its edges: frequencies of the user's own,
-values that are not finite.
+values that are not finite, what becomes of results by themselves.
 
 Tolerances as in test_rotary_gpu.py: y within h |y| + 2e-6 (|u_i| + |u_j|), dgamma
 within ((n + 64) u + 2e-6) sum |vh| (|dy_i| + |dy_j|) over its n rows."""
@@ -109,3 +109,24 @@ def test_columns_that_do_not_rotate_keep_what_is_not_finite(L, dim, rot, interle
     check(bad_q, dy, clean)
     check(q, bad_dy, clean)
     check(bad_q, bad_dy, clean)
+
+
+@pytest.mark.parametrize("tokens", [9, 700])
+def test_each_result_has_memory_of_its_own(L, tokens):
+    g = torch.Generator().manual_seed(5)
+    make = lambda *s: torch.randn(*s, generator=g).cuda()  # noqa: E731
+    q, k, w, v = make(tokens, 4, 64), make(tokens, 2, 64), make(64), make(64)
+    freq = torch.ones(32, device="cuda")
+    out = L.rms_norm_rotary_fwd(q, k, w, v, freq)
+    back = L.rms_norm_rotary_bwd(out[0], out[1], q, k, w, v, out[2], out[3], freq)
+    want = [t.clone() for t in (*out, *back)]
+    assert len({t.untyped_storage().data_ptr() for t in (*out, *back)}) == 8
+    # what a user does with one leaves the others what they are: it grows, or gives its memory back
+    out[2].resize_(2 * tokens * 4).fill_(7.0)
+    back[2].resize_(128).fill_(7.0)
+    assert torch.equal(out[3], want[3]) and torch.equal(back[3], want[7])
+    leaves = [t.clone().requires_grad_() for t in (q, k, w, v)]
+    torch.autograd.backward(L.rms_norm_rotary(*leaves, freq), out[:2])
+    assert torch.equal(leaves[2].grad, want[6]) and torch.equal(leaves[3].grad, want[7])
+    leaves[2].grad.untyped_storage().resize_(0)
+    assert torch.equal(leaves[3].grad, want[7])
