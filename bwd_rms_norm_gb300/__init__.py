@@ -1792,6 +1792,8 @@ class RMSNormEmbeddingFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, ids, weight, scale, padding_idx, dtype):
+        if padding_idx is not None and not 0 <= padding_idx < weight.shape[0]:
+            raise RMSNormError("rms_norm_embedding", RMSN_ERR_ARG)  # as the backward would
         ids, weight = ids.contiguous(), weight.contiguous()
         ctx.save_for_backward(ids)
         ctx.table = weight.shape[0], weight.dtype, scale, padding_idx
@@ -1810,8 +1812,8 @@ def rms_norm_embedding(ids: torch.Tensor, weight: torch.Tensor, scale: float = 1
                        padding_idx: Optional[int] = None,
                        dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """Differentiable ``rms_norm_embedding_fwd``, in the weight.  Tokens of
-    ``padding_idx`` take their row, and give it no gradient.  Captured into a
-    CUDA graph as ``rms_norm_rotary``."""
+    ``padding_idx``, a row of the table, take it, and give it no gradient.
+    Captured into a CUDA graph as ``rms_norm_rotary``."""
     return RMSNormEmbeddingFunction.apply(ids, weight, scale, padding_idx, dtype)
 
 

@@ -49,3 +49,15 @@ def test_frequencies_of_a_module_made_without_memory(L):
     m = L.RMSNormRotary(64, rotary_dim=32, device="meta")
     m.inv_freq = want / 3
     assert torch.equal(m.to_empty(device="cpu").inv_freq, want / 3)
+
+
+def test_padding_outside_the_table_is_refused_with_the_call(L):
+    """Not by the backward alone, in the middle of a step."""
+    ids, w = torch.zeros(4, dtype=torch.int64), torch.zeros(8, 16, requires_grad=True)
+    for pad in (-1, 8, 1 << 40):
+        with pytest.raises(L.RMSNormError) as e:
+            L.rms_norm_embedding(ids, w, padding_idx=pad)
+        assert e.value.status == 8
+    for pad in (None, 0, 7):                # refused for another reason: not on a GPU
+        with pytest.raises(RuntimeError, match="CUDA tensor"):
+            L.rms_norm_embedding(ids, w, padding_idx=pad)
