@@ -1,5 +1,5 @@
 """Calls of the head norm with rotation at its edges: frequencies of the user's own,
-values that are not finite, what becomes of results by themselves.
+values that are not finite, what becomes of results by themselves, SM budgets.
 
 Tolerances as in test_rotary_gpu.py: y within h |y| + 2e-6 (|u_i| + |u_j|), dgamma
 within ((n + 64) u + 2e-6) sum |vh| (|dy_i| + |dy_j|) over its n rows."""
@@ -130,3 +130,37 @@ def test_each_result_has_memory_of_its_own(L, tokens):
     assert torch.equal(leaves[2].grad, want[6]) and torch.equal(leaves[3].grad, want[7])
     leaves[2].grad.untyped_storage().resize_(0)
     assert torch.equal(leaves[3].grad, want[7])
+
+
+@pytest.mark.parametrize("tokens,dim", [(60, 128), (500, 128), (500, 33)])
+def test_same_bits_under_the_same_budget(L, tokens, dim):
+    g = torch.Generator().manual_seed(6)
+    make = lambda *s: torch.randn(*s, generator=g).bfloat16().cuda()  # noqa: E731
+    q, k, dq, dk = (make(tokens, n, dim) for n in (8, 2, 8, 2))
+    w, v, freq = make(dim), make(dim), torch.ones(dim // 2, device="cuda")
+    rstd = L.rms_norm_rotary_fwd(q, k, w, v, freq)[2:]
+    back = lambda: L.rms_norm_rotary_bwd(dq, dk, q, k, w, v, *rstd, freq)  # noqa: E731
+    # two sums of the same terms in fp32, each within (n + 64) u of the terms' sizes
+    other, off = partner(dim, dim // 2 * 2, False), []
+    for x, up, r in ((q, dq, rstd[0]), (k, dk, rstd[1])):
+        d = up.double().abs()
+        size = (x.double() * r.double()[..., None]).abs() * (
+            d + torch.where(other >= 0, d[..., other], 0.0))
+        off.append(2 * (r.numel() + 64) * U * size.sum((0, 1)))
+    whole = back()
+    bits = set()
+    try:
+        for sms in (1, 7, 40, 0):
+            L.rms_norm_set_sm_budget(sms)
+            assert sms == 0 or L.rms_norm_sm_budget() == sms
+            first = back()
+            for _ in range(3):
+                assert all(torch.equal(a, b) for a, b in zip(first, back()))
+            # the rows' gradients know nothing of the budget; the sums' order does
+            assert torch.equal(first[0], whole[0]) and torch.equal(first[1], whole[1])
+            for a, b, most in zip(first[2:], whole[2:], off):
+                assert bool(((a - b).double().abs() <= most).all())
+            bits.add(first[2].cpu().numpy().tobytes())
+    finally:
+        L.rms_norm_set_sm_budget(0)
+    assert torch.equal(back()[2], whole[2]) and len(bits) > 1
