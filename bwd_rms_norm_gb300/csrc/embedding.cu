@@ -4,9 +4,14 @@
 namespace rmsn {
 namespace {
 
-constexpr int kWide = 4;
+// A warp takes K times 32 E columns of a token's row, all loads under way together:
+// kWide times where that leaves kWideWarps units an SM of rows cut so, else one.
+// Large batches gain (32768 x 4096 bf16 80.9 us by ones, 79.5; 32768 x 1024 21.1 and
+// 20.4), the smallest lose warps (256 x 1024 2.1 us by ones, 2.6 by fours).  Columns
+// left over cost a warp (8192 x 1088 8.8 by ones, 10.0), and batches between would
+// gain too (2048 x 1024 3.6 us by ones, as the rule has it, 2.7 by fours).
+constexpr int kWide = 4, kWideWarps = 32;
 
-// A warp takes K times 32 E columns of a token's row, all loads under way together.
 template <typename T, typename U, bool VEC, int K>
 __global__ void __launch_bounds__(kThreads) embedding_rows(Ids ids, const T* weight, U* y,
                                                            int64_t tokens, int64_t vocab,
@@ -57,7 +62,10 @@ int rms_norm_embedding_fwd(const void* ids, int ids_64, const void* weight, void
       out.meets(Span(ids, (size_t)tokens * ib)))
     return RMSN_ERR_ARG;
   const Ids of = {ids, ids_64};
-  const cudaError_t e = with_types(weight_dtype, y_dtype, [&](auto t, auto u) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  e = with_types(weight_dtype, y_dtype, [&](auto t, auto u) {
     using T = decltype(t);
     using U = decltype(u);
     constexpr int E = kElems<T, U>;
@@ -68,7 +76,7 @@ int rms_norm_embedding_fwd(const void* ids, int ids_64, const void* weight, void
                           static_cast<U*>(y), tokens, vocab, (int)hidden, scale);
     };
     constexpr int K = kWide;
-    if (vec && tokens * (hidden / (32 * E * K)) >= 4864)
+    if (vec && tokens * (hidden / (32 * E * K)) >= (int64_t)kWideWarps * sm_count(dev))
       return launch(embedding_rows<T, U, true, K>, K);
     return vec ? launch(embedding_rows<T, U, true, 1>, 1)
                : launch(embedding_rows<T, U, false, 1>, 1);
