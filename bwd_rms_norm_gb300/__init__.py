@@ -1320,7 +1320,8 @@ def rms_norm_rotary_fwd(q: torch.Tensor, k: Optional[torch.Tensor], q_gamma: tor
     head's first ``2 * pairs`` columns, halves of them paired, or neighbours
     where ``interleaved``; None rotates nothing.  ``positions`` (int32 or
     int64) is [tokens] or q's leading dimensions; None: 0, 1, ... in every
-    batch entry.  Returns ``(q_out, k_out, rstd_q, rstd_k)``: outputs like
+    batch entry; the angle is off by 2^-63 of a turn a position, nothing that
+    fp32 shows at positions up to 2^31.  Returns ``(q_out, k_out, rstd_q, rstd_k)``: outputs like
     ``torch.empty_like`` of the inputs, or those given (any strides; the inputs
     themselves for a call in place), and the fp32 statistics that the backward
     reads (None without ``with_rstd``, as in serving)."""
@@ -1455,7 +1456,7 @@ def rms_norm_embedding_fwd(ids: torch.Tensor, weight: torch.Tensor, scale: float
     """The rows of ``weight`` [vocab, hidden] at ``ids`` (int32 or int64, any
     shape), times ``scale``: ``y`` of shape [*ids.shape, hidden] in ``dtype`` (the
     weight's, or float32 from or to a 16-bit one).  An id outside [0, vocab), as a
-    batch's padding, gives a row of zeros."""
+    batch's padding, gives a row of zeros.  No norm is applied."""
     lib = load_library()
     if _binding is not None and stream is None:
         got = _binding.embedding_fwd(ids, weight, scale, dtype, y)
@@ -1820,7 +1821,8 @@ def rms_norm_embedding(ids: torch.Tensor, weight: torch.Tensor, scale: float = 1
 class RMSNormEmbedding(torch.nn.Module):
     """A table of ``vocab`` rows, of which a batch of tokens takes its own, times
     ``scale``; ``out_dtype`` float32 begins an fp32 residual stream under 16-bit
-    weights (as ``RMSNormBlock`` carries it)."""
+    weights (as ``RMSNormBlock`` carries it).  The name has the library's prefix:
+    no norm is applied to the rows."""
 
     def __init__(self, vocab: int, hidden: int, scale: float = 1.0,
                  padding_idx: Optional[int] = None, out_dtype: Optional[torch.dtype] = None,

@@ -54,8 +54,9 @@ __device__ __forceinline__ uint64_t fixed_turns(const RotaryParams& p, int i) {
   return (uint64_t)((long long)(part * 0x1p64)) + (uint64_t)((long long)(rest * 0x1p64));
 }
 
-// (cos, sin) of a position's angle, from 32 bits of its turn (2^-33 turns off)
-// as an fp32 part of a half turn (2^-25).
+// (cos, sin) of a position's angle, from the upper 32 bits of its turn (low by less
+// than 2^-32 of one) as an fp32 part of a half turn (off by 2^-25 of one at most,
+// which is 2^6 times as much).
 __device__ __forceinline__ float2 turn_of(uint64_t fixed, int64_t position) {
   const int part = (int)((fixed * (uint64_t)position) >> 32);
   float2 cs;
@@ -75,8 +76,11 @@ __device__ __forceinline__ int64_t row_at(const HeadView& v, int b, int t, int h
 }
 
 // Few rows: the sums of the gammas' gradients stay inside a cluster of CTAs for
-// each side, without partial rows and a second kernel (256 x (8+8) x 64 fp32 a
-// call 11.6 us with them, 7.0 without).
+// each side, without workspace, partial rows and a second kernel.  It is the calls
+// that gain: 256 x (8+8) x 64 fp32 11.9 us with partial rows, 7.2 so, 64 x (32+8) x
+// 128 bf16 11.8 and 8.7.  In a graph, where a launch costs little, the clusters'
+// passes over the rows take longer but for the fewest: 4.8 and 6.9 us, 5.5 and 8.6;
+// 8 x (32+8) x 128 5.2 and 4.8.
 inline bool few_rows(int64_t all, int64_t q_heads, int64_t k_heads, int64_t dim) {
   const int64_t rows = all * (q_heads > k_heads ? q_heads : k_heads);
   return rows <= 2048 && rows * dim <= 1 << 18;
